@@ -83,6 +83,7 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_BLOCK 2      /* attention: block id outside [0, num_blocks) (block skipped) */
 #define PKV_DEV_TIMEOUT 3        /* a pipeline wait exceeded its bound (tile abandoned) */
 #define PKV_DEV_PLAN_MISMATCH 4  /* device cu_q_lens/context_lens disagree with the plan */
+#define PKV_DEV_BAD_POSITION 5   /* rotating append: position >= max_positions (token skipped) */
 
 typedef struct pkv_pool_desc {
   int32_t num_blocks;   /* physical blocks in kv_pool */
@@ -153,6 +154,8 @@ PKV_API int64_t pkv_kernel_launch_count(void);
 #define PKV_KERNEL_MERGE 2
 #define PKV_KERNEL_PREFILL 3
 #define PKV_KERNEL_STATE 4
+#define PKV_KERNEL_ROPE 5   /* pkv_rope_kv_append and pkv_rope_kv_append_fp8 */
+#define PKV_KERNEL_STAGE 6  /* 8-bit attention: bf16 copies of the tensor-core sequences' blocks */
 
 /*
  * Profiling hook (off by default).  After this call, every launch of kernel
@@ -186,6 +189,85 @@ PKV_API pkv_status pkv_set_profile_events(int32_t which, void *start_event, void
 PKV_API pkv_status pkv_paged_kv_append(const void *k, const void *v, const int32_t *slot_mapping,
                                int32_t num_tokens, void *kv_pool, const pkv_pool_desc *desc,
                                int32_t *dev_status, pkv_stream stream);
+
+/* The position rotation of the two appends below. */
+typedef struct pkv_rope {
+  const float *cos_sin;     /* device fp32 [max_positions][rotary_dim]: of each position the
+                               rotary_dim / 2 cosines, then the rotary_dim / 2 sines */
+  const int32_t *positions; /* device int32 [num_tokens] */
+  int32_t max_positions;
+  int32_t rotary_dim;       /* elements of a head that are rotated, the first ones: a multiple
+                               of 16, at most head_dim; the others pass through */
+  int32_t interleaved;      /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2 i, 2 i + 1) */
+} pkv_rope;
+
+/*
+ * KV append with the position rotation applied on the way (one kernel in place
+ * of a rotation of q and k followed by pkv_paged_kv_append).
+ *   For each token t < num_tokens at position p = positions[t], each head of q
+ *   and k and each pair i < rotary_dim / 2 of its elements (a, b):
+ *     a' = a cos[p][i] - b sin[p][i],   b' = b cos[p][i] + a sin[p][i],
+ *   evaluated in fp32 (each product and sum rounded) and rounded once to bf16.
+ *   q_out[t] gets the rotated q; with slot = slot_mapping[t] the pool gets the
+ *   rotated k and v as pkv_paged_kv_append writes them:
+ *     slot < 0                 : no k or v written (q is rotated all the same);
+ *     slot >= num_blocks*bs    : k and v skipped, PKV_DEV_BAD_SLOT to *dev_status;
+ *     p < 0                    : padding: nothing of the token is read or written;
+ *     p >= max_positions       : the token skipped, PKV_DEV_BAD_POSITION.
+ *   q: device bf16 [num_tokens][num_q_heads][D], k, v: [num_tokens][Hkv][D], the
+ *   heads of a token contiguous, consecutive tokens q_stride, k_stride, v_stride
+ *   elements apart (>= heads * D, a multiple of 8), so the three may be parts of
+ *   one packed projection.  q_out: as q, with q_out_stride; it may be q itself
+ *   with the same stride (rotation in place), and must not overlap the inputs
+ *   otherwise.  num_q_heads = 0: k and v only (q, q_out ignored).
+ *   Two tokens with the same slot: unspecified which one lands.  num_tokens == 0
+ *   enqueues nothing.  Errors: PKV_ERR_UNSUPPORTED (rotary_dim), PKV_ERR_SHAPE
+ *   (a negative count, a stride), PKV_ERR_NULL, PKV_ERR_ALIGN (16 bytes; 4 for
+ *   positions and slot_mapping).
+ *   The kernel lets its dependents launch only when it has finished, so
+ *   pkv_paged_varlen_attention may follow it directly with q = q_out.
+ */
+PKV_API pkv_status pkv_rope_kv_append(const void *q, int64_t q_stride, const void *k,
+                                      int64_t k_stride, const void *v, int64_t v_stride,
+                                      const pkv_rope *rope, const int32_t *slot_mapping,
+                                      int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                                      int64_t q_out_stride, void *kv_pool,
+                                      const pkv_pool_desc *desc, int32_t *dev_status,
+                                      pkv_stream stream);
+
+/*
+ * The 8-bit pool: kv_pool holds e4m3 values (8-bit floats, 4 exponent and 3
+ * mantissa bits, largest 448) in the bf16 pool's layout, one byte a value, and
+ * kv_scales, device fp32 [num_blocks][Hkv][2], the scale of the K (0) and V (1)
+ * rows of each block and KV head: a stored c stands for c * scale.
+ *
+ * pkv_rope_kv_append_fp8 is pkv_rope_kv_append into such a pool (rope NULL: no
+ * rotation; then num_q_heads must be 0).  For each block, KV head and K or V
+ * that the step writes to, N being its new rows and `first` the smallest offset
+ * among them:
+ *   - rows below `first` are kept rows (the block is filled in order); when
+ *     first is 0 the block is new, and its old scale and bytes do not matter;
+ *   - the scale s stays when first > 0 and 448 s >= max |N|; otherwise it becomes
+ *     the smallest power of two s' >= 2^-64 with 448 s' >= max |N| (infinities
+ *     are left out of the maximum) and each kept value c becomes c s / s';
+ *   - the new rows are stored as x / scale.
+ *   Both are rounded to nearest even and saturate at +-448; NaN stays NaN.  Rows
+ *   past the new ones are left as they were.
+ *   The new tokens of one block must lie within 16 consecutive tokens of the
+ *   step (skipped tokens between them counted): a block is looked after by the
+ *   warp of its first one.  Tokens of one block further apart, like two tokens
+ *   with the same slot, leave that block's values unspecified (where the kernel
+ *   sees it, it skips the later token and reports PKV_DEV_BAD_SLOT).
+ *   Other arguments, skipped tokens and errors as pkv_rope_kv_append; kv_scales
+ *   must be 16-byte aligned.
+ */
+PKV_API pkv_status pkv_rope_kv_append_fp8(const void *q, int64_t q_stride, const void *k,
+                                          int64_t k_stride, const void *v, int64_t v_stride,
+                                          const pkv_rope *rope, const int32_t *slot_mapping,
+                                          int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                                          int64_t q_out_stride, void *kv_pool, float *kv_scales,
+                                          const pkv_pool_desc *desc, int32_t *dev_status,
+                                          pkv_stream stream);
 
 /*
  * Host step metadata (the per-threadgroup search over cu_seqlens that the
@@ -375,6 +457,47 @@ PKV_API pkv_status pkv_paged_varlen_attention(const void *q, const int32_t *cu_q
                                       const pkv_plan_info *info, const void *plan_dev, void *out,
                                       void *workspace, int64_t workspace_bytes,
                                       int32_t *dev_status, pkv_stream stream);
+
+/*
+ * What an 8-bit pool adds to a plan.  The split-KV kernel reads the 8-bit blocks
+ * directly; the tensor-core kernel reads bf16 copies of the blocks its sequences
+ * need, made in the workspace by the same attention call.
+ *   plan, info: a finished HOST plan (pkv_plan_step and its relatives).
+ *   stage_begin: HOST int32 [num_seqs + 1], written: sequence s's blocks 0, 1, ..
+ *   get copies stage_begin[s], stage_begin[s] + 1, .. < stage_begin[s + 1] (none
+ *   for a sequence the tensor cores do not read).
+ *   *workspace_bytes receives the workspace pkv_paged_varlen_attention_fp8 needs.
+ * Upload stage_begin beside the plan.  When stage_begin[num_seqs] is 0 (no
+ * tensor-core work) the attention call takes NULL for it.
+ * Errors: PKV_ERR_NULL, PKV_ERR_SHAPE (info and plan disagree),
+ * PKV_ERR_UNSUPPORTED (more copies than 32-bit row coordinates reach).
+ */
+PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *info,
+                                      int32_t *stage_begin, int64_t *workspace_bytes);
+
+/*
+ * pkv_paged_varlen_attention over an 8-bit pool (layout above): the same step,
+ * plan, rules and results, with K[p] = c_k scale_k and V[p] = c_v scale_v.
+ * kv_scales: any positive finite values (not only powers of two).
+ *   stage_begin: DEVICE copy of pkv_plan_stage_fp8's array; staged_blocks: its
+ *   last entry.  workspace_bytes: at least what pkv_plan_stage_fp8 returned.
+ *   Rounding: on the split-KV kernel every stored value enters the products
+ *   exactly (fp16), the weights are rounded to fp16, 2^-12; on the tensor-core
+ *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the
+ *   weights to bf16, 2^-9.  Accumulation is fp32; out is rounded once to bf16.
+ *   Bytes of a block past its sequence's context are never used, whatever they
+ *   hold.  A NaN stored in a visible row reaches every row of out that sees it,
+ *   and may reach rows of the same sequence's step that come before it.
+ * Kernel order, early launches and errors as pkv_paged_varlen_attention (block
+ * ids are read from the device tables); kv_scales is read after the wait for the
+ * preceding kernel, as kv_pool is.
+ */
+PKV_API pkv_status pkv_paged_varlen_attention_fp8(
+    const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
+    const float *kv_scales, const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
+    const void *plan_dev, const int32_t *stage_begin, int32_t staged_blocks, void *out,
+    void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream);
 
 /*
  * State-row checkpoint (the vllm-metal v0.4.0 page, "Prefix caching on hybrid

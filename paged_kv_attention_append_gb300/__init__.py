@@ -9,6 +9,16 @@ implementation here.  If the library is missing, every call raises.
     kv_pool = torch.empty(num_blocks, 2, Hkv, 16, D, dtype=torch.bfloat16, device="cuda")
     paged_kv_append(k_new, v_new, slot_mapping, kv_pool)
     out = paged_varlen_attention(q, cu_q_lens, context_lens, block_tables, kv_pool, scale)
+
+With the position rotation applied by the append, and with an 8-bit pool:
+
+    q_rot = rope_kv_append(q, k_new, v_new, positions, cos_sin, slot_mapping, kv_pool)
+
+    kv_pool, kv_scales = fp8_pool(num_blocks, Hkv, D, device="cuda")
+    q_rot = rope_kv_append_fp8(q, k_new, v_new, positions, cos_sin, slot_mapping, kv_pool,
+                               kv_scales)
+    out = paged_varlen_attention_fp8(q_rot, cu_q_lens, context_lens, block_tables, kv_pool,
+                                     kv_scales, scale)
 """
 
 from __future__ import annotations
@@ -25,7 +35,9 @@ __all__ = [
     "PkvError", "PoolDesc", "PlanInfo", "StepPlan", "build", "library_path", "version",
     "status_string", "kernel_launch_count", "paged_kv_append", "plan_step",
     "paged_varlen_attention", "DEV_STATUS", "workspace_size", "BoundStep", "BoundPlan",
-    "BoundCopy", "copy_async",
+    "BoundCopy", "copy_async", "rope_cos_sin", "rope_kv_append", "rope_kv_append_fp8",
+    "paged_kv_append_fp8", "fp8_pool", "paged_varlen_attention_fp8", "BoundRopeAppend",
+    "BoundAttentionFp8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +46,7 @@ _lock = threading.Lock()
 _lib = None
 
 DEV_STATUS = {0: "ok", 1: "bad slot", 2: "bad block id", 3: "pipeline wait timed out",
-              4: "plan does not match device metadata"}
+              4: "plan does not match device metadata", 5: "position past the rotation table"}
 
 
 class PkvError(RuntimeError):
@@ -59,6 +71,12 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("max_positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 def build(verbose: bool = False) -> str:
@@ -122,6 +140,17 @@ def _load():
             lib.pkv_planner_post.restype = i32
             lib.pkv_planner_wait.argtypes = [P]
             lib.pkv_planner_wait.restype = i32
+            rope_args = [P, i64, P, i64, P, i64, ctypes.POINTER(Rope), P, i32, i32, P, i64, P]
+            lib.pkv_rope_kv_append.argtypes = rope_args + [ctypes.POINTER(PoolDesc), P, P]
+            lib.pkv_rope_kv_append.restype = i32
+            lib.pkv_rope_kv_append_fp8.argtypes = rope_args + [P, ctypes.POINTER(PoolDesc), P, P]
+            lib.pkv_rope_kv_append_fp8.restype = i32
+            lib.pkv_plan_stage_fp8.argtypes = [P, ctypes.POINTER(PlanInfo), P, ctypes.POINTER(i64)]
+            lib.pkv_plan_stage_fp8.restype = i32
+            lib.pkv_paged_varlen_attention_fp8.argtypes = [
+                P, P, P, P, i32, P, P, ctypes.POINTER(PoolDesc), ctypes.c_float,
+                ctypes.POINTER(PlanInfo), P, P, i32, P, P, i64, P, P]
+            lib.pkv_paged_varlen_attention_fp8.restype = i32
             _lib = lib
     return _lib
 
@@ -138,7 +167,8 @@ def kernel_launch_count() -> int:
     return int(_load().pkv_kernel_launch_count())
 
 
-KERNEL_IDS = {"append": 0, "decode": 1, "merge": 2, "prefill": 3, "state": 4}
+KERNEL_IDS = {"append": 0, "decode": 1, "merge": 2, "prefill": 3, "state": 4, "rope": 5,
+              "stage": 6}
 
 
 def set_profile_events(kernel: str, start=None, stop=None):
@@ -221,6 +251,170 @@ def paged_kv_append(k, v, slot_mapping, kv_pool, *, dev_status=None, stream=None
                                      _stream(stream, kv_pool))
     if st:
         raise PkvError(st, "pkv_paged_kv_append")
+
+
+def rope_cos_sin(max_positions: int, rotary_dim: int, *, base: float = 10000.0, device="cuda"):
+    """The rotation table of positions 0 .. max_positions - 1: fp32 [max_positions,
+    rotary_dim], cosines then sines of position * base^(-2 i / rotary_dim), the
+    angles evaluated in 64 bits (a far position's angle needs them)."""
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = (torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] *
+             torch.pow(torch.tensor(base, dtype=torch.float64, device=device), -i / rotary_dim))
+    return torch.cat([angle.cos(), angle.sin()], dim=1).to(torch.float32)
+
+
+def fp8_pool(num_blocks: int, num_kv_heads: int, head_dim: int, *, device="cuda"):
+    """An 8-bit pool and its scales: (e4m3 [num_blocks, 2, Hkv, 16, D], fp32
+    [num_blocks, Hkv, 2]), all zeros with scales of 1."""
+    pool = torch.zeros((num_blocks, 2, num_kv_heads, 16, head_dim), dtype=torch.uint8,
+                       device=device).view(torch.float8_e4m3fn)
+    return pool, torch.ones((num_blocks, num_kv_heads, 2), dtype=torch.float32, device=device)
+
+
+def _check_rows(name, t, ref=None):
+    """bf16 [n, heads, D] with contiguous heads; tokens may be strided.  Returns
+    the token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    if ref is not None and t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}")
+    n, heads, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    stride = t.stride(0) if n > 1 else heads * d
+    if stride < heads * d or stride % 8 != 0:
+        raise ValueError(f"{name}: the token stride must be a multiple of 8 that covers a token")
+    return stride
+
+
+def _check_fp8_pool(kv_pool, kv_scales):
+    _check_cuda("kv_pool", kv_pool, torch.float8_e4m3fn, 5)
+    _check_cuda("kv_scales", kv_scales, torch.float32, 3)
+    desc = pool_desc(kv_pool)
+    if kv_scales.shape != (desc.num_blocks, desc.num_kv_heads, 2):
+        raise ValueError("kv_scales must be [num_blocks, num_kv_heads, 2]")
+    if kv_scales.device != kv_pool.device:
+        raise ValueError("kv_scales must be on kv_pool's device")
+    return desc
+
+
+class BoundRopeAppend:
+    """A rotating KV append with its arguments checked and marshalled once.
+
+    run() enqueues it on the bound stream: positions, slots and the values of q, k
+    and v are read then, so a loop that rewrites them in place calls run() once
+    per step.  Arguments as rope_kv_append and, with kv_scales, rope_kv_append_fp8;
+    `q_out` holds the rotated q (allocated here when not given)."""
+
+    def __init__(self, q, k, v, positions, cos_sin, slot_mapping, kv_pool, *, kv_scales=None,
+                 q_out=None, interleaved=False, dev_status=None, stream=None):
+        if kv_scales is None:
+            _check_cuda("kv_pool", kv_pool, torch.bfloat16, 5)
+            desc = pool_desc(kv_pool)
+        else:
+            desc = _check_fp8_pool(kv_pool, kv_scales)
+        ks, vs = _check_rows("k", k, kv_pool), _check_rows("v", v, kv_pool)
+        _check_cuda("slot_mapping", slot_mapping, torch.int32, 1)
+        n = slot_mapping.shape[0]
+        if k.shape != (n, desc.num_kv_heads, desc.head_dim) or v.shape != k.shape:
+            raise ValueError(f"k/v must be [{n}, {desc.num_kv_heads}, {desc.head_dim}]")
+        small = [("slot_mapping", slot_mapping), ("dev_status", dev_status)]
+        rope = None
+        if cos_sin is not None:
+            _check_cuda("cos_sin", cos_sin, torch.float32, 2)
+            _check_cuda("positions", positions, torch.int32, 1)
+            small += [("cos_sin", cos_sin), ("positions", positions)]
+            if positions.shape[0] != n:
+                raise ValueError("positions needs one entry per token")
+            rope = Rope(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0],
+                        cos_sin.shape[1], int(bool(interleaved)))
+        elif q is not None or kv_scales is None:
+            raise ValueError("cos_sin may be left out only for the 8-bit append of k and v alone")
+        hq, qs, qos = 0, 0, 0
+        if q is not None:
+            qs = _check_rows("q", q, kv_pool)
+            if q.shape[0] != n or q.shape[2] != desc.head_dim:
+                raise ValueError(f"q must be [{n}, num_q_heads, {desc.head_dim}]")
+            if q_out is None:
+                with torch.cuda.stream(stream) if stream is not None else _nullcontext():
+                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            qos = _check_rows("q_out", q_out, kv_pool)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            if q_out.data_ptr() == q.data_ptr() and qos != qs and n > 1:
+                raise ValueError("rotating q in place needs q_out to have q's strides")
+            hq = q.shape[1]
+        if dev_status is not None:
+            _check_cuda("dev_status", dev_status, torch.int32)
+        for name, t in small:
+            if t is not None and t.device != kv_pool.device:
+                raise ValueError(f"{name} must be on kv_pool's device")
+        self.q_out = q_out
+        self._keep = (q, k, v, positions, cos_sin, slot_mapping, kv_pool, kv_scales, dev_status,
+                      desc, rope)
+        vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        args = [vp(_ptr(q)), i64(qs), vp(k.data_ptr()), i64(ks), vp(v.data_ptr()), i64(vs),
+                None if rope is None else ctypes.byref(rope), vp(slot_mapping.data_ptr()), i32(n),
+                i32(hq), vp(_ptr(q_out)), i64(qos), vp(kv_pool.data_ptr())]
+        if kv_scales is not None:
+            args.append(vp(kv_scales.data_ptr()))
+        self._args = (*args, ctypes.byref(desc), vp(_ptr(dev_status)),
+                      vp(_stream(stream, kv_pool)))
+        self._name = "pkv_rope_kv_append" + ("" if kv_scales is None else "_fp8")
+        self._f = getattr(_load(), self._name)
+        self._device = kv_pool.device.index
+
+    def run(self) -> None:
+        with _on_device(self._device):
+            st = self._f(*self._args)
+        if st:
+            raise PkvError(st, self._name)
+
+
+def rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, kv_pool, *, q_out=None,
+                   interleaved=False, dev_status=None, stream=None):
+    """Rotate q and k by position and write k and v into the pool slots of
+    slot_mapping (pkv_rope_kv_append); returns the rotated q.
+
+    q: bf16 [n, Hq, D] or None (k and v only); k, v: bf16 [n, Hkv, D]; the three may be
+    slices of one packed projection (heads contiguous, tokens strided).
+    positions: int32 [n] (negative: padding, the token is left out); cos_sin: fp32
+    [max_positions, rotary_dim] (rope_cos_sin); interleaved: pairs (2i, 2i + 1)
+    instead of (i, i + rotary_dim / 2).  slot_mapping: int32 [n] (negative: the
+    token's k and v are not written; its q is rotated).  q_out: where the rotated q
+    goes (q itself for a rotation in place; a new tensor by default).
+    """
+    b = BoundRopeAppend(q, k, v, positions, cos_sin, slot_mapping, kv_pool, q_out=q_out,
+                        interleaved=interleaved, dev_status=dev_status, stream=stream)
+    b.run()
+    return b.q_out
+
+
+def rope_kv_append_fp8(q, k, v, positions, cos_sin, slot_mapping, kv_pool, kv_scales, *,
+                       q_out=None, interleaved=False, dev_status=None, stream=None):
+    """rope_kv_append into an 8-bit pool (pkv_rope_kv_append_fp8): kv_pool e4m3
+    [nb, 2, Hkv, 16, D], kv_scales fp32 [nb, Hkv, 2] (K, V scale of each block and head;
+    fp8_pool makes both).  A block's scale grows to the smallest power of two
+    that its new rows need, and the rows it holds are re-expressed.  The new tokens of
+    one block must lie within 16 consecutive tokens of the step."""
+    b = BoundRopeAppend(q, k, v, positions, cos_sin, slot_mapping, kv_pool, kv_scales=kv_scales,
+                        q_out=q_out, interleaved=interleaved, dev_status=dev_status,
+                        stream=stream)
+    b.run()
+    return b.q_out
+
+
+def paged_kv_append_fp8(k, v, slot_mapping, kv_pool, kv_scales, *, dev_status=None, stream=None):
+    """paged_kv_append into an 8-bit pool: rope_kv_append_fp8 without q and without
+    the rotation."""
+    BoundRopeAppend(None, k, v, None, None, slot_mapping, kv_pool, kv_scales=kv_scales,
+                    dev_status=dev_status, stream=stream).run()
 
 
 def state_checkpoint(src, dst_slots, pool, *, dev_status=None, stream=None):
@@ -311,12 +505,16 @@ class BoundCopy:
 class StepPlan:
     """Host step metadata plus its device copy and the workspace it needs."""
 
-    def __init__(self, info: PlanInfo, host: np.ndarray, device: torch.device, stream=None):
+    def __init__(self, info: PlanInfo, host: np.ndarray, device: torch.device, stream=None,
+                 fp8: bool = False):
         self.info = info
         self.host = host
         self.device = device
         self.dev = None
         self.workspace = None
+        self.fp8 = fp8              # planned for an 8-bit pool too (pkv_plan_stage_fp8)
+        self.stage = None           # device int32 [num_seqs + 1], when there are staged blocks
+        self.staged_blocks = 0
         self.upload(stream)
 
     def upload(self, stream=None):
@@ -325,14 +523,52 @@ class StepPlan:
         dev = torch.device(self.device)
         nbytes = max(int(self.info.plan_bytes), 16)
         src = torch.from_numpy(self.host.view(np.uint8)[:nbytes])
+        wsb = workspace_size(self.info)
+        stage = None
+        if self.fp8:
+            stage, wsb = stage_fp8(self.info, self.host)
+            self.staged_blocks = int(stage[-1])
         with torch.cuda.stream(stream) if stream is not None else _nullcontext():
             if self.dev is None or self.dev.numel() < nbytes:
                 self.dev = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             self.dev[:nbytes].copy_(src, non_blocking=False)
-            wsb = workspace_size(self.info)
+            if self.staged_blocks:
+                self.stage = torch.from_numpy(stage).to(dev)
             if wsb > 0 and (self.workspace is None or self.workspace.numel() < wsb):
                 self.workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
         return self
+
+
+def stage_fp8(info: PlanInfo, host: np.ndarray):
+    """(stage_begin int32 [num_seqs + 1], workspace bytes) of a host plan for an
+    8-bit pool (pkv_plan_stage_fp8)."""
+    begin = np.zeros(int(info.num_seqs) + 1, dtype=np.int32)
+    nbytes = ctypes.c_int64(0)
+    st = _load().pkv_plan_stage_fp8(host.ctypes.data_as(ctypes.c_void_p), ctypes.byref(info),
+                                    begin.ctypes.data_as(ctypes.c_void_p), ctypes.byref(nbytes))
+    if st:
+        raise PkvError(st, "pkv_plan_stage_fp8")
+    return begin, int(nbytes.value)
+
+
+class _on_device:
+    """Makes `index` the thread's current device for the call (launches go to the
+    current device's context); does nothing when it already is."""
+
+    def __init__(self, index):
+        self._index = index
+        self._prev = None
+
+    def __enter__(self):
+        prev = torch.cuda.current_device()
+        if prev != self._index:
+            torch.cuda.set_device(self._index)
+            self._prev = prev
+
+    def __exit__(self, *a):
+        if self._prev is not None:
+            torch.cuda.set_device(self._prev)
+        return False
 
 
 class _nullcontext:
@@ -348,7 +584,7 @@ _tls = threading.local()   # per thread: the size of its last plan, to size the 
 
 def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num_sms=None,
               device=None, upload=True, stream=None, chain_steps=None,
-              block_tables=None, prefill_min_q=None, out=None) -> StepPlan | tuple:
+              block_tables=None, prefill_min_q=None, out=None, fp8=False) -> StepPlan | tuple:
     """Build the host plan for one step (pkv_plan_step_ex) and upload it.
 
     cu_q_lens / context_lens: host arrays or tensors (copied to the host if on a GPU).
@@ -361,6 +597,8 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     out (with upload=False): a writable host buffer (numpy array or CPU tensor,
     e.g. pinned memory for an asynchronous upload) the plan is written into; the
     returned host bytes are then a view of it.
+    fp8: the plan also serves paged_varlen_attention_fp8 (a larger workspace when
+    the step has tensor-core work; it still serves a bf16 pool).
     Returns a StepPlan (or (info, host_bytes) when upload=False).
     """
     desc = kv_pool_or_desc if isinstance(kv_pool_or_desc, PoolDesc) else pool_desc(kv_pool_or_desc)
@@ -414,7 +652,7 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     host = host[:n // 4]
     if not upload:
         return info, host
-    return StepPlan(info, host, torch.device(device), stream)
+    return StepPlan(info, host, torch.device(device), stream, fp8)
 
 
 class BoundPlan:
@@ -665,3 +903,86 @@ class BoundStep:
             ctypes.c_int64(0 if ws is None else ws.numel()), *self._tail)
         if st:
             raise PkvError(st, "pkv_paged_varlen_attention")
+
+
+class BoundAttentionFp8:
+    """paged_varlen_attention_fp8 with its arguments checked and marshalled once.
+
+    run() enqueues the attention on the bound stream; like BoundStep, it reads
+    `plan` at run time (made with fp8=True; it may be replaced by each step's
+    plan) and re-checks the sizes the plan states against the bound tensors."""
+
+    def __init__(self, q, cu_q_lens, context_lens, block_tables, kv_pool, kv_scales, scale: float,
+                 plan: StepPlan, out, *, dev_status=None, stream=None):
+        desc = _check_fp8_pool(kv_pool, kv_scales)
+        _check_cuda("q", q, torch.bfloat16, 3)
+        _check_cuda("out", out, torch.bfloat16, 3)
+        for name, t, ndim in (("cu_q_lens", cu_q_lens, 1), ("context_lens", context_lens, 1),
+                              ("block_tables", block_tables, 2)):
+            _check_cuda(name, t, torch.int32, ndim)
+        if dev_status is not None:
+            _check_cuda("dev_status", dev_status, torch.int32)
+        if out.shape != q.shape or q.shape[2] != desc.head_dim:
+            raise ValueError("out must have q's shape, [total_q, num_q_heads, head_dim]")
+        for t in (q, out, cu_q_lens, context_lens, block_tables, dev_status):
+            if t is not None and t.device != kv_pool.device:
+                raise ValueError("every tensor must be on kv_pool's device")
+        self.plan = plan
+        self.out = out
+        self._desc = desc
+        self._keep = (q, cu_q_lens, context_lens, block_tables, kv_pool, kv_scales, out,
+                      dev_status)
+        self._shape = (q.shape[0], q.shape[1], cu_q_lens.shape[0], context_lens.shape[0],
+                       block_tables.shape[0])
+        vp = ctypes.c_void_p
+        self._head = (vp(q.data_ptr()), vp(cu_q_lens.data_ptr()), vp(context_lens.data_ptr()),
+                      vp(block_tables.data_ptr()), ctypes.c_int32(block_tables.shape[1]),
+                      vp(kv_pool.data_ptr()), vp(kv_scales.data_ptr()), ctypes.byref(desc),
+                      ctypes.c_float(scale))
+        self._out = vp(out.data_ptr())
+        self._tail = (vp(_ptr(dev_status)), vp(_stream(stream, q)))
+        self._f = _load().pkv_paged_varlen_attention_fp8
+        self._device = kv_pool.device.index
+
+    def run(self) -> None:
+        plan = self.plan
+        info = plan.info
+        total_q, hq, n_cu, n_ctx, n_bt = self._shape
+        if (info.total_q != total_q or info.num_q_heads != hq or info.num_seqs + 1 != n_cu or
+                info.num_seqs != n_ctx or info.num_seqs != n_bt):
+            raise ValueError("the plan does not match the bound buffers")
+        if not plan.fp8:
+            raise ValueError("the plan was not made for an 8-bit pool: plan_step(..., fp8=True)")
+        ws = plan.workspace
+        with _on_device(self._device):
+            st = self._f(*self._head, ctypes.byref(info), plan.dev.data_ptr(), _ptr(plan.stage),
+                         plan.staged_blocks, self._out, _ptr(ws), 0 if ws is None else ws.numel(),
+                         *self._tail)
+        if st:
+            raise PkvError(st, "pkv_paged_varlen_attention_fp8")
+
+
+def paged_varlen_attention_fp8(q, cu_q_lens, context_lens, block_tables, kv_pool, kv_scales,
+                               scale: float, *, plan: StepPlan | None = None, out=None,
+                               dev_status=None, stream=None):
+    """paged_varlen_attention over an 8-bit pool; returns out [total_q, Hq, D] bf16.
+
+    kv_pool: e4m3 [nb, 2, Hkv, 16, D]; kv_scales: fp32 [nb, Hkv, 2], positive and
+    finite.  plan: one made with plan_step(..., fp8=True); built here when not given.
+    The other arguments mean what they mean for paged_varlen_attention.
+    """
+    desc = _check_fp8_pool(kv_pool, kv_scales)
+    _check_cuda("q", q, torch.bfloat16, 3)
+    dev = q.device
+    with torch.cuda.stream(stream) if stream is not None else _nullcontext():
+        if plan is None:
+            plan = plan_step(cu_q_lens, context_lens, q.shape[1], desc, device=dev, stream=stream,
+                             fp8=True)
+        cu_d = _dev_i32(cu_q_lens, dev, "cu_q_lens")
+        ctx_d = _dev_i32(context_lens, dev, "context_lens")
+        bt_d = _dev_i32(block_tables, dev, "block_tables")
+        if out is None:
+            out = torch.empty_like(q)
+        BoundAttentionFp8(q, cu_d, ctx_d, bt_d, kv_pool, kv_scales, scale, plan, out,
+                          dev_status=dev_status, stream=stream).run()
+    return out

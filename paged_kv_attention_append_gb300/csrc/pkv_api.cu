@@ -29,7 +29,7 @@ int device_sm_count() {
   return n;
 }
 
-constexpr int kNumKernelIds = 5;  // PKV_KERNEL_APPEND .. PKV_KERNEL_STATE
+constexpr int kNumKernelIds = 7;  // PKV_KERNEL_APPEND .. PKV_KERNEL_STAGE
 
 struct ProfileEvents {
   void *start[kNumKernelIds] = {};
@@ -147,11 +147,14 @@ extern "C" pkv_status pkv_decode_advance(int32_t *context_lens, int32_t *slot_ma
   return e ? PKV_ERR_CUDA : PKV_OK;
 }
 
-extern "C" pkv_status pkv_paged_varlen_attention(
-    const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
-    const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
-    const pkv_pool_desc *desc, float scale, const pkv_plan_info *info, const void *plan_dev,
-    void *out, void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
+// Both attention entry points: kv_scales NULL is a bf16 pool.
+static pkv_status attention(const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq,
+                            const void *kv_pool, const float *kv_scales,
+                            const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
+                            const void *plan_dev, const int32_t *stage_begin,
+                            int32_t staged_blocks, void *out, void *workspace,
+                            int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
   pkv_status st = check_pool(desc);
   if (st != PKV_OK) return st;
   if (!info) return PKV_ERR_NULL;
@@ -228,17 +231,134 @@ extern "C" pkv_status pkv_paged_varlen_attention(
   if (info->lookahead < 0 || (info->lookahead > 0 && info->num_prefill_tiles > 0))
     return PKV_ERR_SHAPE;
   a.lookahead = info->lookahead;
-  if (ws_total_bytes(info->num_partials, info->num_prefill_partials, d) > workspace_bytes)
-    return PKV_ERR_WORKSPACE;
+  const int64_t ws = ws_total_bytes(info->num_partials, info->num_prefill_partials, d);
+  if (ws > workspace_bytes) return PKV_ERR_WORKSPACE;
+  a.kv_scales = kv_scales;
+  if (kv_scales && info->num_prefill_tiles > 0) {
+    // the tensor-core kernel reads bf16 copies, behind the partial results
+    if (staged_blocks <= 0 || !staged_fits(staged_blocks, *desc)) return PKV_ERR_SHAPE;
+    if (!stage_begin || !workspace) return PKV_ERR_NULL;
+    if (workspace_bytes < ws + staged_bytes(staged_blocks, *desc)) return PKV_ERR_WORKSPACE;
+    a.stage_begin = stage_begin;
+    a.staged_blocks = staged_blocks;
+    a.staged = wb + ws;
+  }
   a.dev_status = dev_status;
   a.stream = stream;
 
   if (info->plan_bytes != off.total) return PKV_ERR_SHAPE;
   int launches = 0;
+  if (launch_stage(a, &launches)) return PKV_ERR_CUDA;
   if (launch_prefill(a, &launches)) return PKV_ERR_CUDA;
   if (launch_decode(a, &launches)) return PKV_ERR_CUDA;
   if (launch_merge(a, &launches)) return PKV_ERR_CUDA;
   return PKV_OK;
+}
+
+extern "C" pkv_status pkv_paged_varlen_attention(
+    const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
+    const pkv_pool_desc *desc, float scale, const pkv_plan_info *info, const void *plan_dev,
+    void *out, void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
+  return attention(q, cu_q_lens, context_lens, block_tables, max_blocks_per_seq, kv_pool, nullptr,
+                   desc, scale, info, plan_dev, nullptr, 0, out, workspace, workspace_bytes,
+                   dev_status, stream);
+}
+
+extern "C" pkv_status pkv_paged_varlen_attention_fp8(
+    const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
+    const float *kv_scales, const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
+    const void *plan_dev, const int32_t *stage_begin, int32_t staged_blocks, void *out,
+    void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
+  if (!kv_scales) return PKV_ERR_NULL;
+  if (!aligned16(kv_scales)) return PKV_ERR_ALIGN;
+  return attention(q, cu_q_lens, context_lens, block_tables, max_blocks_per_seq, kv_pool, kv_scales,
+                   desc, scale, info, plan_dev, stage_begin, staged_blocks, out, workspace,
+                   workspace_bytes, dev_status, stream);
+}
+
+// Both rotating appends: kv_scales NULL is a bf16 pool.
+static pkv_status rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, const pkv_rope *rope,
+                              const int32_t *slot_mapping, int32_t num_tokens,
+                              int32_t num_q_heads, void *q_out, int64_t q_out_stride,
+                              void *kv_pool, float *kv_scales, const pkv_pool_desc *desc,
+                              int32_t *dev_status, pkv_stream stream) {
+  const pkv_status st = check_pool(desc);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_q_heads < 0) return PKV_ERR_SHAPE;
+  if (!rope && num_q_heads > 0) return PKV_ERR_NULL;
+  const int64_t d = desc->head_dim, kv_row = d * desc->num_kv_heads, q_row = d * num_q_heads;
+  if (rope) {
+    if (rope->rotary_dim < 16 || rope->rotary_dim > d || rope->rotary_dim % 16 != 0)
+      return PKV_ERR_UNSUPPORTED;
+    if (rope->max_positions < 0) return PKV_ERR_SHAPE;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return PKV_ERR_RANGE;
+  }
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || !kv_pool || (num_q_heads > 0 && (!q || !q_out)))
+    return PKV_ERR_NULL;
+  if (rope && (!rope->positions || !rope->cos_sin)) return PKV_ERR_NULL;
+  if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return PKV_ERR_SHAPE;
+  if (num_q_heads > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 != 0 ||
+                          q_out_stride % 8 != 0))
+    return PKV_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kv_pool) || !aligned16(kv_scales) ||
+      (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out))) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 3u))
+    return PKV_ERR_ALIGN;
+  if (rope && (!aligned16(rope->cos_sin) || (reinterpret_cast<uintptr_t>(rope->positions) & 3u)))
+    return PKV_ERR_ALIGN;
+  RopeAppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.cos_sin = rope ? rope->cos_sin : nullptr;
+  a.positions = rope ? rope->positions : nullptr;
+  a.max_positions = rope ? rope->max_positions : 0;
+  a.rotary_dim = rope ? rope->rotary_dim : 0;
+  a.interleaved = rope ? rope->interleaved : 0;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.kv_pool = kv_pool;
+  a.kv_scales = kv_scales;
+  a.desc = *desc;
+  a.dev_status = dev_status;
+  a.stream = stream;
+  return launch_rope_append(a) ? PKV_ERR_CUDA : PKV_OK;
+}
+
+extern "C" pkv_status pkv_rope_kv_append(const void *q, int64_t q_stride, const void *k,
+                                         int64_t k_stride, const void *v, int64_t v_stride,
+                                         const pkv_rope *rope, const int32_t *slot_mapping,
+                                         int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                                         int64_t q_out_stride, void *kv_pool,
+                                         const pkv_pool_desc *desc, int32_t *dev_status,
+                                         pkv_stream stream) {
+  if (!rope) return PKV_ERR_NULL;
+  return rope_append(q, q_stride, k, k_stride, v, v_stride, rope, slot_mapping, num_tokens,
+                     num_q_heads, q_out, q_out_stride, kv_pool, nullptr, desc, dev_status, stream);
+}
+
+extern "C" pkv_status pkv_rope_kv_append_fp8(const void *q, int64_t q_stride, const void *k,
+                                             int64_t k_stride, const void *v, int64_t v_stride,
+                                             const pkv_rope *rope, const int32_t *slot_mapping,
+                                             int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                                             int64_t q_out_stride, void *kv_pool,
+                                             float *kv_scales, const pkv_pool_desc *desc,
+                                             int32_t *dev_status, pkv_stream stream) {
+  if (!kv_scales) return PKV_ERR_NULL;
+  return rope_append(q, q_stride, k, k_stride, v, v_stride, rope, slot_mapping, num_tokens,
+                     num_q_heads, q_out, q_out_stride, kv_pool, kv_scales, desc, dev_status,
+                     stream);
 }
 
 extern "C" size_t pkv_workspace_size(const pkv_plan_info *info) {

@@ -202,6 +202,15 @@ inline int64_t ws_total_bytes(int32_t parts, int32_t pparts, int32_t d) {
          ws_ppart_ml_bytes(pparts);
 }
 
+// bf16 copies of 8-bit blocks (behind the partials), 256-byte aligned; their
+// rows must stay within the tensor map's 32-bit coordinates.
+inline int64_t staged_bytes(int64_t blocks, const pkv_pool_desc &d) {
+  return align_up(blocks * 2 * d.num_kv_heads * kBlockSize * d.head_dim * 2, 256);
+}
+inline bool staged_fits(int64_t blocks, const pkv_pool_desc &d) {
+  return blocks * 2 * d.num_kv_heads * kBlockSize < (int64_t)1 << 31;
+}
+
 // Kernel launchers (defined in the .cu files).  Return a cudaError_t value.
 int launch_append(const void *k, const void *v, const int32_t *slot_mapping, int32_t num_tokens,
                   void *kv_pool, const pkv_pool_desc &desc, int32_t *dev_status,
@@ -245,7 +254,35 @@ struct AttnArgs {
   int32_t lookahead;          // further decode steps the plan covers (chained decode)
   int32_t *dev_status;
   pkv_stream stream;
+  // 8-bit pool (kv_scales non-null: [num_blocks][Hkv][2] fp32): the split-KV kernel
+  // reads it directly; the tensor-core kernel reads bf16 copies of the blocks its
+  // sequences need, sequence s's logical block j as block stage_begin[s] + j of
+  // `staged`, which launch_stage writes first.
+  const float *kv_scales = nullptr;
+  const int32_t *stage_begin = nullptr;
+  int32_t staged_blocks = 0;
+  void *staged = nullptr;
 };
+
+int launch_stage(const AttnArgs &a, int *launches);
+
+// The rotating append (pkv_rope.cu).  Strides in elements.
+struct RopeAppendArgs {
+  const void *q, *k, *v;
+  void *q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float *cos_sin;       // null: no rotation
+  const int32_t *positions;
+  int32_t max_positions, rotary_dim, interleaved;
+  const int32_t *slot_mapping;
+  int32_t num_tokens, num_q_heads;
+  void *kv_pool;
+  float *kv_scales;           // null: bf16 pool
+  pkv_pool_desc desc;
+  int32_t *dev_status;
+  pkv_stream stream;
+};
+int launch_rope_append(const RopeAppendArgs &a);
 
 int launch_state_checkpoint(const void *src, const int32_t *dst_slots, int32_t num_rows,
                             void *pool, int64_t num_slots, int64_t row_bytes, int32_t *dev_status,

@@ -1032,6 +1032,45 @@ extern "C" pkv_status pkv_plan_step_ex(const int32_t *cu_q_lens, const int32_t *
                       block_tables, max_blocks_per_seq, prefill_min_q, plan, plan_capacity, info);
 }
 
+extern "C" pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *info,
+                                         int32_t *stage_begin, int64_t *workspace_bytes) {
+  if (!plan || !info || !stage_begin || !workspace_bytes) return PKV_ERR_NULL;
+  if (info->num_seqs < 0 || info->num_prefill_tiles < 0 || info->num_kv_heads < 1)
+    return PKV_ERR_SHAPE;
+  PlanHeader h;
+  std::memcpy(&h, plan, sizeof h);
+  const PlanOffsets off =
+      plan_offsets(info->num_decode_warps, info->num_decode_pieces, info->num_merge_groups,
+                   info->num_shared_items, info->num_prefill_tiles, info->num_prefill_ctas,
+                   info->num_gather_rows);
+  if (h.magic != kPlanMagic || h.num_seqs != info->num_seqs ||
+      h.num_prefill_tiles != info->num_prefill_tiles || info->plan_bytes != off.total)
+    return PKV_ERR_SHAPE;
+  // the blocks of sequence s that tensor-core items read: 0 .. 8 max(kt1) - 1
+  // (those past the context are zero-filled copies, at most 7)
+  std::memset(stage_begin, 0, sizeof(int32_t) * ((size_t)info->num_seqs + 1));
+  const char *tiles = static_cast<const char *>(plan) + off.prefill;
+  for (int32_t i = 0; i < info->num_prefill_tiles; ++i) {
+    PrefillTile t;
+    std::memcpy(&t, tiles + (int64_t)i * (int64_t)sizeof t, sizeof t);
+    if (t.seq < 0 || t.seq >= info->num_seqs) return PKV_ERR_SHAPE;
+    stage_begin[t.seq + 1] = std::max(stage_begin[t.seq + 1], t.kt1 * kKeyTileBlocks);
+  }
+  pkv_pool_desc d;
+  d.num_blocks = 0;
+  d.block_size = kBlockSize;
+  d.num_kv_heads = info->num_kv_heads;
+  d.head_dim = info->head_dim;
+  int64_t total = 0;
+  for (int32_t s = 0; s < info->num_seqs; ++s) {
+    total += stage_begin[s + 1];
+    if (!staged_fits(total, d)) return PKV_ERR_UNSUPPORTED;
+    stage_begin[s + 1] = (int32_t)total;
+  }
+  *workspace_bytes = info->workspace_bytes + (total > 0 ? staged_bytes(total, d) : 0);
+  return PKV_OK;
+}
+
 extern "C" pkv_status pkv_plan_step(const int32_t *cu_q_lens, const int32_t *context_lens,
                                     int32_t num_seqs, int32_t num_q_heads,
                                     const pkv_pool_desc *desc, int32_t num_sms, void *plan,

@@ -149,6 +149,9 @@ struct PrefillParams {
   int32_t group;
   int32_t pool_groups;  // rows of the pool / 8 (out-of-range group coordinate)
   float scale_log2;
+  // not null: the pool is the bf16 staging copy of an 8-bit pool's blocks, block j
+  // of sequence s at stage_begin[s] + j; the block tables are not read
+  const int32_t *stage_begin;
 };
 
 
@@ -376,13 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int32_t *table = p.block_tables + (int64_t)m.t.seq * p.max_blocks_per_seq;
+      const int stage0 = p.stage_begin ? __ldg(p.stage_begin + m.t.seq) : -1;
       const int nblk_ctx = (m.ctx + kBlockSize - 1) / kBlockSize;
       const int nblk = min(nblk_ctx, p.max_blocks_per_seq);
       // entry of block `lane` of the four tiles from relative tile 4 k on
       // (-1: past the context or the table, zero fill)
       auto read_group = [&](int k) -> int {
         const int kb = (m.t.kt0 + kTablePrefetchTiles * k) * kBlocksPerTile + lane;
-        return kb < nblk ? __ldg(table + kb) : -1;
+        return kb >= nblk ? -1 : stage0 >= 0 ? stage0 + kb : __ldg(table + kb);
       };
       for (int x = 0; x < 2 && good; ++x) {
         const int ntx = x ? m.nt[1] : m.nt[0];
@@ -972,11 +976,13 @@ int launch_prefill_t(const AttnArgs &a, const CUtensorMap &qmap, const CUtensorM
   p.dev_status = a.dev_status;
   p.num_seqs = a.num_seqs;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
-  p.num_blocks = a.desc.num_blocks;
+  const int32_t pool_blocks = a.kv_scales ? a.staged_blocks : a.desc.num_blocks;
+  p.num_blocks = pool_blocks;
+  p.stage_begin = a.kv_scales ? a.stage_begin : nullptr;
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.desc.num_kv_heads;
   p.group = a.num_q_heads / a.desc.num_kv_heads;
-  p.pool_groups = a.desc.num_blocks * 2 * a.desc.num_kv_heads * (kBlockSize / 8);
+  p.pool_groups = pool_blocks * 2 * a.desc.num_kv_heads * (kBlockSize / 8);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   profile_begin(PKV_KERNEL_PREFILL, a.stream);
   e = launch_kernel(kern, dim3((unsigned)a.num_prefill_ctas), dim3(kThreads), C::kSmemBytes,
@@ -998,7 +1004,9 @@ int launch_prefill(const AttnArgs &a, int *launches) {
   e = make_q_map(&qrmap, a.q, a.total_q, a.num_q_heads, a.desc.head_dim, group,
                  kPrefillRows / group);
   if (e) return e;
-  e = make_pool_map(&kvmap, a.kv_pool, a.desc);
+  pkv_pool_desc pool_desc = a.desc;
+  if (a.kv_scales) pool_desc.num_blocks = a.staged_blocks;
+  e = make_pool_map(&kvmap, a.kv_scales ? a.staged : a.kv_pool, pool_desc);
   if (e) return e;
   // out has q's shape: whole 128-token sub-tiles are stored through this map
   e = make_q_map(&omap, a.out, a.total_q, a.num_q_heads, a.desc.head_dim, 1, kPrefillRows);

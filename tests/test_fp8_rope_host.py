@@ -1,0 +1,151 @@
+"""CPU tests of the rotating append's and the 8-bit attention's entry points: every
+refusal happens before anything is enqueued, and the staging array matches the plan."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import paged_kv_attention_append_gb300 as pkv
+import workloads
+
+A = 0x1000                      # an aligned address that is never dereferenced
+OK, NULL, SHAPE, RANGE, UNSUPPORTED, WORKSPACE, ALIGN = 0, 1, 2, 3, 4, 5, 8
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pkv.build()
+    return pkv._load()
+
+
+def rope_call(lib, fp8=False, **kw):
+    a = dict(q=A, qs=8 * 128, k=A, ks=2 * 128, v=A, vs=2 * 128, cos_sin=A, positions=A, max_pos=10,
+             rot=128, inter=0, slots=A, n=4, hq=8, q_out=A, qos=8 * 128, pool=A, scales=A, nb=4,
+             bs=16, hkv=2, d=128, rope=True)
+    a.update(kw)
+    rope = pkv.Rope(a["cos_sin"], a["positions"], a["max_pos"], a["rot"], a["inter"])
+    desc = pkv.PoolDesc(a["nb"], a["bs"], a["hkv"], a["d"])
+    args = [a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"],
+            ctypes.byref(rope) if a["rope"] else None, a["slots"], a["n"], a["hq"], a["q_out"],
+            a["qos"], a["pool"]]
+    if fp8:
+        return lib.pkv_rope_kv_append_fp8(*args, a["scales"], ctypes.byref(desc), None, None)
+    return lib.pkv_rope_kv_append(*args, ctypes.byref(desc), None, None)
+
+
+REFUSED = [
+    (dict(k=None), NULL), (dict(v=None), NULL), (dict(slots=None), NULL), (dict(pool=None), NULL),
+    (dict(q=None), NULL), (dict(q_out=None), NULL), (dict(cos_sin=None), NULL),
+    (dict(positions=None), NULL), (dict(n=-1), SHAPE), (dict(hq=-1), SHAPE),
+    (dict(rot=0), UNSUPPORTED), (dict(rot=8), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(rot=144), UNSUPPORTED), (dict(rot=-16), UNSUPPORTED), (dict(max_pos=-1), SHAPE),
+    (dict(inter=2), RANGE), (dict(ks=128), SHAPE), (dict(vs=2 * 128 + 4), SHAPE),
+    (dict(qs=7 * 128), SHAPE), (dict(qos=8 * 128 + 1), SHAPE), (dict(k=A + 8), ALIGN),
+    (dict(q=A + 2), ALIGN), (dict(q_out=A + 4), ALIGN), (dict(pool=A + 8), ALIGN),
+    (dict(cos_sin=A + 4), ALIGN), (dict(positions=A + 2), ALIGN), (dict(slots=A + 1), ALIGN),
+    (dict(d=96), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(hkv=0), SHAPE),
+    (dict(nb=1 << 26), UNSUPPORTED), (dict(n=0), OK), (dict(n=0, k=None), OK),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(REFUSED)))
+def test_rope_refusals(lib, fp8, case):
+    kw, want = REFUSED[case]
+    before = pkv.kernel_launch_count()
+    assert rope_call(lib, fp8, **kw) == want
+    assert pkv.kernel_launch_count() == before
+
+
+def test_rope_only_refusals(lib):
+    assert rope_call(lib, rope=False) == NULL
+    assert rope_call(lib, True, rope=False) == NULL             # q without a rotation
+    assert rope_call(lib, True, scales=None) == NULL
+    assert rope_call(lib, True, scales=A + 4) == ALIGN
+    assert rope_call(lib, True, rope=False, hq=0, n=0) == OK
+
+
+def plan_of(meta, **kw):
+    info, host = pkv.plan_step(meta.cu_q_lens, meta.context_lens, meta.num_q_heads,
+                               pkv.PoolDesc(meta.num_blocks, 16, meta.num_kv_heads, meta.head_dim),
+                               num_sms=kw.pop("num_sms", 152), upload=False, **kw)
+    return info, host
+
+
+@pytest.mark.parametrize("seed", range(8))
+@pytest.mark.parametrize("shared", [0, 20])
+def test_stage_covers_the_tensor_core_sequences(lib, seed, shared):
+    rng = np.random.default_rng(seed)
+    meta = workloads.random_step(rng, max_ctx=700, num_seqs=40 if shared else None,
+                                 shared_prefix_blocks=shared)
+    info, host = plan_of(meta, block_tables=meta.block_tables)
+    begin, nbytes = pkv.stage_fp8(info, host)
+    counts = np.diff(begin)
+    assert begin[0] == 0 and (counts >= 0).all()
+    for s in range(meta.num_seqs):
+        nb = -(-int(meta.context_lens[s]) // 16)
+        if meta.q_lens[s] >= 64:
+            assert nb <= counts[s] <= nb + 7
+        else:                           # only as the table of a gathered prefix
+            assert counts[s] <= max(shared, 0)
+    if info.num_prefill_tiles == 0:
+        assert begin[-1] == 0 and nbytes == info.workspace_bytes
+    else:
+        slab = 2 * meta.num_kv_heads * 16 * meta.head_dim * 2
+        assert nbytes >= info.workspace_bytes + int(begin[-1]) * slab
+    # the plan itself is the one a bf16 pool gets
+    assert info.plan_bytes <= host.nbytes
+
+
+def test_stage_refusals(lib):
+    meta = workloads.build_step("s", 1, [70, 1], [70, 40], 4, 2, 64)
+    info, host = plan_of(meta)
+    begin = np.zeros(3, dtype=np.int32)
+    out = ctypes.c_int64()
+    ptr = lambda a: a.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+    f = lib.pkv_plan_stage_fp8
+    assert f(None, ctypes.byref(info), ptr(begin), ctypes.byref(out)) == NULL
+    assert f(ptr(host), None, ptr(begin), ctypes.byref(out)) == NULL
+    assert f(ptr(host), ctypes.byref(info), None, ctypes.byref(out)) == NULL
+    assert f(ptr(host), ctypes.byref(info), ptr(begin), None) == NULL
+    other = host.copy()
+    other[0] ^= 1
+    assert f(ptr(other), ctypes.byref(info), ptr(begin), ctypes.byref(out)) == SHAPE
+    bad = pkv.PlanInfo.from_buffer_copy(info)
+    bad.num_prefill_tiles += 1
+    assert f(ptr(host), ctypes.byref(bad), ptr(begin), ctypes.byref(out)) == SHAPE
+
+
+def attention_call(lib, info, **kw):
+    a = dict(q=A, cu=A, ctx=A, bt=A, mb=64, pool=A, scales=A, scale=0.1, plan=A, stage=A, blocks=12,
+             out=A, ws=A, wsb=1 << 30)
+    a.update(kw)
+    desc = pkv.PoolDesc(100, 16, info.num_kv_heads, info.head_dim)
+    return lib.pkv_paged_varlen_attention_fp8(
+        a["q"], a["cu"], a["ctx"], a["bt"], a["mb"], a["pool"], a["scales"], ctypes.byref(desc),
+        a["scale"], ctypes.byref(info), a["plan"], a["stage"], a["blocks"], a["out"], a["ws"],
+        a["wsb"], None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(scales=None), NULL), (dict(scales=A + 8), ALIGN), (dict(q=None), NULL),
+    (dict(pool=None), NULL), (dict(stage=None), NULL), (dict(ws=None), NULL), (dict(blocks=0), SHAPE),
+    (dict(blocks=-3), SHAPE), (dict(blocks=1 << 30), SHAPE), (dict(wsb=4096), WORKSPACE),
+    (dict(mb=2), RANGE), (dict(scale=float("inf")), RANGE), (dict(scale=float("nan")), RANGE),
+    (dict(ws=A + 16), ALIGN), (dict(out=A + 2), ALIGN)])
+def test_attention_refusals(lib, kw, want):
+    meta = workloads.build_step("s", 1, [70, 1], [70, 40], 4, 2, 64)
+    info, _ = plan_of(meta)
+    assert info.num_prefill_tiles > 0
+    before = pkv.kernel_launch_count()
+    assert attention_call(lib, info, **kw) == want
+    assert pkv.kernel_launch_count() == before
+
+
+def test_empty_step_is_ok(lib):
+    meta = workloads.build_step("s", 1, [0], [9], 4, 2, 64)
+    info, host = plan_of(meta)
+    begin, nbytes = pkv.stage_fp8(info, host)
+    assert begin.tolist() == [0, 0] and nbytes == info.workspace_bytes
+    assert attention_call(lib, info, q=None, pool=None, stage=None, blocks=0) == OK
