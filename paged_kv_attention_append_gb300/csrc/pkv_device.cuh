@@ -265,7 +265,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// Coherent 16-byte load (the source may be written by this kernel: in place).
+// Coherent loads (the source may be written by this kernel: in place).
+__device__ __forceinline__ uint2 ldg64(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 ldg128(const void *p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
