@@ -26,10 +26,6 @@
 //    memory phase hits 8 distinct 16-byte bank groups (conflict-free).
 //  * Online softmax in the log2 domain with warp-shuffle row max; O is rescaled
 //    only when some row's max moved.
-//  * The same kernel reads an 8-bit pool (kF8: e4m3 values, one fp32 scale per
-//    block, KV head and K or V): half the bytes, so twice the stages; a stage is
-//    one box (K and V of a block and head) plus its two scales, and the values
-//    become fp16 in registers, exactly (block_update8).
 //  * merge_kernel (launched behind the decode kernel with programmatic stream
 //    serialisation) combines the partials of a segment cut into pieces:
 //    M = max_j m_j, out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
@@ -39,103 +35,27 @@
 #include <cmath>
 #include <mutex>
 
+#include "pkv_decode.cuh"
 #include "pkv_device.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kWarps = kDecodeWarpsPerCta;
-constexpr int kThreads = kWarps * 32;
 constexpr int kBoxBytes = kBlockSize * 128;  // 16 rows x 64 bf16, 128-byte swizzled
 
-template <int D, int NSTAGE, bool kF8>
+template <int D, int NSTAGE>
 struct DecodeCfg {
   static constexpr int kHalves = D / 64;
-  // one K or V slab of a block
-  static constexpr int kSlabBytes = kF8 ? kBlockSize * D : kHalves * kBoxBytes;
+  static constexpr int kSlabBytes = kHalves * kBoxBytes;  // one K or V slab of a block
   static constexpr int kStageBytes = 2 * kSlabBytes;
   static constexpr int kRingBytes = NSTAGE * kStageBytes;
   static constexpr int kBarOffset = kWarps * kRingBytes;
   // barriers: the warps' own rings use kWarps * NSTAGE; a shared-prefix CTA uses
   // that many full and as many empty barriers for its pooled ring
   static constexpr int kFlagOffset = kBarOffset + 2 * kWarps * NSTAGE * 8;
-  static constexpr int kScaleOffset = kFlagOffset + kWarps * NSTAGE * 4;  // kF8: float2 a stage
-  static constexpr int kSmemBytes = kScaleOffset + (kF8 ? kWarps * NSTAGE * 8 : 0) + 1024;
-  static_assert(kScaleOffset % 8 == 0, "scales are copied 8 bytes at a time");
-  // arrivals that fill a stage: the box's bytes, and with kF8 the scales' copy
-  static constexpr int kFillArrivals = kF8 ? 2 : 1;
+  static constexpr int kSmemBytes = kFlagOffset + kWarps * NSTAGE * 4 + 1024;
 };
-
-struct DecodeParams {
-  const __nv_bfloat16 *q;
-  __nv_bfloat16 *out;
-  const int32_t *cu_q_lens;
-  const int32_t *context_lens;
-  const int32_t *block_tables;
-  const int32_t *warp_begin;
-  const WarpHead *warp_head;
-  const Piece *pieces;
-  const SharedItem *shared;    // shared-prefix CTAs, after the num_indep_ctas CTAs of warp ranges
-  int32_t num_indep_ctas;
-  int32_t num_shared_items;    // entries of `shared` (the pairs' chains)
-  const MergeGroup *merges;
-  float *part_o;
-  float2 *part_ml;
-  const float *ppart_o;
-  const float2 *ppart_ml;
-  int32_t *dev_status;
-  int32_t lookahead;           // plan sized for this many further steps (chained decode)
-  int32_t after_prefill;       // launched right behind this call's tensor-core kernel: the
-                               // pool is complete when this kernel starts (that kernel lets
-                               // it launch only after its own wait for the append), so no
-                               // wait precedes the pool reads; every warp waits at its end
-                               // instead, so this kernel completes after that one
-  int32_t num_merges;          // all merge groups: decode ones, then prefill ones
-  int32_t num_decode_merges;
-  int32_t merge_lanes_log2;    // lanes that share one decode row's splits (merge kernel)
-  int32_t merge_rows;          // rows the merge launch covers per decode group
-  int32_t num_partials;
-  int32_t num_warps;
-  int32_t num_seqs;
-  int32_t max_blocks_per_seq;
-  int32_t num_blocks;
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
-  int32_t group;
-  float scale_log2;
-  int64_t total_q;
-  const uint8_t *pool;  // for address-translation warm-up only (data goes through pool_map)
-  int64_t pool_bytes;
-  const float2 *kv_scales;  // kF8: [num_blocks][Hkv] (K scale, V scale)
-};
-
-// Fills one stage with block `phys` of KV head h (one lane).  An 8-bit block is
-// one box, its K and V slabs 16 D bytes apart in the stage, with its two scales
-// beside it; both arrive on the stage's barrier.
-template <class C, bool kF8>
-__device__ __forceinline__ void fill_stage(const CUtensorMap &pool_map, const DecodeParams &p,
-                                           uint32_t dst, uint32_t scale_dst, uint32_t bar,
-                                           int phys, int h) {
-  mbar_arrive_expect_tx(bar, C::kStageBytes);
-  if constexpr (kF8) {
-    tma_load_4d(dst, &pool_map, 0, 0, h, phys * 2, bar);
-    cp_async_8(scale_dst, p.kv_scales + (int64_t)phys * p.num_kv_heads + h);
-    cp_async_arrive(bar);
-  } else {
-    const int row_k = ((phys * 2 + 0) * p.num_kv_heads + h) * kBlockSize;
-    const int row_v = row_k + p.num_kv_heads * kBlockSize;
-    // one 4-D box per slab: the whole block of one head (rows / 8 = group coordinate)
-    tma_load_4d(dst, &pool_map, 0, 0, 0, row_k >> 3, bar);
-    tma_load_4d(dst + C::kSlabBytes, &pool_map, 0, 0, 0, row_v >> 3, bar);
-  }
-}
-// Completes a stage's phase without data (a bad block: it is skipped).
-template <class C>
-__device__ __forceinline__ void skip_stage(uint32_t bar) {
-#pragma unroll
-  for (int i = 0; i < C::kFillArrivals; ++i) mbar_arrive(bar);
-}
 
 // Byte offset of 16-byte chunk `chunk` (0 .. D/8-1) of key row `row` (0..15) of
 // a paged block as one 4-D TMA box lands it: [8-row group][64-column half]
@@ -147,24 +67,10 @@ __device__ __forceinline__ uint32_t blk_off(int row, int chunk) {
                     (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// Running state of the two query rows a lane shares in (rows r and r + 8).
-// (m, l): reference (log2 units) and sum of the softmax weights.  mo: the
-// reference of O.  16-bit pool: mo is m.  8-bit pool: O's weights are the softmax
-// weights times the V scale of their block, so O has a reference of its own (see
-// block_update8).  qs: the factor from an S product to log2 units, kF8 only (the
-// row's own part; the block's K scale comes on top).
-struct RowState {
-  float m_lo, m_hi, l_lo, l_hi, mo_lo, mo_hi, qs_lo, qs_hi;
-  __device__ __forceinline__ void reset() {
-    m_lo = m_hi = mo_lo = mo_hi = -INFINITY;
-    l_lo = l_hi = 0.f;
-  }
-};
-
-template <int D, bool kF8>
+template <int D>
 __device__ __forceinline__ void write_piece(const DecodeParams &p, const Piece &pc,
-                                            float (&o)[D / 8][4], RowState &st, int R, int cu0,
-                                            int r, int c);
+                                            float (&o)[D / 8][4], float m_lo, float m_hi,
+                                            float l_lo, float l_hi, int R, int cu0, int r, int c);
 
 // LSE merge of results whose keys were cut into several parts (decode segments
 // cut into several pieces; prefill sub-tiles cut into several work items):
@@ -228,16 +134,6 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16 *dst, float4 acc, float
   pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2 *>(dst) = pk;
-}
-
-// A piece that cannot contribute a result (its plan disagrees with the device
-// metadata) writes nothing to out; when it is one part of a merge group, every
-// row of its partial slot is marked (m = NaN) so the merge writes none of the
-// group's rows either.
-__device__ __forceinline__ void poison_piece(const DecodeParams &p, int part, int lane) {
-  if (part < 0 || part >= p.num_partials) return;
-  if (lane < kRowsPerTile)
-    p.part_ml[(int64_t)part * kRowsPerTile + lane] = make_float2(__int_as_float(0x7fc00000), 0.f);
 }
 
 template <int D, int kBatch>
@@ -343,7 +239,8 @@ __device__ __forceinline__ void load_q_frags(const DecodeParams &p, int q_row0, 
 template <int D>
 __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uint32_t (&qa)[D / 16][4],
                                              int p0, int q_pos0, int lim_lo, int lim_hi, float sl2,
-                                             int r, int c, RowState &st, float (&o)[D / 8][4]) {
+                                             int r, int c, float &m_lo, float &m_hi, float &l_lo,
+                                             float &l_hi, float (&o)[D / 8][4]) {
   constexpr int kL = D / 32;
   constexpr int kNt = D / 8;
   constexpr int kHalves = D / 64;
@@ -382,12 +279,12 @@ __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uin
   mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 2));
   mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 1));
   mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 2));
-  const float mn_lo = fmaxf(st.m_lo, mx_lo), mn_hi = fmaxf(st.m_hi, mx_hi);
+  const float mn_lo = fmaxf(m_lo, mx_lo), mn_hi = fmaxf(m_hi, mx_hi);
   const float base_lo = mn_lo == -INFINITY ? 0.f : mn_lo;
   const float base_hi = mn_hi == -INFINITY ? 0.f : mn_hi;
-  const float a_lo = fast_exp2(st.m_lo - base_lo), a_hi = fast_exp2(st.m_hi - base_hi);
-  st.m_lo = mn_lo;
-  st.m_hi = mn_hi;
+  const float a_lo = fast_exp2(m_lo - base_lo), a_hi = fast_exp2(m_hi - base_hi);
+  m_lo = mn_lo;
+  m_hi = mn_hi;
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
     s[nt][0] = fast_exp2(s[nt][0] - base_lo);
@@ -395,8 +292,8 @@ __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uin
     s[nt][2] = fast_exp2(s[nt][2] - base_hi);
     s[nt][3] = fast_exp2(s[nt][3] - base_hi);
   }
-  st.l_lo = st.l_lo * a_lo + (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-  st.l_hi = st.l_hi * a_hi + (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+  l_lo = l_lo * a_lo + (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+  l_hi = l_hi * a_hi + (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
   if (__any_sync(0xffffffffu, a_lo != 1.f || a_hi != 1.f)) {
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
@@ -433,192 +330,6 @@ __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uin
   }
 }
 
-// Q fragments for an 8-bit pool: rows as in load_q_frags, head_dim permuted to
-// match block_update8's K fragments (lane (r, c) of k16 step 4 L + i holds head_dim
-// 16 e + 4 i .. + 3, e = c D / 64 + L), as fp16 scaled by a power of two of the row so
-// that its largest value lies in [2^14, 2^15): fp16 then holds every bf16 value
-// of the row down to 2^-28 of the largest exactly, and smaller ones to 2^-39 of
-// it.  st.qs takes the scale back out, times the softmax scale in log2 units.
-template <int D>
-__device__ __forceinline__ void load_q_frags8(const DecodeParams &p, int q_row0, int R, int h,
-                                              int r, int c, uint32_t (&qa)[D / 16][4],
-                                              RowState &st) {
-  constexpr int kL = D / 64;  // 16-element chunks per lane per row
-  const int G = p.group;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = r + 8 * half;
-    const bool rv = row < R;
-    const __nv_bfloat16 *qrow =
-        p.q + ((int64_t)(q_row0 + (rv ? row / G : 0)) * p.num_q_heads + h * G +
-               (rv ? row % G : 0)) * D + 16 * kL * c;
-    uint4 raw[2 * kL];
-#pragma unroll
-    for (int i = 0; i < 2 * kL; ++i) raw[i] = rv ? ldg128_nc(qrow + 8 * i) : make_uint4(0, 0, 0, 0);
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(raw);
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8 * kL; ++i)
-      top = max3(top, fabsf(__uint_as_float(w[i] << 16)),
-                 fabsf(__uint_as_float(w[i] & 0xffff0000u)));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent of the row's largest
-    // 2^(14 - exponent); a row holding an infinity is left as it is
-    const int f = e == 255 ? 127 : min(268 - e, 253);
-    const float up = __uint_as_float((uint32_t)f << 23);
-    const float down = __uint_as_float((uint32_t)(254 - f) << 23);
-#pragma unroll
-    for (int i = 0; i < 8 * kL; ++i) {
-      const uint32_t v = pack_f16x2(__uint_as_float(w[i] << 16) * up,
-                                    __uint_as_float(w[i] & 0xffff0000u) * up);
-      qa[i >> 1][(i & 1) * 2 + half] = v;
-    }
-    (half ? st.qs_hi : st.qs_lo) = down * p.scale_log2;
-  }
-}
-
-// One block of an 8-bit pool (the counterpart of block_update).  With K8, V8 the
-// stored e4m3 values and ks, vs the block's scales,
-//   x = (q . K8) ks scale log2(e),  w = 2^x,  out = sum w vs V8 / sum w.
-// Both products run on fp16 operands with fp32 accumulation: e4m3 values are
-// exact in fp16, q is scaled per row (load_q_frags8), ks multiplies the fp32
-// products.  The weights of O carry vs inside their exponent,
-//   u = 2^(x + log2 vs - mo + kPUp),
-// against a reference mo of their own (the running maximum of x + log2 vs), so
-// they lie in (0, 2^kPUp] whatever the scales are: fp16 rounds them to 2^-12 of
-// their value down to 2^-28 of the row's largest, against 2^-9 for bf16.
-// Keys past the row's limit get x = -inf.  V rows at or past the context end
-// (stale bytes, NaN codes among them) are read as zeros: 0 x NaN would reach O.
-constexpr float kPUp = 14.f;
-template <int D>
-__device__ __forceinline__ void block_update8(uint32_t sK, uint32_t sV, float2 scales,
-                                              const uint32_t (&qa)[D / 16][4], int p0, int q_pos0,
-                                              int lim_lo, int lim_hi, int ctx, int r, int c,
-                                              RowState &st, float (&o)[D / 8][4]) {
-  static_assert(D == 64 || D == 128, "head_dim");
-  constexpr int kNt = D / 8;
-  float s[2][4];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-    const int t = r + 8 * nt;
-#pragma unroll
-    for (int L = 0; L < D / 64; ++L) {
-      // 16-byte chunk e of key row t: rows of 128 bytes are swizzled over 128
-      // bytes, rows of 64 over 64; every 8-lane phase hits 8 distinct banks
-      const uint32_t off = D == 128 ? t * 128 + (((2 * c + L) ^ (t & 7)) << 4)
-                                    : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
-      const uint4 kv = lds128(sK + off);
-      const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * L + i;
-        mma_16816_f16(s[nt], qa[k][0], qa[k][1], qa[k][2], qa[k][3], e4m3x2_to_f16x2(w[i]),
-                      e4m3x2_to_f16x2(w[i] >> 16));
-      }
-    }
-  }
-  const bool need_mask = p0 + kBlockSize - 1 > q_pos0;
-  const float f_lo = st.qs_lo * scales.x, f_hi = st.qs_hi * scales.x;
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x = s[nt][j] * (j < 2 ? f_lo : f_hi);
-      if (need_mask) {
-        const int pos = p0 + 8 * nt + 2 * c + (j & 1);
-        if (pos > (j < 2 ? lim_lo : lim_hi)) x = -INFINITY;
-      }
-      s[nt][j] = x;
-    }
-  float mx_lo = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-  float mx_hi = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-  mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 1));
-  mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 2));
-  mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 1));
-  mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 2));
-  // the softmax sum's reference and O's (a row that has seen no key: 0)
-  const float lv = fast_log2(scales.y);
-  const float mn_lo = fmaxf(st.m_lo, mx_lo), mn_hi = fmaxf(st.m_hi, mx_hi);
-  const float on_lo = fmaxf(st.mo_lo, mx_lo + lv), on_hi = fmaxf(st.mo_hi, mx_hi + lv);
-  const float base_lo = mn_lo == -INFINITY ? 0.f : mn_lo;
-  const float base_hi = mn_hi == -INFINITY ? 0.f : mn_hi;
-  const float obase_lo = on_lo == -INFINITY ? 0.f : on_lo;
-  const float obase_hi = on_hi == -INFINITY ? 0.f : on_hi;
-  const float al_lo = fast_exp2(st.m_lo - base_lo), al_hi = fast_exp2(st.m_hi - base_hi);
-  const float a_lo = fast_exp2(st.mo_lo - obase_lo), a_hi = fast_exp2(st.mo_hi - obase_hi);
-  st.m_lo = mn_lo;
-  st.m_hi = mn_hi;
-  st.mo_lo = on_lo;
-  st.mo_hi = on_hi;
-  float u[2][4];
-  const float ub_lo = lv - obase_lo + kPUp, ub_hi = lv - obase_hi + kPUp;
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    u[nt][0] = fast_exp2(s[nt][0] + ub_lo);
-    u[nt][1] = fast_exp2(s[nt][1] + ub_lo);
-    u[nt][2] = fast_exp2(s[nt][2] + ub_hi);
-    u[nt][3] = fast_exp2(s[nt][3] + ub_hi);
-    s[nt][0] = fast_exp2(s[nt][0] - base_lo);
-    s[nt][1] = fast_exp2(s[nt][1] - base_lo);
-    s[nt][2] = fast_exp2(s[nt][2] - base_hi);
-    s[nt][3] = fast_exp2(s[nt][3] - base_hi);
-  }
-  st.l_lo = st.l_lo * al_lo + (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-  st.l_hi = st.l_hi * al_hi + (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-  if (__any_sync(0xffffffffu, a_lo != 1.f || a_hi != 1.f)) {
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
-      o[nt][0] *= a_lo;
-      o[nt][1] *= a_lo;
-      o[nt][2] *= a_hi;
-      o[nt][3] *= a_hi;
-    }
-  }
-  const uint32_t pa0 = pack_f16x2(u[0][0], u[0][1]);
-  const uint32_t pa1 = pack_f16x2(u[0][2], u[0][3]);
-  const uint32_t pa2 = pack_f16x2(u[1][0], u[1][1]);
-  const uint32_t pa3 = pack_f16x2(u[1][2], u[1][3]);
-  // O += P V: lane (r, c) reads keys 2c, 2c+1, 2c+8, 2c+9 at head_dim D/8 r .. + D/8 - 1;
-  // column r of n-tile j is head_dim D/8 r + j
-  constexpr int kW = D / 32;  // 4-byte words of a lane's piece of a key row
-  uint32_t w[4][kW];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-    if constexpr (D == 128) {
-      const uint4 v = lds128(sV + key * 128 + ((r ^ (key & 7)) << 4));
-      w[i][0] = v.x;
-      w[i][1] = v.y;
-      w[i][2] = v.z;
-      w[i][3] = v.w;
-    } else {
-      const uint2 v = lds64(sV + key * 64 + (((r >> 1) ^ ((key >> 1) & 3)) << 4) + ((r & 1) << 3));
-      w[i][0] = v.x;
-      w[i][1] = v.y;
-    }
-    if (need_mask && p0 + key >= ctx) {
-#pragma unroll
-      for (int k = 0; k < kW; ++k) w[i][k] = 0;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kW; ++k) {
-    // the bytes of two keys side by side: a pair per head_dim
-    const uint32_t b0l = __byte_perm(w[0][k], w[1][k], 0x5140);
-    const uint32_t b0h = __byte_perm(w[0][k], w[1][k], 0x7362);
-    const uint32_t b1l = __byte_perm(w[2][k], w[3][k], 0x5140);
-    const uint32_t b1h = __byte_perm(w[2][k], w[3][k], 0x7362);
-    mma_16816_f16(o[4 * k], pa0, pa1, pa2, pa3, e4m3x2_to_f16x2(b0l), e4m3x2_to_f16x2(b1l));
-    mma_16816_f16(o[4 * k + 1], pa0, pa1, pa2, pa3, e4m3x2_to_f16x2(b0l >> 16),
-                  e4m3x2_to_f16x2(b1l >> 16));
-    mma_16816_f16(o[4 * k + 2], pa0, pa1, pa2, pa3, e4m3x2_to_f16x2(b0h), e4m3x2_to_f16x2(b1h));
-    mma_16816_f16(o[4 * k + 3], pa0, pa1, pa2, pa3, e4m3x2_to_f16x2(b0h >> 16),
-                  e4m3x2_to_f16x2(b1h >> 16));
-  }
-}
-
 // Shared-block CTA: two independent pairs of warps.  Each pair runs a chain of
 // items one after another (its first item at index = pair, then through
 // SharedItem::next) -- an item is up to two row groups that read the same
@@ -630,10 +341,10 @@ __device__ __forceinline__ void block_update8(uint32_t sK, uint32_t sV, float2 s
 // released it (an empty mbarrier with two arrivals).  An item with no row group
 // contributes nothing; an invalid item is reported and skipped; a `next` that
 // is not a later index inside the array ends the chain.  Every wait is bounded.
-template <int D, int NSTAGE, bool kF8>
+template <int D, int NSTAGE>
 __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const DecodeParams &p,
                                            uint8_t *smem, int warp, int lane) {
-  using C = DecodeCfg<D, NSTAGE, kF8>;
+  using C = DecodeCfg<D, NSTAGE>;
   constexpr int kS = kSharedRowGroups * NSTAGE;  // stages of a pair's pooled ring
   constexpr int kL = D / 32, kNt = D / 8;
   const int r = lane >> 2, c = lane & 3;
@@ -644,10 +355,9 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset) + pair * 2 * kS;
   uint64_t *empty = full + kS;
   int *stage_ok = reinterpret_cast<int *>(smem + C::kFlagOffset) + pair * kS;
-  float2 *stage_scale = reinterpret_cast<float2 *>(smem + C::kScaleOffset) + pair * kS;  // kF8
   if (lw == 0 && lane == 0) {
     for (int s = 0; s < kS; ++s) {
-      mbar_init(smem_u32(&full[s]), C::kFillArrivals);
+      mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), kSharedRowGroups);
     }
     fence_mbar_init();
@@ -695,7 +405,6 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
   // the current item: the fields used, its checks, this warp's row group
   int c_idx = first, c_h = 0, c_kb0 = 0, c_kb1 = 0, c_next = -1;
   uint32_t qa[2 * kL][4];
-  RowState st;
   SharedRowGroup rg;
   int cu0 = 0, qs = 0, ctx = 0;
   bool cur_ok = false, has_rg = false, mine = false;
@@ -716,10 +425,7 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
     mine = has_rg && rg.seq >= 0 && rg.seq < p.num_seqs && rg.qi0 >= 0 &&
            rg.n_q >= 1 && rg.n_q * G <= kRowsPerTile && rg.q_row0 >= 0 &&
            rg.q_row0 + rg.n_q <= p.total_q;
-    if constexpr (kF8)
-      load_q_frags8<D>(p, mine ? rg.q_row0 : 0, mine ? rg.n_q * G : 0, c_h, r, c, qa, st);
-    else
-      load_q_frags<D>(p, mine ? rg.q_row0 : 0, mine ? rg.n_q * G : 0, c_h, r, c, qa);
+    load_q_frags<D>(p, mine ? rg.q_row0 : 0, mine ? rg.n_q * G : 0, c_h, r, c, qa);
     cu0 = qs = ctx = 0;
     if (mine) {
       cu0 = __ldg(p.cu_q_lens + rg.seq);
@@ -750,11 +456,14 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
     if (lane == 0) {
       stage_ok[s] = ok ? 1 : 0;
       if (ok) {
-        fill_stage<C, kF8>(pool_map, p, smem_u32(ring + s * C::kStageBytes),
-                           smem_u32(&stage_scale[s]), bar, phys, p_h);
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        const int row_k = ((phys * 2 + 0) * hkv + p_h) * kBlockSize;
+        const uint32_t dst = smem_u32(ring + s * C::kStageBytes);
+        tma_load_4d(dst, &pool_map, 0, 0, 0, row_k >> 3, bar);
+        tma_load_4d(dst + C::kSlabBytes, &pool_map, 0, 0, 0, (row_k + hkv * kBlockSize) >> 3, bar);
       } else {
         report(p.dev_status, PKV_DEV_BAD_BLOCK);
-        skip_stage<C>(bar);
+        mbar_arrive(bar);  // complete the phase without data; the block is skipped
       }
     }
     ++p_j;
@@ -776,7 +485,7 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
     float o[kNt][4];
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    st.reset();
+    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
     for (int j = 0; j < nblk; ++j) {
       const int s = done % kS;
       const uint32_t par = (uint32_t)((done / kS) & 1);
@@ -788,12 +497,8 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
       ++done;
       if (mine && stage_ok[s]) {
         const uint32_t sK = smem_u32(ring + s * C::kStageBytes);
-        if constexpr (kF8)
-          block_update8<D>(sK, sK + C::kSlabBytes, stage_scale[s], qa, (kb0 + j) * kBlockSize,
-                           q_pos0, lim_lo, lim_hi, ctx, r, c, st, o);
-        else
-          block_update<D>(sK, sK + C::kSlabBytes, qa, (kb0 + j) * kBlockSize, q_pos0, lim_lo,
-                          lim_hi, sl2, r, c, st, o);
+        block_update<D>(sK, sK + C::kSlabBytes, qa, (kb0 + j) * kBlockSize, q_pos0, lim_lo,
+                        lim_hi, sl2, r, c, m_lo, m_hi, l_lo, l_hi, o);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
@@ -817,7 +522,7 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
       pc.kb_end = c_kb1;
       pc.part = rg.part;
       pc.q_row0 = rg.q_row0;
-      write_piece<D, kF8>(p, pc, o, st, R, cu0, r, c);
+      write_piece<D>(p, pc, o, m_lo, m_hi, l_lo, l_hi, R, cu0, r, c);
     } else if (has_rg) {  // this warp's row group, which could not be attended
       poison_piece(p, rg.part, lane);
     }
@@ -830,10 +535,10 @@ __device__ __forceinline__ void shared_cta(const CUtensorMap &pool_map, const De
       mbar_wait(smem_u32(&full[j % kS]), (uint32_t)((j / kS) & 1));
 }
 
-template <int D, int NSTAGE, bool kF8>
+template <int D, int NSTAGE>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap pool_map, const DecodeParams p) {
-  using C = DecodeCfg<D, NSTAGE, kF8>;
+  using C = DecodeCfg<D, NSTAGE>;
   constexpr int kL = D / 32;   // 16-byte Q/K chunks per lane per row
   constexpr int kNt = D / 8;   // n-tiles of the P V product
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -849,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_trigger();
   if (lane == 0) prefetch_tmap(&pool_map);  // fetched beside the metadata reads below
   if (blockIdx.x >= p.num_indep_ctas) {  // CTA-uniform: a shared-prefix CTA
-    shared_cta<D, NSTAGE, kF8>(pool_map, p, smem, warp, lane);
+    shared_cta<D, NSTAGE>(pool_map, p, smem, warp, lane);
     if (p.after_prefill) pdl_wait();
     return;
   }
@@ -908,9 +613,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *ring = smem + warp * C::kRingBytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOffset) + warp * NSTAGE;
   int *stage_ok = reinterpret_cast<int *>(smem + C::kFlagOffset) + warp * NSTAGE;
-  float2 *stage_scale = reinterpret_cast<float2 *>(smem + C::kScaleOffset) + warp * NSTAGE;  // kF8
   if (lane == 0 && has_warp) {
-    for (int s = 0; s < NSTAGE; ++s) mbar_init(smem_u32(&bars[s]), C::kFillArrivals);
+    for (int s = 0; s < NSTAGE; ++s) mbar_init(smem_u32(&bars[s]), 1);
     fence_mbar_init();
   }
   if (!p.after_prefill) pdl_wait();
@@ -965,11 +669,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       stage_ok[stage] = ok ? 1 : 0;
       if (ok) {
-        fill_stage<C, kF8>(pool_map, p, smem_u32(ring + stage * C::kStageBytes),
-                           smem_u32(&stage_scale[stage]), bar, phys, pp.h);
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        const int row_k = ((phys * 2 + 0) * hkv + pp.h) * kBlockSize;
+        const int row_v = row_k + hkv * kBlockSize;
+        const uint32_t dst = smem_u32(ring + stage * C::kStageBytes);
+        // one 4-D box per slab: the whole block of one head (rows / 8 = group coordinate)
+        tma_load_4d(dst, &pool_map, 0, 0, 0, row_k >> 3, bar);
+        tma_load_4d(dst + C::kSlabBytes, &pool_map, 0, 0, 0, row_v >> 3, bar);
       } else {
         report(p.dev_status, in_table ? PKV_DEV_BAD_BLOCK : PKV_DEV_PLAN_MISMATCH);
-        skip_stage<C>(bar);
+        mbar_arrive(bar);  // complete the phase without data; the block is skipped
       }
     }
     ++pkb;
@@ -1001,11 +710,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // these loads do not wait for the length loads below; a piece that then
     // fails the check (R = 0) uses none of them.
     uint32_t qa[2 * kL][4];
-    RowState st;
-    if constexpr (kF8)
-      load_q_frags8<D>(p, pc.q_row0, valid ? pc.n_q * G : 0, pc.h, r, c, qa, st);
-    else
-      load_q_frags<D>(p, pc.q_row0, valid ? pc.n_q * G : 0, pc.h, r, c, qa);
+    load_q_frags<D>(p, pc.q_row0, valid ? pc.n_q * G : 0, pc.h, r, c, qa);
     int cu0 = 0, qs = 0, ctx = 0;
     if (valid) {
       cu0 = pi == pb ? f_cu0 : __ldg(p.cu_q_lens + pc.seq);
@@ -1023,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float o[kNt][4];
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    st.reset();
+    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
     bool head_bad = false;  // the plan's block ids for this piece disagree with the table
 
     for (int kb = pc.kb_begin; kb < pc.kb_end; ++kb) {
@@ -1044,12 +749,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (valid && !head_bad && stage_ok[stage]) {
         const uint32_t sK = smem_u32(ring + stage * C::kStageBytes);
-        if constexpr (kF8)
-          block_update8<D>(sK, sK + C::kSlabBytes, stage_scale[stage], qa, kb * kBlockSize, q_pos0,
-                           lim_lo, lim_hi, ctx, r, c, st, o);
-        else
-          block_update<D>(sK, sK + C::kSlabBytes, qa, kb * kBlockSize, q_pos0, lim_lo, lim_hi, sl2,
-                          r, c, st, o);
+        block_update<D>(sK, sK + C::kSlabBytes, qa, kb * kBlockSize, q_pos0, lim_lo, lim_hi, sl2,
+                        r, c, m_lo, m_hi, l_lo, l_hi, o);
       }
       __syncwarp();
       issue_next(stage);  // refill this stage with the stream's next block
@@ -1060,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (abandoned) break;
     if (valid && !head_bad)
-      write_piece<D, kF8>(p, pc, o, st, R, cu0, r, c);
+      write_piece<D>(p, pc, o, m_lo, m_hi, l_lo, l_hi, R, cu0, r, c);
     else
       poison_piece(p, pc.part, lane);
   }
@@ -1072,19 +773,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.after_prefill) pdl_wait();
 }
 
-// ---- piece epilogue straight from registers: lane (r, c) holds 2 kRun contiguous
-// head_dims of each of its kRuns pieces of rows r and r + 8 (16-bit pool: 16 per
-// 64-column half; 8-bit pool: D / 4 in one piece): n-tile t of piece j holds
-// dims base + t (even column) and base + kRun + t (odd column).  A whole segment
-// writes the normalised bf16 output; a split piece writes its fp32 partial (O,
-// m, l), O against m (the 8-bit pool's own reference of O is taken out first).
-template <int D, bool kF8>
+// ---- piece epilogue straight from registers: lane (r, c) holds head_dim
+// [64j + 16c, 64j + 16c + 16) of rows r and r + 8.  A whole segment writes the
+// normalised bf16 output; a split piece writes its fp32 partial (O, m, l).
+template <int D>
 __device__ __forceinline__ void write_piece(const DecodeParams &p, const Piece &pc,
-                                            float (&o)[D / 8][4], RowState &st, int R, int cu0,
-                                            int r, int c) {
-  constexpr int kRun = kF8 ? D / 8 : 8, kRuns = D / (8 * kRun);
+                                            float (&o)[D / 8][4], float m_lo, float m_hi,
+                                            float l_lo, float l_hi, int R, int cu0, int r, int c) {
   const int G = p.group;
-  float l_lo = st.l_lo, l_hi = st.l_hi;
   l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
   l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
   l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
@@ -1094,46 +790,39 @@ __device__ __forceinline__ void write_piece(const DecodeParams &p, const Piece &
     const int row = r + 8 * half;
     if (row >= R) continue;
     const float l = half ? l_hi : l_lo;
-    const float m = half ? st.m_hi : st.m_lo;
-    float f = 1.f;
-    if constexpr (kF8) {
-      const float mo = half ? st.mo_hi : st.mo_lo;
-      f = mo == -INFINITY ? 0.f : fast_exp2(mo - m - kPUp);
-    }
+    const float m = half ? m_hi : m_lo;
     const int64_t tok = cu0 + pc.qi0 + row / G;
     const int hq = pc.h * G + row % G;
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
-      const int d0 = 8 * kRun * j + 2 * kRun * c;
-      float v[2 * kRun];
+    for (int j = 0; j < D / 64; ++j) {
+      float v[16];
 #pragma unroll
-      for (int t = 0; t < kRun; ++t) {
-        v[t] = o[kRun * j + t][2 * half];
-        v[kRun + t] = o[kRun * j + t][2 * half + 1];
-      }
-      if constexpr (kF8) {
-#pragma unroll
-        for (int t = 0; t < 2 * kRun; ++t) v[t] *= f;
+      for (int t = 0; t < 8; ++t) {
+        v[t] = o[8 * j + t][2 * half];
+        v[8 + t] = o[8 * j + t][2 * half + 1];
       }
       if (pc.part < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (tok * p.num_q_heads + hq) * D + d0);
-#pragma unroll
-        for (int t = 0; t < kRun / 4; ++t) {
-          const float *x = v + 8 * t;
-          uint4 a;
-          a.x = pack_bf16x2(x[0] * inv, x[1] * inv);
-          a.y = pack_bf16x2(x[2] * inv, x[3] * inv);
-          a.z = pack_bf16x2(x[4] * inv, x[5] * inv);
-          a.w = pack_bf16x2(x[6] * inv, x[7] * inv);
-          dst[t] = a;
-        }
+        uint4 a, b;
+        a.x = pack_bf16x2(v[0] * inv, v[1] * inv);
+        a.y = pack_bf16x2(v[2] * inv, v[3] * inv);
+        a.z = pack_bf16x2(v[4] * inv, v[5] * inv);
+        a.w = pack_bf16x2(v[6] * inv, v[7] * inv);
+        b.x = pack_bf16x2(v[8] * inv, v[9] * inv);
+        b.y = pack_bf16x2(v[10] * inv, v[11] * inv);
+        b.z = pack_bf16x2(v[12] * inv, v[13] * inv);
+        b.w = pack_bf16x2(v[14] * inv, v[15] * inv);
+        uint4 *dst =
+            reinterpret_cast<uint4 *>(p.out + (tok * p.num_q_heads + hq) * D + 64 * j + 16 * c);
+        dst[0] = a;
+        dst[1] = b;
       } else {
         float4 *dst = reinterpret_cast<float4 *>(
-            p.part_o + ((int64_t)pc.part * kRowsPerTile + row) * D + d0);
-#pragma unroll
-        for (int t = 0; t < kRun / 2; ++t)
-          dst[t] = make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+            p.part_o + ((int64_t)pc.part * kRowsPerTile + row) * D + 64 * j + 16 * c);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        dst[2] = make_float4(v[8], v[9], v[10], v[11]);
+        dst[3] = make_float4(v[12], v[13], v[14], v[15]);
       }
     }
     if (pc.part >= 0 && c == 0)
@@ -1143,72 +832,11 @@ __device__ __forceinline__ void write_piece(const DecodeParams &p, const Piece &
 
 // ------------------------------------------------------------------ host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
-DecodeParams make_params(const AttnArgs &a) {
-  DecodeParams p;
-  p.q = static_cast<const __nv_bfloat16 *>(a.q);
-  p.out = static_cast<__nv_bfloat16 *>(a.out);
-  p.cu_q_lens = a.cu_q_lens;
-  p.context_lens = a.context_lens;
-  p.block_tables = a.block_tables;
-  p.warp_begin = a.warp_begin;
-  p.warp_head = a.warp_head;
-  p.shared = a.shared_items;
-  p.num_indep_ctas = (a.num_decode_warps + kWarps - 1) / kWarps;
-  p.num_shared_items = a.num_shared_items;
-  p.pieces = a.pieces;
-  p.merges = a.merge_groups;
-  p.part_o = a.part_o;
-  p.part_ml = reinterpret_cast<float2 *>(a.part_ml);
-  p.num_merges = a.num_merge_groups;
-  p.lookahead = a.lookahead;
-  p.after_prefill = a.num_prefill_tiles > 0 && a.num_prefill_ctas > 0 ? 1 : 0;
-  p.num_decode_merges = a.num_decode_merges;
-  p.merge_lanes_log2 = 0;
-  p.merge_rows = a.merge_rows;
-  p.num_partials = a.num_partials;
-  p.ppart_o = a.ppart_o;
-  p.ppart_ml = reinterpret_cast<const float2 *>(a.ppart_ml);
-  p.dev_status = a.dev_status;
-  p.num_warps = a.num_decode_warps;
-  p.num_seqs = a.num_seqs;
-  p.max_blocks_per_seq = a.max_blocks_per_seq;
-  p.num_blocks = a.desc.num_blocks;
-  p.num_q_heads = a.num_q_heads;
-  p.num_kv_heads = a.desc.num_kv_heads;
-  p.group = a.num_q_heads / a.desc.num_kv_heads;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.total_q = a.total_q;
-  p.pool = static_cast<const uint8_t *>(a.kv_pool);
-  p.pool_bytes = (int64_t)a.desc.num_blocks * 2 * a.desc.num_kv_heads * kBlockSize *
-                 a.desc.head_dim * (a.kv_scales ? 1 : 2);
-  p.kv_scales = reinterpret_cast<const float2 *>(a.kv_scales);
-  return p;
-}
-
-template <int D, int NSTAGE, bool kF8>
+template <int D, int NSTAGE>
 int launch_decode_t(const AttnArgs &a, const CUtensorMap &map) {
-  using C = DecodeCfg<D, NSTAGE, kF8>;
-  auto kern = decode_kernel<D, NSTAGE, kF8>;
-  cudaError_t e = prepare_kernel<decode_kernel<D, NSTAGE, kF8>>(C::kSmemBytes);
+  using C = DecodeCfg<D, NSTAGE>;
+  auto kern = decode_kernel<D, NSTAGE>;
+  cudaError_t e = prepare_kernel<decode_kernel<D, NSTAGE>>(C::kSmemBytes);
   if (e != cudaSuccess) return (int)e;
   const unsigned grid = (unsigned)((a.num_decode_warps + kWarps - 1) / kWarps + a.num_shared_ctas);
   profile_begin(PKV_KERNEL_DECODE, a.stream);
@@ -1241,37 +869,17 @@ int make_pool_map(void *map_out, const void *pool, const pkv_pool_desc &desc) {
   return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
-// 4-D view of an 8-bit pool: (D bytes, 16 rows, KV heads, K and V of every
-// block); a box (D, 16, 1, 2) is the K and the V slab of one block and head.
-static int make_pool_map8(CUtensorMap *map, const void *pool, const pkv_pool_desc &desc) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return (int)cudaErrorNotSupported;
-  const cuuint64_t d = (cuuint64_t)desc.head_dim, hkv = (cuuint64_t)desc.num_kv_heads;
-  cuuint64_t dims[4] = {d, kBlockSize, hkv,
-                        (cuuint64_t)(desc.num_blocks > 0 ? desc.num_blocks : 1) * 2};
-  cuuint64_t strides[3] = {d, d * kBlockSize, d * kBlockSize * hkv};
-  cuuint32_t box[4] = {(cuuint32_t)d, kBlockSize, 1, 2};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(pool), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
-}
-
 int launch_decode(const AttnArgs &a, int *launches) {
   if (a.num_decode_warps <= 0 && a.num_shared_ctas <= 0) return 0;
-  CUtensorMap map;
-  int e = a.kv_scales ? make_pool_map8(&map, a.kv_pool, a.desc)
-                      : make_pool_map(&map, a.kv_pool, a.desc);
-  if (e) return e;
-  // stages: 24 KB in flight a warp (12 for D = 64) either way
-  if (a.kv_scales)
-    e = a.desc.head_dim == 128 ? launch_decode_t<128, 6, true>(a, map)
-                               : launch_decode_t<64, 6, true>(a, map);
-  else
-    e = a.desc.head_dim == 128 ? launch_decode_t<128, 3, false>(a, map)
-                               : launch_decode_t<64, 3, false>(a, map);
+  int e;
+  if (a.kv_scales) {
+    e = launch_decode8(a);
+  } else {
+    CUtensorMap map;
+    e = make_pool_map(&map, a.kv_pool, a.desc);
+    if (e) return e;
+    e = a.desc.head_dim == 128 ? launch_decode_t<128, 3>(a, map) : launch_decode_t<64, 3>(a, map);
+  }
   if (!e) {
     ++*launches;
     count_launches(1);
