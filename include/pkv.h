@@ -459,6 +459,25 @@ PKV_API pkv_status pkv_paged_varlen_attention(const void *q, const int32_t *cu_q
                                       int32_t *dev_status, pkv_stream stream);
 
 /*
+ * pkv_plan_step_ex with the work cut for the kernels of an 8-bit pool (more
+ * split-KV warps an SM).  The plan serves a bf16 pool too, as any other plan
+ * serves an 8-bit pool: only the division of the work differs.
+ */
+PKV_API pkv_status pkv_plan_step_fp8(const int32_t *cu_q_lens, const int32_t *context_lens,
+                                     int32_t num_seqs, int32_t num_q_heads,
+                                     const pkv_pool_desc *desc, int32_t num_sms, int32_t steps,
+                                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                     int32_t prefill_min_q, void *plan, int64_t plan_capacity,
+                                     pkv_plan_info *info);
+
+/* What an 8-bit pool adds to a plan's summary, written by pkv_plan_stage_fp8. */
+typedef struct pkv_fp8_info {
+  int32_t staged_blocks;   /* bf16 copies of blocks the tensor-core kernel reads */
+  int32_t max_rows;        /* query rows of the largest split-KV row group */
+  int64_t workspace_bytes; /* workspace pkv_paged_varlen_attention_fp8 needs */
+} pkv_fp8_info;
+
+/*
  * What an 8-bit pool adds to a plan.  The split-KV kernel reads the 8-bit blocks
  * directly; the tensor-core kernel reads bf16 copies of the blocks its sequences
  * need, made in the workspace by the same attention call.
@@ -466,21 +485,21 @@ PKV_API pkv_status pkv_paged_varlen_attention(const void *q, const int32_t *cu_q
  *   stage_begin: HOST int32 [num_seqs + 1], written: sequence s's blocks 0, 1, ..
  *   get copies stage_begin[s], stage_begin[s] + 1, .. < stage_begin[s + 1] (none
  *   for a sequence the tensor cores do not read).
- *   *workspace_bytes receives the workspace pkv_paged_varlen_attention_fp8 needs.
- * Upload stage_begin beside the plan.  When stage_begin[num_seqs] is 0 (no
+ * Upload stage_begin beside the plan.  When fp8->staged_blocks is 0 (no
  * tensor-core work) the attention call takes NULL for it.
  * Errors: PKV_ERR_NULL, PKV_ERR_SHAPE (info and plan disagree),
  * PKV_ERR_UNSUPPORTED (more copies than 32-bit row coordinates reach).
  */
 PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *info,
-                                      int32_t *stage_begin, int64_t *workspace_bytes);
+                                      int32_t *stage_begin, pkv_fp8_info *fp8);
 
 /*
  * pkv_paged_varlen_attention over an 8-bit pool (layout above): the same step,
  * plan, rules and results, with K[p] = c_k scale_k and V[p] = c_v scale_v.
  * kv_scales: any positive finite values (not only powers of two).
- *   stage_begin: DEVICE copy of pkv_plan_stage_fp8's array; staged_blocks: its
- *   last entry.  workspace_bytes: at least what pkv_plan_stage_fp8 returned.
+ *   fp8, stage_begin: the summary pkv_plan_stage_fp8 wrote, and a DEVICE copy of
+ *   its array.  workspace_bytes: at least fp8->workspace_bytes.  A row group with
+ *   more than fp8->max_rows rows is reported (PKV_DEV_PLAN_MISMATCH), not attended.
  *   Rounding: on the split-KV kernel every stored value enters the products
  *   exactly (fp16), the weights are rounded to fp16, 2^-12; on the tensor-core
  *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the
@@ -496,7 +515,7 @@ PKV_API pkv_status pkv_paged_varlen_attention_fp8(
     const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
     const float *kv_scales, const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
-    const void *plan_dev, const int32_t *stage_begin, int32_t staged_blocks, void *out,
+    const void *plan_dev, const pkv_fp8_info *fp8, const int32_t *stage_begin, void *out,
     void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream);
 
 /*

@@ -73,6 +73,11 @@ class PlanInfo(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class Fp8Info(ctypes.Structure):
+    _fields_ = [("staged_blocks", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 class Rope(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("max_positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
@@ -145,11 +150,14 @@ def _load():
             lib.pkv_rope_kv_append.restype = i32
             lib.pkv_rope_kv_append_fp8.argtypes = rope_args + [P, ctypes.POINTER(PoolDesc), P, P]
             lib.pkv_rope_kv_append_fp8.restype = i32
-            lib.pkv_plan_stage_fp8.argtypes = [P, ctypes.POINTER(PlanInfo), P, ctypes.POINTER(i64)]
+            lib.pkv_plan_step_fp8.argtypes = lib.pkv_plan_step_ex.argtypes
+            lib.pkv_plan_step_fp8.restype = i32
+            lib.pkv_plan_stage_fp8.argtypes = [P, ctypes.POINTER(PlanInfo), P,
+                                               ctypes.POINTER(Fp8Info)]
             lib.pkv_plan_stage_fp8.restype = i32
             lib.pkv_paged_varlen_attention_fp8.argtypes = [
                 P, P, P, P, i32, P, P, ctypes.POINTER(PoolDesc), ctypes.c_float,
-                ctypes.POINTER(PlanInfo), P, P, i32, P, P, i64, P, P]
+                ctypes.POINTER(PlanInfo), P, ctypes.POINTER(Fp8Info), P, P, P, i64, P, P]
             lib.pkv_paged_varlen_attention_fp8.restype = i32
             _lib = lib
     return _lib
@@ -512,9 +520,9 @@ class StepPlan:
         self.device = device
         self.dev = None
         self.workspace = None
-        self.fp8 = fp8              # planned for an 8-bit pool too (pkv_plan_stage_fp8)
+        self._for_fp8 = fp8
+        self.fp8 = None             # Fp8Info of a plan for an 8-bit pool (pkv_plan_stage_fp8)
         self.stage = None           # device int32 [num_seqs + 1], when there are staged blocks
-        self.staged_blocks = 0
         self.upload(stream)
 
     def upload(self, stream=None):
@@ -524,15 +532,14 @@ class StepPlan:
         nbytes = max(int(self.info.plan_bytes), 16)
         src = torch.from_numpy(self.host.view(np.uint8)[:nbytes])
         wsb = workspace_size(self.info)
-        stage = None
-        if self.fp8:
-            stage, wsb = stage_fp8(self.info, self.host)
-            self.staged_blocks = int(stage[-1])
+        if self._for_fp8:
+            stage, self.fp8 = stage_fp8(self.info, self.host)
+            wsb = int(self.fp8.workspace_bytes)
         with torch.cuda.stream(stream) if stream is not None else _nullcontext():
             if self.dev is None or self.dev.numel() < nbytes:
                 self.dev = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             self.dev[:nbytes].copy_(src, non_blocking=False)
-            if self.staged_blocks:
+            if self._for_fp8 and self.fp8.staged_blocks:
                 self.stage = torch.from_numpy(stage).to(dev)
             if wsb > 0 and (self.workspace is None or self.workspace.numel() < wsb):
                 self.workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
@@ -540,15 +547,15 @@ class StepPlan:
 
 
 def stage_fp8(info: PlanInfo, host: np.ndarray):
-    """(stage_begin int32 [num_seqs + 1], workspace bytes) of a host plan for an
-    8-bit pool (pkv_plan_stage_fp8)."""
+    """(stage_begin int32 [num_seqs + 1], Fp8Info) of a host plan for an 8-bit pool
+    (pkv_plan_stage_fp8)."""
     begin = np.zeros(int(info.num_seqs) + 1, dtype=np.int32)
-    nbytes = ctypes.c_int64(0)
+    fp8 = Fp8Info()
     st = _load().pkv_plan_stage_fp8(host.ctypes.data_as(ctypes.c_void_p), ctypes.byref(info),
-                                    begin.ctypes.data_as(ctypes.c_void_p), ctypes.byref(nbytes))
+                                    begin.ctypes.data_as(ctypes.c_void_p), ctypes.byref(fp8))
     if st:
         raise PkvError(st, "pkv_plan_stage_fp8")
-    return begin, int(nbytes.value)
+    return begin, fp8
 
 
 class _on_device:
@@ -597,8 +604,8 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     out (with upload=False): a writable host buffer (numpy array or CPU tensor,
     e.g. pinned memory for an asynchronous upload) the plan is written into; the
     returned host bytes are then a view of it.
-    fp8: the plan also serves paged_varlen_attention_fp8 (a larger workspace when
-    the step has tensor-core work; it still serves a bf16 pool).
+    fp8: plan for paged_varlen_attention_fp8 (pkv_plan_step_fp8; a larger workspace
+    when the step has tensor-core work.  The plan still serves a bf16 pool).
     Returns a StepPlan (or (info, host_bytes) when upload=False).
     """
     desc = kv_pool_or_desc if isinstance(kv_pool_or_desc, PoolDesc) else pool_desc(kv_pool_or_desc)
@@ -613,7 +620,8 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
                    if torch.cuda.is_available() else 152)
     info = PlanInfo()
     lib = _load()
-    name = "pkv_plan_step_ex"
+    name = "pkv_plan_step_fp8" if fp8 else "pkv_plan_step_ex"
+    plan_fn = getattr(lib, name)
     bt = None
     if block_tables is not None:
         bt = _host_i32(block_tables)
@@ -622,7 +630,7 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     pmq = 0 if prefill_min_q is None else int(prefill_min_q)
 
     def call(buf, cap):
-        return lib.pkv_plan_step_ex(
+        return plan_fn(
             cu.ctypes.data_as(ctypes.c_void_p), ctx.ctypes.data_as(ctypes.c_void_p), ctx.shape[0],
             int(num_q_heads), ctypes.byref(desc), int(num_sms),
             1 if chain_steps is None else int(chain_steps),
@@ -951,13 +959,13 @@ class BoundAttentionFp8:
         if (info.total_q != total_q or info.num_q_heads != hq or info.num_seqs + 1 != n_cu or
                 info.num_seqs != n_ctx or info.num_seqs != n_bt):
             raise ValueError("the plan does not match the bound buffers")
-        if not plan.fp8:
+        if plan.fp8 is None:
             raise ValueError("the plan was not made for an 8-bit pool: plan_step(..., fp8=True)")
         ws = plan.workspace
         with _on_device(self._device):
-            st = self._f(*self._head, ctypes.byref(info), plan.dev.data_ptr(), _ptr(plan.stage),
-                         plan.staged_blocks, self._out, _ptr(ws), 0 if ws is None else ws.numel(),
-                         *self._tail)
+            st = self._f(*self._head, ctypes.byref(info), plan.dev.data_ptr(),
+                         ctypes.byref(plan.fp8), _ptr(plan.stage), self._out, _ptr(ws),
+                         0 if ws is None else ws.numel(), *self._tail)
         if st:
             raise PkvError(st, "pkv_paged_varlen_attention_fp8")
 

@@ -152,8 +152,8 @@ static pkv_status attention(const void *q, const int32_t *cu_q_lens, const int32
                             const int32_t *block_tables, int32_t max_blocks_per_seq,
                             const void *kv_pool, const float *kv_scales,
                             const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
-                            const void *plan_dev, const int32_t *stage_begin,
-                            int32_t staged_blocks, void *out, void *workspace,
+                            const void *plan_dev, const pkv_fp8_info *fp8,
+                            const int32_t *stage_begin, void *out, void *workspace,
                             int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
   pkv_status st = check_pool(desc);
   if (st != PKV_OK) return st;
@@ -234,13 +234,14 @@ static pkv_status attention(const void *q, const int32_t *cu_q_lens, const int32
   const int64_t ws = ws_total_bytes(info->num_partials, info->num_prefill_partials, d);
   if (ws > workspace_bytes) return PKV_ERR_WORKSPACE;
   a.kv_scales = kv_scales;
+  if (kv_scales) a.max_rows = fp8->max_rows;
   if (kv_scales && info->num_prefill_tiles > 0) {
     // the tensor-core kernel reads bf16 copies, behind the partial results
-    if (staged_blocks <= 0 || !staged_fits(staged_blocks, *desc)) return PKV_ERR_SHAPE;
+    if (fp8->staged_blocks <= 0 || !staged_fits(fp8->staged_blocks, *desc)) return PKV_ERR_SHAPE;
     if (!stage_begin || !workspace) return PKV_ERR_NULL;
-    if (workspace_bytes < ws + staged_bytes(staged_blocks, *desc)) return PKV_ERR_WORKSPACE;
+    if (workspace_bytes < ws + staged_bytes(fp8->staged_blocks, *desc)) return PKV_ERR_WORKSPACE;
     a.stage_begin = stage_begin;
-    a.staged_blocks = staged_blocks;
+    a.staged_blocks = fp8->staged_blocks;
     a.staged = wb + ws;
   }
   a.dev_status = dev_status;
@@ -261,7 +262,7 @@ extern "C" pkv_status pkv_paged_varlen_attention(
     const pkv_pool_desc *desc, float scale, const pkv_plan_info *info, const void *plan_dev,
     void *out, void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
   return attention(q, cu_q_lens, context_lens, block_tables, max_blocks_per_seq, kv_pool, nullptr,
-                   desc, scale, info, plan_dev, nullptr, 0, out, workspace, workspace_bytes,
+                   desc, scale, info, plan_dev, nullptr, nullptr, out, workspace, workspace_bytes,
                    dev_status, stream);
 }
 
@@ -269,13 +270,13 @@ extern "C" pkv_status pkv_paged_varlen_attention_fp8(
     const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const void *kv_pool,
     const float *kv_scales, const pkv_pool_desc *desc, float scale, const pkv_plan_info *info,
-    const void *plan_dev, const int32_t *stage_begin, int32_t staged_blocks, void *out,
+    const void *plan_dev, const pkv_fp8_info *fp8, const int32_t *stage_begin, void *out,
     void *workspace, int64_t workspace_bytes, int32_t *dev_status, pkv_stream stream) {
-  if (!kv_scales) return PKV_ERR_NULL;
+  if (!kv_scales || !fp8) return PKV_ERR_NULL;
   if (!aligned16(kv_scales)) return PKV_ERR_ALIGN;
   return attention(q, cu_q_lens, context_lens, block_tables, max_blocks_per_seq, kv_pool, kv_scales,
-                   desc, scale, info, plan_dev, stage_begin, staged_blocks, out, workspace,
-                   workspace_bytes, dev_status, stream);
+                   desc, scale, info, plan_dev, fp8, stage_begin, out, workspace, workspace_bytes,
+                   dev_status, stream);
 }
 
 // Both rotating appends: kv_scales NULL is a bf16 pool.

@@ -10,9 +10,15 @@
 //
 // What bounds it.  A block of a head is 4 KB at D = 128, half a bf16 one, so at
 // HBM's rate an SM has ~180 cycles for a block that took a bf16 warp ~200
-// instructions.  The first version (fp16 products of converted K and V, one block
-// at a time, ~500 instructions a block) streamed 1.13 GB in 235 us where HBM needs
-// 166: bound by instruction issue at 2 warps a scheduler.  Hence:
+// instructions.  The first version (the bf16 kernel's products on converted K and V,
+// a block at a time, ~500 instructions a block) streamed 1.13 GB in 235 us where HBM
+// needs 166: bound by instruction issue at 2 warps a scheduler.  Hence:
+//  * The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys and head_dims are
+//    the 16-row side of an m16n8k16 product and the query rows the 8-column side, so a
+//    row group of at most 8 rows (one token of up to 8 query heads a KV head, a verify
+//    pair of 4) takes half the products, exponentials and accumulators; larger ones
+//    take two column tiles.  The 8 x 8 transposes of P^T between the two products are
+//    one movmatrix each.
 //  * Both products run on fp16 operands with fp32 sums.  e4m3 values are exact in fp16;
 //    a row of q is scaled by a power of two so that its largest value lies in [2^14,
 //    2^15): fp16 then holds every bf16 value down to 2^-28 of the row's largest exactly
@@ -25,10 +31,11 @@
 //    rounded to fp16 (2^-12; smallest step 2^-38 of the largest weight) where bf16
 //    would round to 2^-9.
 //  * Two consecutive blocks are a stage of the ring (one barrier) and are attended
-//    together: one maximum, one rescale, and two independent chains of products.
+//    together: one maximum, one rescale, and independent chains of products.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_decode.cuh"
 
@@ -46,30 +53,57 @@ struct Stage8 {
   static constexpr int kBlockBytes = 2 * kSlabBytes;
   static constexpr int kStageBytes = kPair * kBlockBytes;
 };
-template <int D, int NSTAGE>
+// NT: the column tiles of the largest row group (1: at most 8 rows).
+template <int D, int NT>
 struct Decode8Cfg : Stage8<D> {
-  static constexpr int kRingBytes = NSTAGE * Stage8<D>::kStageBytes;
+  // CTAs an SM: with one column tile a lane's state fits 128 registers, so 16 warps.
+  // Stages: what fits beside (12 or 24 KB a warp at most)
+  static constexpr int kCtas = NT == 1 ? 4 : 2;
+  static constexpr int kStages = (NT == 1 ? 1 : 3) * (D == 128 ? 1 : 2);
+
+  static constexpr int kRingBytes = kStages * Stage8<D>::kStageBytes;
   static constexpr int kScaleOffset = kWarps * kRingBytes;  // float2 x 2 a stage
   // a shared-prefix CTA uses as many empty barriers as full ones
-  static constexpr int kBarOffset = kScaleOffset + kWarps * NSTAGE * kPair * 8;
-  static constexpr int kFlagOffset = kBarOffset + 2 * kWarps * NSTAGE * 8;  // int x 2 a stage
-  static constexpr int kSmemBytes = kFlagOffset + kWarps * NSTAGE * kPair * 4 + 1024;
+  static constexpr int kBarOffset = kScaleOffset + kWarps * kStages * kPair * 8;
+  static constexpr int kFlagOffset = kBarOffset + 2 * kWarps * kStages * 8;  // int x 2 a stage
+  static constexpr int kSmemBytes = kFlagOffset + kWarps * kStages * kPair * 4 + 1024;
 };
 
-// Running state of the two query rows a lane shares in (rows r and r + 8).
-struct RowState {
-  float m_lo, m_hi;    // running maximum of x
-  float l_lo, l_hi;    // this lane's part of sum w
-  float qs_lo, qs_hi;  // from a product to x, but for the block's K scale
-  float vref;          // the largest V scale seen; O is in units of vref / 2^14
-  float inv_vref;
+// A row group's running state in one lane: query rows 8 t + 2 c + j, t < NT, j < 2
+// (NT column tiles: 1 for a row group of at most 8 rows, else 2), and this lane's
+// fragments of q and O.
+template <int D, int NT>
+struct Rows {
+  float m[NT][2];        // running maximum of x
+  float l[NT][2];        // this lane's part of sum w
+  float qs[NT][2];       // from a product to x, but for the block's K scale
+  int lim[NT][2];        // last visible key
+  float vref, inv_vref;  // the largest V scale seen; O is in units of vref / 2^14
+  uint32_t q[D / 16][NT][2];
+  float o[D / 16][NT][4];  // head_dims 16 i + r (+ 8 in the last two), rows 8 t + 2 c, + 1
   __device__ __forceinline__ void reset() {
-    m_lo = m_hi = -INFINITY;
-    l_lo = l_hi = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[t][j] = -INFINITY;
+        l[t][j] = 0.f;
+      }
     vref = inv_vref = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
   }
 };
 
+// 8 x 8 transpose across the warp: lane (r, c) gives row r, columns 2 c and 2 c + 1, and
+// gets row r, columns 2 c and 2 c + 1 of the transposed matrix.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
 // Two 16 x 16 byte matrices, transposed: register 2 m + i holds keys 4 (lane % 4) ..
 // + 3 of column 8 i + lane / 4 of matrix m; lane j < 16 gives row j of matrix 0, lane
 // 16 + j of matrix 1.
@@ -89,20 +123,20 @@ __device__ __forceinline__ uint32_t slab_off(int row, int chunk) {
                   : (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// q as A fragments (m16 x k16) in fp16: rows r and r + 8 of the row group's R rows
-// (token row / G, head h * G + row % G from packed query row q_row0; rows >= R read as
-// zeros).  Lane (r, c) of step 4 L + i holds head_dims 16 e + 4 i .. + 3 of chunk e =
-// c D / 64 + L, the ones its K chunk loads supply.  A row that holds an infinity becomes
-// NaN.  The sign of the softmax scale goes into q (a scale of 0 makes q zero), so x
-// grows with the products.
-template <int D>
-__device__ __forceinline__ void load_q8(const DecodeParams &p, int q_row0, int R, int h, int r,
-                                        int c, uint32_t (&qa)[D / 16][4], RowState &st) {
+// q as B fragments (k16 x n8) in fp16, and what belongs to its rows: row 8 t + r of the
+// row group's R rows (token row / G, head h * G + row % G from packed query row q_row0;
+// rows >= R read as zeros and see no key).  Lane (r, c) of step 4 L + i holds head_dims
+// 16 e + 4 i .. + 3 of chunk e = c D / 64 + L, the ones its K chunk loads supply.  A row
+// that holds an infinity becomes NaN.  The sign of the softmax scale goes into q (a
+// scale of 0 makes q zero), so x grows with the products.
+template <int D, int NT>
+__device__ __forceinline__ void load_rows(const DecodeParams &p, int q_row0, int R, int h,
+                                          int q_pos0, int r, int c, Rows<D, NT> &rows) {
   constexpr int kL = D / 64;  // 16-element chunks per lane per row
   const int G = p.group;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = r + 8 * half;
+  for (int t = 0; t < NT; ++t) {
+    const int row = r + 8 * t;
     const bool rv = row < R;
     const __nv_bfloat16 *qrow =
         p.q + ((int64_t)(q_row0 + (rv ? row / G : 0)) * p.num_q_heads + h * G +
@@ -126,129 +160,138 @@ __device__ __forceinline__ void load_q8(const DecodeParams &p, int q_row0, int R
     if (sl2 < 0.f) up = -up;
     if (sl2 == 0.f) up = 0.f;
     down = sl2 == 0.f ? 1.f : down * fabsf(sl2);
-    (half ? st.qs_hi : st.qs_lo) = down;
 #pragma unroll
     for (int i = 0; i < 8 * kL; ++i)
-      qa[i >> 1][(i & 1) * 2 + half] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
-                                                  __uint_as_float(w[i] & 0xffff0000u) * up);
+      rows.q[i >> 1][t][i & 1] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
+                                            __uint_as_float(w[i] & 0xffff0000u) * up);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      rows.qs[t][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
+      const int mine = 8 * t + 2 * c + j;
+      rows.lim[t][j] = mine < R ? q_pos0 + mine / G : -1;
+    }
   }
 }
 
-// A stage in shared memory: its two blocks' slabs, scales (K0, V0, K1, V1) and the
-// position of each block's first key (kNoBlock: no block, every key is masked).
+// Two blocks of a stage in shared memory: sc holds their scales (K0, V0, K1, V1), p0 the
+// position of each one's first key (kNoBlock: no block, every key is masked).
 constexpr int kNoBlock = 1 << 30;
 
-template <int D>
+template <int D, int NT>
 __device__ __forceinline__ void attend_pair(uint32_t stage, const float4 sc, const int (&p0)[kPair],
-                                            const uint32_t (&qa)[D / 16][4], int q_pos0, int lim_lo,
-                                            int lim_hi, int ctx, int lane, RowState &st,
-                                            float (&o)[D / 8][4]) {
+                                            int q_pos0, int ctx, int lane, Rows<D, NT> &rows) {
   constexpr int kSlab = Stage8<D>::kSlabBytes;
   const int r = lane >> 2, c = lane & 3;
-  // ---- S.  Column n of n-tile t (block t / 2) is key 4 (n / 2) + 2 (t & 1) + (n & 1): the
-  // accumulators of lane c then hold keys 4 c .. 4 c + 3, as ldmatrix gives V
-  float s[4][4];
+  // ---- S^T.  Row i of a tile is key 4 (i % 8 / 2) + 2 (i / 8) + i % 2 of the block: once
+  // transposed, lane c holds keys 4 c .. 4 c + 3, as ldmatrix gives V
+  const int key0 = 4 * (r >> 1) + (r & 1);
+  float s[kPair][NT][4];  // keys key0 (first two) and key0 + 2; rows 2 c, 2 c + 1 of tile t
 #pragma unroll
-  for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+  for (int b = 0; b < kPair; ++b)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[b][t][0] = s[b][t][1] = s[b][t][2] = s[b][t][3] = 0.f;
 #pragma unroll
   for (int L = 0; L < D / 64; ++L) {
-    uint4 kv[4];
+    const int chunk = D == 128 ? 2 * c + L : c;
+    uint4 kv[kPair][2];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      kv[t] = lds128(stage + (t >> 1) * 2 * kSlab +
-                     slab_off<D>(4 * (r >> 1) + 2 * (t & 1) + (r & 1), D == 128 ? 2 * c + L : c));
+    for (int b = 0; b < kPair; ++b) {
+      kv[b][0] = lds128(stage + b * 2 * kSlab + slab_off<D>(key0, chunk));
+      kv[b][1] = lds128(stage + b * 2 * kSlab + slab_off<D>(key0 + 2, chunk));
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t w = i == 0 ? kv[t].x : i == 1 ? kv[t].y : i == 2 ? kv[t].z : kv[t].w;
-        const uint32_t(&q)[4] = qa[4 * L + i];
-        mma_16816_f16(s[t], q[0], q[1], q[2], q[3], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+      for (int b = 0; b < kPair; ++b) {
+        const uint4 &x = kv[b][0], &y = kv[b][1];
+        const uint32_t w0 = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+        const uint32_t w1 = i == 0 ? y.x : i == 1 ? y.y : i == 2 ? y.z : y.w;
+        const uint32_t a0 = e4m3x2_to_f16x2(w0), a2 = e4m3x2_to_f16x2(w0 >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          mma_16816_f16(s[b][t], a0, a1, a2, a3, rows.q[4 * L + i][t][0], rows.q[4 * L + i][t][1]);
       }
   }
   if (max(p0[0], p0[1]) + kBlockSize - 1 > q_pos0) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int b = 0; b < kPair; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (p0[t >> 1] + 4 * c + 2 * (t & 1) + (j & 1) > (j < 2 ? lim_lo : lim_hi))
-          s[t][j] = -INFINITY;
-  }
-  // ---- the running maximum (f > 0, so the largest product is the largest x; kept off
-  // zero, where a masked -inf would become NaN)
-  constexpr float kTiny = 1.17549435e-38f;
-  const float f_lo[2] = {fmaxf(st.qs_lo * sc.x, kTiny), fmaxf(st.qs_lo * sc.z, kTiny)};
-  const float f_hi[2] = {fmaxf(st.qs_hi * sc.x, kTiny), fmaxf(st.qs_hi * sc.z, kTiny)};
-  auto top = [&](int b, int j) {
-    return max3(fmaxf(s[2 * b][j], s[2 * b][j + 1]), s[2 * b + 1][j], s[2 * b + 1][j + 1]);
-  };
-  float mx_lo = fmaxf(top(0, 0) * f_lo[0], top(1, 0) * f_lo[1]);
-  float mx_hi = fmaxf(top(0, 2) * f_hi[0], top(1, 2) * f_hi[1]);
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-  for (int d = 1; d <= 2; d <<= 1) {
-    mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, d));
-    mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, d));
+        for (int j = 0; j < 4; ++j)
+          if (p0[b] + key0 + (j & 2) > rows.lim[t][j & 1]) s[b][t][j] = -INFINITY;
   }
-  const float mn_lo = fmaxf(st.m_lo, mx_lo), mn_hi = fmaxf(st.m_hi, mx_hi);
-  const float base_lo = mn_lo == -INFINITY ? 0.f : mn_lo;  // a row that has seen no key
-  const float base_hi = mn_hi == -INFINITY ? 0.f : mn_hi;
-  float a_lo = fast_exp2(st.m_lo - base_lo), a_hi = fast_exp2(st.m_hi - base_hi);
-  st.m_lo = mn_lo;
-  st.m_hi = mn_hi;
-  st.l_lo *= a_lo;
-  st.l_hi *= a_hi;
   const float vmax = fmaxf(sc.y, sc.w);
-  if (vmax > st.vref) {  // the same in every lane
-    const float down = st.vref / vmax;
-    a_lo *= down;
-    a_hi *= down;
-    st.vref = vmax;
-    st.inv_vref = 1.f / vmax;
+  float down = 1.f;
+  if (vmax > rows.vref) {  // the same in every lane
+    down = rows.vref / vmax;
+    rows.vref = vmax;
+    rows.inv_vref = 1.f / vmax;
   }
-  // ---- weights: their sum, and as fp16 with their V scale for the product
-  uint32_t pa[2][4];
-  uint64_t sum_lo = 0, sum_hi = 0;
-  const uint64_t nb_lo = f2_pack(-base_lo, -base_lo), nb_hi = f2_pack(-base_hi, -base_hi);
+  // ---- weights: the running maximum, their sum, and as fp16 with their V scale
+  uint32_t pb[kPair][NT][2];
+  float alpha[NT][2];
+  bool moved = down != 1.f;
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const float g = (b ? sc.w : sc.y) * st.inv_vref * kUScale;
-    const uint64_t fl = f2_pack(f_lo[b], f_lo[b]), fh = f2_pack(f_hi[b], f_hi[b]);
+  for (int t = 0; t < NT; ++t) {
+    // f > 0, so the largest product is the largest x; kept off zero, where a masked
+    // -inf would become NaN
+    constexpr float kTiny = 1.17549435e-38f;
+    float f[kPair][2], nbase[2];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float *x = s[2 * b + nt];
-      float e0, e1, e2, e3;
-      f2_unpack(f2_fma(f2_pack(x[0], x[1]), fl, nb_lo), e0, e1);
-      f2_unpack(f2_fma(f2_pack(x[2], x[3]), fh, nb_hi), e2, e3);
-      e0 = fast_exp2(e0);
-      e1 = fast_exp2(e1);
-      e2 = fast_exp2(e2);
-      e3 = fast_exp2(e3);
-      sum_lo = f2_add(sum_lo, f2_pack(e0, e1));
-      sum_hi = f2_add(sum_hi, f2_pack(e2, e3));
-      pa[b][2 * nt] = pack_f16x2(e0 * g, e1 * g);
-      pa[b][2 * nt + 1] = pack_f16x2(e2 * g, e3 * g);
+    for (int j = 0; j < 2; ++j) {
+      f[0][j] = fmaxf(rows.qs[t][j] * sc.x, kTiny);
+      f[1][j] = fmaxf(rows.qs[t][j] * sc.z, kTiny);
+      float mx = fmaxf(fmaxf(s[0][t][j], s[0][t][2 + j]) * f[0][j],
+                       fmaxf(s[1][t][j], s[1][t][2 + j]) * f[1][j]);
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mx = fmaxf(rows.m[t][j], mx);
+      const float base = mx == -INFINITY ? 0.f : mx;  // a row that has seen no key
+      const float a = fast_exp2(rows.m[t][j] - base);
+      rows.m[t][j] = mx;
+      rows.l[t][j] *= a;
+      alpha[t][j] = a * down;
+      moved |= a != 1.f;
+      nbase[j] = -base;
     }
-  }
-  {
+    uint64_t sum = 0;
+    const uint64_t nb = f2_pack(nbase[0], nbase[1]);
+#pragma unroll
+    for (int b = 0; b < kPair; ++b) {
+      const float g = (b ? sc.w : sc.y) * rows.inv_vref * kUScale;
+      const uint64_t fb = f2_pack(f[b][0], f[b][1]);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(s[b][t][2 * hh], s[b][t][2 * hh + 1]), fb, nb), e0, e1);
+        e0 = fast_exp2(e0);
+        e1 = fast_exp2(e1);
+        sum = f2_add(sum, f2_pack(e0, e1));
+        pb[b][t][hh] = transpose8(pack_f16x2(e0 * g, e1 * g));
+      }
+    }
     float x, y;
-    f2_unpack(sum_lo, x, y);
-    st.l_lo += x + y;
-    f2_unpack(sum_hi, x, y);
-    st.l_hi += x + y;
+    f2_unpack(sum, x, y);
+    rows.l[t][0] += x;
+    rows.l[t][1] += y;
   }
-  if (__any_sync(0xffffffffu, a_lo != 1.f || a_hi != 1.f)) {
+  if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-    for (int nt = 0; nt < D / 8; ++nt) {
-      o[nt][0] *= a_lo;
-      o[nt][1] *= a_lo;
-      o[nt][2] *= a_hi;
-      o[nt][3] *= a_hi;
-    }
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        rows.o[i][t][0] *= alpha[t][0];
+        rows.o[i][t][1] *= alpha[t][1];
+        rows.o[i][t][2] *= alpha[t][0];
+        rows.o[i][t][3] *= alpha[t][1];
+      }
   }
-  // ---- O += u V8; rows at or past the context end (stale bytes, NaN codes among
-  // them) are read as zeros: 0 x NaN would reach O
+  // ---- O^T += V8^T u; rows of V at or past the context end (stale bytes, NaN codes
+  // among them) are read as zeros: 0 x NaN would reach O
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < kPair; ++b) {
     const uint32_t sv = stage + b * 2 * kSlab + kSlab;
     const int left = ctx - p0[b] - 4 * c;  // keys of this lane's four that are the sequence's
     const bool edge = p0[b] + kBlockSize > ctx;
@@ -257,50 +300,67 @@ __device__ __forceinline__ void attend_pair(uint32_t stage, const float4 sc, con
     for (int m = 0; m < D / 32; ++m) {
       uint32_t v[4];
       ldmatrix_t8x2(v, sv + slab_off<D>(lane & 15, 2 * m + (lane >> 4)));
+      if (edge) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (edge) v[i] &= keep;
-        mma_16816_f16(o[4 * m + i], pa[b][0], pa[b][1], pa[b][2], pa[b][3], e4m3x2_to_f16x2(v[i]),
-                      e4m3x2_to_f16x2(v[i] >> 16));
+        for (int i = 0; i < 4; ++i) v[i] &= keep;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t a0 = e4m3x2_to_f16x2(v[2 * k]), a2 = e4m3x2_to_f16x2(v[2 * k] >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(v[2 * k + 1]), a3 = e4m3x2_to_f16x2(v[2 * k + 1] >> 16);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          mma_16816_f16(rows.o[2 * m + k][t], a0, a1, a2, a3, pb[b][t][0], pb[b][t][1]);
       }
     }
   }
 }
 
-// Lane (r, c) holds head_dims 8 t + 2 c and + 1 of rows r and r + 8.  A whole segment
-// writes the normalised bf16 output; a split piece its fp32 partial (O, m, l).
-template <int D>
-__device__ __forceinline__ void write_piece8(const DecodeParams &p, int part, int64_t row0, int h,
-                                             const float (&o)[D / 8][4], const RowState &st, int R,
-                                             int r, int c) {
+// A whole segment writes the normalised bf16 output (8 x 8 tiles of O^T transposed, so
+// that a lane stores two head_dims of a row); a split piece its fp32 partial (O, m, l).
+template <int D, int NT>
+__device__ __forceinline__ void write_rows(const DecodeParams &p, int part, int64_t row0, int h,
+                                           const Rows<D, NT> &rows, int R, int r, int c) {
   const int G = p.group;
-  float l_lo = st.l_lo, l_hi = st.l_hi;
+  const float unit = rows.vref * (1.f / kUScale);
 #pragma unroll
-  for (int d = 1; d <= 2; d <<= 1) {
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, d);
-    l_hi += __shfl_xor_sync(0xffffffffu, l_hi, d);
-  }
-  const float unit = st.vref * (1.f / kUScale);
+  for (int t = 0; t < NT; ++t) {
+    float l[2], f[2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = r + 8 * half;
-    if (row >= R) continue;
-    const float l = half ? l_hi : l_lo;
+    for (int j = 0; j < 2; ++j) {
+      l[j] = rows.l[t][j];
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+      f[j] = part >= 0 ? unit : l[j] > 0.f ? unit / l[j] : 0.f;
+    }
     if (part < 0) {
-      const float f = l > 0.f ? unit / l : 0.f;
-      __nv_bfloat16 *dst = p.out + ((row0 + row / G) * p.num_q_heads + h * G + row % G) * D + 2 * c;
+      const int row = 8 * t + r;
+      __nv_bfloat16 *dst =
+          p.out + ((row0 + row / G) * p.num_q_heads + h * G + row % G) * D + 2 * c;
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
-        *reinterpret_cast<uint32_t *>(dst + 8 * t) =
-            pack_bf16x2(o[t][2 * half] * f, o[t][2 * half + 1] * f);
+      for (int i = 0; i < D / 16; ++i) {
+        const float *o = rows.o[i][t];
+        const uint32_t x = transpose8(pack_bf16x2(o[0] * f[0], o[1] * f[1]));
+        const uint32_t y = transpose8(pack_bf16x2(o[2] * f[0], o[3] * f[1]));
+        if (row < R) {
+          *reinterpret_cast<uint32_t *>(dst + 16 * i) = x;
+          *reinterpret_cast<uint32_t *>(dst + 16 * i + 8) = y;
+        }
+      }
     } else {
-      float *dst = p.part_o + ((int64_t)part * kRowsPerTile + row) * D + 2 * c;
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
-        *reinterpret_cast<float2 *>(dst + 8 * t) =
-            make_float2(o[t][2 * half] * unit, o[t][2 * half + 1] * unit);
-      if (c == 0)
-        p.part_ml[(int64_t)part * kRowsPerTile + row] = make_float2(half ? st.m_hi : st.m_lo, l);
+      for (int j = 0; j < 2; ++j) {
+        const int row = 8 * t + 2 * c + j;
+        if (row >= R) continue;
+        float *dst = p.part_o + ((int64_t)part * kRowsPerTile + row) * D + r;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          dst[16 * i] = rows.o[i][t][j] * f[j];
+          dst[16 * i + 8] = rows.o[i][t][2 + j] * f[j];
+        }
+        if (r == 0)
+          p.part_ml[(int64_t)part * kRowsPerTile + row] = make_float2(rows.m[t][j], l[j]);
+      }
     }
   }
 }
@@ -352,11 +412,11 @@ struct Ring {
 
 // Shared-block CTA: as in pkv_decode.cu, two pairs of warps, each pair streaming a chain
 // of items once for two row groups through a ring pooled from its two warps' rings.
-template <int D, int NSTAGE>
+template <int D, int MAXT>
 __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const DecodeParams &p,
                                             uint8_t *smem, int warp, int lane) {
-  using C = Decode8Cfg<D, NSTAGE>;
-  constexpr int kS = kSharedRowGroups * NSTAGE;  // stages of a pair's pooled ring
+  using C = Decode8Cfg<D, MAXT>;
+  constexpr int kS = kSharedRowGroups * C::kStages;  // stages of a pair's pooled ring
   const int r = lane >> 2, c = lane & 3;
   const int G = p.group, hkv = p.num_kv_heads;
   const int pair = warp / kSharedRowGroups, lw = warp % kSharedRowGroups;
@@ -418,12 +478,10 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
 
   // ---- the consumers' current item
   int c_idx = first, c_h = 0, c_kb0 = 0, c_kb1 = 0, c_next = -1;
-  uint32_t qa[D / 16][4];
-  RowState st;
   SharedRowGroup rg;
   int cu0 = 0, qs = 0, ctx = 0;
   bool has_rg = false, mine = false;
-  auto c_setup = [&]() {  // both warps: item c_idx's row group, q and lengths
+  auto c_setup = [&]() {  // both warps: item c_idx's row group and lengths
     const SharedItem &it = p.shared[c_idx];
     const bool ok = item_ok(it);
     const int n_rg = it.n_rg;
@@ -438,8 +496,7 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
     has_rg = ok && lw < n_rg;
     if (has_rg) rg = it.rg[lw];
     mine = has_rg && rg.seq >= 0 && rg.seq < p.num_seqs && rg.qi0 >= 0 && rg.n_q >= 1 &&
-           rg.n_q * G <= kRowsPerTile && rg.q_row0 >= 0 && rg.q_row0 + rg.n_q <= p.total_q;
-    load_q8<D>(p, mine ? rg.q_row0 : 0, mine ? rg.n_q * G : 0, c_h, r, c, qa, st);
+           rg.n_q * G <= 8 * MAXT && rg.q_row0 >= 0 && rg.q_row0 + rg.n_q <= p.total_q;
     cu0 = qs = ctx = 0;
     if (mine) {
       cu0 = __ldg(p.cu_q_lens + rg.seq);
@@ -468,29 +525,27 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
 
   bool good = true;
   int done = 0;  // stages consumed (both warps walk the same chain)
-  while (c_idx >= 0 && good) {
+  // one item: this warp's row group (of at most 8 NT rows) over the item's stages
+  auto run_item = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
     const int R = mine ? rg.n_q * G : 0;
     const int q_pos0 = ctx - qs + rg.qi0;
-    const int lim_lo = r < R ? q_pos0 + r / G : -1;
-    const int lim_hi = r + 8 < R ? q_pos0 + (r + 8) / G : -1;
-    float o[D / 8][4];
-#pragma unroll
-    for (int nt = 0; nt < D / 8; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    st.reset();
+    Rows<D, NT> rows;
+    load_rows<D, NT>(p, mine ? rg.q_row0 : 0, R, c_h, q_pos0, r, c, rows);
+    rows.reset();
     for (int kb = c_kb0; kb < c_kb1; kb += kPair) {
       const int s = done % kS;
       const uint32_t par = (uint32_t)((done / kS) & 1);
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), par))) {
         if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
         good = false;
-        break;
+        return;
       }
       ++done;
       if (mine) {
         int p0[kPair];
         const float4 sc = ring.scale_of(s, min(kPair, c_kb1 - kb), kb, p0);
-        attend_pair<D>(ring.base + s * C::kStageBytes, sc, p0, qa, q_pos0, lim_lo, lim_hi, ctx,
-                       lane, st, o);
+        attend_pair<D, NT>(ring.base + s * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
@@ -498,16 +553,26 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), par))) {
           if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
           good = false;
-          break;
+          return;
         }
         issue();
       }
     }
-    if (!good) break;
     if (mine)
-      write_piece8<D>(p, rg.part, cu0 + rg.qi0, c_h, o, st, R, r, c);
+      write_rows<D, NT>(p, rg.part, cu0 + rg.qi0, c_h, rows, R, r, c);
     else if (has_rg)  // this warp's row group, which could not be attended
       poison_piece(p, rg.part, lane);
+  };
+  while (c_idx >= 0 && good) {
+    if constexpr (MAXT == 2) {
+      if (mine && rg.n_q * G > kDecode8SmallRows)
+        run_item(std::integral_constant<int, 2>());
+      else
+        run_item(std::integral_constant<int, 1>());
+    } else {
+      run_item(std::integral_constant<int, 1>());
+    }
+    if (!good) break;
     c_idx = c_next;
     if (c_idx >= 0) c_setup();
   }
@@ -517,10 +582,11 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
       mbar_wait(smem_u32(&full[j % kS]), (uint32_t)((j / kS) & 1));
 }
 
-template <int D, int NSTAGE>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int MAXT>
+__global__ void __launch_bounds__(kThreads, (Decode8Cfg<D, MAXT>::kCtas))
     decode8_kernel(const __grid_constant__ CUtensorMap pool_map, const DecodeParams p) {
-  using C = Decode8Cfg<D, NSTAGE>;
+  using C = Decode8Cfg<D, MAXT>;
+  constexpr int NSTAGE = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
@@ -531,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_trigger();
   if (lane == 0) prefetch_tmap(&pool_map);
   if (blockIdx.x >= p.num_indep_ctas) {  // CTA-uniform: a shared-prefix CTA
-    shared_cta8<D, NSTAGE>(pool_map, p, smem, warp, lane);
+    shared_cta8<D, MAXT>(pool_map, p, smem, warp, lane);
     if (p.after_prefill) pdl_wait();
     return;
   }
@@ -654,11 +720,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool valid = pc.seq >= 0 && pc.seq < p.num_seqs && pc.h >= 0 && pc.h < hkv &&
                  pc.kb_begin >= 0 && pc.kb_begin <= pc.kb_end &&
                  pc.kb_end <= p.max_blocks_per_seq && pc.n_q >= 1 &&
-                 pc.n_q * G <= kRowsPerTile && pc.q_row0 >= 0 &&
+                 pc.n_q * G <= 8 * MAXT && pc.q_row0 >= 0 &&
                  pc.q_row0 + pc.n_q <= p.total_q;
-    uint32_t qa[D / 16][4];
-    RowState st;
-    load_q8<D>(p, valid ? pc.q_row0 : 0, valid ? pc.n_q * G : 0, valid ? pc.h : 0, r, c, qa, st);
     int cu0 = 0, qs = 0, ctx = 0;
     if (valid) {
       cu0 = pi == pb ? f_cu0 : __ldg(p.cu_q_lens + pc.seq);
@@ -668,48 +731,53 @@ __global__ void __launch_bounds__(kThreads, 2)
               pc.kb_end <= (ctx + p.lookahead * qs - qs + pc.qi0 + pc.n_q - 1) / kBlockSize + 1;
     }
     if (!valid && lane == 0) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
-    const int R = valid ? pc.n_q * G : 0;
-    const int q_pos0 = ctx - qs + pc.qi0;  // causal position of the group's first token
-    const int lim_lo = r < R ? q_pos0 + r / G : -1;            // last visible key of row r
-    const int lim_hi = r + 8 < R ? q_pos0 + (r + 8) / G : -1;  // ... of row r + 8
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int nt = 0; nt < D / 8; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    st.reset();
-    bool head_bad = false;  // the plan's block ids for this piece disagree with the table
-
-    for (int kb = pc.kb_begin; kb < pc.kb_end; kb += kPair) {
-      if (!__all_sync(0xffffffffu, mbar_wait(ring.bars + stage * 8, phase))) {
-        if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
-        abandoned = true;
-        break;
+    // the piece's row group (of at most 8 NT rows) over its stages
+    auto run_piece = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const int R = valid ? pc.n_q * G : 0;
+      const int q_pos0 = ctx - qs + pc.qi0;  // causal position of the group's first token
+      Rows<D, NT> rows;
+      load_rows<D, NT>(p, valid ? pc.q_row0 : 0, R, valid ? pc.h : 0, q_pos0, r, c, rows);
+      rows.reset();
+      bool head_bad = false;  // the plan's block ids for this piece disagree with the table
+      for (int kb = pc.kb_begin; kb < pc.kb_end; kb += kPair) {
+        if (!__all_sync(0xffffffffu, mbar_wait(ring.bars + stage * 8, phase))) {
+          if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
+          abandoned = true;
+          return;
+        }
+        if (consumed++ == 0) {  // the check entries have landed by now: compare the inline ids
+          const bool bad = fb >= 0 && fb != head_chk;
+          if (bad) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
+          // blocks loaded from ids the table does not hold: nothing of this
+          // piece is used or written
+          head_bad = __any_sync(0xffffffffu, bad);
+        }
+        if (valid && !head_bad) {
+          int p0[kPair];
+          const float4 sc = ring.scale_of(stage, min(kPair, pc.kb_end - kb), kb, p0);
+          attend_pair<D, NT>(ring.base + stage * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
+        }
+        __syncwarp();
+        issue_next(stage);  // refill this stage with the stream's next blocks
+        if (++stage == NSTAGE) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (consumed++ == 0) {  // the check entries have landed by now: compare the inline ids
-        const bool bad = fb >= 0 && fb != head_chk;
-        if (bad) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
-        // blocks loaded from ids the table does not hold: nothing of this
-        // piece is used or written
-        head_bad = __any_sync(0xffffffffu, bad);
-      }
-      if (valid && !head_bad) {
-        int p0[kPair];
-        const float4 sc = ring.scale_of(stage, min(kPair, pc.kb_end - kb), kb, p0);
-        attend_pair<D>(ring.base + stage * C::kStageBytes, sc, p0, qa, q_pos0, lim_lo, lim_hi,
-                       ctx, lane, st, o);
-      }
-      __syncwarp();
-      issue_next(stage);  // refill this stage with the stream's next blocks
-      if (++stage == NSTAGE) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      if (valid && !head_bad)
+        write_rows<D, NT>(p, pc.part, cu0 + pc.qi0, pc.h, rows, R, r, c);
+      else
+        poison_piece(p, pc.part, lane);
+    };
+    if constexpr (MAXT == 2) {
+      if (valid && pc.n_q * G > kDecode8SmallRows)
+        run_piece(std::integral_constant<int, 2>());
+      else
+        run_piece(std::integral_constant<int, 1>());
+    } else {
+      run_piece(std::integral_constant<int, 1>());
     }
-    if (abandoned) break;
-    if (valid && !head_bad)
-      write_piece8<D>(p, pc.part, cu0 + pc.qi0, pc.h, o, st, R, r, c);
-    else
-      poison_piece(p, pc.part, lane);
   }
   if (abandoned) {
     // drain this warp's copies still in flight (bounded) before exiting
@@ -737,15 +805,15 @@ int make_pool_map8(CUtensorMap *map, const void *pool, const pkv_pool_desc &desc
   return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
-template <int D, int NSTAGE>
+template <int D, int MAXT>
 int launch_t(const AttnArgs &a, const CUtensorMap &map) {
-  using C = Decode8Cfg<D, NSTAGE>;
-  static_assert(C::kSmemBytes * 2 + 2048 <= 228 * 1024, "two CTAs an SM");
-  cudaError_t e = prepare_kernel<decode8_kernel<D, NSTAGE>>(C::kSmemBytes);
+  using C = Decode8Cfg<D, MAXT>;
+  static_assert((C::kSmemBytes + 1024) * C::kCtas <= 228 * 1024, "the CTAs share an SM");
+  cudaError_t e = prepare_kernel<decode8_kernel<D, MAXT>>(C::kSmemBytes);
   if (e != cudaSuccess) return (int)e;
   const unsigned grid = (unsigned)((a.num_decode_warps + kWarps - 1) / kWarps + a.num_shared_ctas);
   profile_begin(PKV_KERNEL_DECODE, a.stream);
-  e = launch_kernel(decode8_kernel<D, NSTAGE>, dim3(grid), dim3(kThreads), C::kSmemBytes, a.stream,
+  e = launch_kernel(decode8_kernel<D, MAXT>, dim3(grid), dim3(kThreads), C::kSmemBytes, a.stream,
                     !profiling_active(), map, make_params(a));
   profile_end(PKV_KERNEL_DECODE, a.stream);
   return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
@@ -757,8 +825,11 @@ int launch_decode8(const AttnArgs &a) {
   CUtensorMap map;
   const int e = make_pool_map8(&map, a.kv_pool, a.desc);
   if (e) return e;
-  // 24 KB in flight a warp, as the bf16 kernel has; D = 64 the same in more stages
-  return a.desc.head_dim == 128 ? launch_t<128, 3>(a, map) : launch_t<64, 6>(a, map);
+  // no row group of more than 8 rows: the kernel with one column tile and 16 warps an
+  // SM (256 decodes of 4 heads: 193 us with 8 warps of either, 180 us with 16)
+  if (a.max_rows <= kDecode8SmallRows)
+    return a.desc.head_dim == 128 ? launch_t<128, 1>(a, map) : launch_t<64, 1>(a, map);
+  return a.desc.head_dim == 128 ? launch_t<128, 2>(a, map) : launch_t<64, 2>(a, map);
 }
 
 }  // namespace pkv

@@ -13,6 +13,7 @@ constexpr int kBlockSize = 16;
 constexpr int kRowsPerTile = 16;    // query rows (token x head-in-group) per decode row group
 constexpr int kPrefillRows = 128;   // query tokens per tensor-core tile
 constexpr int kDecodeWarpsPerCta = 4;
+constexpr int kDecode8SmallRows = 8;  // 8-bit pool: row groups that take one column tile
 
 // Plan buffer layout (all offsets are functions of the counts):
 //   [PlanHeader 64 B]
@@ -261,6 +262,7 @@ struct AttnArgs {
   const float *kv_scales = nullptr;
   const int32_t *stage_begin = nullptr;
   int32_t staged_blocks = 0;
+  int32_t max_rows = 0;  // no row group of the split-KV work has more rows
   void *staged = nullptr;
 };
 

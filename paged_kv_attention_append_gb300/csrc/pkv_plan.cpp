@@ -50,6 +50,9 @@ namespace pkv {
 namespace {
 
 constexpr int kDecodeWarpsPerSm = 8;
+// The split-KV kernel of an 8-bit pool runs 16 warps an SM when no row group has
+// more than 8 rows (pkv_decode8.cu), else 8.
+constexpr int kDecode8WarpsPerSm = 16;
 constexpr int kMinBlocksPerWarp = 4;
 // Query tokens from which a sequence's rows go to the tensor-core kernel, when
 // the caller leaves the choice to the planner (prefill_min_q == 0).
@@ -130,11 +133,12 @@ using namespace pkv;
 // sequences are not supported there.
 // block_tables (host, may be NULL): each warp's first blocks are then written
 // into its head.
+// f8: work cut for the kernels of an 8-bit pool.
 static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_lens,
                             int32_t num_seqs, int32_t num_q_heads, const pkv_pool_desc *desc,
                             int32_t num_sms, int32_t lookahead, const int32_t *block_tables,
-                            int32_t max_blocks_per_seq, int32_t prefill_min_q, void *plan,
-                            int64_t plan_capacity, pkv_plan_info *info) {
+                            int32_t max_blocks_per_seq, int32_t prefill_min_q, bool f8,
+                            void *plan, int64_t plan_capacity, pkv_plan_info *info) {
   if (!info) return PKV_ERR_NULL;
   if (lookahead < 0) return PKV_ERR_RANGE;
   pkv_status st = check_desc(desc, num_q_heads);
@@ -216,6 +220,11 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       dunits.push_back({s, qi0, n_q, nb});
     }
   }
+
+  int32_t max_rows = 0;  // rows of the largest row group
+  for (const DUnit &du : dunits) max_rows = std::max(max_rows, du.n_q * group);
+  const int32_t warps_per_sm =
+      f8 && max_rows <= kDecode8SmallRows ? kDecode8WarpsPerSm : kDecodeWarpsPerSm;
 
   // ---- shared prefixes (needs the host block tables): decode-class sequences
   // whose tables start with the same physical blocks, over blocks every query
@@ -309,7 +318,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     }
     // windows only while one chunk each leaves half the warp slots to the rest
     // (else the shared items alone would take more than a wave)
-    if (kSharedRowGroups * window_items * 2 > (int64_t)num_sms * kDecodeWarpsPerSm)
+    if (kSharedRowGroups * window_items * 2 > (int64_t)num_sms * warps_per_sm)
       streams.resize(n_group_streams);
     for (size_t i = n_group_streams; i < streams.size(); ++i)
       for (int32_t u : streams[i].units) unit_kb0[u] = streams[i].len;
@@ -354,7 +363,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   // as the slots left over for the independent segments (same-box steps with
   // 4- and 8-token windows, the pair's time per block taken as 3/4, 9/10, 1,
   // 11/10, 5/4 and 3/2 of a warp's: 1 was best).
-  const int64_t slots = (int64_t)dec_sms * kDecodeWarpsPerSm;
+  const int64_t slots = (int64_t)dec_sms * warps_per_sm;
   std::vector<SharedItem> &sitems = S.sitems;
   sitems.clear();
   int32_t n_pairs = 0;  // heads: sitems[0 .. n_pairs)
@@ -576,7 +585,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   // the same warps taking 4 times a late warp's share, 54.0 / 49.1 at 8 times).
   if (pairs.empty() && !casc_items.empty() && (int64_t)casc_items.size() < dec_sms)
     nw64 = std::min<int64_t>(nw64, std::max<int64_t>(1, (dec_sms - (int64_t)casc_items.size()) *
-                                                            kDecodeWarpsPerSm));
+                                                            warps_per_sm));
   // Small steps: when every segment fits a warp slot and the longest is within a
   // few blocks of the equal share, one warp per whole segment runs about as long
   // as the equal-cost cut and needs no partials or merge launch.
@@ -1010,11 +1019,12 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
 static pkv_status plan_guarded(const int32_t *cu_q_lens, const int32_t *context_lens,
                                int32_t num_seqs, int32_t num_q_heads, const pkv_pool_desc *desc,
                                int32_t num_sms, int32_t lookahead, const int32_t *block_tables,
-                               int32_t max_blocks_per_seq, int32_t prefill_min_q, void *plan,
-                               int64_t plan_capacity, pkv_plan_info *info) {
+                               int32_t max_blocks_per_seq, int32_t prefill_min_q, bool f8,
+                               void *plan, int64_t plan_capacity, pkv_plan_info *info) {
   try {
     return plan_impl(cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, lookahead,
-                     block_tables, max_blocks_per_seq, prefill_min_q, plan, plan_capacity, info);
+                     block_tables, max_blocks_per_seq, prefill_min_q, f8, plan, plan_capacity,
+                     info);
   } catch (...) {
     return PKV_ERR_HOST_MEMORY;
   }
@@ -1029,13 +1039,29 @@ extern "C" pkv_status pkv_plan_step_ex(const int32_t *cu_q_lens, const int32_t *
   if (steps < 1) return PKV_ERR_RANGE;
   if (block_tables && max_blocks_per_seq < 0) return PKV_ERR_SHAPE;
   return plan_guarded(cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, steps - 1,
-                      block_tables, max_blocks_per_seq, prefill_min_q, plan, plan_capacity, info);
+                      block_tables, max_blocks_per_seq, prefill_min_q, false, plan, plan_capacity,
+                      info);
+}
+
+extern "C" pkv_status pkv_plan_step_fp8(const int32_t *cu_q_lens, const int32_t *context_lens,
+                                        int32_t num_seqs, int32_t num_q_heads,
+                                        const pkv_pool_desc *desc, int32_t num_sms, int32_t steps,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        int32_t prefill_min_q, void *plan, int64_t plan_capacity,
+                                        pkv_plan_info *info) {
+  if (steps < 1) return PKV_ERR_RANGE;
+  if (block_tables && max_blocks_per_seq < 0) return PKV_ERR_SHAPE;
+  return plan_guarded(cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, steps - 1,
+                      block_tables, max_blocks_per_seq, prefill_min_q, true, plan, plan_capacity,
+                      info);
 }
 
 extern "C" pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *info,
-                                         int32_t *stage_begin, int64_t *workspace_bytes) {
-  if (!plan || !info || !stage_begin || !workspace_bytes) return PKV_ERR_NULL;
-  if (info->num_seqs < 0 || info->num_prefill_tiles < 0 || info->num_kv_heads < 1)
+                                         int32_t *stage_begin, pkv_fp8_info *fp8) {
+  if (!plan || !info || !stage_begin || !fp8) return PKV_ERR_NULL;
+  if (info->num_seqs < 0 || info->num_prefill_tiles < 0 || info->num_kv_heads < 1 ||
+      info->num_decode_pieces < 0 || info->num_shared_items < 0 || info->num_q_heads < 1 ||
+      info->num_decode_warps < 0 || info->num_merge_groups < 0)
     return PKV_ERR_SHAPE;
   PlanHeader h;
   std::memcpy(&h, plan, sizeof h);
@@ -1049,10 +1075,10 @@ extern "C" pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *
   // the blocks of sequence s that tensor-core items read: 0 .. 8 max(kt1) - 1
   // (those past the context are zero-filled copies, at most 7)
   std::memset(stage_begin, 0, sizeof(int32_t) * ((size_t)info->num_seqs + 1));
-  const char *tiles = static_cast<const char *>(plan) + off.prefill;
+  const char *base = static_cast<const char *>(plan);
   for (int32_t i = 0; i < info->num_prefill_tiles; ++i) {
     PrefillTile t;
-    std::memcpy(&t, tiles + (int64_t)i * (int64_t)sizeof t, sizeof t);
+    std::memcpy(&t, base + off.prefill + (int64_t)i * (int64_t)sizeof t, sizeof t);
     if (t.seq < 0 || t.seq >= info->num_seqs) return PKV_ERR_SHAPE;
     stage_begin[t.seq + 1] = std::max(stage_begin[t.seq + 1], t.kt1 * kKeyTileBlocks);
   }
@@ -1067,7 +1093,23 @@ extern "C" pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *
     if (!staged_fits(total, d)) return PKV_ERR_UNSUPPORTED;
     stage_begin[s + 1] = (int32_t)total;
   }
-  *workspace_bytes = info->workspace_bytes + (total > 0 ? staged_bytes(total, d) : 0);
+  // rows of the largest row group of the split-KV work
+  const int32_t group = info->num_q_heads / info->num_kv_heads;
+  int32_t rows = 0;
+  for (int32_t i = 0; i < info->num_decode_pieces; ++i) {
+    Piece pc;
+    std::memcpy(&pc, base + off.pieces + (int64_t)i * (int64_t)sizeof pc, sizeof pc);
+    rows = std::max(rows, pc.n_q * group);
+  }
+  for (int32_t i = 0; i < info->num_shared_items; ++i) {
+    SharedItem it;
+    std::memcpy(&it, base + off.shared + (int64_t)i * (int64_t)sizeof it, sizeof it);
+    for (int32_t w = 0; w < std::min<int32_t>(it.n_rg, kSharedRowGroups); ++w)
+      rows = std::max(rows, it.rg[w].n_q * group);
+  }
+  fp8->staged_blocks = (int32_t)total;
+  fp8->max_rows = rows;
+  fp8->workspace_bytes = info->workspace_bytes + (total > 0 ? staged_bytes(total, d) : 0);
   return PKV_OK;
 }
 
@@ -1076,7 +1118,7 @@ extern "C" pkv_status pkv_plan_step(const int32_t *cu_q_lens, const int32_t *con
                                     const pkv_pool_desc *desc, int32_t num_sms, void *plan,
                                     int64_t plan_capacity, pkv_plan_info *info) {
   return plan_guarded(cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, 0, nullptr, 0,
-                      0, plan, plan_capacity, info);
+                      0, false, plan, plan_capacity, info);
 }
 
 extern "C" pkv_status pkv_plan_decode_chain(const int32_t *cu_q_lens, const int32_t *context_lens,

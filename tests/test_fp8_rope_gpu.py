@@ -147,7 +147,7 @@ def test_split_kv_rows(pkv, cuda_device, case, kind, sms):
     want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables,
                          values_of(codes, scales), meta.scale)
     got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales, num_sms=sms)
-    assert plan.staged_blocks == 0
+    assert plan.fp8.staged_blocks == 0
     check_attention(got, *want, max(ctx), tensor_cores=False, scales=scales)
 
 
@@ -202,7 +202,7 @@ def test_tensor_core_chunks(pkv, cuda_device, case, kind, sms):
     want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables,
                          values_of(codes, scales), meta.scale)
     got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales, num_sms=sms)
-    assert plan.staged_blocks >= sum(-(-c // 16) for n, c in zip(ql, ctx) if n >= 64)
+    assert plan.fp8.staged_blocks >= sum(-(-c // 16) for n, c in zip(ql, ctx) if n >= 64)
     check_attention(got, *want, max(ctx), tensor_cores=True, scales=scales, exact_scales=kind == "pow2")
 
 
@@ -221,7 +221,7 @@ def test_shared_prefix(pkv, cuda_device, group, n_seqs, q_len, blocks, d, sms):
     want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables,
                          values_of(codes, scales), meta.scale)
     got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales, num_sms=sms)
-    check_attention(got, *want, int(ctx.max()), tensor_cores=plan.staged_blocks > 0, scales=scales)
+    check_attention(got, *want, int(ctx.max()), tensor_cores=plan.fp8.staged_blocks > 0, scales=scales)
 
 
 def test_wide_windows_share_blocks(pkv, cuda_device):
@@ -269,7 +269,7 @@ def test_random_steps(pkv, cuda_device, seed):
                          values_of(codes, scales), meta.scale)
     got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales,
                               num_sms=int(rng.choice([1, 8, 152])))
-    check_attention(got, *want, 400, tensor_cores=plan.staged_blocks > 0, scales=scales)
+    check_attention(got, *want, 400, tensor_cores=plan.fp8.staged_blocks > 0, scales=scales)
 
 
 def test_long_context_and_far_blocks(pkv, cuda_device):
@@ -311,7 +311,7 @@ def test_bad_block_is_reported_and_skipped(pkv, cuda_device, pmq):
                               dev_tables=bad, pmq=pmq, expect=2)
     want = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens, meta.block_tables,
                          values_of(codes, scales), meta.scale)
-    check_attention(got[66:], *(x[66:] for x in want), 64, tensor_cores=plan.staged_blocks > 0, scales=scales)
+    check_attention(got[66:], *(x[66:] for x in want), 64, tensor_cores=plan.fp8.staged_blocks > 0, scales=scales)
 
 
 def test_side_stream_graphs_and_two_plans(pkv, cuda_device):

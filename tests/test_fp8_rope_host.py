@@ -80,7 +80,8 @@ def test_stage_covers_the_tensor_core_sequences(lib, seed, shared):
     meta = workloads.random_step(rng, max_ctx=700, num_seqs=40 if shared else None,
                                  shared_prefix_blocks=shared)
     info, host = plan_of(meta, block_tables=meta.block_tables)
-    begin, nbytes = pkv.stage_fp8(info, host)
+    begin, fp8 = pkv.stage_fp8(info, host)
+    nbytes = int(fp8.workspace_bytes)
     counts = np.diff(begin)
     assert begin[0] == 0 and (counts >= 0).all()
     for s in range(meta.num_seqs):
@@ -94,15 +95,36 @@ def test_stage_covers_the_tensor_core_sequences(lib, seed, shared):
     else:
         slab = 2 * meta.num_kv_heads * 16 * meta.head_dim * 2
         assert nbytes >= info.workspace_bytes + int(begin[-1]) * slab
-    # the plan itself is the one a bf16 pool gets
-    assert info.plan_bytes <= host.nbytes
+    group = meta.num_q_heads // meta.num_kv_heads
+    rows = [min(int(q), 16 // group) * group for q in meta.q_lens if 0 < q < 64]
+    assert fp8.max_rows <= 16 and fp8.staged_blocks == begin[-1]
+    if not shared and info.num_prefill_tiles == 0:
+        assert fp8.max_rows == max(rows, default=0)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_fp8_plan_covers_the_same_keys(lib, seed):
+    """pkv_plan_step_fp8 divides the work otherwise; what it covers is the same: every
+    (row group, KV head)'s blocks once, over pieces, shared items and gathered tiles."""
+    rng = np.random.default_rng(100 + seed)
+    meta = workloads.random_step(rng, max_ctx=900, max_q=3 if seed % 2 else None,
+                                 shared_prefix_blocks=[0, 12][seed // 3])
+    infos = []
+    for fp8 in (False, True):
+        info, host = plan_of(meta, block_tables=meta.block_tables, fp8=fp8, num_sms=4)
+        assert pkv.stage_fp8(info, host)[1].max_rows <= 16
+        infos.append(info)
+    a, b = infos
+    assert (a.kv_tokens, a.decode_blocks, a.max_blocks_needed) == (
+        b.kv_tokens, b.decode_blocks, b.max_blocks_needed)
+    assert b.num_decode_warps <= 4 * 16
 
 
 def test_stage_refusals(lib):
     meta = workloads.build_step("s", 1, [70, 1], [70, 40], 4, 2, 64)
     info, host = plan_of(meta)
     begin = np.zeros(3, dtype=np.int32)
-    out = ctypes.c_int64()
+    out = pkv.Fp8Info()
     ptr = lambda a: a.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
     f = lib.pkv_plan_stage_fp8
     assert f(None, ctypes.byref(info), ptr(begin), ctypes.byref(out)) == NULL
@@ -118,19 +140,20 @@ def test_stage_refusals(lib):
 
 
 def attention_call(lib, info, **kw):
-    a = dict(q=A, cu=A, ctx=A, bt=A, mb=64, pool=A, scales=A, scale=0.1, plan=A, stage=A, blocks=12,
-             out=A, ws=A, wsb=1 << 30)
+    a = dict(q=A, cu=A, ctx=A, bt=A, mb=64, pool=A, scales=A, scale=0.1, plan=A, stage=A, blocks=12, rows=16,
+             fp8=True, out=A, ws=A, wsb=1 << 30)
     a.update(kw)
     desc = pkv.PoolDesc(100, 16, info.num_kv_heads, info.head_dim)
+    fp8 = pkv.Fp8Info(a["blocks"], a["rows"], a["wsb"])
     return lib.pkv_paged_varlen_attention_fp8(
         a["q"], a["cu"], a["ctx"], a["bt"], a["mb"], a["pool"], a["scales"], ctypes.byref(desc),
-        a["scale"], ctypes.byref(info), a["plan"], a["stage"], a["blocks"], a["out"], a["ws"],
-        a["wsb"], None, None)
+        a["scale"], ctypes.byref(info), a["plan"], ctypes.byref(fp8) if a["fp8"] else None, a["stage"],
+        a["out"], a["ws"], a["wsb"], None, None)
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(scales=None), NULL), (dict(scales=A + 8), ALIGN), (dict(q=None), NULL),
-    (dict(pool=None), NULL), (dict(stage=None), NULL), (dict(ws=None), NULL), (dict(blocks=0), SHAPE),
+    (dict(scales=None), NULL), (dict(fp8=False), NULL), (dict(scales=A + 8), ALIGN),
+    (dict(q=None), NULL), (dict(pool=None), NULL), (dict(stage=None), NULL), (dict(ws=None), NULL), (dict(blocks=0), SHAPE),
     (dict(blocks=-3), SHAPE), (dict(blocks=1 << 30), SHAPE), (dict(wsb=4096), WORKSPACE),
     (dict(mb=2), RANGE), (dict(scale=float("inf")), RANGE), (dict(scale=float("nan")), RANGE),
     (dict(ws=A + 16), ALIGN), (dict(out=A + 2), ALIGN)])
@@ -146,6 +169,7 @@ def test_attention_refusals(lib, kw, want):
 def test_empty_step_is_ok(lib):
     meta = workloads.build_step("s", 1, [0], [9], 4, 2, 64)
     info, host = plan_of(meta)
-    begin, nbytes = pkv.stage_fp8(info, host)
+    begin, fp8 = pkv.stage_fp8(info, host)
+    nbytes = int(fp8.workspace_bytes)
     assert begin.tolist() == [0, 0] and nbytes == info.workspace_bytes
     assert attention_call(lib, info, q=None, pool=None, stage=None, blocks=0) == OK
