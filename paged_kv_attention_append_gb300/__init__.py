@@ -198,6 +198,30 @@ def _ptr(t):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _bound_fn(name):
+    """The library function `name` for calls whose arguments are marshalled already
+    (ctypes objects all): without argument types they go through unconverted, about
+    0.5 us less of a call with 16 of them."""
+    _load()
+    f = _lib[name]          # a function object of its own; argtypes stay unset
+    f.restype = ctypes.c_int32
+    return f
+
+
+def _call_on(device, f, args):
+    """f(*args) with `device` as the thread's current device: launches go to the
+    current device's context."""
+    prev = _current_device()
+    if prev == device:
+        return f(*args)
+    torch.cuda.set_device(device)
+    try:
+        return f(*args)
+    finally:
+        torch.cuda.set_device(prev)
 
 
 def _stream(stream, t):
@@ -368,19 +392,18 @@ class BoundRopeAppend:
                       desc, rope)
         vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         args = [vp(_ptr(q)), i64(qs), vp(k.data_ptr()), i64(ks), vp(v.data_ptr()), i64(vs),
-                None if rope is None else ctypes.byref(rope), vp(slot_mapping.data_ptr()), i32(n),
+                vp(None) if rope is None else ctypes.byref(rope), vp(slot_mapping.data_ptr()), i32(n),
                 i32(hq), vp(_ptr(q_out)), i64(qos), vp(kv_pool.data_ptr())]
         if kv_scales is not None:
             args.append(vp(kv_scales.data_ptr()))
         self._args = (*args, ctypes.byref(desc), vp(_ptr(dev_status)),
                       vp(_stream(stream, kv_pool)))
         self._name = "pkv_rope_kv_append" + ("" if kv_scales is None else "_fp8")
-        self._f = getattr(_load(), self._name)
+        self._f = _bound_fn(self._name)
         self._device = kv_pool.device.index
 
     def run(self) -> None:
-        with _on_device(self._device):
-            st = self._f(*self._args)
+        st = _call_on(self._device, self._f, self._args)
         if st:
             raise PkvError(st, self._name)
 
@@ -556,26 +579,6 @@ def stage_fp8(info: PlanInfo, host: np.ndarray):
     if st:
         raise PkvError(st, "pkv_plan_stage_fp8")
     return begin, fp8
-
-
-class _on_device:
-    """Makes `index` the thread's current device for the call (launches go to the
-    current device's context); does nothing when it already is."""
-
-    def __init__(self, index):
-        self._index = index
-        self._prev = None
-
-    def __enter__(self):
-        prev = torch.cuda.current_device()
-        if prev != self._index:
-            torch.cuda.set_device(self._index)
-            self._prev = prev
-
-    def __exit__(self, *a):
-        if self._prev is not None:
-            torch.cuda.set_device(self._prev)
-        return False
 
 
 class _nullcontext:
@@ -949,7 +952,7 @@ class BoundAttentionFp8:
                       ctypes.c_float(scale))
         self._out = vp(out.data_ptr())
         self._tail = (vp(_ptr(dev_status)), vp(_stream(stream, q)))
-        self._f = _load().pkv_paged_varlen_attention_fp8
+        self._f = _bound_fn("pkv_paged_varlen_attention_fp8")
         self._device = kv_pool.device.index
 
     def run(self) -> None:
@@ -962,10 +965,11 @@ class BoundAttentionFp8:
         if plan.fp8 is None:
             raise ValueError("the plan was not made for an 8-bit pool: plan_step(..., fp8=True)")
         ws = plan.workspace
-        with _on_device(self._device):
-            st = self._f(*self._head, ctypes.byref(info), plan.dev.data_ptr(),
-                         ctypes.byref(plan.fp8), _ptr(plan.stage), self._out, _ptr(ws),
-                         0 if ws is None else ws.numel(), *self._tail)
+        vp = ctypes.c_void_p
+        st = _call_on(self._device, self._f, (
+            *self._head, ctypes.byref(info), vp(plan.dev.data_ptr()), ctypes.byref(plan.fp8),
+            vp(_ptr(plan.stage)), self._out, vp(_ptr(ws)),
+            ctypes.c_int64(0 if ws is None else ws.numel()), *self._tail))
         if st:
             raise PkvError(st, "pkv_paged_varlen_attention_fp8")
 
