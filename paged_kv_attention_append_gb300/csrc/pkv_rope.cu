@@ -458,11 +458,13 @@ __device__ __forceinline__ void append_blocks(const RopeParams &p, int64_t unit,
   }
 }
 
-// No early release of the next kernel: the attention kernels read q before they
-// wait for this one, so q_out has to be complete and visible when they start (the
-// pool is read after that wait).
+// Launched early behind the preceding kernel, whose completion is waited for before
+// anything is read.  No early release of the next kernel: the attention kernels read
+// q before they wait for this one, so q_out has to be complete and visible when they
+// start (the pool is read after that wait).
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeParams p) {
+  pdl_wait();
   const int64_t unit = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
   token_rows<D, kInter, true>(p, unit, threadIdx.x & 31);
   __threadfence();
@@ -476,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopePara
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_fp8_kernel(const RopeParams p) {
   __shared__ AppendSmem sm;
+  pdl_wait();
   const int b = (int)blockIdx.x, at = b / p.every;
   if (b % p.every == 0 && at < p.append_ctas) {
     append_blocks<D, kInter>(p, at, sm);
@@ -544,14 +547,13 @@ int launch_t(const RopeAppendArgs &a) {
                             : prepare_kernel<rope_append_kernel<D, kInter>>(0);
   if (pe != cudaSuccess) return (int)pe;
   profile_begin(PKV_KERNEL_ROPE, a.stream);
-  if (f8)
-    rope_append_fp8_kernel<D, kInter><<<(unsigned)ctas, kThreads, 0, a.stream>>>(p);
-  else
-    rope_append_kernel<D, kInter><<<(unsigned)ctas, kThreads, 0, a.stream>>>(p);
+  cudaError_t e = launch_kernel(
+      f8 ? rope_append_fp8_kernel<D, kInter> : rope_append_kernel<D, kInter>,
+      dim3((unsigned)ctas), dim3(kThreads), 0, a.stream, !profiling_active(), p);
   profile_end(PKV_KERNEL_ROPE, a.stream);
-  const int e = (int)cudaGetLastError();
-  if (!e) count_launches(1);
-  return e;
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) count_launches(1);
+  return (int)e;
 }
 
 }  // namespace
