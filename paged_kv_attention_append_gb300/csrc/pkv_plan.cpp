@@ -94,6 +94,14 @@ constexpr int32_t kMinSharedBlocks = 8;
 // head from which a shared prefix goes to it as gathered sub-tiles.
 constexpr int32_t kKeyTileBlocks = 128 / kBlockSize;
 constexpr int64_t kGatherMinRows = 64;
+// 8-bit pool: a shared prefix is gathered when streaming it per row group instead
+// would take at least this many blocks of 128-wide heads an SM.  The streams run from L2
+// at half the bytes, and the gathered form pays its copies, a tensor-core launch and
+// partials (8 heads, 2 tokens x 4 heads a sequence, 152 SMs; gathered against streamed:
+// 16 sequences on 32 blocks 18 and 12 us, on 256 25.0 and 24.8; 32 on 128 21.9 and 25.8;
+// 64 on 32 19.2 and 19.8, on 256 33 and 66).  Below it nothing is shared: pairs of warps
+// on one stream were no faster (32 sequences on 128 blocks 27.1 us).
+constexpr int64_t kGather8MinBlocksPerSm = 131;
 
 // The planner's working arrays, kept per host thread so a plan allocates
 // nothing once a thread has planned a step of that size.
@@ -272,7 +280,15 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       int64_t rows = 0;
       for (int32_t m : mem) rows += (int64_t)(cu_q_lens[m + 1] - cu_q_lens[m]) * group;
       const int32_t len_tc = len / kKeyTileBlocks * kKeyTileBlocks;
-      const bool tc = lookahead == 0 && len_tc >= kKeyTileBlocks && rows >= kGatherMinRows;
+      bool tc = lookahead == 0 && len_tc >= kKeyTileBlocks && rows >= kGatherMinRows;
+      if (f8) {
+        int64_t streams = 0;  // row groups of the members
+        for (int32_t m : mem)
+          streams += (cu_q_lens[m + 1] - cu_q_lens[m] + nq_tile - 1) / nq_tile;
+        tc = tc && streams * len_tc * hkv * desc->head_dim >=
+                       kGather8MinBlocksPerSm * 128 * (int64_t)num_sms;
+        if (!tc) continue;
+      }
       if (tc) len = len_tc;
       groups.push_back({mem, len, tc});
       for (int32_t m : mem) shared_len[m] = len;
@@ -765,9 +781,12 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       total += item_cost(t);
       ntiles += (t.kt1 - t.kt0) * (t.n_q[1] > 0 ? 2 : 1);
     }
+    // 8-bit pool: at least a CTA a sub-tile (a 64-token prompt of 32 heads: 16.2 -> 8.5 us)
+    int64_t min_ctas = (int64_t)casc_items.size();
+    if (f8)
+      for (const auto &nt : pair_nt) min_ctas += (nt[0] > 0) + (nt[1] > 0);
     n_pf_ctas = (int32_t)std::max<int64_t>(
-        1, std::min<int64_t>(pf_sms, std::max<int64_t>(ntiles / kMinTilesPerCta,
-                                                        (int64_t)casc_items.size())));
+        1, std::min<int64_t>(pf_sms, std::max<int64_t>(ntiles / kMinTilesPerCta, min_ctas)));
     const int64_t target = (total + n_pf_ctas - 1) / n_pf_ctas;
     std::vector<size_t> order(pairs.size());
     for (size_t i = 0; i < order.size(); ++i) order[i] = i;

@@ -207,11 +207,12 @@ def test_tensor_core_chunks(pkv, cuda_device, case, kind, sms):
 
 
 @pytest.mark.parametrize("group,n_seqs,q_len,blocks", [(4, 20, 1, 17), (2, 6, 2, 33), (8, 9, 3, 8),
-                                                       (1, 3, 2, 20)])
+                                                       (1, 3, 2, 20), (4, 40, 2, 40)])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("sms", [9, 152])
+@pytest.mark.parametrize("sms", [1, 9, 152])
 def test_shared_prefix(pkv, cuda_device, group, n_seqs, q_len, blocks, d, sms):
-    """Gathered tensor-core sub-tiles (many rows) and split-KV shared CTAs (few)."""
+    """Gathered tensor-core sub-tiles (long prefixes of many rows for the SMs) and
+    streamed ones."""
     rng = np.random.default_rng(300 + blocks)
     ctx = blocks * 16 + q_len + rng.integers(0, 90, size=n_seqs)
     meta = workloads.build_step("fp8", 27, [q_len] * n_seqs, ctx, 2 * group, 2, d, rng=rng,
@@ -222,6 +223,58 @@ def test_shared_prefix(pkv, cuda_device, group, n_seqs, q_len, blocks, d, sms):
                          values_of(codes, scales), meta.scale)
     got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales, num_sms=sms)
     check_attention(got, *want, int(ctx.max()), tensor_cores=plan.fp8.staged_blocks > 0, scales=scales)
+
+
+@pytest.mark.parametrize("group,n_seqs,q_len,blocks", [(4, 20, 1, 17), (8, 3, 1, 9), (2, 6, 3, 33)])
+def test_shared_prefix_of_a_bf16_plan(pkv, cuda_device, group, n_seqs, q_len, blocks):
+    """A plan made for a bf16 pool (pkv_plan_step_ex: gathered at 64 rows, else shared
+    split-KV CTAs) serves an 8-bit pool with pkv_plan_stage_fp8's summary."""
+    rng = np.random.default_rng(320 + blocks)
+    ctx = blocks * 16 + q_len + rng.integers(0, 90, size=n_seqs)
+    meta = workloads.build_step("fp8", 28, [q_len] * n_seqs, ctx, 2 * group, 2, 128, rng=rng,
+                                shared_prefix_blocks=blocks)
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+    q = ref.bf16(rng.standard_normal((meta.total_q, 2 * group, 128)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    dev = cuda_device
+    info, host = pkv.plan_step(meta.cu_q_lens, meta.context_lens, 2 * group,
+                               pkv.pool_desc(codes), block_tables=meta.block_tables,
+                               upload=False, device=dev)
+    assert info.num_gather_rows > 0 or info.num_shared_ctas > 0
+    plan = pkv.StepPlan(info, host, dev, fp8=True)
+    st = status_of(dev)
+    out = pkv.paged_varlen_attention_fp8(q.to(dev), meta.cu_q_lens, meta.context_lens,
+                                         meta.block_tables, codes.to(dev), scales.to(dev),
+                                         meta.scale, plan=plan, dev_status=st)
+    torch.cuda.synchronize(dev)
+    assert int(st.item()) == 0
+    check_attention(out.cpu(), *want, int(ctx.max()), tensor_cores=info.num_gather_rows > 0,
+                    scales=scales)
+
+
+def test_summary_of_a_smaller_plan_is_reported(pkv, cuda_device):
+    """fp8.max_rows below what the plan holds: the larger row groups are reported and
+    their rows left as they were; the others are right."""
+    dev = cuda_device
+    rng = np.random.default_rng(33)
+    meta = workloads.build_step("fp8", 33, [1, 4], [200, 90], 8, 2, 128, rng=rng)
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+    q = ref.bf16(rng.standard_normal((5, 8, 128)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    plan = pkv.plan_step(meta.cu_q_lens, meta.context_lens, 8, codes.to(dev), fp8=True)
+    assert plan.fp8.max_rows == 16
+    plan.fp8.max_rows = 8
+    out = torch.full((5, 8, 128), 7.0, dtype=torch.bfloat16, device=dev)
+    st = status_of(dev)
+    pkv.paged_varlen_attention_fp8(q.to(dev), meta.cu_q_lens, meta.context_lens,
+                                   meta.block_tables, codes.to(dev), scales.to(dev), meta.scale,
+                                   plan=plan, out=out, dev_status=st)
+    torch.cuda.synchronize(dev)
+    assert int(st.item()) == 4
+    assert bool((out[1:] == 7.0).all())
+    check_attention(out[:1].cpu(), *(x[:1] for x in want), 200, tensor_cores=False, scales=scales)
 
 
 def test_wide_windows_share_blocks(pkv, cuda_device):

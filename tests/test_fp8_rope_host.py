@@ -104,8 +104,9 @@ def test_stage_covers_the_tensor_core_sequences(lib, seed, shared):
 
 @pytest.mark.parametrize("seed", range(6))
 def test_fp8_plan_covers_the_same_keys(lib, seed):
-    """pkv_plan_step_fp8 divides the work otherwise; what it covers is the same: every
-    (row group, KV head)'s blocks once, over pieces, shared items and gathered tiles."""
+    """pkv_plan_step_fp8 divides the work otherwise; what it covers is the same.  Without
+    a shared prefix every (row group, KV head)'s blocks are read as often as in the bf16
+    plan; a short shared prefix is streamed by each row group instead of shared."""
     rng = np.random.default_rng(100 + seed)
     meta = workloads.random_step(rng, max_ctx=900, max_q=3 if seed % 2 else None,
                                  shared_prefix_blocks=[0, 12][seed // 3])
@@ -115,8 +116,8 @@ def test_fp8_plan_covers_the_same_keys(lib, seed):
         assert pkv.stage_fp8(info, host)[1].max_rows <= 16
         infos.append(info)
     a, b = infos
-    assert (a.kv_tokens, a.decode_blocks, a.max_blocks_needed) == (
-        b.kv_tokens, b.decode_blocks, b.max_blocks_needed)
+    assert (a.kv_tokens, a.max_blocks_needed) == (b.kv_tokens, b.max_blocks_needed)
+    assert b.decode_blocks == a.decode_blocks if seed < 3 else b.decode_blocks >= a.decode_blocks
     assert b.num_decode_warps <= 4 * 16
 
 
