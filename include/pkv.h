@@ -498,7 +498,8 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
  * plan, rules and results, with K[p] = c_k scale_k and V[p] = c_v scale_v.
  * kv_scales: any positive finite values (not only powers of two).
  *   fp8, stage_begin: the summary pkv_plan_stage_fp8 wrote, and a DEVICE copy of
- *   its array.  workspace_bytes: at least fp8->workspace_bytes.  A row group with
+ *   its array.  workspace_bytes: at least fp8->workspace_bytes; a workspace serves one
+ *   call at a time (calls that may overlap need one each).  A row group with
  *   more than fp8->max_rows rows is reported (PKV_DEV_PLAN_MISMATCH), not attended.
  *   Rounding: on the split-KV kernel every stored value enters the products
  *   exactly (fp16), the weights are rounded to fp16, 2^-12; on the tensor-core

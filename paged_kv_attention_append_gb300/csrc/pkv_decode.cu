@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const DecodeParams
   float4 acc = merge_row<D, kBatch>(ml, po, g.nsplit - sub, S, rows, M, L, poisoned);
   if (S > 1) {
     // lanes sub and sub ^ o hold disjoint sets of the row's splits: combine
-    const unsigned mask = ((1u << S) - 1u) << ((threadIdx.x & 31) & ~(S - 1));
+    const unsigned mask = (S == 32 ? 0xffffffffu : (1u << S) - 1u)
+                          << ((threadIdx.x & 31) & ~(S - 1));
     for (int o = 1; o < S; o <<= 1) {
       const float Mo = __shfl_xor_sync(mask, M, o);
       const float Lo = __shfl_xor_sync(mask, L, o);
@@ -899,7 +900,10 @@ int launch_merge(const AttnArgs &a, int *launches) {
     const int64_t avg = ((int64_t)a.num_partials + a.num_decode_merges - 1) / a.num_decode_merges;
     const int64_t budget = (int64_t)std::max(device_sm_count(), 1) * 1024;
     const int64_t base = (int64_t)a.num_decode_merges * a.merge_rows * chunks;
-    while (lanes_log2 < 3 && avg > (8ll << lanes_log2) && (base << (lanes_log2 + 1)) <= budget)
+    // (an 8-bit pool's 16 warps an SM cut a few long sequences into hundreds of splits: up
+    // to 32 lanes there, one 32 000-token decode 26 -> 19 us)
+    const int max_log2 = a.kv_scales ? 5 : 3;
+    while (lanes_log2 < max_log2 && avg > (8ll << lanes_log2) && (base << (lanes_log2 + 1)) <= budget)
       ++lanes_log2;
   }
   const int64_t threads =

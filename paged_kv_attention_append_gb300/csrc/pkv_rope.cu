@@ -394,6 +394,7 @@ __device__ __forceinline__ void append_blocks(const RopeParams &p, int64_t unit,
   __syncthreads();
   if (settles) {
     const float amax = __uint_as_float(sm.amax[tg][ts]);
+    if (!(s_old <= FLT_MAX)) s_old = 0.f;  // not a scale: as if the block were new
     const bool keep = s_old > 0.f && s_old * kE4m3Max >= amax;
     const float s_new = keep ? s_old : pow2_scale(amax);
     sm.scale[tg][ts] = s_new;
