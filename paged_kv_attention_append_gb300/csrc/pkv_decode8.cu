@@ -56,10 +56,13 @@ struct Stage8 {
 // NT: the column tiles of the largest row group (1: at most 8 rows).
 template <int D, int NT>
 struct Decode8Cfg : Stage8<D> {
-  // CTAs an SM: with one column tile a lane's state fits 128 registers, so 16 warps.
-  // Stages: what fits beside (12 or 24 KB a warp at most)
+  // CTAs an SM: with one column tile a lane's state fits 128 registers, so 16 warps (8
+  // warps and 3 stages, 256 decodes: 193 us, 12 and 2: 184, 16 and 1: 180).  With two
+  // it does not (12 warps spill: 107 -> 152 us on 64 windows of 2 to 4 tokens).  Stages a
+  // warp: 16 KB at D = 128, 8 KB at D = 64, where they fit; more ran slower (256 decodes
+  // of 16 heads a KV head: 3 stages 130 us, 2 120, 1 133).
   static constexpr int kCtas = NT == 1 ? 4 : 2;
-  static constexpr int kStages = (NT == 1 ? 1 : 3) * (D == 128 ? 1 : 2);
+  static constexpr int kStages = NT == 1 && D == 128 ? 1 : 2;
 
   static constexpr int kRingBytes = kStages * Stage8<D>::kStageBytes;
   static constexpr int kScaleOffset = kWarps * kRingBytes;  // float2 x 2 a stage
