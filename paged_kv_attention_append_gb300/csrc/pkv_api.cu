@@ -74,7 +74,7 @@ static pkv_status check_pool(const pkv_pool_desc *desc) {
 
 using namespace pkv;
 
-extern "C" int32_t pkv_version(void) { return 200; }
+extern "C" int32_t pkv_version(void) { return 300; }
 
 extern "C" int64_t pkv_kernel_launch_count(void) { return g_launches.load(); }
 

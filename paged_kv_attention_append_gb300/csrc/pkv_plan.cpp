@@ -536,8 +536,11 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       for (const CPair &cp : cpairs) pf_work += (int64_t)cp.nsub * (groups[cp.gi].len / kKeyTileBlocks);
       const int64_t ncp = (int64_t)cpairs.size();
       int64_t num = 16 * pf_work, den = 16 * pf_work + total_blocks;  // share = num / den
-      if (16 * num < 7 * den) {
-        num = 7;
+      // An 8-bit pool's floor is 5/16: long suffixes want the SMs (64 sequences of 4096
+      // shared and up to 4000 own tokens, 64 CTAs 79.6 us, 32 70.7).
+      const int64_t floor16 = f8 ? 5 : 7;
+      if (16 * num < floor16 * den) {
+        num = floor16;
         den = 16;
       }
       const int64_t want = std::max<int64_t>(1, (2 * num * pf_sms + den * ncp) / (2 * den * ncp));
