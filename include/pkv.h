@@ -496,7 +496,7 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
 /*
  * pkv_paged_varlen_attention over an 8-bit pool (layout above): the same step,
  * plan, rules and results, with K[p] = c_k scale_k and V[p] = c_v scale_v.
- * kv_scales: any positive finite values (not only powers of two).
+ * kv_scales: any positive normal values (not only powers of two).
  *   fp8, stage_begin: the summary pkv_plan_stage_fp8 wrote, and a DEVICE copy of
  *   its array.  workspace_bytes: at least fp8->workspace_bytes; a workspace serves one
  *   call at a time (calls that may overlap need one each).  A row group with

@@ -979,8 +979,8 @@ def paged_varlen_attention_fp8(q, cu_q_lens, context_lens, block_tables, kv_pool
                                dev_status=None, stream=None):
     """paged_varlen_attention over an 8-bit pool; returns out [total_q, Hq, D] bf16.
 
-    kv_pool: e4m3 [nb, 2, Hkv, 16, D]; kv_scales: fp32 [nb, Hkv, 2], positive and
-    finite.  plan: one made with plan_step(..., fp8=True); built here when not given.
+    kv_pool: e4m3 [nb, 2, Hkv, 16, D]; kv_scales: fp32 [nb, Hkv, 2], positive normal
+    values.  plan: one made with plan_step(..., fp8=True); built here when not given.
     The other arguments mean what they mean for paged_varlen_attention.
     """
     desc = _check_fp8_pool(kv_pool, kv_scales)

@@ -807,3 +807,113 @@ def test_serving_steps(pkv, cuda_device, fp8):
                 # cores do (u_w = 2^-8); the 8-bit pool's to fp16
                 check_attention(outs[i].cpu(), *want, int(c.max()), tensor_cores=not fp8,
                                 scales=None if sc is None else sc.cpu().nan_to_num())
+
+
+def test_two_streams_at_once(pkv, cuda_device):
+    """Appends and attentions of two independent batches on two streams, interleaved
+    without ordering between them: each has its own pool, plan and workspace."""
+    dev = cuda_device
+    jobs = []
+    for k in range(2):
+        rng = np.random.default_rng(800 + k)
+        meta = workloads.build_step("two", 80 + k, [1] * 40, rng.integers(2, 900, size=40), 8, 2,
+                                    128, rng=rng)
+        codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+        pool, sc = codes.to(dev), scales.to(dev)
+        (q, kk, v), (qd, kd, vd) = rope_inputs(rng, 40, 8, 2, 128, True, dev)
+        cs = ref.table(1000, 128)
+        pos = meta.context_lens - 1
+        side = torch.cuda.Stream(dev)
+        plan = pkv.plan_step(meta.cu_q_lens, meta.context_lens, 8, pool, fp8=True)
+        out, st = torch.empty((40, 8, 128), dtype=torch.bfloat16, device=dev), status_of(dev)
+        app = pkv.BoundRopeAppend(qd, kd, vd, i32(pos, dev), torch.from_numpy(cs).to(dev),
+                                  i32(meta.slot_mapping, dev), pool, kv_scales=sc, dev_status=st,
+                                  stream=side)
+        att = pkv.BoundAttentionFp8(app.q_out, i32(meta.cu_q_lens, dev), i32(meta.context_lens, dev),
+                                    i32(meta.block_tables, dev), pool, sc, meta.scale, plan, out,
+                                    dev_status=st, stream=side)
+        jobs.append((meta, q, pos, cs, pool, sc, app, att, out, st))
+    torch.cuda.synchronize(dev)
+    for _ in range(5):                 # the append of the same tokens again changes nothing
+        for j in jobs:
+            j[6].run()
+        for j in jobs:
+            j[7].run()
+    torch.cuda.synchronize(dev)
+    for meta, q, pos, cs, pool, sc, app, att, out, st in jobs:
+        assert int(st.item()) == 0
+        check_rotated(app.q_out, q, pos, cs, False)
+        want = ref.attention(ref.f64(app.q_out), meta.cu_q_lens, meta.context_lens,
+                             meta.block_tables, values_of(pool.cpu(), sc.cpu()), meta.scale)
+        check_attention(out.cpu(), *want, 900, tensor_cores=False, scales=sc.cpu())
+
+
+def test_padded_batch_leaves_its_tail(pkv, cuda_device):
+    """A batch padded to a fixed size: padding tokens have position and slot -1, padding
+    sequences no query; their rows of q_out and every other row stay as they were."""
+    dev = cuda_device
+    rng = np.random.default_rng(820)
+    n, pad = 5, 11
+    meta = workloads.build_step("pad", 82, [1] * n, [3, 40, 17, 200, 65], 4, 2, 64, rng=rng)
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 64)
+    pool, sc, st = codes.to(dev), scales.to(dev), status_of(dev)
+    (q, k, v), (qd, kd, vd) = rope_inputs(rng, n + pad, 4, 2, 64, False, dev)
+    cs = ref.table(300, 64)
+    pos = np.concatenate([meta.context_lens - 1, np.full(pad, -1)])
+    slots = np.concatenate([meta.slot_mapping, np.full(pad, -1)])
+    q_out = torch.full((n + pad, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
+    pkv.rope_kv_append_fp8(qd, kd, vd, i32(pos, dev), torch.from_numpy(cs).to(dev), i32(slots, dev),
+                           pool, sc, q_out=q_out, dev_status=st)
+    cu = np.concatenate([np.arange(n + 1), np.full(pad, n)]).astype(np.int32)
+    ctx = np.concatenate([meta.context_lens, np.zeros(pad)]).astype(np.int32)
+    bt = np.concatenate([meta.block_tables, np.full((pad, meta.max_blocks), -1)]).astype(np.int32)
+    out = pkv.paged_varlen_attention_fp8(q_out[:n], cu, ctx, bt, pool, sc, meta.scale, dev_status=st)
+    torch.cuda.synchronize(dev)
+    assert int(st.item()) == 0
+    assert bool((q_out[n:] == 3.0).all())
+    check_rotated(q_out[:n], q[:n], pos[:n], cs, False)
+    want = ref.attention(ref.f64(q_out[:n]), cu, ctx, bt, values_of(pool.cpu(), sc.cpu()), meta.scale)
+    check_attention(out.cpu(), *want, 200, tensor_cores=False, scales=sc.cpu())
+
+
+def test_python_refusals(pkv, cuda_device):
+    dev = cuda_device
+    pool, sc = pkv.fp8_pool(4, 2, 64, device=dev)
+    k = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device=dev)
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16, device=dev)
+    pos, slots = i32([0, 1, 2], dev), i32([0, 1, 2], dev)
+    cs = pkv.rope_cos_sin(8, 64, device=dev)
+    ok = dict(q=q, k=k, v=k, positions=pos, cos_sin=cs, slot_mapping=slots, kv_pool=pool,
+              kv_scales=sc)
+    pkv.BoundRopeAppend(**ok).run()
+    wide = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device=dev)
+    bad = [dict(k=k.cpu()), dict(k=k.float()), dict(v=k[:2]), dict(k=wide[:, :, ::2], v=k),
+           dict(k=wide[:, :, :64], v=k), dict(positions=pos[:2]), dict(positions=pos.long()),
+           dict(slot_mapping=slots[:2]), dict(cos_sin=cs.double()), dict(cos_sin=None, positions=None),
+           dict(q=q[:2]), dict(q_out=q[:, :2].contiguous()), dict(kv_scales=sc[:3]),
+           dict(kv_pool=pool.view(torch.uint8)), dict(kv_scales=None), dict(kv_scales=sc.half())]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError)):
+            pkv.BoundRopeAppend(**{**ok, **kw})
+    for kw in (dict(cos_sin=cs[:, :24].contiguous()), dict(cos_sin=cs[:, :8].contiguous())):
+        with pytest.raises(pkv.PkvError):
+            pkv.BoundRopeAppend(**{**ok, **kw}).run()
+    meta = workloads.build_step("r", 1, [1, 2], [20, 30], 4, 2, 64, pool_blocks=4)
+    args = (torch.zeros((3, 4, 64), dtype=torch.bfloat16, device=dev), meta.cu_q_lens,
+            meta.context_lens, meta.block_tables, pool)
+    plan = pkv.plan_step(meta.cu_q_lens, meta.context_lens, 4, pool)      # not for an 8-bit pool
+    with pytest.raises(ValueError):
+        pkv.paged_varlen_attention_fp8(*args, sc, 0.1, plan=plan)
+    plan = pkv.plan_step([0, 1], [20], 4, pool, fp8=True)                 # of another step
+    with pytest.raises(ValueError):
+        pkv.paged_varlen_attention_fp8(*args, sc, 0.1, plan=plan)
+    with pytest.raises((ValueError, TypeError)):
+        pkv.paged_varlen_attention_fp8(*args, sc.double(), 0.1)
+    with pytest.raises((ValueError, TypeError)):
+        pkv.paged_varlen_attention(*args, 0.1)
+    # nothing to do is no error, and nothing is launched
+    before = pkv.kernel_launch_count()
+    pkv.rope_kv_append_fp8(q[:0], k[:0], k[:0], pos[:0], cs, slots[:0], pool, sc)
+    pkv.paged_kv_append_fp8(k[:0], k[:0], slots[:0], pool, sc)
+    assert pkv.paged_varlen_attention_fp8(q[:0], [0, 0], [5], [[0]], pool, sc, 0.1).shape == (0, 4, 64)
+    assert pkv.kernel_launch_count() == before

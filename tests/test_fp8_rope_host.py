@@ -6,6 +6,8 @@ import ctypes
 import numpy as np
 import pytest
 
+import fp8_ref as ref
+import oracle
 import paged_kv_attention_append_gb300 as pkv
 import workloads
 
@@ -174,3 +176,56 @@ def test_empty_step_is_ok(lib):
     nbytes = int(fp8.workspace_bytes)
     assert begin.tolist() == [0, 0] and nbytes == info.workspace_bytes
     assert attention_call(lib, info, q=None, pool=None, stage=None, blocks=0) == OK
+
+
+# ------------------------------------------------- the plain forms the GPU tests compare with
+
+@pytest.mark.parametrize("seed", range(4))
+def test_plain_attention_is_the_oracle(seed):
+    rng = np.random.default_rng(seed)
+    meta = workloads.random_step(rng, max_ctx=90)
+    q, _, _, pool = workloads.make_values(meta)
+    want = oracle.paged_varlen_attention(q, meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                                         pool, meta.scale)
+    got, wabs, mag = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens,
+                                   meta.block_tables, ref.f64(pool), meta.scale)
+    assert np.abs(got - want).max() <= 1e-12
+    assert (np.abs(got) <= wabs + 1e-12).all() and (mag >= 0).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_plain_rotation_is_a_complex_product(interleaved):
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((7, 2, 64))
+    pos = rng.integers(0, 50, size=7)
+    cs = ref.table(50, 32)
+    y, size = ref.rotate(x, pos, cs, interleaved)
+    h = x[..., :32]
+    z = h[..., 0::2] + 1j * h[..., 1::2] if interleaved else h[..., :16] + 1j * h[..., 16:]
+    t = z * (cs[pos, :16] + 1j * cs[pos, 16:].astype(np.float64))[:, None]
+    want = np.stack([t.real, t.imag], axis=-1 if interleaved else -2).reshape(h.shape)
+    assert np.abs(y[..., :32] - want).max() <= 1e-12
+    assert np.array_equal(y[..., 32:], x[..., 32:]) and (np.abs(y) <= size + 1e-12).all()
+    # a rotation keeps each pair's length up to the table's rounding, 2^-23 relative
+    assert np.abs(np.abs(t) / np.abs(z) - 1).max() <= 2.0 ** -22
+
+
+def test_plain_append_fp8():
+    """Values stand within half a step of what was appended; kept rows keep theirs."""
+    rng = np.random.default_rng(4)
+    codes = ref.decode(ref.encode(rng.standard_normal((3, 2, 1, 16, 64)) * 100))
+    scales = np.full((3, 1, 2), 0.25)
+    rows = rng.standard_normal((4, 2, 1, 64)) * np.array([1, 1, 1, 5000.0])[:, None, None, None]
+    new, sc, rounded = ref.append_fp8(codes, scales, rows, [5, 6, 16, 35])
+    assert rounded.sum() == 2 * (2 + 1 + 4)          # block 2 grew: its rows 0-2 and the new one
+    assert (sc[0] == 0.25).all() and (sc[1] < 0.25).all() and (sc[2] > 0.25).all()
+    for b, off, t in ((0, 5, 0), (0, 6, 1), (1, 0, 2), (2, 3, 3)):
+        held = ref.decode(ref.encode(new[b, :, 0, off])) * sc[b, 0][:, None]
+        assert (np.abs(held - rows[t, :, 0]) <=
+                np.maximum(2.0 ** -4 * np.abs(rows[t, :, 0]), 2.0 ** -10 * sc[b, 0][:, None])).all()
+    assert np.allclose(new[2, :, 0, :3] * sc[2, 0][:, None, None],
+                       codes[2, :, 0, :3] * 0.25)
+    assert np.array_equal(new[0, :, 0, :5], codes[0, :, 0, :5])
+    for a in (448.0, 448.0001, 447.9, 1e-30, 0.0, 3.5, 1e30):
+        s = ref.pow2_scale(a)
+        assert a <= 448 * s and (s == 2.0 ** -64 or a > 224 * s)
