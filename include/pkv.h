@@ -470,6 +470,15 @@ PKV_API pkv_status pkv_plan_step_fp8(const int32_t *cu_q_lens, const int32_t *co
                                      int32_t prefill_min_q, void *plan, int64_t plan_capacity,
                                      pkv_plan_info *info);
 
+/* pkv_planner_post for a pkv_plan_step_fp8 call (pkv_planner_wait returns its status). */
+PKV_API pkv_status pkv_planner_post_fp8(pkv_planner *planner, const int32_t *cu_q_lens,
+                                        const int32_t *context_lens, int32_t num_seqs,
+                                        int32_t num_q_heads, const pkv_pool_desc *desc,
+                                        int32_t num_sms, int32_t steps,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        int32_t prefill_min_q, void *plan, int64_t plan_capacity,
+                                        pkv_plan_info *info);
+
 /* What an 8-bit pool adds to a plan's summary, written by pkv_plan_stage_fp8. */
 typedef struct pkv_fp8_info {
   int32_t staged_blocks;   /* bf16 copies of blocks the tensor-core kernel reads */
@@ -502,9 +511,9 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
  *   call at a time (calls that may overlap need one each).  A row group with
  *   more than fp8->max_rows rows is reported (PKV_DEV_PLAN_MISMATCH), not attended.
  *   Rounding: on the split-KV kernel every stored value enters the products
- *   exactly (fp16), the weights are rounded to fp16, 2^-12; on the tensor-core
+ *   exactly (fp16), the weights are rounded to fp16, 2^-11; on the tensor-core
  *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the
- *   weights to bf16, 2^-9.  Accumulation is fp32; out is rounded once to bf16.
+ *   weights to bf16, 2^-8.  Accumulation is fp32; out is rounded once to bf16.
  *   Bytes of a block past its sequence's context are never used, whatever they
  *   hold.  A NaN stored in a visible row reaches every row of out that sees it,
  *   and may reach rows of the same sequence's step that come before it.

@@ -152,6 +152,8 @@ def _load():
             lib.pkv_rope_kv_append_fp8.restype = i32
             lib.pkv_plan_step_fp8.argtypes = lib.pkv_plan_step_ex.argtypes
             lib.pkv_plan_step_fp8.restype = i32
+            lib.pkv_planner_post_fp8.argtypes = lib.pkv_planner_post.argtypes
+            lib.pkv_planner_post_fp8.restype = i32
             lib.pkv_plan_stage_fp8.argtypes = [P, ctypes.POINTER(PlanInfo), P,
                                                ctypes.POINTER(Fp8Info)]
             lib.pkv_plan_stage_fp8.restype = i32
@@ -683,12 +685,18 @@ class BoundPlan:
     run() returns once it has finished.  spin_us is how long the thread polls
     for the next post before it sleeps.  The arrays and `out` must stay
     unchanged from post() to wait().
+
+    fp8=True plans for an 8-bit pool (pkv_plan_step_fp8); `stage_out`, an int32
+    array of num_seqs + 1 entries, then receives the plan's staging array
+    (pkv_plan_stage_fp8) and self.fp8 its Fp8Info with every run() or wait().
     """
 
     def __init__(self, cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, out, *,
                  num_sms=None, chain_steps=None, block_tables=None, prefill_min_q=None,
-                 spin_us=None):
+                 spin_us=None, fp8=False, stage_out=None):
         arrays = [("cu_q_lens", cu_q_lens), ("context_lens", context_lens)]
+        if fp8:
+            arrays.append(("stage_out", stage_out))
         if block_tables is not None:
             arrays.append(("block_tables", block_tables))
         for name, a in arrays:
@@ -711,7 +719,11 @@ class BoundPlan:
             num_sms = (torch.cuda.get_device_properties(torch.device(device)).multi_processor_count
                        if torch.cuda.is_available() else 152)
         self.info = PlanInfo()
-        self._keep = (cu_q_lens, context_lens, block_tables, buf)
+        if fp8 and stage_out.shape != cu_q_lens.shape:
+            raise ValueError("stage_out must have num_seqs + 1 entries")
+        self._keep = (cu_q_lens, context_lens, block_tables, buf, stage_out)
+        self._stage_out = stage_out if fp8 else None
+        self.fp8 = Fp8Info() if fp8 else None
         self._out = buf.reshape(-1).view(np.uint8)
         vp = ctypes.c_void_p
         self._args = (vp(cu_q_lens.ctypes.data), vp(context_lens.ctypes.data),
@@ -722,7 +734,8 @@ class BoundPlan:
                       ctypes.c_int32(0 if block_tables is None else block_tables.shape[1]),
                       ctypes.c_int32(0 if prefill_min_q is None else int(prefill_min_q)),
                       vp(buf.ctypes.data), ctypes.c_int64(buf.nbytes), ctypes.byref(self.info))
-        self._f = _load().pkv_plan_step_ex
+        self._name = "pkv_plan_step_fp8" if fp8 else "pkv_plan_step_ex"
+        self._f = getattr(_load(), self._name)
         self._worker = None
         if spin_us is not None:
             lib = _load()
@@ -731,14 +744,23 @@ class BoundPlan:
             if st:
                 raise PkvError(st, "pkv_planner_create")
             self._worker = handle
-            self._post, self._wait = lib.pkv_planner_post, lib.pkv_planner_wait
+            self._post = lib.pkv_planner_post_fp8 if fp8 else lib.pkv_planner_post
+            self._wait = lib.pkv_planner_wait
             self._fin = weakref.finalize(self, lib.pkv_planner_destroy, handle)
+
+    def _planned(self):
+        if self.fp8 is not None:
+            st = _load().pkv_plan_stage_fp8(self._out.ctypes.data, ctypes.byref(self.info),
+                                            self._stage_out.ctypes.data, ctypes.byref(self.fp8))
+            if st:
+                raise PkvError(st, "pkv_plan_stage_fp8")
+        return self.info, (max(int(self.info.plan_bytes), 16) + 15) // 16 * 16
 
     def run(self):
         st = self._f(*self._args)
         if st:
-            raise PkvError(st, "pkv_plan_step_ex")
-        return self.info, (max(int(self.info.plan_bytes), 16) + 15) // 16 * 16
+            raise PkvError(st, self._name)
+        return self._planned()
 
     def post(self) -> None:
         if self._worker is None:
@@ -753,7 +775,7 @@ class BoundPlan:
         st = self._wait(self._worker)
         if st:
             raise PkvError(st, "pkv_planner_wait")
-        return self.info, (max(int(self.info.plan_bytes), 16) + 15) // 16 * 16
+        return self._planned()
 
     def close(self) -> None:
         """Stop and join the planning thread (also done when the object is collected)."""

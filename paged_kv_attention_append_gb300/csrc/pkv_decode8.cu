@@ -28,8 +28,8 @@
 //  * V8 is read as fragments by ldmatrix (16 x 16 bytes, transposed), whose register
 //    holds four keys of one head_dim: two fp16 pairs, no byte shuffling.  The weights
 //    carry vs, relative to the largest V scale seen so far: u = w vs / vref * 2^14,
-//    rounded to fp16 (2^-12; smallest step 2^-38 of the largest weight) where bf16
-//    would round to 2^-9.
+//    rounded to fp16 (2^-11; smallest step 2^-38 of the largest weight) where bf16
+//    would round to 2^-8.
 //  * Two consecutive blocks are a stage of the ring (one barrier) and are attended
 //    together: one maximum, one rescale, and independent chains of products.
 #include <cuda_runtime.h>

@@ -6,7 +6,7 @@
 // all but the longest contexts), instead of once per query tile inside the
 // attention kernel, whose shared-memory bandwidth the two MMAs already fill.
 // Each value is c s rounded to bf16: exact for the power-of-two scales the
-// append writes (e4m3 has 4 significant bits, bf16 8), one rounding of 2^-9 for
+// append writes (e4m3 has 4 significant bits, bf16 8), one rounding of 2^-8 for
 // any other scale.  Rows past the context are written as zeros, so that stale
 // bytes (NaN codes among them) never meet a zero weight.
 //

@@ -3,7 +3,7 @@
 // A step's plan depends only on host data (lengths, block tables), while its
 // KV append needs none, so a serving loop can queue the input copy and the
 // append while the plan is being made.  One thread per planner runs the
-// pkv_plan_step_ex calls posted to it; the caller polls for the result.  The
+// pkv_plan_step_ex (or pkv_plan_step_fp8) calls posted to it; the caller polls for the result.  The
 // hand-over is a single atomic state word: the poster writes the job and then
 // publishes it (release), the worker reads it after seeing it (acquire), and
 // the same pairing carries the result back.  Between jobs the worker polls for
@@ -31,6 +31,7 @@ struct Job {
   void *plan;
   int64_t plan_capacity;
   pkv_plan_info *info;
+  bool f8;
 };
 
 }  // namespace
@@ -61,9 +62,9 @@ struct pkv_planner {
       }
       if (state.load(std::memory_order_acquire) != kPosted) return;  // stopped with no job
       const Job &j = job;
-      result = pkv_plan_step_ex(j.cu_q_lens, j.context_lens, j.num_seqs, j.num_q_heads, j.desc,
-                                j.num_sms, j.steps, j.block_tables, j.max_blocks_per_seq,
-                                j.prefill_min_q, j.plan, j.plan_capacity, j.info);
+      result = (j.f8 ? pkv_plan_step_fp8 : pkv_plan_step_ex)(
+          j.cu_q_lens, j.context_lens, j.num_seqs, j.num_q_heads, j.desc, j.num_sms, j.steps,
+          j.block_tables, j.max_blocks_per_seq, j.prefill_min_q, j.plan, j.plan_capacity, j.info);
       state.store(kDone, std::memory_order_release);
     }
   }
@@ -97,13 +98,11 @@ extern "C" void pkv_planner_destroy(pkv_planner *p) {
   delete p;
 }
 
-extern "C" pkv_status pkv_planner_post(pkv_planner *p, const int32_t *cu_q_lens,
-                                       const int32_t *context_lens, int32_t num_seqs,
-                                       int32_t num_q_heads, const pkv_pool_desc *desc,
-                                       int32_t num_sms, int32_t steps,
-                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                       int32_t prefill_min_q, void *plan, int64_t plan_capacity,
-                                       pkv_plan_info *info) {
+static pkv_status post(pkv_planner *p, const int32_t *cu_q_lens, const int32_t *context_lens,
+                       int32_t num_seqs, int32_t num_q_heads, const pkv_pool_desc *desc,
+                       int32_t num_sms, int32_t steps, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, int32_t prefill_min_q, void *plan,
+                       int64_t plan_capacity, pkv_plan_info *info, bool f8) {
   if (!p) return PKV_ERR_NULL;
   if (p->state.load(std::memory_order_acquire) != kIdle) return PKV_ERR_STATE;
   if (num_sms <= 0) {
@@ -112,7 +111,7 @@ extern "C" pkv_status pkv_planner_post(pkv_planner *p, const int32_t *cu_q_lens,
     if (num_sms <= 0) return PKV_ERR_CUDA;
   }
   p->job = Job{cu_q_lens, context_lens, block_tables, num_seqs, num_q_heads, num_sms, steps,
-               max_blocks_per_seq, prefill_min_q, desc, plan, plan_capacity, info};
+               max_blocks_per_seq, prefill_min_q, desc, plan, plan_capacity, info, f8};
   {
     // under the lock, so a worker about to sleep either sees the job or is woken
     std::lock_guard<std::mutex> lk(p->mu);
@@ -120,6 +119,28 @@ extern "C" pkv_status pkv_planner_post(pkv_planner *p, const int32_t *cu_q_lens,
   }
   p->cv.notify_one();
   return PKV_OK;
+}
+
+extern "C" pkv_status pkv_planner_post(pkv_planner *p, const int32_t *cu_q_lens,
+                                       const int32_t *context_lens, int32_t num_seqs,
+                                       int32_t num_q_heads, const pkv_pool_desc *desc,
+                                       int32_t num_sms, int32_t steps,
+                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       int32_t prefill_min_q, void *plan, int64_t plan_capacity,
+                                       pkv_plan_info *info) {
+  return post(p, cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, steps, block_tables,
+              max_blocks_per_seq, prefill_min_q, plan, plan_capacity, info, false);
+}
+
+extern "C" pkv_status pkv_planner_post_fp8(pkv_planner *p, const int32_t *cu_q_lens,
+                                           const int32_t *context_lens, int32_t num_seqs,
+                                           int32_t num_q_heads, const pkv_pool_desc *desc,
+                                           int32_t num_sms, int32_t steps,
+                                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                           int32_t prefill_min_q, void *plan,
+                                           int64_t plan_capacity, pkv_plan_info *info) {
+  return post(p, cu_q_lens, context_lens, num_seqs, num_q_heads, desc, num_sms, steps, block_tables,
+              max_blocks_per_seq, prefill_min_q, plan, plan_capacity, info, true);
 }
 
 extern "C" pkv_status pkv_planner_wait(pkv_planner *p) {

@@ -178,6 +178,40 @@ def test_empty_step_is_ok(lib):
     assert attention_call(lib, info, q=None, pool=None, stage=None, blocks=0) == OK
 
 
+@pytest.mark.parametrize("thread", [False, True])
+def test_bound_planner_for_an_8_bit_pool(lib, thread):
+    """BoundPlan(fp8=True) writes what plan_step(fp8=True) and stage_fp8 write, run after
+    run, on the calling thread or on the planning thread."""
+    meta = workloads.make_config("agent_mixed")
+    desc = pkv.PoolDesc(meta.num_blocks, 16, meta.num_kv_heads, meta.head_dim)
+    cu, ctx = meta.cu_q_lens.astype(np.int32).copy(), meta.context_lens.astype(np.int32).copy()
+    bt = meta.block_tables.astype(np.int32).copy()
+    out, stage = np.zeros(1 << 18, np.int32), np.full(len(cu), -7, np.int32)
+    bp = pkv.BoundPlan(cu, ctx, meta.num_q_heads, desc, out, num_sms=152, block_tables=bt, fp8=True,
+                       stage_out=stage, spin_us=50 if thread else None)
+    for _ in range(2):
+        if thread:
+            bp.post()
+            info, nb = bp.wait()
+        else:
+            info, nb = bp.run()
+        want_info, want = plan_of(meta if ctx[-1] == meta.context_lens[-1] else
+                                  workloads.StepMeta(**{**meta.__dict__, "context_lens": ctx}),
+                                  block_tables=bt, fp8=True)
+        begin, fp8 = pkv.stage_fp8(want_info, want)
+        assert nb == want.nbytes and np.array_equal(out.view(np.uint8)[:nb], want.view(np.uint8)[:nb])
+        assert np.array_equal(stage, begin) and begin[-1] > 0
+        for f in ("staged_blocks", "max_rows", "workspace_bytes"):
+            assert getattr(bp.fp8, f) == getattr(fp8, f)
+        ctx[-1] -= 16
+    bp.close()
+    with pytest.raises(TypeError):
+        pkv.BoundPlan(cu, ctx, meta.num_q_heads, desc, out, num_sms=152, fp8=True)
+    with pytest.raises(ValueError):
+        pkv.BoundPlan(cu, ctx, meta.num_q_heads, desc, out, num_sms=152, fp8=True,
+                      stage_out=stage[:-1].copy())
+
+
 # ------------------------------------------------- the plain forms the GPU tests compare with
 
 @pytest.mark.parametrize("seed", range(4))
