@@ -851,18 +851,18 @@ int launch_decode_t(const AttnArgs &a, const CUtensorMap &map) {
 
 }  // namespace
 
-int make_pool_map(void *map_out, const void *pool, const pkv_pool_desc &desc) {
+int make_pool_map(void *map_out, const void *pool, const pkv_pool_desc &desc, int blocks) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return (int)cudaErrorNotSupported;
   CUtensorMap *map = static_cast<CUtensorMap *>(map_out);
   // rows of D bf16 ([num_blocks][2][Hkv][16] rows) seen as (64 columns, 8 rows,
   // D/64 column halves, row groups of 8) with strides (2D, 128, 16D) bytes: a box
-  // (64, 8, D/64, 2) is one paged block of one head
+  // (64, 8, D/64, 2 blocks) is one paged block of one head, or that many of the copies'
   const int d = desc.head_dim, halves = d / 64;
   const int64_t rows = (int64_t)desc.num_blocks * 2 * desc.num_kv_heads * kBlockSize;
   cuuint64_t dims[4] = {64, 8, (cuuint64_t)halves, (cuuint64_t)(rows > 0 ? rows / 8 : 1)};
   cuuint64_t strides[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 2 * 8};
-  cuuint32_t box[4] = {64, 8, (cuuint32_t)halves, 2};
+  cuuint32_t box[4] = {64, 8, (cuuint32_t)halves, (cuuint32_t)(2 * blocks)};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

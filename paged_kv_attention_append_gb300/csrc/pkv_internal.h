@@ -257,8 +257,8 @@ struct AttnArgs {
   pkv_stream stream;
   // 8-bit pool (kv_scales non-null: [num_blocks][Hkv][2] fp32): the split-KV kernel
   // reads it directly; the tensor-core kernel reads bf16 copies of the blocks its
-  // sequences need, sequence s's logical block j as block stage_begin[s] + j of
-  // `staged`, which launch_stage writes first.
+  // sequences need, which launch_stage writes first: staged is [K, V][Hkv][staged_blocks]
+  // [16][D], sequence s's logical block j its block stage_begin[s] + j.
   const float *kv_scales = nullptr;
   const int32_t *stage_begin = nullptr;
   int32_t staged_blocks = 0;
@@ -302,7 +302,9 @@ int launch_prefill(const AttnArgs &a, int *launches);
 // 4-D TMA view of the pool whose box is one paged block of one head, landing
 // as [8-row group][64-column half][8 rows][128 B], 128-byte swizzled; `map`
 // points to a CUtensorMap.
-int make_pool_map(void *map, const void *pool, const pkv_pool_desc &desc);
+// blocks > 1: that many consecutive blocks of one head, in an array that keeps a
+// head's blocks together (the copies of an 8-bit pool's blocks).
+int make_pool_map(void *map, const void *pool, const pkv_pool_desc &desc, int blocks = 1);
 
 void count_launches(int n);
 

@@ -149,8 +149,9 @@ struct PrefillParams {
   int32_t group;
   int32_t pool_groups;  // rows of the pool / 8 (out-of-range group coordinate)
   float scale_log2;
-  // not null: the pool is the bf16 staging copy of an 8-bit pool's blocks, block j
-  // of sequence s at stage_begin[s] + j; the block tables are not read
+  // not null: keys and values come from the bf16 copies of an 8-bit pool's blocks
+  // ([K, V][KV head][num_blocks blocks], sequence s's block j at stage_begin[s] + j), a
+  // whole key tile one box of kv_map; the block tables are not read
   const int32_t *stage_begin;
 };
 
@@ -372,6 +373,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nld;
       return true;
     };
+    // the same from the copies: key tile kt of the sequence at blocks stage0 .. stage1 - 1
+    // (a tile outside them is zero-filled and reported)
+    auto load_staged = [&](int h, int stage0, int stage1, int kt) -> bool {
+      const int n = nld, s = n % C::kSlots;
+      if (n >= C::kSlots &&
+          !__all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + r * kMaxSlots + s),
+                                             (uint32_t)(((n / C::kSlots) - 1) & 1)))) {
+        if (lane == 0) fail();
+        return false;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(B_FULL + r * kMaxSlots + s), C::kSlotBytes);
+        const int64_t b0 = (int64_t)stage0 + (int64_t)kt * kBlocksPerTile;
+        int g = p.pool_groups;
+        if (stage0 >= 0 && b0 + kBlocksPerTile <= stage1 && stage1 <= p.num_blocks)
+          g = ((r * hkv + h) * p.num_blocks + (int)b0) * (kBlockSize / 8);
+        else if (r == 0)
+          report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
+        tma_load_4d(smem_u32(smem + C::kOffRing + (r * C::kSlots + s) * C::kSlotBytes), &kv_map, 0,
+                    0, 0, g, bar(B_FULL + r * kMaxSlots + s));
+      }
+      __syncwarp();
+      ++nld;
+      return true;
+    };
     for (int it = it0; it < it1 && good; ++it) {
       const ItemMeta m = load_item(p, it);
       if (!m.ok) {
@@ -380,13 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int32_t *table = p.block_tables + (int64_t)m.t.seq * p.max_blocks_per_seq;
       const int stage0 = p.stage_begin ? __ldg(p.stage_begin + m.t.seq) : -1;
+      const int stage1 = p.stage_begin ? __ldg(p.stage_begin + m.t.seq + 1) : 0;
       const int nblk_ctx = (m.ctx + kBlockSize - 1) / kBlockSize;
       const int nblk = min(nblk_ctx, p.max_blocks_per_seq);
       // entry of block `lane` of the four tiles from relative tile 4 k on
       // (-1: past the context or the table, zero fill)
       auto read_group = [&](int k) -> int {
         const int kb = (m.t.kt0 + kTablePrefetchTiles * k) * kBlocksPerTile + lane;
-        return kb >= nblk ? -1 : stage0 >= 0 ? stage0 + kb : __ldg(table + kb);
+        return kb < nblk && !p.stage_begin ? __ldg(table + kb) : -1;
       };
       for (int x = 0; x < 2 && good; ++x) {
         const int ntx = x ? m.nt[1] : m.nt[0];
@@ -483,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             good = false;
             break;
           }
-          good = load_tile(m.t.h, tile_phys(j));
+          good = p.stage_begin ? load_staged(m.t.h, stage0, stage1, m.t.kt0 + j)
+                               : load_tile(m.t.h, tile_phys(j));
         }
         // after a pass that stages its output, the V ring's next index holds no
         // tile: it is that output's staging slot.  Its FULL phase completes
@@ -1006,7 +1034,8 @@ int launch_prefill(const AttnArgs &a, int *launches) {
   if (e) return e;
   pkv_pool_desc pool_desc = a.desc;
   if (a.kv_scales) pool_desc.num_blocks = a.staged_blocks;
-  e = make_pool_map(&kvmap, a.kv_scales ? a.staged : a.kv_pool, pool_desc);
+  e = make_pool_map(&kvmap, a.kv_scales ? a.staged : a.kv_pool, pool_desc,
+                    a.kv_scales ? kBlocksPerTile : 1);
   if (e) return e;
   // out has q's shape: whole 128-token sub-tiles are stored through this map
   e = make_q_map(&omap, a.out, a.total_q, a.num_q_heads, a.desc.head_dim, 1, kPrefillRows);

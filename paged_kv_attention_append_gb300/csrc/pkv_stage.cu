@@ -1,4 +1,5 @@
-// bf16 copies of the 8-bit blocks the tensor-core kernel needs.
+// bf16 copies of the 8-bit blocks the tensor-core kernel needs, each KV head's blocks of a
+// sequence one after another, so that a key tile is one box of a tensor map.
 //
 // A tensor-core sequence of q_len query tokens and context ctx does 4 D q_len ctx
 // FLOPs a head and reads D ctx e4m3 values once more per 128-token tile; its keys
@@ -34,7 +35,7 @@ struct StageParams {
   const int32_t *stage_begin;  // [num_seqs + 1]
   const int32_t *context_lens;
   const int32_t *block_tables;
-  uint4 *staged;               // bf16 [staged_blocks][2][Hkv][16][D]
+  uint4 *staged;               // bf16 [2][Hkv][staged_blocks][16][D]
   int32_t num_seqs, max_blocks_per_seq, num_blocks, hkv, staged_blocks;
   int32_t early;
   int32_t *dev_status;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) stage_kernel(const StageParams p) {
       const int row = (i * 32 + lane) * 16 / D;
       x[i] = phys >= 0 && row < rows ? ldg128_nc(src + i * 32 + lane) : make_uint4(0, 0, 0, 0);
     }
-    uint4 *dst = p.staged + ((int64_t)blk * slabs + sl) * (kBlockSize * D / 8);
+    uint4 *dst = p.staged + ((int64_t)sl * p.staged_blocks + blk) * (kBlockSize * D / 8);
 #pragma unroll
     for (int i = 0; i < kIn; ++i) {
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
