@@ -255,7 +255,7 @@ PKV_API pkv_status pkv_rope_kv_append(const void *q, int64_t q_stride, const voi
  *   past the new ones are left as they were.
  *   The new tokens of one block must lie within 16 consecutive tokens of the
  *   step (skipped tokens between them counted): a block is looked after by the
- *   warp of its first one.  Tokens of one block further apart, like two tokens
+ *   thread block of its first one.  Tokens of one block further apart, like two tokens
  *   with the same slot, leave that block's values unspecified (where the kernel
  *   sees it, it skips the later token and reports PKV_DEV_BAD_SLOT).
  *   Other arguments, skipped tokens and errors as pkv_rope_kv_append; kv_scales

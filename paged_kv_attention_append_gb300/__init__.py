@@ -536,7 +536,10 @@ class BoundCopy:
 
 
 class StepPlan:
-    """Host step metadata plus its device copy and the workspace it needs."""
+    """Host step metadata plus its device copy and the workspace it needs.
+
+    The workspace serves one attention call at a time: calls that may overlap
+    (two streams, two graphs replayed side by side) need a plan each."""
 
     def __init__(self, info: PlanInfo, host: np.ndarray, device: torch.device, stream=None,
                  fp8: bool = False):
@@ -565,7 +568,11 @@ class StepPlan:
                 self.dev = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             self.dev[:nbytes].copy_(src, non_blocking=False)
             if self._for_fp8 and self.fp8.staged_blocks:
-                self.stage = torch.from_numpy(stage).to(dev)
+                # into the same array while it is large enough, as with the plan: a
+                # captured graph holds its address
+                if self.stage is None or self.stage.numel() < stage.size:
+                    self.stage = torch.empty(stage.size, dtype=torch.int32, device=dev)
+                self.stage[:stage.size].copy_(torch.from_numpy(stage), non_blocking=False)
             if wsb > 0 and (self.workspace is None or self.workspace.numel() < wsb):
                 self.workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
         return self
@@ -976,6 +983,7 @@ class BoundAttentionFp8:
         self._tail = (vp(_ptr(dev_status)), vp(_stream(stream, q)))
         self._f = _bound_fn("pkv_paged_varlen_attention_fp8")
         self._device = kv_pool.device.index
+        self._checked = None        # the plan whose kind and device were found right
 
     def run(self) -> None:
         plan = self.plan
@@ -984,8 +992,12 @@ class BoundAttentionFp8:
         if (info.total_q != total_q or info.num_q_heads != hq or info.num_seqs + 1 != n_cu or
                 info.num_seqs != n_ctx or info.num_seqs != n_bt):
             raise ValueError("the plan does not match the bound buffers")
-        if plan.fp8 is None:
-            raise ValueError("the plan was not made for an 8-bit pool: plan_step(..., fp8=True)")
+        if plan is not self._checked:
+            if plan.fp8 is None:
+                raise ValueError("the plan was not made for an 8-bit pool: plan_step(..., fp8=True)")
+            if plan.dev.device.index != self._device:
+                raise ValueError("the plan must be on kv_pool's device")
+            self._checked = plan
         ws = plan.workspace
         vp = ctypes.c_void_p
         st = _call_on(self._device, self._f, (

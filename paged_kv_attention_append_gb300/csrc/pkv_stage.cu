@@ -17,7 +17,7 @@
 // context are read together, before the wait for the preceding kernel.  288 blocks of 8
 // heads: 6.4 us, 1024: 18.5 us (100 MB moved, 5.4 TB/s).  The tensor-core
 // kernel is let launch early only when its CTAs, each a whole SM, leave half of the SMs
-// to the CTAs here (64 CTAs of a gathered prefix, same box: 44.8 us a step with the early
+// to the CTAs here (64 CTAs of a gathered prefix: 44.8 us a step with the early
 // launch, 48.7 without; 152 CTAs of a 2048-token chunk: 153 us with, 144 without).
 #include <cuda_runtime.h>
 

@@ -352,6 +352,40 @@ def test_long_context_and_far_blocks(pkv, cuda_device):
     check_attention(out.cpu(), *want, 40_000, tensor_cores=False, scales=scales)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_far_blocks_of_append_and_tensor_cores(pkv, cuda_device, fp8):
+    """A chunk appended to and attended from blocks past 4 GiB gives the bits that it
+    gives in a pool of 7 blocks."""
+    dev = cuda_device
+    rng = np.random.default_rng(53)
+    hkv, d, n, nb = 8, 128, 100, 140_000
+    q, k, v = (ref.bf16(rng.standard_normal((n, h, d))).to(dev) for h in (16, hkv, hkv))
+    cs, pos = pkv.rope_cos_sin(n, d, device=dev), i32(np.arange(n), dev)
+    got = []
+    for blocks in (7, nb):
+        if fp8:
+            pool, sc = pkv.fp8_pool(blocks, hkv, d, device=dev)
+            assert blocks == 7 or pool.numel() > 1 << 32
+        else:
+            pool = torch.zeros((blocks, 2, hkv, 16, d), dtype=torch.bfloat16, device=dev)
+        t = np.arange(n)
+        slots = i32((blocks - 1 - t // 16) * 16 + t % 16, dev)
+        table = blocks - 1 - np.arange(7, dtype=np.int32)[None]
+        if fp8:
+            qr = pkv.rope_kv_append_fp8(q, k, v, pos, cs, slots, pool, sc)
+            out = pkv.paged_varlen_attention_fp8(qr, [0, n], [n], table, pool, sc, d ** -0.5)
+        else:
+            qr = pkv.rope_kv_append(q, k, v, pos, cs, slots, pool)
+            out = pkv.paged_varlen_attention(qr, [0, n], [n], table, pool, d ** -0.5)
+        raw = pool.view(torch.uint8)
+        got.append([qr, out, raw[blocks - 7:].clone()] + ([sc[blocks - 7:].clone()] if fp8 else []))
+        assert not bool(raw[:blocks - 7].any())
+        del pool, raw
+    assert bool(got[0][1].isfinite().all()) and bool(got[0][2].any())
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("pmq", [-1, 1])
 def test_bad_block_is_reported_and_skipped(pkv, cuda_device, pmq):
     rng = np.random.default_rng(61)

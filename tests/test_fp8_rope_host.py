@@ -5,6 +5,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import fp8_ref as ref
 import oracle
@@ -121,6 +122,25 @@ def test_fp8_plan_covers_the_same_keys(lib, seed):
     assert (a.kv_tokens, a.max_blocks_needed) == (b.kv_tokens, b.max_blocks_needed)
     assert b.decode_blocks == a.decode_blocks if seed < 3 else b.decode_blocks >= a.decode_blocks
     assert b.num_decode_warps <= 4 * 16
+
+
+def test_upload_again_keeps_the_addresses():
+    """A plan uploaded again, here for a step with fewer sequences, stays where it was: a
+    captured graph holds the addresses of the plan, the staging array and the workspace."""
+    metas = [workloads.build_step("fp8", 9, ql, ctx, 8, 2, 128) for ql, ctx in
+             (([200, 1, 90], [400, 33, 700]), ([130, 1], [300, 40]))]
+    (info0, host0), (info1, host1) = (plan_of(m, fp8=True) for m in metas)
+    plan = pkv.StepPlan(info0, host0, torch.device("cpu"), fp8=True)
+    begin0, _ = pkv.stage_fp8(info0, host0)
+    assert np.array_equal(plan.stage.numpy(), begin0)
+    kept = [t.data_ptr() for t in (plan.dev, plan.stage, plan.workspace)]
+    plan.info, plan.host = info1, host1
+    plan.upload()
+    begin1, fp8 = pkv.stage_fp8(info1, host1)
+    assert fp8.staged_blocks > 0
+    assert np.array_equal(plan.stage.numpy()[:begin1.size], begin1)
+    assert [t.data_ptr() for t in (plan.dev, plan.stage, plan.workspace)] == kept
+    assert plan.workspace.numel() >= plan.fp8.workspace_bytes
 
 
 def test_stage_refusals(lib):
