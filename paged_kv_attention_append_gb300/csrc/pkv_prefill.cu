@@ -149,9 +149,10 @@ struct PrefillParams {
   int32_t group;
   int32_t pool_groups;  // rows of the pool / 8 (out-of-range group coordinate)
   float scale_log2;
-  // not null: keys and values come from the bf16 copies of an 8-bit pool's blocks
+  // kCopies: keys and values come from the bf16 copies of an 8-bit pool's blocks
   // ([K, V][KV head][num_blocks blocks], sequence s's block j at stage_begin[s] + j), a
-  // whole key tile one box of kv_map; the block tables are not read
+  // whole key tile one box of kv_map; the block tables are not read.  (An instance of its
+  // own: with the choice made at run time the bf16 pool's steps took 3.5 % longer.)
   const int32_t *stage_begin;
 };
 
@@ -257,7 +258,7 @@ __device__ __forceinline__ bool stages_output(const ItemMeta &m, int x) {
 // (the instance for steps without gathered sub-tiles); without it every output
 // row is stored directly, which keeps the gathered sub-tiles' code as lean as
 // before.  Both compute the same result.
-template <int D, bool kStage>
+template <int D, bool kStage, bool kCopies>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap qg_map,
@@ -405,15 +406,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int32_t *table = p.block_tables + (int64_t)m.t.seq * p.max_blocks_per_seq;
-      const int stage0 = p.stage_begin ? __ldg(p.stage_begin + m.t.seq) : -1;
-      const int stage1 = p.stage_begin ? __ldg(p.stage_begin + m.t.seq + 1) : 0;
+      int stage0 = 0, stage1 = 0;
+      if constexpr (kCopies) {
+        stage0 = __ldg(p.stage_begin + m.t.seq);
+        stage1 = __ldg(p.stage_begin + m.t.seq + 1);
+      }
       const int nblk_ctx = (m.ctx + kBlockSize - 1) / kBlockSize;
       const int nblk = min(nblk_ctx, p.max_blocks_per_seq);
       // entry of block `lane` of the four tiles from relative tile 4 k on
       // (-1: past the context or the table, zero fill)
       auto read_group = [&](int k) -> int {
         const int kb = (m.t.kt0 + kTablePrefetchTiles * k) * kBlocksPerTile + lane;
-        return kb < nblk && !p.stage_begin ? __ldg(table + kb) : -1;
+        return !kCopies && kb < nblk ? __ldg(table + kb) : -1;
       };
       for (int x = 0; x < 2 && good; ++x) {
         const int ntx = x ? m.nt[1] : m.nt[0];
@@ -510,8 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             good = false;
             break;
           }
-          good = p.stage_begin ? load_staged(m.t.h, stage0, stage1, m.t.kt0 + j)
-                               : load_tile(m.t.h, tile_phys(j));
+          if constexpr (kCopies)
+            good = load_staged(m.t.h, stage0, stage1, m.t.kt0 + j);
+          else
+            good = load_tile(m.t.h, tile_phys(j));
         }
         // after a pass that stages its output, the V ring's next index holds no
         // tile: it is that output's staging slot.  Its FULL phase completes
@@ -974,7 +980,7 @@ int make_q_map(CUtensorMap *map, const void *q, int64_t total_q, int hq, int d, 
   return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int D, bool kCopies>
 int launch_prefill_t(const AttnArgs &a, const CUtensorMap &qmap, const CUtensorMap &qgmap,
                      const CUtensorMap &qrmap, const CUtensorMap &kvmap,
                      const CUtensorMap &omap) {
@@ -982,9 +988,9 @@ int launch_prefill_t(const AttnArgs &a, const CUtensorMap &qmap, const CUtensorM
   // staging pays on contiguous prefill; the gathered sub-tiles' passes run
   // faster in the instance without it
   const bool stage = a.num_gather_rows == 0;
-  auto kern = stage ? prefill_kernel<D, true> : prefill_kernel<D, false>;
-  cudaError_t e = stage ? prepare_kernel<prefill_kernel<D, true>>(C::kSmemBytes)
-                        : prepare_kernel<prefill_kernel<D, false>>(C::kSmemBytes);
+  auto kern = stage ? prefill_kernel<D, true, kCopies> : prefill_kernel<D, false, kCopies>;
+  cudaError_t e = stage ? prepare_kernel<prefill_kernel<D, true, kCopies>>(C::kSmemBytes)
+                        : prepare_kernel<prefill_kernel<D, false, kCopies>>(C::kSmemBytes);
   if (e != cudaSuccess) return (int)e;
   PrefillParams p;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
@@ -1004,9 +1010,9 @@ int launch_prefill_t(const AttnArgs &a, const CUtensorMap &qmap, const CUtensorM
   p.dev_status = a.dev_status;
   p.num_seqs = a.num_seqs;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
-  const int32_t pool_blocks = a.kv_scales ? a.staged_blocks : a.desc.num_blocks;
+  const int32_t pool_blocks = kCopies ? a.staged_blocks : a.desc.num_blocks;
   p.num_blocks = pool_blocks;
-  p.stage_begin = a.kv_scales ? a.stage_begin : nullptr;
+  p.stage_begin = a.stage_begin;
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.desc.num_kv_heads;
   p.group = a.num_q_heads / a.desc.num_kv_heads;
@@ -1040,8 +1046,10 @@ int launch_prefill(const AttnArgs &a, int *launches) {
   // out has q's shape: whole 128-token sub-tiles are stored through this map
   e = make_q_map(&omap, a.out, a.total_q, a.num_q_heads, a.desc.head_dim, 1, kPrefillRows);
   if (e) return e;
-  e = a.desc.head_dim == 128 ? launch_prefill_t<128>(a, qmap, qgmap, qrmap, kvmap, omap)
-                             : launch_prefill_t<64>(a, qmap, qgmap, qrmap, kvmap, omap);
+  const auto launch = a.desc.head_dim == 128
+                          ? (a.kv_scales ? launch_prefill_t<128, true> : launch_prefill_t<128, false>)
+                          : (a.kv_scales ? launch_prefill_t<64, true> : launch_prefill_t<64, false>);
+  e = launch(a, qmap, qgmap, qrmap, kvmap, omap);
   if (!e) {
     ++*launches;
     count_launches(1);
