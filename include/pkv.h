@@ -251,7 +251,8 @@ PKV_API pkv_status pkv_rope_kv_append(const void *q, int64_t q_stride, const voi
  *     the smallest power of two s' >= 2^-64 with 448 s' >= max |N| (infinities
  *     are left out of the maximum) and each kept value c becomes c s / s';
  *   - the new rows are stored as x / scale.
- *   Both are rounded to nearest even and saturate at +-448; NaN stays NaN.  Rows
+ *   Both are evaluated in fp32 (exactly, when the scales are powers of two), rounded
+ *   to nearest even and saturate at +-448; NaN stays NaN.  Rows
  *   past the new ones are left as they were.
  *   The new tokens of one block must lie within 16 consecutive tokens of the
  *   step (skipped tokens between them counted): a block is looked after by the

@@ -277,6 +277,34 @@ def test_summary_of_a_smaller_plan_is_reported(pkv, cuda_device):
     check_attention(out[:1].cpu(), *(x[:1] for x in want), 200, tensor_cores=False, scales=scales)
 
 
+@pytest.mark.parametrize("stage", ["none", "past", "other"])
+def test_wrong_staging_array_is_reported(pkv, cuda_device, stage):
+    """A staging array that does not give a tensor-core sequence its copies: reported,
+    nothing outside the workspace and out is written, the other rows are right."""
+    dev = cuda_device
+    rng = np.random.default_rng(34)
+    meta = workloads.build_step("fp8", 34, [1, 70], [200, 90], 8, 2, 128, rng=rng)
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+    q = ref.bf16(rng.standard_normal((71, 8, 128)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    plan = pkv.plan_step(meta.cu_q_lens, meta.context_lens, 8, codes.to(dev), fp8=True)
+    n = plan.fp8.staged_blocks
+    assert n == 8 and plan.stage.tolist() == [0, 0, n]
+    plan.stage = i32({"none": [0, 0, 0], "past": [0, n, 2 * n], "other": [0, n, n]}[stage], dev)
+    ws = torch.full((plan.workspace.numel() + 2 * GUARD,), 0xA5, dtype=torch.uint8, device=dev)
+    plan.workspace = ws[GUARD:-GUARD]
+    out = torch.full((71, 8, 128), 7.0, dtype=torch.bfloat16, device=dev)
+    st = status_of(dev)
+    pkv.paged_varlen_attention_fp8(q.to(dev), meta.cu_q_lens, meta.context_lens,
+                                   meta.block_tables, codes.to(dev), scales.to(dev), meta.scale,
+                                   plan=plan, out=out, dev_status=st)
+    torch.cuda.synchronize(dev)
+    assert int(st.item()) == 4
+    assert bool((ws[:GUARD] == 0xA5).all()) and bool((ws[-GUARD:] == 0xA5).all())
+    check_attention(out[:1].cpu(), *(x[:1] for x in want), 200, tensor_cores=False, scales=scales)
+
+
 def test_wide_windows_share_blocks(pkv, cuda_device):
     """Verify windows of more than 16 rows: two row groups read each block once."""
     rng = np.random.default_rng(31)
