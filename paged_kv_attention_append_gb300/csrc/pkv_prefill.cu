@@ -254,6 +254,37 @@ __device__ __forceinline__ bool stages_output(const ItemMeta &m, int x) {
   return kStage && !m.gathered && part < 0 && nq == kPrefillRows;
 }
 
+// The unnormalised O of a warp's 32 rows (TMEM at `to`) to each lane's row `prow`
+// (null: none).  Each lane holds its row's 32-column chunk as 8 pieces of 16 bytes;
+// transposed within groups of 8 lanes, one store covers 4 rows x 128 contiguous bytes
+// rather than 32 rows x 16 bytes.  Neither inlined nor unrolled: a CTA with one gathered
+// item runs this once, and each copy of the loop's code cost it 2 us of instruction
+// fetches (verify step on a shared prefix, 8-bit pool: 45.6 -> 40.8 us).
+template <int D>
+__device__ __noinline__ void store_partial(uint32_t to, float *prow, int lane) {
+  const int gl8 = lane & 7, gbase = lane & ~7;
+  float *rows8[8];  // destination rows of this lane's group
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    rows8[k] = reinterpret_cast<float *>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(prow), gbase + k));
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tc::ld32(to + 32 * c, o);
+    tc::wait_ld();
+    float4 pc[8];
+#pragma unroll
+    for (int v4 = 0; v4 < 8; ++v4)
+      pc[v4] = make_float4(__uint_as_float(o[4 * v4]), __uint_as_float(o[4 * v4 + 1]),
+                           __uint_as_float(o[4 * v4 + 2]), __uint_as_float(o[4 * v4 + 3]));
+    transpose8x8(pc, gl8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (rows8[k]) reinterpret_cast<float4 *>(rows8[k] + 32 * c)[gl8] = pc[k];
+  }
+}
+
 // kStage: whole sub-tiles leave through a staging slot and bulk tensor stores
 // (the instance for steps without gathered sub-tiles); without it every output
 // row is stored directly, which keeps the gathered sub-tiles' code as lean as
@@ -835,12 +866,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc::fence_after_sync();
+        if constexpr (!kStage) {
+          if (part >= 0) {
+            store_partial<D>(to, prow, lane);
+            if (pml) *pml = make_float2(m_used, l);
+            tc::fence_before_sync();
+            continue;
+          }
+        }
         // the row's whole O in one round trip
         uint32_t ov[D / 32][32];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tc::ld32(to + 32 * c, ov[c]);
         tc::wait_ld();
-        if (part >= 0) {
+        if (kStage && part >= 0) {
+          // (inline here: with the function the tile loop of long chunks came out 1 % slower)
           // unnormalised O: each lane holds its row's 32-column chunk as 8 pieces
           // of 16 bytes; transposed within groups of 8 lanes, one store covers
           // 4 rows x 128 contiguous bytes rather than 32 rows x 16 bytes
