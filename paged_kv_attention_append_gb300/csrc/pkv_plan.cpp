@@ -103,6 +103,10 @@ constexpr int64_t kGatherMinRows = 64;
 // on one stream were no faster (32 sequences on 128 blocks 27.1 us).
 constexpr int64_t kGather8MinBlocksPerSm = 131;
 
+// 8-bit pool: what streaming one block of one KV head costs an SM beside a full prefill, in
+// the units of kTileCost (0.1 us).
+constexpr int64_t kStream8CostNum = 3, kStream8CostDen = 4;
+
 // The planner's working arrays, kept per host thread so a plan allocates
 // nothing once a thread has planned a step of that size.
 struct PlanScratch {
@@ -363,9 +367,9 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     }
   }
 
-  // Both kernels get every SM: the tensor-core kernel's persistent CTAs take one
-  // SM each, and the split-KV kernel, which it lets launch once the pool is
-  // complete, starts on each SM as soon as that SM's CTA has finished.
+  // Both kernels get every SM (but see stream_sms below): the tensor-core kernel's
+  // persistent CTAs take one SM each, and the split-KV kernel, which it lets launch once
+  // the pool is complete, starts on each SM as soon as that SM's CTA has finished.
   const int32_t pf_sms = num_sms, dec_sms = num_sms;
 
   // ---- shared-block items: per stream and KV head, its row groups in pairs
@@ -589,14 +593,35 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   // (agent-shaped step, same box: 146.5 -> 144.3 us; 2/3 and 2/5 of the slots
   // in between, a quarter 149.7).  A smaller prefill leaves SMs free from the
   // start and keeps every slot.
+  int32_t stream_sms = 0;  // SMs that a full prefill leaves to the split-KV kernel
   if (!pairs.empty()) {
-    int64_t pf_tiles = 0;
-    for (const auto &nt : pair_nt) pf_tiles += nt[0] + nt[1];
-    // (counted at 8 warps an SM: with 16, 8-bit pool, the same number of warps on half as
-    // many SMs, 147.5 us against 148.4 on as many and 149.9 on a third of them)
-    if (pf_tiles >= (int64_t)pf_sms * kMinTilesPerCta)
-      nw64 = std::min<int64_t>(
-          nw64, std::max<int64_t>(1, avail * kDecodeWarpsPerSm / (2 * warps_per_sm)));
+    int64_t pf_tiles = 0, pf_cost = 0;
+    for (const auto &nt : pair_nt) {
+      pf_tiles += nt[0] + nt[1];
+      pf_cost += kPassStartCost * ((nt[0] > 0) + (nt[1] > 0)) + kTileCost * (nt[0] + nt[1]);
+    }
+    for (const PrefillTile &t : casc_items) pf_cost += kPassStartCost + kTileCost * (t.kt1 - t.kt0);
+    if (pf_tiles >= (int64_t)pf_sms * kMinTilesPerCta) {
+      if (f8 && n_pairs == 0 && total_blocks > 0 && pf_sms > 2) {
+        // 8-bit pool: the prefill leaves SMs to the split-KV kernel, which streams beside
+        // it instead of behind it, in proportion to the two kernels' work; an even number,
+        // since a streaming SM that shares its pair with a prefill CTA is slower (5 SMs
+        // took longer than 4).  A 2048-token chunk at 4608 with 3, 8, 16 and 32 decodes of
+        // 2048 to 8192 keys: 147, 169, 202 and 288 us behind the prefill, 143, 152, 163
+        // and 186 beside it; 4096 tokens at 16384 with 64: 931 and 734.  A block's cost
+        // taken as 2/3, 5/6 and 1: 185, 185, 198 with 32 decodes, 750, 748, 755 with 64.
+        // Spread evenly over the grid, the same SMs took 233 and 871.
+        const int64_t stream =
+            kStream8CostNum * total_blocks * (max_rows <= kDecode8SmallRows ? 1 : 2);
+        const int64_t all = stream + kStream8CostDen * pf_cost;
+        const int64_t x = (stream * pf_sms + all - 1) / all;
+        const int64_t most = (nw64 + warps_per_sm - 1) / warps_per_sm;
+        stream_sms = (int32_t)std::min<int64_t>((std::min(x, most) + 1) / 2 * 2, pf_sms - 1);
+        nw64 = std::min<int64_t>(nw64, (int64_t)stream_sms * warps_per_sm);
+      } else {
+        nw64 = std::min<int64_t>(nw64, std::max<int64_t>(1, avail / 2));
+      }
+    }
   }
   // With gathered prefix items as the step's only tensor-core work, the
   // lowest-index split-KV CTAs start at once on the SMs the items leave free
@@ -614,7 +639,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   int32_t max_seg = 0;
   for (const Segment &g : segs) max_seg = std::max(max_seg, g.nb);
   const bool whole_segments =
-      !segs.empty() && (int64_t)segs.size() <= avail &&
+      !segs.empty() && stream_sms == 0 && (int64_t)segs.size() <= avail &&
       max_seg <= std::max<int64_t>(2 * kMinBlocksPerWarp,
                                    (total_blocks + avail - 1) / avail + kMinBlocksPerWarp);
   if (whole_segments) nw64 = (int64_t)segs.size();
@@ -789,7 +814,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     if (f8)
       for (const auto &nt : pair_nt) min_ctas += (nt[0] > 0) + (nt[1] > 0);
     n_pf_ctas = (int32_t)std::max<int64_t>(
-        1, std::min<int64_t>(pf_sms, std::max<int64_t>(ntiles / kMinTilesPerCta, min_ctas)));
+        1, std::min<int64_t>(pf_sms - stream_sms, std::max<int64_t>(ntiles / kMinTilesPerCta, min_ctas)));
     const int64_t target = (total + n_pf_ctas - 1) / n_pf_ctas;
     std::vector<size_t> order(pairs.size());
     for (size_t i = 0; i < order.size(); ++i) order[i] = i;

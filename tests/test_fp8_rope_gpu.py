@@ -305,6 +305,26 @@ def test_wrong_staging_array_is_reported(pkv, cuda_device, stage):
     check_attention(out[:1].cpu(), *(x[:1] for x in want), 200, tensor_cores=False, scales=scales)
 
 
+@pytest.mark.parametrize("q_lens", [[1] * 6, [1], [3, 2, 4], [1] * 40])
+@pytest.mark.parametrize("sms", [3, 4, 9])
+def test_split_kv_beside_a_full_prefill(pkv, cuda_device, q_lens, sms):
+    """The tensor-core kernel takes every SM that the plan does not leave to the split-KV
+    kernel; both kernels' rows are right."""
+    rng = np.random.default_rng(35)
+    ql = q_lens + [330]
+    ctx = [int(x) for x in rng.integers(8, 900, size=len(q_lens))] + [700]
+    meta = workloads.build_step("fp8", 35, ql, ctx, 8, 2, 128, rng=rng)
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+    q = ref.bf16(rng.standard_normal((meta.total_q, 8, 128)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    got, plan = run_attention(pkv, cuda_device, meta, q, codes, scales, num_sms=sms)
+    assert plan.info.num_prefill_ctas < sms and plan.info.num_decode_warps > 0
+    n = meta.total_q - 330
+    for rows, tc in ((slice(0, n), False), (slice(n, None), True)):
+        check_attention(got[rows], *(x[rows] for x in want), 900, tensor_cores=tc, scales=scales)
+
+
 def test_wide_windows_share_blocks(pkv, cuda_device):
     """Verify windows of more than 16 rows: two row groups read each block once."""
     rng = np.random.default_rng(31)

@@ -143,6 +143,26 @@ def test_upload_again_keeps_the_addresses():
     assert plan.workspace.numel() >= plan.fp8.workspace_bytes
 
 
+@pytest.mark.parametrize("decodes", [1, 3, 16, 64])
+@pytest.mark.parametrize("chunk,ctx", [(2048, 4608), (4096, 16384), (8192, 8192)])
+def test_full_prefill_leaves_sms_to_the_split_kv_work(lib, decodes, chunk, ctx):
+    """8-bit pool: with a prefill for every SM, an even number of SMs is left for the
+    decodes, whose warps all fit there; more with more decodes.  A plan for a bf16 pool
+    gives the prefill every SM."""
+    def plan(n, **kw):
+        ql, cl = [1] * n + [chunk], [4096 + 16 * i for i in range(n)] + [ctx]
+        cu = np.concatenate([[0], np.cumsum(ql)])
+        return pkv.plan_step(cu, cl, 32, pkv.PoolDesc(sum(cl) // 16 + len(cl), 16, 8, 128),
+                             num_sms=152, upload=False, **kw)[0]
+    info = plan(decodes, fp8=True)
+    left = 152 - info.num_prefill_ctas
+    assert left > 0 and left % 2 == 0
+    assert 0 < info.num_decode_warps <= 16 * left
+    assert 152 - plan(2 * decodes, fp8=True).num_prefill_ctas >= left
+    assert plan(decodes).num_prefill_ctas == 152
+    assert plan(0, fp8=True).num_prefill_ctas == 152
+
+
 def test_stage_refusals(lib):
     meta = workloads.build_step("s", 1, [70, 1], [70, 40], 4, 2, 64)
     info, host = plan_of(meta)
