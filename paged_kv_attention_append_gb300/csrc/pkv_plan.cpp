@@ -106,6 +106,8 @@ constexpr int64_t kGather8MinBlocksPerSm = 131;
 // 8-bit pool: what streaming one block of one KV head costs an SM beside a full prefill, in
 // the units of kTileCost (0.1 us).
 constexpr int64_t kStream8CostNum = 3, kStream8CostDen = 4;
+// Blocks a warp up to which the split-KV work beside a smaller prefill is short.
+constexpr int64_t kShort8BlocksPerWarp = 20;
 
 // The planner's working arrays, kept per host thread so a plan allocates
 // nothing once a thread has planned a step of that size.
@@ -593,11 +595,13 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   // (agent-shaped step, same box: 146.5 -> 144.3 us; 2/3 and 2/5 of the slots
   // in between, a quarter 149.7).  A smaller prefill leaves SMs free from the
   // start and keeps every slot.
-  int32_t stream_sms = 0;  // SMs that a full prefill leaves to the split-KV kernel
+  int32_t stream_sms = 0;     // SMs that a full prefill leaves to the split-KV kernel
+  int64_t whole_room = avail;  // warp slots for whole segments (below)
   if (!pairs.empty()) {
-    int64_t pf_tiles = 0, pf_cost = 0;
+    int64_t pf_tiles = 0, pf_cost = 0, pf_subs = (int64_t)casc_items.size();
     for (const auto &nt : pair_nt) {
       pf_tiles += nt[0] + nt[1];
+      pf_subs += (nt[0] > 0) + (nt[1] > 0);
       pf_cost += kPassStartCost * ((nt[0] > 0) + (nt[1] > 0)) + kTileCost * (nt[0] + nt[1]);
     }
     for (const PrefillTile &t : casc_items) pf_cost += kPassStartCost + kTileCost * (t.kt1 - t.kt0);
@@ -618,8 +622,21 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
         const int64_t most = (nw64 + warps_per_sm - 1) / warps_per_sm;
         stream_sms = (int32_t)std::min<int64_t>((std::min(x, most) + 1) / 2 * 2, pf_sms - 1);
         nw64 = std::min<int64_t>(nw64, (int64_t)stream_sms * warps_per_sm);
+        whole_room = 0;
       } else {
         nw64 = std::min<int64_t>(nw64, std::max<int64_t>(1, avail / 2));
+      }
+    } else if (f8 && n_pairs == 0) {
+      // A smaller prefill leaves SMs free.  The warps that find one start at once, the
+      // others 10 us later: a short stream goes to the first alone (32 heads: 16 decodes
+      // of 500 to 4000 keys beside a 64-token prompt 35.9 -> 30.2 us, 8 beside 256 tokens
+      // 32.1 -> 29.3), a long one takes every SM (64 beside 128 tokens, 38 blocks a warp
+      // on the free SMs: 80.0 us, 86.9 there alone).
+      const int64_t free_slots =
+          (pf_sms - std::max<int64_t>(pf_tiles / kMinTilesPerCta, pf_subs)) * warps_per_sm;
+      if (free_slots > 0 && total_blocks <= kShort8BlocksPerWarp * free_slots) {
+        nw64 = std::min<int64_t>(nw64, free_slots);
+        whole_room = free_slots;
       }
     }
   }
@@ -639,7 +656,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   int32_t max_seg = 0;
   for (const Segment &g : segs) max_seg = std::max(max_seg, g.nb);
   const bool whole_segments =
-      !segs.empty() && stream_sms == 0 && (int64_t)segs.size() <= avail &&
+      !segs.empty() && (int64_t)segs.size() <= whole_room &&
       max_seg <= std::max<int64_t>(2 * kMinBlocksPerWarp,
                                    (total_blocks + avail - 1) / avail + kMinBlocksPerWarp);
   if (whole_segments) nw64 = (int64_t)segs.size();

@@ -163,6 +163,18 @@ def test_full_prefill_leaves_sms_to_the_split_kv_work(lib, decodes, chunk, ctx):
     assert plan(0, fp8=True).num_prefill_ctas == 152
 
 
+@pytest.mark.parametrize("decodes,ctx,beside", [(16, 2000, True), (8, 100, True), (64, 4000, False)])
+def test_short_stream_stays_on_the_sms_a_small_prefill_leaves(lib, decodes, ctx, beside):
+    """8-bit pool: the split-KV warps beside a 64-token prompt all find a free SM, unless
+    the stream is long."""
+    cu = np.concatenate([[0], np.cumsum([1] * decodes + [64])])
+    cl = [ctx] * decodes + [64]
+    info = pkv.plan_step(cu, cl, 32, pkv.PoolDesc(sum(cl) // 16 + len(cl), 16, 8, 128),
+                         num_sms=152, upload=False, fp8=True)[0]
+    assert info.num_prefill_ctas == 32
+    assert (info.num_decode_warps <= 16 * (152 - 32)) == beside
+
+
 def test_stage_refusals(lib):
     meta = workloads.build_step("s", 1, [70, 1], [70, 40], 4, 2, 64)
     info, host = plan_of(meta)
