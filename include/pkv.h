@@ -461,8 +461,9 @@ PKV_API pkv_status pkv_paged_varlen_attention(const void *q, const int32_t *cu_q
 
 /*
  * pkv_plan_step_ex with the work cut for the kernels of an 8-bit pool (more
- * split-KV warps an SM).  The plan serves a bf16 pool too, as any other plan
- * serves an 8-bit pool: only the division of the work differs.
+ * split-KV warps an SM; beside a prefill they get SMs of their own).  The plan
+ * serves a bf16 pool too, as any other plan serves an 8-bit pool: only the
+ * division of the work differs, and with it the time.
  */
 PKV_API pkv_status pkv_plan_step_fp8(const int32_t *cu_q_lens, const int32_t *context_lens,
                                      int32_t num_seqs, int32_t num_q_heads,
