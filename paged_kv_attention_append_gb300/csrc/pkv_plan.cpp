@@ -340,7 +340,13 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     }
     // windows only while one chunk each leaves half the warp slots to the rest
     // (else the shared items alone would take more than a wave)
-    if (kSharedRowGroups * window_items * 2 > (int64_t)num_sms * warps_per_sm)
+    // 8-bit pool: nor beside a prefill for every SM, where the row groups stream on SMs of
+    // their own (8 windows of 8 tokens x 4 heads beside 2048 tokens: 172 -> 150 us, beside
+    // 1024 75 -> 48)
+    int64_t pf_tiles = 0;
+    for (const auto &nt : pair_nt) pf_tiles += nt[0] + nt[1];
+    if (kSharedRowGroups * window_items * 2 > (int64_t)num_sms * warps_per_sm ||
+        (f8 && pf_tiles >= (int64_t)num_sms * kMinTilesPerCta))
       streams.resize(n_group_streams);
     for (size_t i = n_group_streams; i < streams.size(); ++i)
       for (int32_t u : streams[i].units) unit_kb0[u] = streams[i].len;
@@ -615,9 +621,14 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
         // and 186 beside it; 4096 tokens at 16384 with 64: 931 and 734.  A block's cost
         // taken as 2/3, 5/6 and 1: 185, 185, 198 with 32 decodes, 750, 748, 755 with 64.
         // Spread evenly over the grid, the same SMs took 233 and 871.
-        const int64_t stream =
-            kStream8CostNum * total_blocks * (max_rows <= kDecode8SmallRows ? 1 : 2);
-        const int64_t all = stream + kStream8CostDen * pf_cost;
+        // Blocks of row groups of more than 8 rows count half as much again (8 windows of 8
+        // tokens x 4 heads: 150 us, 161 at twice, 151 at the same; 32 of them with 4096
+        // tokens at 16384: 767, 808, 862).
+        int64_t stream = 0;
+        for (const Segment &g : segs)
+          stream += (int64_t)g.nb * (g.n_q * group > kDecode8SmallRows ? 3 : 2);
+        stream *= kStream8CostNum;
+        const int64_t all = stream + 2 * kStream8CostDen * pf_cost;
         const int64_t x = (stream * pf_sms + all - 1) / all;
         const int64_t most = (nw64 + warps_per_sm - 1) / warps_per_sm;
         stream_sms = (int32_t)std::min<int64_t>((std::min(x, most) + 1) / 2 * 2, pf_sms - 1);

@@ -305,7 +305,7 @@ def test_wrong_staging_array_is_reported(pkv, cuda_device, stage):
     check_attention(out[:1].cpu(), *(x[:1] for x in want), 200, tensor_cores=False, scales=scales)
 
 
-@pytest.mark.parametrize("q_lens", [[1] * 6, [1], [3, 2, 4], [1] * 40])
+@pytest.mark.parametrize("q_lens", [[1] * 6, [1], [3, 2, 4], [1] * 40, [8, 1, 8, 5]])
 @pytest.mark.parametrize("sms", [3, 4, 9])
 def test_split_kv_beside_a_full_prefill(pkv, cuda_device, q_lens, sms):
     """The tensor-core kernel takes every SM that the plan does not leave to the split-KV
