@@ -1,0 +1,136 @@
+"""GPU tests of the rotating append and the 8-bit pool at their edges: codes compared
+byte for byte with a rounding of its own, scales of blocks past the context, stored
+scales that are none, padding, staging arrays that do not fit, large copies.
+
+The append's arithmetic is defined in fp32 with every operation rounded, so its codes
+and scales have no tolerance.  Attention is compared with tests/fp8_ref.py within
+the bounds that test_fp8_rope_gpu.py derives, or bit for bit with a second call.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+import workloads
+from fp8_bytes import E4M3, append_bytes, value_of
+from test_fp8_rope_gpu import (check_attention, check_rotated, i32, make_pool, rope_inputs,
+                               status_of, values_of)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv(cuda_device):
+    import paged_kv_attention_append_gb300 as m
+    m.build()
+    return m
+
+
+# ------------------------------------------------------------------------- attention
+
+# ------------------------------------------------------------------------ 8-bit append
+
+def assert_same_codes(got, want, scales, want_scales):
+    assert np.array_equal(scales.cpu().numpy(), want_scales)
+    g = got.cpu().view(torch.uint8).numpy()
+    nan = (want & 127) == 127
+    assert np.array_equal(nan, (g & 127) == 127)
+    assert np.array_equal(g[~nan], want[~nan])
+
+
+def grid_rows(d, scale):
+    """Rows whose values over `scale` are e4m3 midpoints (ties of either parity), codes'
+    own values, values just past half the smallest step and just below powers of two."""
+    mid = (E4M3[1:] + E4M3[:-1]) / 2
+    x = np.concatenate([[448.0], mid, E4M3, 2.0 ** -10 * np.array([1, 1.0078125, 0.9921875]),
+                        np.exp2(np.arange(-8, 9.0)) * 0.99609375, [446.0]])
+    x = np.concatenate([x, -x]) * scale
+    x = np.concatenate([x, np.zeros(-len(x) % d)]).reshape(-1, d)
+    return x
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -64, 2.0 ** 40, 2.0 ** -7])
+def test_codes_of_ties_and_borders(pkv, cuda_device, d, scale):
+    """New rows on the borders between two codes, into new blocks; then a larger row in
+    each block, so that every code is re-expressed, ties in e4m3's subnormals among them."""
+    dev = cuda_device
+    x = grid_rows(d, scale)
+    x = np.concatenate([x] + [x * 2.0 ** -k for k in (1, 3, 9)])
+    x[:, 0] = 448.0 * scale                        # each row alone would need this scale
+    n = len(x)
+    rows = ref.bf16(x)
+    assert np.array_equal(ref.f64(rows), x)
+    rows = rows[:, None].contiguous()
+    nb = n // 8 + 1
+    slots = np.array([t // 8 * 16 + t % 8 for t in range(n)])
+    for grow in (1.0, 2.0, 8.0, 512.0, 2.0 ** 20):
+        pool, sc = pkv.fp8_pool(nb, 1, d, device=dev)
+        want, want_sc = np.zeros((nb, 2, 1, 16, d), np.uint8), np.ones((nb, 1, 2), np.float32)
+        r = np.stack([ref.f64(rows), -ref.f64(rows)], axis=1).astype(np.float32)
+        pkv.paged_kv_append_fp8(rows.to(dev), -rows.to(dev), i32(slots, dev), pool, sc)
+        want, want_sc = append_bytes(want, want_sc, r, slots.tolist())
+        assert_same_codes(pool, want, sc, want_sc)
+        big = ref.bf16(np.full((nb, 1, d), 448.0 * scale * grow))
+        pkv.paged_kv_append_fp8(big.to(dev), big.to(dev), i32(np.arange(nb) * 16 + 9, dev), pool, sc)
+        r = np.repeat(ref.f64(big)[:, None], 2, axis=1).astype(np.float32)
+        want, want_sc = append_bytes(want, want_sc, r, (np.arange(nb) * 16 + 9).tolist())
+        assert_same_codes(pool, want, sc, want_sc)
+
+
+@pytest.mark.parametrize("kind", ["pow2", "any"])
+@pytest.mark.parametrize("size", [1e-4, 1.0, 3e3])
+@pytest.mark.parametrize("rot,inter,d", [(0, False, 128), (128, False, 128), (32, True, 64),
+                                         (48, False, 64)])
+def test_codes_of_random_rows(pkv, cuda_device, kind, size, rot, inter, d):
+    """Runs of tokens that start anywhere in a block, new rows of sizes spread over 2^16
+    a row: codes, scales and untouched rows to the byte."""
+    dev = cuda_device
+    rng = np.random.default_rng(960 + rot)
+    slots, b = [], 0
+    while len(slots) < 300:
+        off = int(rng.integers(0, 16))
+        slots += list(range(b * 16 + off, b * 16 + off + int(rng.integers(1, 40))))
+        b = slots[-1] // 16 + 1
+    nb, n, hkv = b, len(slots), 3
+    perm = rng.permutation(nb)
+    slots = [int(perm[s // 16]) * 16 + s % 16 for s in slots]
+    x = rng.standard_normal((n, 2 + 2 * hkv, d)) * np.exp2(rng.uniform(-8, 8, (n, 2 + 2 * hkv, 1)))
+    xb = ref.bf16(x * size)
+    q, k, v = xb[:, :2], xb[:, 2:2 + hkv], xb[:, 2 + hkv:]
+    before, sc = make_pool(rng, nb, hkv, d, kind)
+    pool, scd, st = before.to(dev), sc.to(dev), status_of(dev)
+    kr = ref.f64(k).astype(np.float32)
+    if rot:
+        cs = ref.table(3000, rot)
+        pos = rng.integers(0, 3000, size=n)
+        xd = xb.to(dev)
+        out = pkv.rope_kv_append_fp8(xd[:, :2], xd[:, 2:2 + hkv], xd[:, 2 + hkv:], i32(pos, dev),
+                                     torch.from_numpy(cs).to(dev), i32(slots, dev), pool, scd,
+                                     interleaved=inter, dev_status=st)
+        check_rotated(out, q, pos, cs, inter)
+        kr = ref.rotate(ref.f64(k), pos, cs, inter, np.float32)[0]
+    else:
+        pkv.paged_kv_append_fp8(k.contiguous().to(dev), v.contiguous().to(dev), i32(slots, dev), pool,
+                                scd, dev_status=st)
+    assert int(st.item()) == 0
+    rows = np.stack([kr, ref.f64(v).astype(np.float32)], axis=1)
+    want = append_bytes(before.view(torch.uint8).numpy(), sc.numpy(), rows, slots)
+    assert_same_codes(pool, want[0], scd, want[1])
+
+
+def test_token_by_token_to_the_byte(pkv, cuda_device):
+    """A block filled one token at a time, its scales growing on the way: the bytes that
+    the defined sequence of re-expressions gives."""
+    dev = cuda_device
+    rng = np.random.default_rng(970)
+    k = ref.bf16(rng.standard_normal((16, 2, 128)) * np.exp2(np.arange(16) / 2)[:, None, None])
+    pool, sc = pkv.fp8_pool(2, 2, 128, device=dev)
+    want, want_sc = np.zeros((2, 2, 2, 16, 128), np.uint8), np.ones((2, 2, 2), np.float32)
+    rows = np.repeat(ref.f64(k)[:, None], 2, axis=1).astype(np.float32)
+    for t in range(16):
+        kt = k[t:t + 1].to(dev)
+        pkv.paged_kv_append_fp8(kt, kt, i32([t], dev), pool, sc)
+        want, want_sc = append_bytes(want, want_sc, rows[t:t + 1], [t])
+        assert_same_codes(pool, want, sc, want_sc)
