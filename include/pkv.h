@@ -517,7 +517,8 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
  *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the
  *   weights to bf16, 2^-8.  Accumulation is fp32; out is rounded once to bf16.
  *   Bytes of a block past its sequence's context are never used, whatever they
- *   hold.  A NaN stored in a visible row reaches every row of out that sees it,
+ *   hold, nor are the scales of a block that lies past it altogether (one that a
+ *   chained plan's later steps will fill).  A NaN stored in a visible row reaches every row of out that sees it,
  *   and may reach rows of the same sequence's step that come before it.
  * Kernel order, early launches and errors as pkv_paged_varlen_attention (block
  * ids are read from the device tables); kv_scales is read after the wait for the

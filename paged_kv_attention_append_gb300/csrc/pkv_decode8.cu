@@ -398,17 +398,20 @@ struct Ring {
       mbar_arrive(bar);
     }
   }
-  // what the consumers read of a stage once its barrier completed
+  // what the consumers read of a stage once its barrier completed: n >= 1 of its blocks
+  // (from logical block kb on) hold keys of the row group's sequence
   __device__ __forceinline__ float4 scale_of(int stage, int n, int kb, int (&p0)[kPair]) const {
     const uint4 v = lds128(scales + stage * kPair * 8);
     float4 sc = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                             __uint_as_float(v.w));
     const int2 ok = *reinterpret_cast<const int2 *>(flags + stage * kPair);
     p0[0] = ok.x ? kb * kBlockSize : kNoBlock;
-    p0[1] = n > 1 && ok.y ? (kb + 1) * kBlockSize : kNoBlock;
-    // a block that is not there weighs nothing, and its scales are not looked at
+    const bool second = n > 1 && ok.y;
+    p0[1] = second ? (kb + 1) * kBlockSize : kNoBlock;
+    // a block that is not there, or that a later step of a chain will fill, weighs nothing,
+    // and its scales (which may hold anything) are not looked at
     if (!ok.x) sc.x = 1.f, sc.y = 0.f;
-    if (!ok.y) sc.z = 1.f, sc.w = 0.f;
+    if (!second) sc.z = 1.f, sc.w = 0.f;
     return sc;
   }
 };
@@ -545,9 +548,11 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
         return;
       }
       ++done;
-      if (mine) {
+      // blocks with keys of the sequence: a chain's plan holds some past its context
+      const int n = min(c_kb1, (ctx + kBlockSize - 1) / kBlockSize) - kb;
+      if (mine && n > 0) {
         int p0[kPair];
-        const float4 sc = ring.scale_of(s, min(kPair, c_kb1 - kb), kb, p0);
+        const float4 sc = ring.scale_of(s, n, kb, p0);
         attend_pair<D, NT>(ring.base + s * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
       }
       __syncwarp();
@@ -756,9 +761,11 @@ __global__ void __launch_bounds__(kThreads, (Decode8Cfg<D, MAXT>::kCtas))
           // piece is used or written
           head_bad = __any_sync(0xffffffffu, bad);
         }
-        if (valid && !head_bad) {
+        // blocks with keys of the sequence: a chain's plan holds some past its context
+        const int n = min(pc.kb_end, (ctx + kBlockSize - 1) / kBlockSize) - kb;
+        if (valid && !head_bad && n > 0) {
           int p0[kPair];
-          const float4 sc = ring.scale_of(stage, min(kPair, pc.kb_end - kb), kb, p0);
+          const float4 sc = ring.scale_of(stage, n, kb, p0);
           attend_pair<D, NT>(ring.base + stage * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
         }
         __syncwarp();

@@ -29,6 +29,47 @@ def pkv(cuda_device):
 
 # ------------------------------------------------------------------------- attention
 
+CHAINS = [  # (q_lens, ctx_lens, steps, hkv, group, d): blocks past the context in the plan
+    ([1, 1, 1, 1], [15, 16, 40, 300], 20, 2, 4, 128),
+    ([1, 1], [31, 700], 40, 1, 8, 64),
+    ([4, 6, 2], [64, 300, 30], 7, 2, 4, 128),        # windows of two row groups share blocks
+    ([3, 1], [160, 47], 9, 2, 5, 64),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CHAINS)))
+@pytest.mark.parametrize("past", [float("nan"), float("inf"), -1.0, 2.0 ** 90])
+@pytest.mark.parametrize("sms", [1, 152])
+def test_scales_past_the_context_do_not_matter(pkv, cuda_device, case, past, sms):
+    """A chain's plan covers blocks that later steps fill.  Until then neither their bytes
+    nor their scales count: the first step gives the bits it gives with small scales there."""
+    ql, ctx, steps, hkv, group, d = CHAINS[case]
+    dev = cuda_device
+    rng = np.random.default_rng(900 + case)
+    last = [c + n * (steps - 1) for n, c in zip(ql, ctx)]
+    meta = workloads.build_step("chain", 90 + case, ql, last, hkv * group, hkv, d, rng=rng)
+    codes, scales = make_pool(rng, meta.num_blocks, hkv, d)
+    q = ref.bf16(rng.standard_normal((meta.total_q, hkv * group, d)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    later = [int(b) for s, c in enumerate(ctx) for b in meta.block_tables[s, -(-c // 16):] if b >= 0]
+    assert later
+    outs = []
+    for s in (2.0 ** -30, past):
+        raw, sc = codes.clone().view(torch.uint8), scales.clone()
+        raw[later] = 0 if s == 2.0 ** -30 else 0x7F
+        sc[later] = s
+        pool, st = raw.to(dev).view(torch.float8_e4m3fn), status_of(dev)
+        plan = pkv.plan_step(meta.cu_q_lens, ctx, hkv * group, pool, num_sms=sms, chain_steps=steps,
+                             block_tables=meta.block_tables, fp8=True)
+        outs.append(pkv.paged_varlen_attention_fp8(
+            q.to(dev), meta.cu_q_lens, i32(ctx, dev), meta.block_tables, pool, sc.to(dev),
+            meta.scale, plan=plan, dev_status=st).cpu())
+        assert int(st.item()) == 0
+    check_attention(outs[0], *want, max(ctx), tensor_cores=False, scales=scales)
+    assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+
+
 # ------------------------------------------------------------------------ 8-bit append
 
 def assert_same_codes(got, want, scales, want_scales):
