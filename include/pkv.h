@@ -247,9 +247,11 @@ PKV_API pkv_status pkv_rope_kv_append(const void *q, int64_t q_stride, const voi
  * among them:
  *   - rows below `first` are kept rows (the block is filled in order); when
  *     first is 0 the block is new, and its old scale and bytes do not matter;
- *   - the scale s stays when first > 0 and 448 s >= max |N|; otherwise it becomes
- *     the smallest power of two s' >= 2^-64 with 448 s' >= max |N| (infinities
- *     are left out of the maximum) and each kept value c becomes c s / s';
+ *   - the scale s stays when first > 0, s > 0 and 448 s >= max |N|; otherwise it
+ *     becomes the smallest power of two s' >= 2^-64 with 448 s' >= max |N|
+ *     (infinities and NaN are left out of the maximum) and each kept value c
+ *     becomes c s / s'.  A stored s that is not positive and finite counts as 0:
+ *     the rows kept under it become zeros;
  *   - the new rows are stored as x / scale.
  *   Both are evaluated in fp32 (exactly, when the scales are powers of two), rounded
  *   to nearest even and saturate at +-448; NaN stays NaN.  Rows

@@ -15,9 +15,10 @@
 // new rows and `first` the smallest offset among them, rows below `first` are
 // kept rows of the same sequence (a sequence fills its blocks in order), rows
 // from `first` on that are not in N are stale.
-//   s' = s when first > 0 and 448 s >= max |N|, else the smallest power of two
+//   s' = s when first > 0, s > 0 and 448 s >= max |N|, else the smallest power of two
 //        >= 2^-64 with 448 s' >= max |N|
-//   new rows: rn_sat(x / s');   kept rows, when s' != s: rn(c s / s').
+//   new rows: rn_sat(x / s');   kept rows, when s' != s: rn(c s / s'), an s that is not
+//   positive and finite counting as 0.
 // Powers of two make x / s' and c s / s' exact before the rounding, so a kept
 // row loses nothing but bits that fall below e4m3's smallest step.
 //
@@ -230,7 +231,7 @@ struct AppendSmem {
   int pos[kMaxTile + kWindow];
   int blk[kMaxTile], first[kMaxTile];
   uint32_t amax[kMaxTile][kMaxSlabs];
-  float scale[kMaxTile][kMaxSlabs], ratio[kMaxTile][kMaxSlabs];  // ratio 0: nothing to re-express
+  float scale[kMaxTile][kMaxSlabs], ratio[kMaxTile][kMaxSlabs];  // ratio 1: nothing to re-express
 };
 
 template <int D, bool kInter>
@@ -397,11 +398,11 @@ __device__ __forceinline__ void append_blocks(const RopeParams &p, int64_t unit,
   __syncthreads();
   if (settles) {
     const float amax = __uint_as_float(sm.amax[tg][ts]);
-    if (!(s_old <= FLT_MAX)) s_old = 0.f;  // not a scale: as if the block were new
+    if (!(s_old > 0.f && s_old <= FLT_MAX)) s_old = 0.f;  // not a scale: its rows become zeros
     const bool keep = s_old > 0.f && s_old * kE4m3Max >= amax;
     const float s_new = keep ? s_old : pow2_scale(amax);
     sm.scale[tg][ts] = s_new;
-    sm.ratio[tg][ts] = !keep && s_old > 0.f ? s_old / s_new : 0.f;
+    sm.ratio[tg][ts] = keep || sm.first[tg] == 0 ? 1.f : s_old / s_new;
     if (!keep) *scale_at = s_new;
   }
   __syncthreads();
@@ -446,7 +447,7 @@ __device__ __forceinline__ void append_blocks(const RopeParams &p, int64_t unit,
   for (int i = lg; i < n_groups * slabs; i += kLaneGroups) {
     const int g = i / slabs, sl = i % slabs;
     const float ratio = sm.ratio[g][sl];
-    if (ratio == 0.f) continue;
+    if (ratio == 1.f) continue;
     uint2 *at = reinterpret_cast<uint2 *>(block_of(g) + slab_off(sl)) + l;
     for (int r = 0; r < sm.first[g]; ++r, at += D / 8) {
       const uint2 w = __ldcg(at);

@@ -175,3 +175,26 @@ def test_token_by_token_to_the_byte(pkv, cuda_device):
         pkv.paged_kv_append_fp8(kt, kt, i32([t], dev), pool, sc)
         want, want_sc = append_bytes(want, want_sc, rows[t:t + 1], [t])
         assert_same_codes(pool, want, sc, want_sc)
+
+
+@pytest.mark.parametrize("stored", [0.0, -0.0, -2.0, float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("size", [0.0, 1.0])
+def test_stored_scale_that_is_none(pkv, cuda_device, stored, size):
+    """Kept rows under a scale that is not positive and finite stand for nothing: they
+    become zeros of the new scale (NaN codes stay NaN), which is a proper one."""
+    dev = cuda_device
+    rng = np.random.default_rng(980)
+    before, sc = make_pool(rng, 3, 2, 64)
+    before.view(torch.uint8)[0, 0, 0, 1, 5] = 0x7F
+    sc[0] = stored
+    sc[1, 1, 0] = stored
+    pool, scd, st = before.to(dev), sc.to(dev), status_of(dev)
+    k = ref.bf16(size * rng.standard_normal((3, 2, 64)))
+    slots = [4, 16 + 7, 32]
+    pkv.paged_kv_append_fp8(k.to(dev), k.to(dev), i32(slots, dev), pool, scd, dev_status=st)
+    assert int(st.item()) == 0
+    rows = np.repeat(ref.f64(k)[:, None], 2, axis=1).astype(np.float32)
+    want = append_bytes(before.view(torch.uint8).numpy(), sc.numpy(), rows, slots)
+    assert np.array_equal(value_of(want[0][0, :, :, :4])[~np.isnan(value_of(want[0][0, :, :, :4]))] == 0,
+                          np.ones(2 * 2 * 4 * 64 - 1, bool))
+    assert_same_codes(pool, want[0], scd, want[1])
