@@ -212,8 +212,10 @@ typedef struct pkv_rope {
  *   rotated k and v as pkv_paged_kv_append writes them:
  *     slot < 0                 : no k or v written (q is rotated all the same);
  *     slot >= num_blocks*bs    : k and v skipped, PKV_DEV_BAD_SLOT to *dev_status;
- *     p < 0                    : padding: nothing of the token is read or written;
- *     p >= max_positions       : the token skipped, PKV_DEV_BAD_POSITION.
+ *     p < 0                    : padding: nothing of the token is read or written,
+ *                                and its slot may be anything;
+ *     p >= max_positions       : the token skipped, PKV_DEV_BAD_POSITION (whatever
+ *                                its slot).
  *   q: device bf16 [num_tokens][num_q_heads][D], k, v: [num_tokens][Hkv][D], the
  *   heads of a token contiguous, consecutive tokens q_stride, k_stride, v_stride
  *   elements apart (>= heads * D, a multiple of 8), so the three may be parts of

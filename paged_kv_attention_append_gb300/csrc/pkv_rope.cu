@@ -178,8 +178,11 @@ __device__ __forceinline__ void token_rows(const RopeParams &p, int64_t unit, in
   const int64_t slot = kPool ? __ldg(p.slots + t) : -1;
   const bool bad_pos = pos >= p.max_pos;
   if (ch == 0 && lane == 0) {
-    if (bad_pos) report(p.dev_status, PKV_DEV_BAD_POSITION);
-    if (kPool && slot >= (int64_t)p.num_blocks * kBlockSize) report(p.dev_status, PKV_DEV_BAD_SLOT);
+    // a skipped token's slot is not looked at: padding (pos < 0) may hold any
+    if (bad_pos)
+      report(p.dev_status, PKV_DEV_BAD_POSITION);
+    else if (kPool && pos >= 0 && slot >= (int64_t)p.num_blocks * kBlockSize)
+      report(p.dev_status, PKV_DEV_BAD_SLOT);
   }
   if (pos < 0 || bad_pos) return;
   const bool put = kPool && slot >= 0 && slot < (int64_t)p.num_blocks * kBlockSize;
@@ -257,7 +260,9 @@ __device__ __forceinline__ void append_blocks(const RopeParams &p, int64_t unit,
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool bad_slot = slot[i] >= nslots, bad_pos = p.rot > 0 && pos[i] >= p.max_pos;
+      const bool bad_pos = p.rot > 0 && pos[i] >= p.max_pos;
+      // (a skipped token's slot is not looked at: padding may hold any)
+      const bool bad_slot = !bad_pos && pos[i] >= 0 && slot[i] >= nslots;
       if (i == 1 && lane < p.tile && h0 == 0) {
         if (bad_slot) report(p.dev_status, PKV_DEV_BAD_SLOT);
         if (bad_pos) report(p.dev_status, PKV_DEV_BAD_POSITION);

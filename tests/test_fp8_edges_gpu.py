@@ -198,3 +198,53 @@ def test_stored_scale_that_is_none(pkv, cuda_device, stored, size):
     assert np.array_equal(value_of(want[0][0, :, :, :4])[~np.isnan(value_of(want[0][0, :, :, :4]))] == 0,
                           np.ones(2 * 2 * 4 * 64 - 1, bool))
     assert_same_codes(pool, want[0], scd, want[1])
+
+
+# ---------------------------------------------------------------------------- padding
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_padding_by_position_alone(pkv, cuda_device, fp8):
+    """A token at a negative position is padding whatever its slot holds: no status, and
+    nothing written.  At a position past the table the position is what is reported."""
+    dev = cuda_device
+    rng = np.random.default_rng(990)
+    n, hq, hkv, d, nb = 40, 4, 2, 64, 4
+    (q, k, v), (qd, kd, vd) = rope_inputs(rng, n, hq, hkv, d, True, dev)
+    cs = ref.table(100, d)
+    pos = rng.integers(0, 100, size=n)
+    slots = np.arange(n)
+    pad = np.array([1, 17, 30, 39])
+    pos[pad] = [-1, -7, -1, -2 ** 31]
+    slots[pad] = [nb * 16, 2 ** 31 - 1, 5, -1]
+    before, sc = make_pool(rng, nb, hkv, d)
+    if not fp8:
+        before = ref.bf16(rng.standard_normal((nb, 2, hkv, 16, d)))
+    for late in (False, True):
+        p, s = pos.copy(), slots.copy()
+        if late:
+            p[20], s[20] = 100, nb * 16 + 3       # both wrong: the position is reported
+        pool, scd, st = before.to(dev), sc.to(dev), status_of(dev)
+        q_out = torch.full((n, hq, d), 3.0, dtype=torch.bfloat16, device=dev)
+        args = (qd, kd, vd, i32(p, dev), torch.from_numpy(cs).to(dev), i32(s, dev), pool)
+        if fp8:
+            pkv.rope_kv_append_fp8(*args, scd, q_out=q_out, dev_status=st)
+        else:
+            pkv.rope_kv_append(*args, q_out=q_out, dev_status=st)
+        assert int(st.item()) == (5 if late else 0)
+        out = [20] if late else []
+        skipped = np.array(sorted(pad.tolist() + out))
+        rows = np.array([t for t in range(n) if t not in skipped])
+        assert bool((q_out[skipped] == 3.0).all())
+        check_rotated(q_out, q, np.clip(p, 0, 99), cs, False, rows)
+        kr = ref.rotate(ref.f64(k), np.clip(p, 0, 99), cs, False, np.float32)[0]
+        if fp8:
+            r = np.stack([kr, ref.f64(v).astype(np.float32)], axis=1)
+            live = [int(x) if t in rows else -1 for t, x in enumerate(s)]
+            want = append_bytes(before.view(torch.uint8).numpy(), sc.numpy(), r, live)
+            assert_same_codes(pool, want[0], scd, want[1])
+        else:
+            want = before.clone()
+            for t in rows:
+                want[s[t] // 16, 0, :, s[t] % 16] = ref.bf16(kr[t])
+                want[s[t] // 16, 1, :, s[t] % 16] = v[t]
+            assert torch.equal(pool.cpu().view(torch.int16), want.view(torch.int16))
