@@ -225,7 +225,11 @@ __device__ __forceinline__ void attend_pair(uint32_t stage, const float4 sc, con
         for (int j = 0; j < 4; ++j)
           if (p0[b] + key0 + (j & 2) > rows.lim[t][j & 1]) s[b][t][j] = -INFINITY;
   }
-  const float vmax = fmaxf(sc.y, sc.w);
+  // A block past the context (not there, or one that a later step of a chain will fill)
+  // weighs nothing, and its V scale, which may hold anything, is not looked at.  Its K
+  // scale needs no care: a masked -inf times any f > 0 below stays -inf.
+  const float vs[kPair] = {p0[0] < ctx ? sc.y : 0.f, p0[1] < ctx ? sc.w : 0.f};
+  const float vmax = fmaxf(vs[0], vs[1]);
   float down = 1.f;
   if (vmax > rows.vref) {  // the same in every lane
     down = rows.vref / vmax;
@@ -263,7 +267,7 @@ __device__ __forceinline__ void attend_pair(uint32_t stage, const float4 sc, con
     const uint64_t nb = f2_pack(nbase[0], nbase[1]);
 #pragma unroll
     for (int b = 0; b < kPair; ++b) {
-      const float g = (b ? sc.w : sc.y) * rows.inv_vref * kUScale;
+      const float g = vs[b] * rows.inv_vref * kUScale;
       const uint64_t fb = f2_pack(f[b][0], f[b][1]);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -398,20 +402,15 @@ struct Ring {
       mbar_arrive(bar);
     }
   }
-  // what the consumers read of a stage once its barrier completed: n >= 1 of its blocks
-  // (from logical block kb on) hold keys of the row group's sequence
+  // what the consumers read of a stage once its barrier completed; the scales of a block
+  // that is not there (kNoBlock) may be anything
   __device__ __forceinline__ float4 scale_of(int stage, int n, int kb, int (&p0)[kPair]) const {
     const uint4 v = lds128(scales + stage * kPair * 8);
-    float4 sc = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+    const float4 sc = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                             __uint_as_float(v.w));
     const int2 ok = *reinterpret_cast<const int2 *>(flags + stage * kPair);
     p0[0] = ok.x ? kb * kBlockSize : kNoBlock;
-    const bool second = n > 1 && ok.y;
-    p0[1] = second ? (kb + 1) * kBlockSize : kNoBlock;
-    // a block that is not there, or that a later step of a chain will fill, weighs nothing,
-    // and its scales (which may hold anything) are not looked at
-    if (!ok.x) sc.x = 1.f, sc.y = 0.f;
-    if (!second) sc.z = 1.f, sc.w = 0.f;
+    p0[1] = n > 1 && ok.y ? (kb + 1) * kBlockSize : kNoBlock;
     return sc;
   }
 };
@@ -548,11 +547,9 @@ __device__ __forceinline__ void shared_cta8(const CUtensorMap &pool_map, const D
         return;
       }
       ++done;
-      // blocks with keys of the sequence: a chain's plan holds some past its context
-      const int n = min(c_kb1, (ctx + kBlockSize - 1) / kBlockSize) - kb;
-      if (mine && n > 0) {
+      if (mine) {
         int p0[kPair];
-        const float4 sc = ring.scale_of(s, n, kb, p0);
+        const float4 sc = ring.scale_of(s, min(kPair, c_kb1 - kb), kb, p0);
         attend_pair<D, NT>(ring.base + s * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
       }
       __syncwarp();
@@ -761,11 +758,9 @@ __global__ void __launch_bounds__(kThreads, (Decode8Cfg<D, MAXT>::kCtas))
           // piece is used or written
           head_bad = __any_sync(0xffffffffu, bad);
         }
-        // blocks with keys of the sequence: a chain's plan holds some past its context
-        const int n = min(pc.kb_end, (ctx + kBlockSize - 1) / kBlockSize) - kb;
-        if (valid && !head_bad && n > 0) {
+        if (valid && !head_bad) {
           int p0[kPair];
-          const float4 sc = ring.scale_of(stage, n, kb, p0);
+          const float4 sc = ring.scale_of(stage, min(kPair, pc.kb_end - kb), kb, p0);
           attend_pair<D, NT>(ring.base + stage * C::kStageBytes, sc, p0, q_pos0, ctx, lane, rows);
         }
         __syncwarp();
