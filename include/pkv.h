@@ -515,7 +515,9 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
  *   fp8, stage_begin: the summary pkv_plan_stage_fp8 wrote, and a DEVICE copy of
  *   its array.  workspace_bytes: at least fp8->workspace_bytes; a workspace serves one
  *   call at a time (calls that may overlap need one each).  A row group with
- *   more than fp8->max_rows rows is reported (PKV_DEV_PLAN_MISMATCH), not attended.
+ *   more than fp8->max_rows rows, and tensor-core rows whose sequence stage_begin
+ *   does not give all the copies they read, are reported (PKV_DEV_PLAN_MISMATCH)
+ *   and not attended: their rows of out are left as they were.
  *   Rounding: on the split-KV kernel every stored value enters the products
  *   exactly (fp16), the weights are rounded to fp16, 2^-11; on the tensor-core
  *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the

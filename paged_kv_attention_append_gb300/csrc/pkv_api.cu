@@ -210,6 +210,7 @@ static pkv_status attention(const void *q, const int32_t *cu_q_lens, const int32
   a.gather_rows = reinterpret_cast<const GatherRow *>(pb + off.gather);
   a.num_gather_rows = info->num_gather_rows;
   a.num_partials = info->num_partials;
+  a.num_prefill_partials = info->num_prefill_partials;
   a.num_prefill_tiles = info->num_prefill_tiles;
   a.num_prefill_ctas = info->num_prefill_ctas;
   if (info->num_prefill_merges < 0 || info->num_prefill_merges > info->num_merge_groups ||

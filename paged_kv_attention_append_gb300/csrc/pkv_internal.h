@@ -244,6 +244,7 @@ struct AttnArgs {
   const GatherRow *gather_rows;
   int32_t num_gather_rows;
   int32_t num_partials;       // decode partial slots (gathered sub-tiles write into them)
+  int32_t num_prefill_partials;  // partial slots of sub-tiles cut along keys
   int32_t num_prefill_tiles;
   int32_t num_prefill_ctas;
   float *part_o;

@@ -154,6 +154,7 @@ struct PrefillParams {
   // whole key tile one box of kv_map; the block tables are not read.  (An instance of its
   // own: with the choice made at run time the bf16 pool's steps took 3.5 % longer.)
   const int32_t *stage_begin;
+  int32_t num_pparts;  // slots of ppart_o
 };
 
 
@@ -191,9 +192,11 @@ struct ItemMeta {
   int nt[2];  // key tiles sub-tile x runs in this item, from t.kt0 (0 when absent)
   int nkt;    // key tiles loaded: t.kt0 .. t.kt1-1
   bool gathered;  // both present sub-tiles are gathered (else both contiguous)
+  int stage0;     // kCopies: the copy of the sequence's block 0
   bool ok;
 };
 
+template <bool kCopies>
 __device__ __forceinline__ ItemMeta load_item(const PrefillParams &p, int it) {
   ItemMeta m;
   m.t = p.tiles[it];
@@ -214,12 +217,19 @@ __device__ __forceinline__ ItemMeta load_item(const PrefillParams &p, int it) {
              t.hq[x] < p.num_q_heads && t.qi0[x] >= 0;
     }
   ok = ok && t.kt0 >= 0 && t.kt0 < t.kt1;
-  m.cu0 = m.qs = m.ctx = 0;
+  m.cu0 = m.qs = m.ctx = m.stage0 = 0;
   if (ok) {
     m.cu0 = __ldg(p.cu_q_lens + t.seq);
     m.qs = __ldg(p.cu_q_lens + t.seq + 1) - m.cu0;
     m.ctx = __ldg(p.context_lens + t.seq);
     ok = m.qs <= m.ctx;
+    if constexpr (kCopies) {
+      // the sequence's copies reach the item's last key tile, inside the buffer
+      m.stage0 = __ldg(p.stage_begin + t.seq);
+      const int64_t end = __ldg(p.stage_begin + t.seq + 1);
+      ok = ok && m.stage0 >= 0 && end <= p.num_blocks &&
+           m.stage0 + (int64_t)t.kt1 * kBlocksPerTile <= end;
+    }
     if (m.gathered)  // every row of the table's own sequence sees all of the item's keys
       ok = ok && (int64_t)t.kt1 * kKeysPerTile <= (int64_t)m.ctx - m.qs + 1;
     else
@@ -241,6 +251,38 @@ __device__ __forceinline__ ItemMeta load_item(const PrefillParams &p, int it) {
   m.nkt = ok ? t.kt1 - t.kt0 : 0;
   m.ok = ok;
   return m;
+}
+
+// The partial results that a skipped item would have written and the merge kernel will
+// read are marked (m = NaN), so that it writes none of their rows.  Nothing of the item
+// is taken on trust.  Not inlined: inlined, it made the code around it slower (a 2048-token
+// chunk by 1 %, the verify step on a shared prefix by 2 %).
+__device__ __noinline__ void poison_item(const PrefillTile *item, float2 *ppart_ml, int num_pparts,
+                                         float2 *dpart_ml, int num_dparts, const GatherRow *gather,
+                                         int num_gather, int group) {
+  const int lane = threadIdx.x & 31;
+  const float2 bad = make_float2(__int_as_float(0x7fc00000), 0.f);
+#pragma unroll 1
+  for (int x = 0; x < 2; ++x) {
+    const int part = item->part[x], g0 = item->gather[x], n_q = item->n_q[x];
+    if (n_q <= 0 || part < 0) continue;
+    if (g0 < 0) {
+      if (part >= num_pparts) continue;
+#pragma unroll 1
+      for (int row = lane; row < kPrefillRows; row += 32)
+        ppart_ml[(int64_t)part * kPrefillRows + row] = bad;
+    } else {
+#pragma unroll 1
+      for (int i = lane; i < n_q && g0 + (int64_t)i < num_gather; i += 32) {
+        const GatherRow gr = gather[g0 + i];
+        const int64_t slot = (int64_t)gr.part0 + part;
+        if (gr.part0 < 0 || slot >= num_dparts || gr.row0 < 0) continue;
+#pragma unroll 1
+        for (int row = gr.row0; row < min(gr.row0 + group, kRowsPerTile); ++row)
+          dpart_ml[slot * kRowsPerTile + row] = bad;
+      }
+    }
+  }
 }
 
 // Whether pass x of an item writes its output through a staging slot: a whole
@@ -405,9 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nld;
       return true;
     };
-    // the same from the copies: key tile kt of the sequence at blocks stage0 .. stage1 - 1
-    // (a tile outside them is zero-filled and reported)
-    auto load_staged = [&](int h, int stage0, int stage1, int kt) -> bool {
+    // the same from the copies: key tile kt of the sequence whose block 0 is copy stage0
+    auto load_staged = [&](int h, int stage0, int kt) -> bool {
       const int n = nld, s = n % C::kSlots;
       if (n >= C::kSlots &&
           !__all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + r * kMaxSlots + s),
@@ -417,12 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(B_FULL + r * kMaxSlots + s), C::kSlotBytes);
-        const int64_t b0 = (int64_t)stage0 + (int64_t)kt * kBlocksPerTile;
-        int g = p.pool_groups;
-        if (stage0 >= 0 && b0 + kBlocksPerTile <= stage1 && stage1 <= p.num_blocks)
-          g = ((r * hkv + h) * p.num_blocks + (int)b0) * (kBlockSize / 8);
-        else if (r == 0)
-          report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
+        const int g = ((r * hkv + h) * p.num_blocks + stage0 + kt * kBlocksPerTile) *
+                      (kBlockSize / 8);
         tma_load_4d(smem_u32(smem + C::kOffRing + (r * C::kSlots + s) * C::kSlotBytes), &kv_map, 0,
                     0, 0, g, bar(B_FULL + r * kMaxSlots + s));
       }
@@ -431,17 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     for (int it = it0; it < it1 && good; ++it) {
-      const ItemMeta m = load_item(p, it);
+      const ItemMeta m = load_item<kCopies>(p, it);
       if (!m.ok) {
         if (lane == 0 && r == 0) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
+        if constexpr (kCopies) {
+          if (r == 0) {
+            pdl_wait();  // the last reader of these partials may be the preceding kernel
+            poison_item(p.tiles + it, p.ppart_ml, p.num_pparts, p.dpart_ml, p.num_dparts, p.gather,
+                        p.num_gather, p.group);
+          }
+        }
         continue;
       }
       const int32_t *table = p.block_tables + (int64_t)m.t.seq * p.max_blocks_per_seq;
-      int stage0 = 0, stage1 = 0;
-      if constexpr (kCopies) {
-        stage0 = __ldg(p.stage_begin + m.t.seq);
-        stage1 = __ldg(p.stage_begin + m.t.seq + 1);
-      }
       const int nblk_ctx = (m.ctx + kBlockSize - 1) / kBlockSize;
       const int nblk = min(nblk_ctx, p.max_blocks_per_seq);
       // entry of block `lane` of the four tiles from relative tile 4 k on
@@ -546,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if constexpr (kCopies)
-            good = load_staged(m.t.h, stage0, stage1, m.t.kt0 + j);
+            good = load_staged(m.t.h, m.stage0, m.t.kt0 + j);
           else
             good = load_tile(m.t.h, tile_phys(j));
         }
@@ -611,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nst = 0;           // passes that staged their output (V ring indices)
       bool good = true;
       for (int it = it0; it < it1 && good; ++it) {
-        const ItemMeta m = load_item(p, it);
+        const ItemMeta m = load_item<kCopies>(p, it);
         if (!m.ok) continue;
         for (int x = 0; x < 2 && good; ++x) {
           const int ntx = x ? m.nt[1] : m.nt[0];
@@ -678,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nstaged = 0;  // passes whose output went through a staging slot
     bool good = true;
     for (int it = it0; it < it1 && good; ++it) {
-      const ItemMeta m = load_item(p, it);
+      const ItemMeta m = load_item<kCopies>(p, it);
       if (!m.ok) continue;
       for (int x = 0; x < 2 && good; ++x) {
         // per-sub-tile fields by selects (no dynamically indexed local arrays)
@@ -834,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *prow = nullptr;  // partial destination of this row, if any
         float2 *pml = nullptr;
         {
-          const ItemMeta me = load_item(p, it);
+          const ItemMeta me = load_item<kCopies>(p, it);
           out_row = me.cu0 + (x ? me.t.qi0[1] : me.t.qi0[0]) + row;
           hq = x ? me.t.hq[1] : me.t.hq[0];
           part = x ? me.t.part[1] : me.t.part[0];
@@ -1049,6 +1088,7 @@ int launch_prefill_t(const AttnArgs &a, const CUtensorMap &qmap, const CUtensorM
   p.dpart_o = a.part_o;
   p.dpart_ml = reinterpret_cast<float2 *>(a.part_ml);
   p.num_dparts = a.num_partials;
+  p.num_pparts = a.num_prefill_partials;
   p.total_q = a.total_q;
   p.dev_status = a.dev_status;
   p.num_seqs = a.num_seqs;

@@ -70,6 +70,70 @@ def test_scales_past_the_context_do_not_matter(pkv, cuda_device, case, past, sms
     assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
 
 
+STAGED = [  # (q_lens, ctx_lens, hkv, group, d, num_sms, shared blocks, sequence with copies)
+    ([1, 70], [200, 90], 2, 4, 128, None, 0, 1),             # written directly
+    ([1, 128, 200], [30, 1000, 700], 2, 2, 64, None, 0, 2),  # whole sub-tiles staged out
+    ([64, 1], [4000, 50], 1, 2, 64, 152, 0, 0),              # keys cut into many items
+    ([64], [4000], 1, 2, 128, 152, 0, 0),
+    ([1] * 20, [17 * 16 + 1 + i for i in range(20)], 2, 4, 128, 1, 17, 0),   # gathered prefix
+    ([2] * 40, [40 * 16 + 2 + i for i in range(40)], 2, 4, 64, 9, 40, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(STAGED)))
+@pytest.mark.parametrize("kind", ["none", "short", "past", "negative"])
+def test_rows_without_their_copies_are_not_written(pkv, cuda_device, case, kind):
+    """A staging array that does not give a tensor-core sequence all its copies: reported,
+    and every row that would need them stays as it was, whether it is written directly,
+    merged from parts or gathered with other sequences' rows.  The others are right."""
+    ql, ctx, hkv, group, d, sms, shared, bad = STAGED[case]
+    dev = cuda_device
+    rng = np.random.default_rng(920 + case)
+    meta = workloads.build_step("stage", 92 + case, ql, ctx, hkv * group, hkv, d, rng=rng,
+                                shared_prefix_blocks=shared)
+    codes, scales = make_pool(rng, meta.num_blocks, hkv, d)
+    q = ref.bf16(rng.standard_normal((meta.total_q, hkv * group, d)))
+    plan = pkv.plan_step(meta.cu_q_lens, ctx, hkv * group, codes.to(dev), num_sms=sms,
+                         block_tables=meta.block_tables, fp8=True)
+    begin, n = plan.stage.cpu().numpy(), plan.fp8.staged_blocks
+    assert n > 0 and begin[bad + 1] > begin[bad]
+    if kind == "none":
+        begin[bad + 1:] = begin[bad]
+    elif kind == "short":
+        begin[bad + 1:] -= 8
+    elif kind == "past":
+        begin[bad + 1:] += n
+        begin[bad] += n
+    else:
+        begin[bad] = -8
+    plan.stage = i32(begin, dev)
+    # what an earlier call may have left there: finite partial results
+    plan.workspace.view(torch.float32).fill_(1.0)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=dev)
+    st = status_of(dev)
+    pkv.paged_varlen_attention_fp8(q.to(dev), meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                                   codes.to(dev), scales.to(dev), meta.scale, plan=plan, out=out,
+                                   dev_status=st)
+    assert int(st.item()) == 4
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, meta.context_lens, meta.block_tables,
+                         values_of(codes, scales), meta.scale)
+    got = out.cpu()
+    untouched = (got == 7.0).all(dim=2).numpy()                 # [row, head]
+    if shared:
+        must = np.ones(meta.total_q, dtype=bool)
+    else:
+        must = np.zeros(meta.total_q, dtype=bool)
+        a, b = int(meta.cu_q_lens[bad]), int(meta.cu_q_lens[bad + 1])
+        must[b - 1 if kind == "short" else a:b] = True          # the last token sees every key
+    assert untouched[must].all()
+    # every row of a head holds either its result or what it held before
+    done = ~untouched
+    check_attention(got[done], *(x[done] for x in want), max(ctx), tensor_cores=True, scales=scales)
+    for s in range(0 if not shared else len(ql), len(ql)):
+        if ql[s] < 64 or (s < bad and kind in ("none", "short")):   # not touched by the change
+            assert done[int(meta.cu_q_lens[s]):int(meta.cu_q_lens[s + 1])].all()
+
+
 # ------------------------------------------------------------------------ 8-bit append
 
 def assert_same_codes(got, want, scales, want_scales):
