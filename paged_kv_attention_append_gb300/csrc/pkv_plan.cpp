@@ -103,16 +103,32 @@ constexpr int64_t kGatherMinRows = 64;
 // on one stream were no faster (32 sequences on 128 blocks 27.1 us).
 constexpr int64_t kGather8MinBlocksPerSm = 131;
 
+// 8-bit pool: the bytes of bf16 copies that a plan may ask for.  A tensor-core sequence
+// takes a copy of its whole context (64 Hkv D bytes a block), sequences with the same
+// cached blocks one each, so without a limit many chunks late in long contexts ask for
+// more than the pool holds, or than there is.  8 GiB are 2^21 keys of 8 heads of 128, 3 %
+// of the memory.  Past it the sequences with the fewest query tokens a key, which gain the
+// least from the tensor cores, go to the split-KV kernel; there a chunk of 64 tokens takes
+// five times as long (32 heads, 32 000 keys: 0.40 ms, 0.08 with copies).
+constexpr int64_t kMaxStagedBytes = (int64_t)8 << 30;
+
 // 8-bit pool: what streaming one block of one KV head costs an SM beside a full prefill, in
 // the units of kTileCost (0.1 us).
 constexpr int64_t kStream8CostNum = 3, kStream8CostDen = 4;
 // Blocks a warp up to which the split-KV work beside a smaller prefill is short.
 constexpr int64_t kShort8BlocksPerWarp = 20;
 
+// Copies of a tensor-core sequence: its context in whole key tiles.
+int64_t staged_blocks_of(int32_t ctx) {
+  return ((int64_t)ctx + kKeyTileBlocks * kBlockSize - 1) / (kKeyTileBlocks * kBlockSize) *
+         kKeyTileBlocks;
+}
+
 // The planner's working arrays, kept per host thread so a plan allocates
 // nothing once a thread has planned a step of that size.
 struct PlanScratch {
   std::vector<std::pair<int32_t, int32_t>> by_first;
+  std::vector<char> split_kv;
   std::vector<Segment> segs;
   std::vector<DUnit> dunits;
   std::vector<Piece> pieces;
@@ -178,6 +194,30 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
   std::vector<std::array<int32_t, 2>> pair_nt;   // key tiles seen by each sub-tile
   int64_t kv_tokens = 0, total_blocks = 0;
   int32_t max_nb = 0;
+  // sequences with enough query tokens for the tensor cores that go to the split-KV kernel
+  // all the same (kMaxStagedBytes), and the room for copies that the others leave
+  std::vector<char> &split_kv = S.split_kv;
+  split_kv.assign(num_seqs, 0);
+  int64_t copies_left = kMaxStagedBytes / staged_bytes(1, *desc);  // blocks
+  if (f8) {
+    std::vector<int32_t> tc_seqs;
+    for (int32_t s = 0; s < num_seqs; ++s) {
+      const int64_t qs = (int64_t)cu_q_lens[s + 1] - cu_q_lens[s];
+      if (qs < min_q_prefill || qs > context_lens[s]) continue;
+      tc_seqs.push_back(s);
+      copies_left -= staged_blocks_of(context_lens[s]);
+    }
+    if (copies_left < 0) {
+      std::stable_sort(tc_seqs.begin(), tc_seqs.end(), [&](int32_t a, int32_t b) {
+        return ((int64_t)cu_q_lens[a + 1] - cu_q_lens[a]) * context_lens[b] <
+               ((int64_t)cu_q_lens[b + 1] - cu_q_lens[b]) * context_lens[a];
+      });
+      for (size_t i = 0; i < tc_seqs.size() && copies_left < 0; ++i) {
+        split_kv[tc_seqs[i]] = 1;
+        copies_left += staged_blocks_of(context_lens[tc_seqs[i]]);
+      }
+    }
+  }
   for (int32_t s = 0; s < num_seqs; ++s) {
     int64_t qs64 = (int64_t)cu_q_lens[s + 1] - (int64_t)cu_q_lens[s];
     if (qs64 < 0) return PKV_ERR_SHAPE;
@@ -190,7 +230,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     if (ctx_plan64 > INT32_MAX - kBlockSize) return PKV_ERR_RANGE;
     const int32_t ctx_plan = (int32_t)ctx_plan64;
     max_nb = std::max(max_nb, (ctx_plan + kBlockSize - 1) / kBlockSize);
-    if (qs >= min_q_prefill) {
+    if (qs >= min_q_prefill && !split_kv[s]) {
       // units of 128 tokens x 1 query head; within one KV head, sorted by the
       // keys they see, neighbours pair up into one work item (sub-tile 0 sees
       // at least as many keys as sub-tile 1)
@@ -292,8 +332,10 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
         for (int32_t m : mem)
           streams += (cu_q_lens[m + 1] - cu_q_lens[m] + nq_tile - 1) / nq_tile;
         tc = tc && streams * len_tc * hkv * desc->head_dim >=
-                       kGather8MinBlocksPerSm * 128 * (int64_t)num_sms;
+                       kGather8MinBlocksPerSm * 128 * (int64_t)num_sms &&
+             len_tc <= copies_left;
         if (!tc) continue;
+        copies_left -= len_tc;
       }
       if (tc) len = len_tc;
       groups.push_back({mem, len, tc});

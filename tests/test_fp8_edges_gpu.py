@@ -134,6 +134,41 @@ def test_rows_without_their_copies_are_not_written(pkv, cuda_device, case, kind)
             assert done[int(meta.cu_q_lens[s]):int(meta.cu_q_lens[s + 1])].all()
 
 
+def test_copies_past_their_limit(pkv, cuda_device):
+    """72 chunks of 64 tokens at 32 000 keys each, whose copies would take 9.4 GB: some of
+    them run on the split-KV kernel, and every row is right (64-bit reference on the GPU;
+    the sequences read the same blocks)."""
+    dev = cuda_device
+    rng = np.random.default_rng(930)
+    n, qn, ctx, hkv, d, hq = 72, 64, 32_000, 8, 128, 8
+    nb = ctx // 16
+    codes, scales = make_pool(rng, nb, hkv, d)
+    pool, sc, st = codes.to(dev), scales.to(dev), status_of(dev)
+    table = np.tile(rng.permutation(nb).astype(np.int32), (n, 1))
+    cu = np.arange(n + 1, dtype=np.int32) * qn
+    ctxs = np.full(n, ctx, dtype=np.int32)
+    q = ref.bf16(rng.standard_normal((n * qn, hq, d)))
+    plan = pkv.plan_step(cu, ctxs, hq, pool, block_tables=table, fp8=True)
+    kept = np.diff(plan.stage.cpu().numpy()) > 0
+    assert kept.any() and not kept.all() and plan.workspace.numel() < 9 << 30
+    out = pkv.paged_varlen_attention_fp8(q.to(dev), cu, ctxs, table, pool, sc, d ** -0.5, plan=plan,
+                                         dev_status=st)
+    assert int(st.item()) == 0
+    got = out.cpu()
+    vals = torch.from_numpy(values_of(codes, scales))[torch.from_numpy(table[0]).long()].to(dev)
+    i = torch.arange(n * qn, device=dev) % qn
+    hidden = torch.arange(ctx, device=dev)[None] > (ctx - qn + i)[:, None]
+    for h in range(hq):
+        k, v = (vals[:, j, h].reshape(-1, d) for j in (0, 1))
+        qh = q[:, h].to(dev).double()
+        x = ((qh @ k.T) * d ** -0.5).masked_fill_(hidden, float("-inf"))
+        w = torch.softmax(x, dim=1)
+        want, wabs = w @ v, w @ v.abs()
+        mag = (qh.abs() @ k.abs().T).amax(dim=1, keepdim=True) * d ** -0.5
+        check_attention(got[:, h], *(t.cpu().numpy() for t in (want, wabs, mag)), ctx,
+                        tensor_cores=True, scales=scales)
+
+
 # ------------------------------------------------------------------------ 8-bit append
 
 def assert_same_codes(got, want, scales, want_scales):
