@@ -70,6 +70,66 @@ def test_scales_past_the_context_do_not_matter(pkv, cuda_device, case, past, sms
     assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
 
 
+@pytest.mark.parametrize("window", [1, 3])
+def test_chain_that_fills_new_blocks(pkv, cuda_device, window):
+    """Decode steps of one plan in one graph, append and attention, over a pool whose unused
+    blocks hold NaN codes and NaN scales: the sequences cross into such blocks on the way,
+    and every step is right."""
+    dev = cuda_device
+    rng = np.random.default_rng(910 + window)
+    hq, hkv, d, steps, first = 8, 2, 128, 20, np.array([14, 47, 100, 300])
+    n = len(first)
+    last = first + window * (steps - 1)
+    meta = workloads.build_step("fill", 91, [window] * n, last, hq, hkv, d, rng=rng)
+    tables, nb = meta.block_tables, meta.num_blocks
+    codes, scales = make_pool(rng, nb, hkv, d)
+    raw = codes.view(torch.uint8)
+    for s in range(n):
+        held = int(first[s]) - window                  # keys cached before the first step
+        for j, b in enumerate(tables[s, :-(-int(last[s]) // 16)]):
+            keep = min(max(held - 16 * j, 0), 16)
+            raw[int(b), :, :, keep:] = 0x7F
+            if keep == 0:
+                scales[int(b)] = float("nan")
+    pool, sc, st = codes.to(dev), scales.to(dev), status_of(dev)
+    cs = torch.from_numpy(ref.table(500, d)).to(dev)
+    cu, bt = i32(meta.cu_q_lens, dev), i32(tables, dev)
+    at = lambda c: np.concatenate([np.arange(x - window, x) for x in c])  # noqa: E731
+    seq = np.repeat(np.arange(n), window)
+    pos = at(first)
+    ctx, pp = i32(first, dev), i32(pos, dev)
+    sl = i32([int(tables[s, p // 16]) * 16 + p % 16 for s, p in zip(seq, pos)], dev)
+    plan = pkv.plan_step(meta.cu_q_lens, first, hq, pool, chain_steps=steps, block_tables=tables,
+                         fp8=True)
+    ins = [rope_inputs(rng, n * window, hq, hkv, d, True, dev)[1] for _ in range(steps)]
+    got = []
+
+    def run():
+        for t, (q, k, v) in enumerate(ins):
+            qr = pkv.rope_kv_append_fp8(q, k, v, pp, cs, sl, pool, sc, dev_status=st)
+            out = pkv.paged_varlen_attention_fp8(qr, cu, ctx, bt, pool, sc, meta.scale, plan=plan,
+                                                 dev_status=st)
+            got.append((qr, out, pool.clone(), sc.clone()))
+            if t + 1 < steps:
+                pkv.decode_advance(ctx, sl, cu, bt, pool, dev_status=st)
+                pp.add_(window)
+
+    side = torch.cuda.Stream(dev)
+    torch.cuda.synchronize(dev)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        run()
+    g.replay()
+    torch.cuda.synchronize(dev)
+    assert int(st.item()) == 0
+    for t, (qr, out, pool_t, sc_t) in enumerate(got):
+        c = first + window * t
+        want = ref.attention(ref.f64(qr), meta.cu_q_lens, c, tables,
+                             np.nan_to_num(values_of(pool_t.cpu(), sc_t.cpu())), meta.scale)
+        check_attention(out.cpu(), *want, int(c.max()), tensor_cores=False,
+                        scales=sc_t.cpu().nan_to_num())
+
+
 STAGED = [  # (q_lens, ctx_lens, hkv, group, d, num_sms, shared blocks, sequence with copies)
     ([1, 70], [200, 90], 2, 4, 128, None, 0, 1),             # written directly
     ([1, 128, 200], [30, 1000, 700], 2, 2, 64, None, 0, 2),  # whole sub-tiles staged out
