@@ -229,6 +229,34 @@ def test_copies_past_their_limit(pkv, cuda_device):
                         tensor_cores=True, scales=scales)
 
 
+@pytest.mark.parametrize("ql,ctx,hkv,group,d,shared", [
+    ([1] * 12, list(range(5, 2405, 200)), 8, 4, 128, 0),
+    ([4, 8, 3, 1] * 3, [900, 33, 512, 2000] * 3, 2, 8, 128, 0),
+    ([2] * 64, [1024 + 9 * i + 2 for i in range(64)], 8, 4, 128, 64),
+    ([300, 1, 130], [900, 3000, 131], 2, 5, 64, 0),
+])
+def test_same_call_gives_the_same_bits(pkv, cuda_device, ql, ctx, hkv, group, d, shared):
+    dev = cuda_device
+    rng = np.random.default_rng(940)
+    meta = workloads.build_step("twice", 94, ql, ctx, hkv * group, hkv, d, rng=rng,
+                                shared_prefix_blocks=shared)
+    codes, scales = make_pool(rng, meta.num_blocks, hkv, d, "any")
+    pool, sc = codes.to(dev), scales.to(dev)
+    q = ref.bf16(rng.standard_normal((meta.total_q, hkv * group, d))).to(dev)
+    plan = pkv.plan_step(meta.cu_q_lens, ctx, hkv * group, pool, block_tables=meta.block_tables,
+                         fp8=True)
+    outs = []
+    for k in range(6):
+        if plan.workspace is not None:
+            plan.workspace.fill_(0x11 * k)
+        out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=dev)
+        outs.append(pkv.paged_varlen_attention_fp8(q, meta.cu_q_lens, meta.context_lens,
+                                                   meta.block_tables, pool, sc, meta.scale,
+                                                   plan=plan, out=out))
+    torch.cuda.synchronize(dev)
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs[1:])
+
+
 # ------------------------------------------------------------------------ 8-bit append
 
 def assert_same_codes(got, want, scales, want_scales):
