@@ -37,7 +37,7 @@ __all__ = [
     "paged_varlen_attention", "DEV_STATUS", "workspace_size", "BoundStep", "BoundPlan",
     "BoundCopy", "copy_async", "rope_cos_sin", "rope_kv_append", "rope_kv_append_fp8",
     "paged_kv_append_fp8", "fp8_pool", "paged_varlen_attention_fp8", "BoundRopeAppend",
-    "BoundAttentionFp8",
+    "BoundAttentionFp8", "Fp8Info", "stage_fp8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +74,7 @@ class PlanInfo(ctypes.Structure):
 
 
 class Fp8Info(ctypes.Structure):
+    """pkv_fp8_info: what an 8-bit pool adds to a plan's summary (stage_fp8 fills it)."""
     _fields_ = [("staged_blocks", ctypes.c_int32), ("max_rows", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64)]
 
@@ -580,7 +581,8 @@ class StepPlan:
 
 def stage_fp8(info: PlanInfo, host: np.ndarray):
     """(stage_begin int32 [num_seqs + 1], Fp8Info) of a host plan for an 8-bit pool
-    (pkv_plan_stage_fp8)."""
+    (pkv_plan_stage_fp8).  The attention reads a device copy of stage_begin when
+    Fp8Info.staged_blocks > 0, and a workspace of Fp8Info.workspace_bytes."""
     begin = np.zeros(int(info.num_seqs) + 1, dtype=np.int32)
     fp8 = Fp8Info()
     st = _load().pkv_plan_stage_fp8(host.ctypes.data_as(ctypes.c_void_p), ctypes.byref(info),
@@ -617,8 +619,13 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     e.g. pinned memory for an asynchronous upload) the plan is written into; the
     returned host bytes are then a view of it.
     fp8: plan for paged_varlen_attention_fp8 (pkv_plan_step_fp8; a larger workspace
-    when the step has tensor-core work.  The plan still serves a bf16 pool).
-    Returns a StepPlan (or (info, host_bytes) when upload=False).
+    when the step has tensor-core work, at most 8 GiB more.  The plan still serves a
+    bf16 pool).
+    Returns a StepPlan (or (info, host_bytes) when upload=False; an 8-bit pool then
+    also needs stage_fp8(info, host_bytes): the staging array to upload beside the plan,
+    and the Fp8Info with the workspace's size.  StepPlan(info, host_bytes, device,
+    fp8=True) does both.  A StepPlan's dev, stage and fp8 may be replaced by a caller's
+    own uploads of the same, as a loop over BoundPlan(fp8=True) does).
     """
     desc = kv_pool_or_desc if isinstance(kv_pool_or_desc, PoolDesc) else pool_desc(kv_pool_or_desc)
     if device is None:

@@ -257,6 +257,50 @@ def test_same_call_gives_the_same_bits(pkv, cuda_device, ql, ctx, hkv, group, d,
     assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs[1:])
 
 
+@pytest.mark.parametrize("thread", [False, True])
+def test_bound_planner_of_an_8_bit_pool_serves_the_attention(pkv, cuda_device, thread):
+    """A serving loop that uploads what BoundPlan(fp8=True) writes, plan and staging array,
+    into its own buffers: steps with and without tensor-core work, each against the
+    reference."""
+    dev = cuda_device
+    rng = np.random.default_rng(950)
+    steps = [([1, 90, 2], [333, 200, 50]), ([1, 1, 1], [334, 201, 51]), ([3, 64, 130], [337, 265, 181])]
+    cu_h, ctx_h = np.zeros(4, np.int32), np.zeros(3, np.int32)
+    meta = workloads.build_step("bound", 95, *steps[-1], 8, 2, 128, rng=rng)
+    bt_h = meta.block_tables.astype(np.int32).copy()
+    codes, scales = make_pool(rng, meta.num_blocks, 2, 128)
+    pool, sc, st = codes.to(dev), scales.to(dev), status_of(dev)
+    plan_h, stage_h = np.zeros(1 << 16, np.int32), np.zeros(4, np.int32)
+    bp = pkv.BoundPlan(cu_h, ctx_h, 8, pool, plan_h, block_tables=bt_h, fp8=True, stage_out=stage_h,
+                       spin_us=100 if thread else None)
+    plan_d, stage_d = torch.zeros(1 << 18, dtype=torch.uint8, device=dev), i32(stage_h, dev)
+    bt = i32(bt_h, dev)
+    staged = []
+    for ql, ctx in steps:
+        cu_h[1:], ctx_h[:] = np.cumsum(ql), ctx
+        if thread:
+            bp.post()
+            info, nb = bp.wait()
+        else:
+            info, nb = bp.run()
+        plan_d[:nb] = torch.from_numpy(plan_h.view(np.uint8)[:nb]).to(dev)
+        stage_d.copy_(torch.from_numpy(stage_h))
+        plan = pkv.StepPlan(info, plan_h.view(np.uint8)[:nb].view(np.int32), dev, fp8=True)
+        plan.dev, plan.stage, plan.fp8 = plan_d, stage_d, bp.fp8
+        assert plan.workspace is None or plan.workspace.numel() >= bp.fp8.workspace_bytes
+        staged.append(bp.fp8.staged_blocks)
+        q = ref.bf16(rng.standard_normal((int(cu_h[-1]), 8, 128)))
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        pkv.BoundAttentionFp8(q.to(dev), i32(cu_h, dev), i32(ctx_h, dev), bt, pool, sc, meta.scale,
+                              plan, out, dev_status=st).run()
+        torch.cuda.synchronize(dev)
+        assert int(st.item()) == 0
+        want = ref.attention(ref.f64(q), cu_h, ctx_h, bt_h, values_of(codes, scales), meta.scale)
+        check_attention(out.cpu(), *want, max(ctx), tensor_cores=staged[-1] > 0, scales=scales)
+    bp.close()
+    assert staged[0] > 0 and staged[1] == 0 and staged[2] > 0
+
+
 # ------------------------------------------------------------------------ 8-bit append
 
 def assert_same_codes(got, want, scales, want_scales):

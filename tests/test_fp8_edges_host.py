@@ -85,3 +85,10 @@ def test_gathered_prefix_counts_towards_the_limit():
     begin, f = pkv.stage_fp8(info, host)
     assert info.num_gather_rows == 0
     assert f.staged_blocks * 64 * 8 * 128 <= LIMIT and begin[1] == f.staged_blocks
+
+
+def test_public_names():
+    """What a caller who uploads an 8-bit pool's plan needs is exported and described."""
+    assert set(pkv.__all__) <= set(dir(pkv))
+    assert {"Fp8Info", "stage_fp8", "fp8_pool", "BoundPlan", "StepPlan"} <= set(pkv.__all__)
+    assert "stage_fp8" in pkv.plan_step.__doc__ and pkv.stage_fp8.__doc__ and pkv.Fp8Info.__doc__
