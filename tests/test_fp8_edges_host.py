@@ -8,6 +8,11 @@ import paged_kv_attention_append_gb300 as pkv
 from fp8_bytes import E4M3, code_of, value_of
 
 
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    pkv.build()
+
+
 def test_rounding_of_its_own_agrees_with_torch():
     """(The reference above against another implementation: every code's value, ties.)"""
     all_codes = np.arange(256, dtype=np.uint8)
