@@ -292,6 +292,10 @@ def rope_cos_sin(max_positions: int, rotary_dim: int, *, base: float = 10000.0, 
     """The rotation table of positions 0 .. max_positions - 1: fp32 [max_positions,
     rotary_dim], cosines then sines of position * base^(-2 i / rotary_dim), the
     angles evaluated in 64 bits (a far position's angle needs them)."""
+    if rotary_dim <= 0 or rotary_dim % 2 != 0:   # an odd one's table would pass for the next even one
+        raise ValueError("rotary_dim must be positive and even")
+    if max_positions < 0:
+        raise ValueError("max_positions must not be negative")
     i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
     angle = (torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] *
              torch.pow(torch.tensor(base, dtype=torch.float64, device=device), -i / rotary_dim))

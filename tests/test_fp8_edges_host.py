@@ -97,3 +97,23 @@ def test_public_names():
     assert set(pkv.__all__) <= set(dir(pkv))
     assert {"Fp8Info", "stage_fp8", "fp8_pool", "BoundPlan", "StepPlan"} <= set(pkv.__all__)
     assert "stage_fp8" in pkv.plan_step.__doc__ and pkv.stage_fp8.__doc__ and pkv.Fp8Info.__doc__
+
+
+@pytest.mark.parametrize("rot", [15, 17, 31, 127, 0, -16])
+def test_rotation_table_refusals(rot):
+    """A table of 15 would have 16 columns at the frequencies of 15: the append would take it."""
+    with pytest.raises(ValueError):
+        pkv.rope_cos_sin(4, rot, device="cpu")
+
+
+def test_rotation_table():
+    t = pkv.rope_cos_sin(70000, 32, device="cpu").double().numpy()
+    p = np.array([0, 1, 12345, 69999], dtype=np.float64)[:, None]
+    a = p * 10000.0 ** (-np.arange(16) / 16)
+    want = np.concatenate([np.cos(a), np.sin(a)], axis=1)
+    # one rounding to fp32 of a value of at most 1, and the angle's in 64 bits (2^-53 of 2^17,
+    # each of its two operations)
+    assert np.abs(t[[0, 1, 12345, 69999]] - want).max() <= 2.0 ** -25 + 2.0 ** -34
+    assert pkv.rope_cos_sin(0, 64, device="cpu").shape == (0, 64)
+    with pytest.raises(ValueError):
+        pkv.rope_cos_sin(-1, 64, device="cpu")
