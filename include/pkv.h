@@ -527,9 +527,14 @@ PKV_API pkv_status pkv_plan_stage_fp8(const void *plan, const pkv_plan_info *inf
  *   does not give all the copies they read, are reported (PKV_DEV_PLAN_MISMATCH)
  *   and not attended: their rows of out are left as they were.
  *   Rounding: on the split-KV kernel every stored value enters the products
- *   exactly (fp16), the weights are rounded to fp16, 2^-11; on the tensor-core
- *   kernel c * scale is rounded to bf16 (exact for power-of-two scales) and the
- *   weights to bf16, 2^-8.  Accumulation is fp32; out is rounded once to bf16.
+ *   exactly (fp16); a key's weight w (1 for the row's largest) times its V scale
+ *   is rounded to fp16 relative to the largest V scale v that the row group has
+ *   read: by 2^-11 of itself where w scale >= 2^-28 v, by 2^-39 v below.  So V
+ *   scales of one head within a factor 2^r of each other leave 2^-11 to every
+ *   weight down to 2^(r - 28); a block whose V scale is 2^-28 of another's loses
+ *   bits whatever its weight.  On the tensor-core kernel c * scale is rounded to
+ *   bf16 (exact for power-of-two scales) and the weights to bf16, 2^-8.
+ *   Accumulation is fp32; out is rounded once to bf16.
  *   Bytes of a block past its sequence's context are never used, whatever they
  *   hold, nor are the scales of a block that lies past it altogether (one that a
  *   chained plan's later steps will fill).  A NaN stored in a visible row reaches every row of out that sees it,

@@ -23,13 +23,13 @@
 //    a row of q is scaled by a power of two so that its largest value lies in [2^14,
 //    2^15): fp16 then holds every bf16 value down to 2^-28 of the row's largest exactly
 //    and smaller ones to 2^-39 of it.  (q in two e4m3 parts on the 8-bit mma.sync, which
-//    needs no conversion of K, was right and slower, 239 us: that instruction runs as
-//    fp16 products here, its operands converted each time.)
+//    needs no conversion of K, was right and slower: 239 us for the 256 decodes, where
+//    this form then took 196.)
 //  * V8 is read as fragments by ldmatrix (16 x 16 bytes, transposed), whose register
 //    holds four keys of one head_dim: two fp16 pairs, no byte shuffling.  The weights
 //    carry vs, relative to the largest V scale seen so far: u = w vs / vref * 2^14,
-//    rounded to fp16 (2^-11; smallest step 2^-38 of the largest weight) where bf16
-//    would round to 2^-8.
+//    rounded to fp16 (2^-11; smallest step 2^-38 of the largest weight, at the largest V
+//    scale) where bf16 would round to 2^-8.
 //  * Two consecutive blocks are a stage of the ring (one barrier) and are attended
 //    together: one maximum, one rescale, and independent chains of products.
 #include <cuda_runtime.h>
@@ -56,8 +56,9 @@ struct Stage8 {
 // NT: the column tiles of the largest row group (1: at most 8 rows).
 template <int D, int NT>
 struct Decode8Cfg : Stage8<D> {
-  // CTAs an SM: with one column tile a lane's state fits 128 registers, so 16 warps (8
-  // warps and 3 stages, 256 decodes: 193 us, 12 and 2: 184, 16 and 1: 180).  With two
+  // CTAs an SM: with one column tile a lane's state fits 128 registers (126 at D = 64; at
+  // D = 128 but for 72 bytes of spills), so 16 warps (8 warps and 3 stages, 256 decodes:
+  // 193 us, 12 and 2: 184, 16 and 1: 180).  With two
   // it does not (12 warps spill: 107 -> 152 us on 64 windows of 2 to 4 tokens).  Stages a
   // warp: 16 KB at D = 128, 8 KB at D = 64, where they fit; more ran slower (256 decodes
   // of 16 heads a KV head: 3 stages 130 us, 2 120, 1 133).

@@ -98,9 +98,11 @@ constexpr int64_t kGatherMinRows = 64;
 // would take at least this many blocks of 128-wide heads an SM.  The streams run from L2
 // at half the bytes, and the gathered form pays its copies, a tensor-core launch and
 // partials (8 heads, 2 tokens x 4 heads a sequence, 152 SMs; gathered against streamed:
-// 16 sequences on 32 blocks 18 and 12 us, on 256 25.0 and 24.8; 32 on 128 21.9 and 25.8;
-// 64 on 32 19.2 and 19.8, on 256 33 and 66).  Below it nothing is shared: pairs of warps
-// on one stream were no faster (32 sequences on 128 blocks 27.1 us).
+// 16 sequences on 32 blocks 16.5 and 12.2 us, on 256 26.1 and 25.5; 32 on 128 20.6 and
+// 24.8; 64 on 32 17.3 and 18.2, on 256 36.5 and 68.5).  Below it nothing is shared: pairs
+// of warps on one stream were no faster (32 sequences on 128 blocks 27.1 us).  That was
+// measured where the streams fit L2; a prefix larger than L2 that is too narrow to be
+// gathered, or that a chain's steps share, is read once a sequence too.
 constexpr int64_t kGather8MinBlocksPerSm = 131;
 
 // 8-bit pool: the bytes of bf16 copies that a plan may ask for.  A tensor-core sequence
@@ -383,8 +385,8 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     // windows only while one chunk each leaves half the warp slots to the rest
     // (else the shared items alone would take more than a wave)
     // 8-bit pool: nor beside a prefill for every SM, where the row groups stream on SMs of
-    // their own (8 windows of 8 tokens x 4 heads beside 2048 tokens: 172 -> 150 us, beside
-    // 1024 75 -> 48)
+    // their own (8 windows of 8 tokens x 4 heads beside 2048 tokens: 172 -> 151 us, beside
+    // 1024 73 -> 48)
     int64_t pf_tiles = 0;
     for (const auto &nt : pair_nt) pf_tiles += nt[0] + nt[1];
     if (kSharedRowGroups * window_items * 2 > (int64_t)num_sms * warps_per_sm ||
@@ -591,7 +593,7 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       const int64_t ncp = (int64_t)cpairs.size();
       int64_t num = 16 * pf_work, den = 16 * pf_work + total_blocks;  // share = num / den
       // An 8-bit pool's floor is 5/16: long suffixes want the SMs (64 sequences of 4096
-      // shared and up to 4000 own tokens, 64 CTAs 79.6 us, 32 70.7).
+      // shared and up to 4000 own tokens: 86.7 us at 7/16, 76.7 at 5/16).
       const int64_t floor16 = f8 ? 5 : 7;
       if (16 * num < floor16 * den) {
         num = floor16;
@@ -659,8 +661,8 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
         // it instead of behind it, in proportion to the two kernels' work; an even number,
         // since a streaming SM that shares its pair with a prefill CTA is slower (5 SMs
         // took longer than 4).  A 2048-token chunk at 4608 with 3, 8, 16 and 32 decodes of
-        // 2048 to 8192 keys: 147, 169, 202 and 288 us behind the prefill, 143, 152, 163
-        // and 186 beside it; 4096 tokens at 16384 with 64: 931 and 734.  A block's cost
+        // 2048 to 8192 keys: 148, 155, 175 and 217 us behind the prefill, 145, 154, 163
+        // and 186 beside it; 4096 tokens at 16384 with 64: 783 and 732.  A block's cost
         // taken as 2/3, 5/6 and 1: 185, 185, 198 with 32 decodes, 750, 748, 755 with 64.
         // Spread evenly over the grid, the same SMs took 233 and 871.
         // Blocks of row groups of more than 8 rows count half as much again (8 windows of 8
@@ -682,9 +684,9 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
     } else if (f8 && n_pairs == 0) {
       // A smaller prefill leaves SMs free.  The warps that find one start at once, the
       // others 10 us later: a short stream goes to the first alone (32 heads: 16 decodes
-      // of 500 to 4000 keys beside a 64-token prompt 35.9 -> 30.2 us, 8 beside 256 tokens
-      // 32.1 -> 29.3), a long one takes every SM (64 beside 128 tokens, 38 blocks a warp
-      // on the free SMs: 80.0 us, 86.9 there alone).
+      // of 500 to 4000 keys beside a 64-token prompt 36.6 -> 30.6 us, 8 beside 256 tokens
+      // 32.9 -> 28.5), a long one takes every SM (64 beside 128 tokens, 38 blocks a warp
+      // on the free SMs: 81 us, 87 there alone).
       const int64_t free_slots =
           (pf_sms - std::max<int64_t>(pf_tiles / kMinTilesPerCta, pf_subs)) * warps_per_sm;
       if (free_slots > 0 && total_blocks <= kShort8BlocksPerWarp * free_slots) {

@@ -28,8 +28,8 @@
 // cosines and sines stay in registers across its heads.  35 000 tokens of 40 q and 8 KV
 // heads, D = 128: 1.02 GB in 154 us (6.6 TB/s, 0.97 of the copy bandwidth); into the
 // 8-bit pool 0.95 GB in 162 us (0.86: k and v are read twice, the second time from L1
-// or L2).  Short steps are the launch: 16 decodes 2.0 us in a graph, 256 decodes into the
-// 8-bit pool 4.3 us (three dependent reads and two barriers).
+// or L2).  Short steps are the launch: 16 decodes 3.0 us (2.7 in a graph), 256 decodes into
+// the 8-bit pool 4.3 us (three dependent reads and two barriers).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopePara
 // grid of more than one wave takes one appending CTA in every p.every, so that the
 // two kinds share the SMs (35 000 tokens: 179 -> 164 us); in a single wave the
 // appending ones come first, theirs is the longer chain of dependent steps (256
-// decodes: 6.2 us, against 7.7 us spread).
+// decodes: 4.3 us, against 4.8 us spread).
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) rope_append_fp8_kernel(const RopeParams p) {
   __shared__ AppendSmem sm;
