@@ -473,9 +473,10 @@ PKV_API pkv_status pkv_paged_varlen_attention(const void *q, const int32_t *cu_q
  * whole context, 8 ceil(context / 128) blocks of 64 Hkv D bytes (8 heads of 128:
  * 4 KB a key), sequences that share cached blocks one each; a gathered shared
  * prefix takes one for all its sequences.  This planner keeps the copies of a step
- * within 8 GiB: past that, the sequences with the fewest query tokens a key run on
- * the split-KV kernel (the same results, more time).  A plan of the other planners
- * has no such limit; pkv_plan_stage_fp8 says what it needs.
+ * within 8 GiB beside those of its longest sequence: past that, the sequences with
+ * the fewest query tokens a key run on the split-KV kernel (the same results, more
+ * time).  A plan of the other planners has no such limit; pkv_plan_stage_fp8 says
+ * what it needs.
  */
 PKV_API pkv_status pkv_plan_step_fp8(const int32_t *cu_q_lens, const int32_t *context_lens,
                                      int32_t num_seqs, int32_t num_q_heads,

@@ -623,8 +623,9 @@ def plan_step(cu_q_lens, context_lens, num_q_heads: int, kv_pool_or_desc, *, num
     e.g. pinned memory for an asynchronous upload) the plan is written into; the
     returned host bytes are then a view of it.
     fp8: plan for paged_varlen_attention_fp8 (pkv_plan_step_fp8; a larger workspace
-    when the step has tensor-core work, at most 8 GiB more.  The plan still serves a
-    bf16 pool).
+    when the step has tensor-core work: bf16 copies of its sequences' contexts, 64 Hkv D
+    bytes a block, within 8 GiB beside the longest one's.  The plan still serves a bf16
+    pool).
     Returns a StepPlan (or (info, host_bytes) when upload=False; an 8-bit pool then
     also needs stage_fp8(info, host_bytes): the staging array to upload beside the plan,
     and the Fp8Info with the workspace's size.  StepPlan(info, host_bytes, device,

@@ -105,13 +105,15 @@ constexpr int64_t kGatherMinRows = 64;
 // gathered, or that a chain's steps share, is read once a sequence too.
 constexpr int64_t kGather8MinBlocksPerSm = 131;
 
-// 8-bit pool: the bytes of bf16 copies that a plan may ask for.  A tensor-core sequence
-// takes a copy of its whole context (64 Hkv D bytes a block), sequences with the same
-// cached blocks one each, so without a limit many chunks late in long contexts ask for
-// more than the pool holds, or than there is.  8 GiB are 2^21 keys of 8 heads of 128, 3 %
-// of the memory.  Past it the sequences with the fewest query tokens a key, which gain the
-// least from the tensor cores, go to the split-KV kernel; there a chunk of 64 tokens takes
-// five times as long (32 heads, 32 000 keys: 0.40 ms, 0.08 with copies).
+// 8-bit pool: the bytes of bf16 copies that a plan may ask for, beside those of its
+// longest sequence.  A tensor-core sequence takes a copy of its whole context (64 Hkv D
+// bytes a block), sequences with the same cached blocks one each, so without a limit many
+// chunks late in long contexts ask for more than the pool holds, or than there is.  8 GiB
+// are 2^21 keys of 8 heads of 128, 3 % of the memory; the longest sequence is left out so
+// that a chunk of one very long context stays where it is fast.  Past the limit the
+// sequences with the fewest query tokens a key, which gain the least from the tensor
+// cores, go to the split-KV kernel; there a chunk of 64 tokens takes three times as long
+// (32 heads, 32 000 keys: 0.24 ms, 0.08 with copies).
 constexpr int64_t kMaxStagedBytes = (int64_t)8 << 30;
 
 // 8-bit pool: what streaming one block of one KV head costs an SM beside a full prefill, in
@@ -209,16 +211,23 @@ static pkv_status plan_impl(const int32_t *cu_q_lens, const int32_t *context_len
       tc_seqs.push_back(s);
       copies_left -= staged_blocks_of(context_lens[s]);
     }
-    if (copies_left < 0) {
+    auto longest = [&] {
+      int64_t n = 0;
+      for (const int32_t s : tc_seqs)
+        if (!split_kv[s]) n = std::max(n, staged_blocks_of(context_lens[s]));
+      return n;
+    };
+    if (copies_left + longest() < 0) {
       std::stable_sort(tc_seqs.begin(), tc_seqs.end(), [&](int32_t a, int32_t b) {
         return ((int64_t)cu_q_lens[a + 1] - cu_q_lens[a]) * context_lens[b] <
                ((int64_t)cu_q_lens[b + 1] - cu_q_lens[b]) * context_lens[a];
       });
-      for (size_t i = 0; i < tc_seqs.size() && copies_left < 0; ++i) {
+      for (size_t i = 0; i < tc_seqs.size() && copies_left + longest() < 0; ++i) {
         split_kv[tc_seqs[i]] = 1;
         copies_left += staged_blocks_of(context_lens[tc_seqs[i]]);
       }
     }
+    copies_left += longest();
   }
   for (int32_t s = 0; s < num_seqs; ++s) {
     int64_t qs64 = (int64_t)cu_q_lens[s + 1] - (int64_t)cu_q_lens[s];

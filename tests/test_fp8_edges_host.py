@@ -25,7 +25,8 @@ def test_rounding_of_its_own_agrees_with_torch():
     assert np.array_equal(code_of(x), torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
 
 
-LIMIT = 8 << 30     # bytes of copies that a plan for an 8-bit pool may ask for
+LIMIT = 8 << 30     # bytes of copies that a plan for an 8-bit pool may ask for, its longest
+                    # sequence's aside
 
 
 def staged(ql, ctx, hkv, group, d, *, fp8=True, shared=0):
@@ -43,19 +44,21 @@ def staged(ql, ctx, hkv, group, d, *, fp8=True, shared=0):
 
 @pytest.mark.parametrize("hkv,d", [(8, 128), (2, 64), (1, 128)])
 def test_copies_stay_within_their_limit(hkv, d):
-    """Many short chunks late in long contexts: the plan's copies fit 8 GiB, those that
-    keep theirs have the most query tokens a key, and every sequence's keys are covered."""
+    """Many short chunks late in long contexts: the plan's copies, the longest sequence's
+    aside, fit 8 GiB, those that keep theirs have the most query tokens a key, and every
+    sequence's keys are covered."""
     block = 64 * hkv * d
     ctx = [int(c) for c in np.linspace(0.8, 1.2, 40) * LIMIT / block / 32 * 16]
     ql = [64 + 3 * (i % 7) for i in range(40)]
     ql[3], ql[20] = 2048, 700
     info, counts, f = staged(ql, ctx, hkv, 2, d)
     need = np.array([8 * -(-c // 128) for c in ctx])
-    assert need.sum() * block > LIMIT
+    assert (need.sum() - need.max()) * block > LIMIT
     kept = counts > 0
     assert np.array_equal(counts[kept], need[kept]) and kept[3] and kept[20] and not kept.all()
-    assert f.staged_blocks * block <= LIMIT < (f.staged_blocks + need[~kept].max()) * block
-    assert f.workspace_bytes <= info.workspace_bytes + LIMIT
+    most = need[kept].max()
+    assert (f.staged_blocks - most) * block <= LIMIT < (f.staged_blocks + need.max()) * block
+    assert f.workspace_bytes <= info.workspace_bytes + LIMIT + most * block
     per_key = np.array(ql) / np.array(ctx)
     assert per_key[~kept].max() <= per_key[kept].min()
     assert info.kv_tokens == sum(ctx)
@@ -64,32 +67,36 @@ def test_copies_stay_within_their_limit(hkv, d):
 
 
 def test_a_step_at_the_limit_keeps_its_copies():
-    ctx = [LIMIT // (64 * 8 * 128) * 16]               # 2^21 keys of 8 heads of 128
-    info, counts, f = staged([128], ctx, 8, 1, 128)
-    assert f.staged_blocks * 64 * 8 * 128 == LIMIT and info.num_decode_pieces == 0
-    info, counts, f = staged([128, 64], ctx + [64], 8, 1, 128)
-    assert counts.tolist() == [0, 8] and info.num_decode_pieces > 0
+    full = LIMIT // (64 * 8 * 128) * 16                # 2^21 keys of 8 heads of 128
+    info, counts, f = staged([128, 128], [full, full], 8, 1, 128)
+    assert f.staged_blocks * 64 * 8 * 128 == 2 * LIMIT and info.num_decode_pieces == 0
+    info, counts, f = staged([128, 256, 64], [full, full, 64], 8, 1, 128)
+    assert counts.tolist() == [0, full // 16, 8] and info.num_decode_pieces > 0
+    # one sequence past the limit by itself, alone and beside a short prompt
+    info, counts, f = staged([128, 64], [3 * full, 64], 8, 1, 128)
+    assert counts.tolist() == [3 * full // 16, 8] and info.num_decode_pieces == 0
 
 
 def test_gathered_prefix_counts_towards_the_limit():
     """A prefix that the tensor cores would read for 64 decodes is streamed when the
     prompt chunk beside them leaves no room for its copies."""
     pre = 4096
-    ctx = [LIMIT // (64 * 8 * 128) * 16 - 128 * 8] + [pre * 16 + 20] * 64
-    ql = [256] + [2] * 64
-    info, counts, f = staged(ql[1:], ctx[1:], 8, 4, 128, shared=pre)
+    full = LIMIT // (64 * 8 * 128) * 16
+    ctx = [full, full - 128 * 8] + [pre * 16 + 20] * 64
+    ql = [256, 256] + [2] * 64
+    info, counts, f = staged(ql[2:], ctx[2:], 8, 4, 128, shared=pre)
     assert info.num_gather_rows > 0 and f.staged_blocks == pre
-    nb = -(-ctx[0] // 16)
-    table = np.zeros((65, nb), dtype=np.int32)
-    table[0] = np.arange(nb)
-    table[1:, :pre] = nb + np.arange(pre)
-    table[1:, pre:pre + 2] = nb + pre + np.arange(128).reshape(64, 2)
+    nb = full // 16
+    table = np.zeros((66, nb), dtype=np.int32)
+    table[:2] = np.arange(nb)
+    table[2:, :pre] = nb + np.arange(pre)
+    table[2:, pre:pre + 2] = nb + pre + np.arange(128).reshape(64, 2)
     cu = np.concatenate([[0], np.cumsum(ql)])
     info, host = pkv.plan_step(cu, ctx, 32, pkv.PoolDesc(nb + pre + 128, 16, 8, 128), num_sms=152,
                                block_tables=table, upload=False, fp8=True)
     begin, f = pkv.stage_fp8(info, host)
     assert info.num_gather_rows == 0
-    assert f.staged_blocks * 64 * 8 * 128 <= LIMIT and begin[1] == f.staged_blocks
+    assert (f.staged_blocks - nb) * 64 * 8 * 128 <= LIMIT and begin[2] == f.staged_blocks
 
 
 def test_public_names():
