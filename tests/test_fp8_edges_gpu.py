@@ -130,6 +130,29 @@ def test_chain_that_fills_new_blocks(pkv, cuda_device, window):
                         scales=sc_t.cpu().nan_to_num())
 
 
+@pytest.mark.parametrize("pmq", [-1, 1])
+@pytest.mark.parametrize("group,d", [(4, 128), (8, 64)])
+def test_key_scales_of_blocks_far_apart(pkv, cuda_device, group, d, pmq):
+    """K scales that differ by up to 2^8 from block to block of a head, V scales too."""
+    dev = cuda_device
+    rng = np.random.default_rng(915)
+    ql, ctx, hkv = [1, 3, 70, 1], [700, 90, 300, 17], 2
+    meta = workloads.build_step("kscale", 91, ql, ctx, hkv * group, hkv, d, rng=rng, scale=0.02)
+    codes, scales = make_pool(rng, meta.num_blocks, hkv, d)
+    scales = scales * torch.from_numpy(np.exp2(rng.integers(-4, 5, scales.shape)).astype(np.float32))
+    q = ref.bf16(rng.standard_normal((meta.total_q, hkv * group, d)))
+    want = ref.attention(ref.f64(q), meta.cu_q_lens, ctx, meta.block_tables, values_of(codes, scales),
+                         float(np.float32(meta.scale)))
+    pool, st = codes.to(dev), status_of(dev)
+    plan = pkv.plan_step(meta.cu_q_lens, ctx, hkv * group, pool, block_tables=meta.block_tables,
+                         prefill_min_q=pmq, fp8=True)
+    out = pkv.paged_varlen_attention_fp8(q.to(dev), meta.cu_q_lens, meta.context_lens,
+                                         meta.block_tables, pool, scales.to(dev), meta.scale,
+                                         plan=plan, dev_status=st)
+    assert int(st.item()) == 0
+    check_attention(out.cpu(), *want, max(ctx), tensor_cores=pmq == 1, scales=scales)
+
+
 STAGED = [  # (q_lens, ctx_lens, hkv, group, d, num_sms, shared blocks, sequence with copies)
     ([1, 70], [200, 90], 2, 4, 128, None, 0, 1),             # written directly
     ([1, 128, 200], [30, 1000, 700], 2, 2, 64, None, 0, 2),  # whole sub-tiles staged out

@@ -14,7 +14,7 @@ def lib():
 
 
 def test_rounding_of_its_own_agrees_with_torch():
-    """(The reference above against another implementation: every code's value, ties.)"""
+    """fp8_bytes against another implementation: every code's value, ties, neighbours."""
     all_codes = np.arange(256, dtype=np.uint8)
     v = torch.from_numpy(all_codes).view(torch.float8_e4m3fn).float().numpy()
     assert np.array_equal(np.nan_to_num(v, nan=-1), np.nan_to_num(value_of(all_codes), nan=-1))
