@@ -84,6 +84,9 @@ typedef enum pkv_status {
 #define PKV_DEV_TIMEOUT 3        /* a pipeline wait exceeded its bound (tile abandoned) */
 #define PKV_DEV_PLAN_MISMATCH 4  /* device cu_q_lens/context_lens disagree with the plan */
 #define PKV_DEV_BAD_POSITION 5   /* rotating append: position >= max_positions (token skipped) */
+#define PKV_DEV_BAD_ROW 6        /* pages: a row index past the tables (that row left out) */
+#define PKV_DEV_NO_BLOCKS 7      /* reserve: too few free blocks or table columns (nothing changed) */
+#define PKV_DEV_BAD_COUNT 8      /* pages: a reference count that does not fit the tables */
 
 typedef struct pkv_pool_desc {
   int32_t num_blocks;   /* physical blocks in kv_pool */
@@ -156,6 +159,12 @@ PKV_API int64_t pkv_kernel_launch_count(void);
 #define PKV_KERNEL_STATE 4
 #define PKV_KERNEL_ROPE 5   /* pkv_rope_kv_append and pkv_rope_kv_append_fp8 */
 #define PKV_KERNEL_STAGE 6  /* 8-bit attention: bf16 copies of the tensor-core sequences' blocks */
+#define PKV_KERNEL_PAGES 7  /* every kernel of the fork, free, reserve and compact calls */
+#define PKV_KERNEL_COPY 8   /* pkv_copy_blocks */
+#define PKV_KERNEL_BEAM 9   /* pkv_beam_select: both kernels */
+#define PKV_KERNEL_INDEX 10 /* pkv_update_block_index */
+#define PKV_KERNEL_SELECT 11 /* pkv_select_blocks: both kernels */
+#define PKV_KERNEL_SPARSE 12 /* pkv_paged_sparse_attention */
 
 /*
  * Profiling hook (off by default).  After this call, every launch of kernel
@@ -573,6 +582,234 @@ PKV_API pkv_status pkv_state_checkpoint(const void *src, const int32_t *dst_slot
                                         int32_t num_rows, void *pool, int64_t num_slots,
                                         int64_t row_bytes, int32_t *dev_status,
                                         pkv_stream stream);
+
+/*
+ * Pages of the cache: the block tables of the sequences a scheduler runs, and who
+ * holds which block.  Conventions of the five calls below:
+ *  - block_tables: device int32 [num_rows][max_blocks_per_seq], one row a sequence;
+ *    row r's used entries are its first ceil(context_lens[r] / 16) (at most
+ *    max_blocks_per_seq; a negative length counts as 0), the others are never read
+ *    and are written only where a call says so.  An empty row has length 0.
+ *  - ref_counts: device int32 [num_blocks]: how many used entries of all tables hold
+ *    the block; 0: the block is free.  There is no other free list, and free blocks
+ *    are always handed out from the lowest id up, so results do not depend on the
+ *    order in which threads run.  A caller that holds a block outside the tables
+ *    adds one to its count.
+ *  - A used entry outside [0, num_blocks) is left out of the counts (copied as it is)
+ *    and reported, PKV_DEV_BAD_BLOCK.  Counts that do not match the tables are
+ *    reported where a call sees it, PKV_DEV_BAD_COUNT.
+ *  - None of these kernels lets its dependents launch before it has finished, so the
+ *    appends and the attention may follow directly.
+ *
+ * pkv_copy_blocks: whole blocks copied inside every array of `arrays` (each layer's
+ * pool, the scales of 8-bit pools, block indexes: whatever is stored by block):
+ *   for i < num_pairs (and i < *num_pairs_dev when that is not NULL):
+ *     arrays[a].data row dst[i] = row src[i], raw bytes, row_bytes each.
+ *   src, dst: device int32 [num_pairs]; a pair with a negative entry is skipped, one
+ *   with an entry >= num_blocks too, PKV_DEV_BAD_BLOCK.  No dst may be another pair's
+ *   src or dst (such blocks hold unspecified bytes).  num_pairs_dev: device int32.
+ *   arrays: HOST array of num_arrays; data device, at least 4-byte aligned, row_bytes
+ *   a positive multiple of 4 (16 of both for full speed).  One launch for every
+ *   PKV_COPY_ARRAYS of them.  Nothing is enqueued for 0 pairs or arrays.
+ */
+#define PKV_COPY_ARRAYS 128
+typedef struct pkv_block_array {
+  void *data;        /* device, [num_blocks] rows */
+  int64_t row_bytes;
+} pkv_block_array;
+
+PKV_API pkv_status pkv_copy_blocks(const pkv_block_array *arrays, int32_t num_arrays,
+                                   int32_t num_blocks, const int32_t *src, const int32_t *dst,
+                                   int32_t num_pairs, const int32_t *num_pairs_dev,
+                                   int32_t *dev_status, pkv_stream stream);
+
+/*
+ * Fork: row i of new_tables (num_new rows) takes the used entries of row parents[i]
+ * of block_tables (num_rows rows), and new_context_lens[i] its length.  The blocks
+ * are shared, a partly filled last one too (pkv_reserve_blocks copies it when it is
+ * to be written).  A negative parent gives an empty row; one >= num_rows too,
+ * PKV_DEV_BAD_ROW.  Counts: with keep_parents = 1 every child adds one to each of its
+ * blocks; with 0 the old rows end with the call (beam search's reordering: the new
+ * tables take the old ones' place), which takes one off for each old row.  Both have
+ * max_blocks_per_seq columns; the new arrays must not overlap the old ones.
+ */
+PKV_API pkv_status pkv_fork_sequences(const int32_t *parents, int32_t num_new,
+                                      const int32_t *block_tables, const int32_t *context_lens,
+                                      int32_t num_rows, int32_t max_blocks_per_seq,
+                                      int32_t *ref_counts, int32_t num_blocks,
+                                      int32_t keep_parents, int32_t *new_tables,
+                                      int32_t *new_context_lens, int32_t *dev_status,
+                                      pkv_stream stream);
+
+/*
+ * Free: each row listed in rows (device int32 [num_listed]; negative entries are
+ * skipped, entries >= num_rows too, PKV_DEV_BAD_ROW) takes one off the counts of its
+ * used entries and gets length 0; its entries stay as they are.  A row listed twice is
+ * freed once.  A count that is 0 or less already stays and is reported.
+ */
+PKV_API pkv_status pkv_free_sequences(const int32_t *rows, int32_t num_listed,
+                                      const int32_t *block_tables, int32_t *context_lens,
+                                      int32_t num_rows, int32_t max_blocks_per_seq,
+                                      int32_t *ref_counts, int32_t num_blocks,
+                                      int32_t *dev_status, pkv_stream stream);
+
+/*
+ * Reserve: room for the new tokens of a step.  Row r gets n = cu_new[r + 1] -
+ * cu_new[r] of them (0 where negative; device int32 [num_rows + 1]): its table the
+ * blocks they need, context_lens[r] += n, and slot_mapping[cu_new[r] + i] the slot of
+ * position context_lens[r] + i (old length), for the append; entries of slot_mapping
+ * past num_tokens are not written.
+ *   A partly filled last block that other rows hold too is not written to: the row
+ *   takes a new block in its place, copy_src[r] and copy_dst[r] say which (-1 where
+ *   there is none), for a pkv_copy_blocks before the append.  When every holder of such
+ *   a block gets new tokens in this call, the last of those rows keeps it.  New blocks
+ *   go to the rows in order, to each its copy first.
+ *   When the free blocks or a table's columns do not suffice (PKV_DEV_NO_BLOCKS), a partly
+ *   filled block is outside the pool (PKV_DEV_BAD_BLOCK) or its count is below the number of
+ *   rows that write to it (PKV_DEV_BAD_COUNT), nothing changes, every slot and pair is -1
+ *   and that is reported.
+ *   workspace: device, 16-byte aligned, pkv_pages_workspace_size(num_rows, num_blocks)
+ *   bytes, contents do not matter; one call at a time.  num_rows > 8192:
+ *   PKV_ERR_UNSUPPORTED.
+ */
+PKV_API size_t pkv_pages_workspace_size(int32_t num_rows, int32_t num_blocks);
+PKV_API pkv_status pkv_reserve_blocks(const int32_t *cu_new, int32_t *block_tables,
+                                      int32_t *context_lens, int32_t num_rows,
+                                      int32_t max_blocks_per_seq, int32_t *ref_counts,
+                                      int32_t num_blocks, int32_t *slot_mapping,
+                                      int32_t num_tokens, int32_t *copy_src, int32_t *copy_dst,
+                                      void *workspace, int64_t workspace_bytes,
+                                      int32_t *dev_status, pkv_stream stream);
+
+/*
+ * Compact: the blocks in use (count != 0) move to ids 0 .. L - 1, L being how many
+ * there are.  The i-th block in use with id >= L goes to the i-th free id below L:
+ * copy_src[i], copy_dst[i] (device int32 [num_pairs_max], -1 past the last pair;
+ * num_pairs_max >= num_blocks / 2 holds every case, fewer: PKV_ERR_SHAPE), their number
+ * to *num_pairs (device int32), for a pkv_copy_blocks.  new_tables gets the used entries
+ * renamed, new_ref_counts the counts at the new ids.  new_tables may be block_tables and
+ * new_ref_counts ref_counts (in place).  A used entry of a block whose count is 0 and whose
+ * id is >= L keeps its id, PKV_DEV_BAD_COUNT.  workspace as for pkv_reserve_blocks.
+ */
+PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t *context_lens,
+                                      int32_t num_rows, int32_t max_blocks_per_seq,
+                                      const int32_t *ref_counts, int32_t num_blocks,
+                                      int32_t *new_tables, int32_t *new_ref_counts,
+                                      int32_t *copy_src, int32_t *copy_dst,
+                                      int32_t num_pairs_max, int32_t *num_pairs, void *workspace,
+                                      int64_t workspace_bytes, int32_t *dev_status,
+                                      pkv_stream stream);
+
+/*
+ * Beam search's selection.  For request b and its beam k (row r = b num_beams + k of
+ * logits, vocab entries, row_stride elements apart) every token t is a candidate with
+ *   score = cum_scores[r] + logits[r][t] - log(sum_u exp(logits[r][u]));
+ * a beam with finished[r] != 0 (finished may be NULL: none) has one candidate,
+ * pad_token with score cum_scores[r], and its logits are not read.  The num_select
+ * best candidates of each request, by score, then beam, then token, go to scores
+ * (fp32), tokens and parents (int32; r, the row index), [num_requests][num_select].
+ *   Within a beam candidates are ranked by their logits, between beams by the score in
+ *   64 bits (of a log-sum accumulated in 32).  Candidates whose score is not finite
+ *   (masked logits of -inf; every one of a beam whose logits hold NaN or +inf, or with a
+ *   cum_scores that is not finite) are never selected; where too few remain, score -inf,
+ *   token -1 and parent -1 fill the rest.  parents is what pkv_fork_sequences takes.
+ *   logit_type: PKV_BF16, PKV_FP16 or PKV_FP32; logits aligned to their type.
+ *   num_select <= 128, num_beams <= 1024, vocab >= 1.  workspace: device, 16-byte
+ *   aligned, pkv_beam_workspace_size(...) bytes; one call at a time.
+ */
+#define PKV_BF16 0
+#define PKV_FP16 1
+#define PKV_FP32 2
+PKV_API size_t pkv_beam_workspace_size(int32_t num_requests, int32_t num_beams, int32_t vocab,
+                                       int32_t num_select);
+PKV_API pkv_status pkv_beam_select(const void *logits, int32_t logit_type, int64_t row_stride,
+                                   const float *cum_scores, const uint8_t *finished,
+                                   int32_t num_requests, int32_t num_beams, int32_t vocab,
+                                   int32_t num_select, int32_t pad_token, float *scores,
+                                   int32_t *tokens, int32_t *parents, void *workspace,
+                                   int64_t workspace_bytes, pkv_stream stream);
+
+/*
+ * Attention over selected blocks of a bf16 pool, for contexts too long to be read
+ * whole at every step.  A block index holds, for each block and KV head, bounds of its
+ * keys in 8 bits:
+ *   index: device int8 [num_blocks][Hkv][2][D], index_scales: device fp32
+ *   [num_blocks][Hkv].  With s the scale, the smallest power of two >= 2^-64 with
+ *   |K| <= 127 s for every key of the block, lo = floor(min K / s) and
+ *   hi = ceil(max K / s) by element: lo s <= K <= hi s.  (Keys' infinities and NaN
+ *   count as 0.)
+ *
+ * pkv_update_block_index makes the rows of the blocks a step has written to, after
+ * its append (and rotates nothing: it reads the keys back from the pool):
+ *   slot_mapping as the append's: a block is taken to hold the rows up to its
+ *   largest slot of the step; its bounds are made anew from those rows, so a slot
+ *   written again after rejected tokens shrinks them again.  The tokens of one block must lie within
+ *   16 consecutive ones of the step.  Negative slots are skipped, slots past the pool too,
+ *   PKV_DEV_BAD_SLOT.
+ */
+PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_desc *desc,
+                                          const int32_t *slot_mapping, int32_t num_tokens,
+                                          int8_t *index, float *index_scales,
+                                          int32_t *dev_status, pkv_stream stream);
+
+/*
+ * Selection, for each query token t (at position p of its sequence) and KV head h, of
+ * num_select of its blocks 0 .. p / 16: all of them if there are no more; otherwise
+ * the first sink_blocks, the last recent_blocks (that of p among them) and, of the
+ * rest, those with the largest scores, ties to the lower block.
+ *   Score: an upper bound of the sum over the group's heads of q . k over the keys of
+ *   the block.  With u the smallest power of two with |q| <= 2047 u in the group
+ *   (infinities and NaN count as 0), P and N the sums over the heads of the positive
+ *   and the negative elements of q / u, each rounded to an integer (to even):
+ *     score = float(sum_d P[d] hi[d] + N[d] lo[d]) * index_scale,
+ *   an integer rounded once to fp32 and scaled: the same number in any order.
+ *   q: device bf16 [total_q][num_q_heads][D]; the group (num_q_heads / Hkv) is at most 16.
+ *   cu_q_lens, context_lens, block_tables: DEVICE arrays as pkv_paged_varlen_attention
+ *   takes them.  selected: device int32 [total_q][Hkv][num_select]: logical blocks,
+ *   ascending, then -1.  1 <= recent_blocks, 0 <= sink_blocks, their sum <= num_select.
+ *   A block id outside the pool has score -inf, PKV_DEV_BAD_BLOCK; a token past cu_q_lens'
+ *   last entry, or one whose context is shorter than its window, gets -1 throughout
+ *   (PKV_DEV_PLAN_MISMATCH for the latter).
+ *   workspace: device, 16-byte aligned; any size from pkv_select_workspace_size(1, ...)
+ *   on serves (fewer bytes than pkv_select_workspace_size(total_q, ...): the tokens in
+ *   several passes); one call at a time.
+ */
+PKV_API size_t pkv_select_workspace_size(int64_t total_q, int32_t num_kv_heads,
+                                         int32_t max_blocks_per_seq);
+PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
+                                     const int32_t *context_lens, const int32_t *block_tables,
+                                     int32_t max_blocks_per_seq, int32_t num_seqs,
+                                     int64_t total_q, int32_t num_q_heads, const int8_t *index,
+                                     const float *index_scales, const pkv_pool_desc *desc,
+                                     int32_t num_select, int32_t sink_blocks,
+                                     int32_t recent_blocks, int32_t *selected, void *workspace,
+                                     int64_t workspace_bytes, int32_t *dev_status,
+                                     pkv_stream stream);
+
+/*
+ * Attention of each query token, group by group, over the keys of its selected blocks
+ * that it sees:
+ *   out[t][hq][:] = sum_p softmax_p(scale * q[t][hq] . K[p][h]) V[p][h],  h = hq / G,
+ *   over the positions p <= the token's, p / 16 in selected[t][h].
+ *   With every block of its context selected a token's result is that of
+ *   pkv_paged_varlen_attention.  selected: as pkv_select_blocks writes it, or a caller's
+ *   own choice in any order (entries outside the token's blocks are skipped; one that
+ *   is there twice counts twice).  A block id outside the pool is skipped,
+ *   PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past cu_q_lens' last
+ *   entry is left as it was; one whose context is shorter than its window too,
+ *   PKV_DEV_PLAN_MISMATCH.  num_q_heads / Hkv <= 16.  Weights are rounded to bf16 for
+ *   the product with V, sums are fp32, out is rounded once to bf16.  Bytes of a
+ *   visible block past the token's position do not reach its row.
+ */
+PKV_API pkv_status pkv_paged_sparse_attention(const void *q, const int32_t *cu_q_lens,
+                                              const int32_t *context_lens,
+                                              const int32_t *block_tables,
+                                              int32_t max_blocks_per_seq, int32_t num_seqs,
+                                              int64_t total_q, int32_t num_q_heads,
+                                              const int32_t *selected, int32_t num_select,
+                                              const void *kv_pool, const pkv_pool_desc *desc,
+                                              float scale, void *out, int32_t *dev_status,
+                                              pkv_stream stream);
 
 /*
  * Size of the fixed scratch array used by pkv_paged_varlen_attention_noalloc

@@ -19,6 +19,21 @@ With the position rotation applied by the append, and with an 8-bit pool:
                                kv_scales)
     out = paged_varlen_attention_fp8(q_rot, cu_q_lens, context_lens, block_tables, kv_pool,
                                      kv_scales, scale)
+
+Between the steps, on the device: beams are selected, their pages follow, room for the next
+tokens is reserved (with copies where a partly filled block is shared):
+
+    scores, tokens, parents = beam_select(logits, cum_scores, num_beams)
+    fork_sequences(parents.view(-1), block_tables, context_lens, ref_counts, new_tables, new_lens)
+    slots, src, dst = reserve_blocks(cu_q_lens, new_tables, new_lens, ref_counts, num_tokens=n)
+    copy_blocks(kv_pools, src, dst)
+
+Attention over the blocks that matter of a long context:
+
+    index, index_scales = block_index(num_blocks, Hkv, D)
+    update_block_index(kv_pool, slots, index, index_scales)          # after each append
+    sel = select_blocks(q, cu_q_lens, context_lens, block_tables, index, index_scales, 64)
+    out = paged_sparse_attention(q, cu_q_lens, context_lens, block_tables, sel, kv_pool, scale)
 """
 
 from __future__ import annotations
@@ -37,7 +52,11 @@ __all__ = [
     "paged_varlen_attention", "DEV_STATUS", "workspace_size", "BoundStep", "BoundPlan",
     "BoundCopy", "copy_async", "rope_cos_sin", "rope_kv_append", "rope_kv_append_fp8",
     "paged_kv_append_fp8", "fp8_pool", "paged_varlen_attention_fp8", "BoundRopeAppend",
-    "BoundAttentionFp8", "Fp8Info", "stage_fp8",
+    "BoundAttentionFp8", "Fp8Info", "stage_fp8", "copy_blocks", "fork_sequences",
+    "free_sequences", "reserve_blocks", "compact_blocks", "beam_select", "block_index",
+    "update_block_index", "select_blocks", "paged_sparse_attention", "BoundCopyBlocks",
+    "BoundForkSequences", "BoundFreeSequences", "BoundReserveBlocks", "BoundCompactBlocks",
+    "BoundBeamSelect", "BoundIndexUpdate", "BoundSelectBlocks", "BoundSparseAttention",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -46,7 +65,9 @@ _lock = threading.Lock()
 _lib = None
 
 DEV_STATUS = {0: "ok", 1: "bad slot", 2: "bad block id", 3: "pipeline wait timed out",
-              4: "plan does not match device metadata", 5: "position past the rotation table"}
+              4: "plan does not match device metadata", 5: "position past the rotation table",
+              6: "row past the tables", 7: "too few free blocks or table columns",
+              8: "reference counts do not fit the tables"}
 
 
 class PkvError(RuntimeError):
@@ -77,6 +98,11 @@ class Fp8Info(ctypes.Structure):
     """pkv_fp8_info: what an 8-bit pool adds to a plan's summary (stage_fp8 fills it)."""
     _fields_ = [("staged_blocks", ctypes.c_int32), ("max_rows", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class BlockArray(ctypes.Structure):
+    """pkv_block_array: one array that is stored by block."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
 
 
 class Rope(ctypes.Structure):
@@ -162,6 +188,30 @@ def _load():
                 P, P, P, P, i32, P, P, ctypes.POINTER(PoolDesc), ctypes.c_float,
                 ctypes.POINTER(PlanInfo), P, ctypes.POINTER(Fp8Info), P, P, P, i64, P, P]
             lib.pkv_paged_varlen_attention_fp8.restype = i32
+            lib.pkv_copy_blocks.argtypes = [P, i32, i32, P, P, i32, P, P, P]
+            lib.pkv_fork_sequences.argtypes = [P, i32, P, P, i32, i32, P, i32, i32, P, P, P, P]
+            lib.pkv_free_sequences.argtypes = [P, i32, P, P, i32, i32, P, i32, P, P]
+            lib.pkv_reserve_blocks.argtypes = [P, P, P, i32, i32, P, i32, P, i32, P, P, P, i64, P,
+                                               P]
+            lib.pkv_compact_blocks.argtypes = [P, P, i32, i32, P, i32, P, P, P, P, i32, P, P, i64,
+                                               P, P]
+            lib.pkv_beam_select.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P,
+                                            i64, P]
+            desc_p = ctypes.POINTER(PoolDesc)
+            lib.pkv_update_block_index.argtypes = [P, desc_p, P, i32, P, P, P, P]
+            lib.pkv_select_blocks.argtypes = [P, P, P, P, i32, i32, i64, i32, P, P, desc_p, i32, i32,
+                                              i32, P, P, i64, P, P]
+            lib.pkv_paged_sparse_attention.argtypes = [P, P, P, P, i32, i32, i64, i32, P, i32, P,
+                                                       desc_p, ctypes.c_float, P, P, P]
+            for f in ("copy_blocks", "fork_sequences", "free_sequences", "reserve_blocks",
+                      "compact_blocks", "beam_select", "update_block_index", "select_blocks",
+                      "paged_sparse_attention"):
+                getattr(lib, "pkv_" + f).restype = i32
+            lib.pkv_pages_workspace_size.argtypes = [i32, i32]
+            lib.pkv_beam_workspace_size.argtypes = [i32, i32, i32, i32]
+            lib.pkv_select_workspace_size.argtypes = [i64, i32, i32]
+            for f in ("pages", "beam", "select"):
+                getattr(lib, f"pkv_{f}_workspace_size").restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -179,7 +229,7 @@ def kernel_launch_count() -> int:
 
 
 KERNEL_IDS = {"append": 0, "decode": 1, "merge": 2, "prefill": 3, "state": 4, "rope": 5,
-              "stage": 6}
+              "stage": 6, "pages": 7, "copy": 8, "beam": 9, "index": 10, "select": 11, "sparse": 12}
 
 
 def set_profile_events(kernel: str, start=None, stop=None):
@@ -1044,3 +1094,469 @@ def paged_varlen_attention_fp8(q, cu_q_lens, context_lens, block_tables, kv_pool
         BoundAttentionFp8(q, cu_d, ctx_d, bt_d, kv_pool, kv_scales, scale, plan, out,
                           dev_status=dev_status, stream=stream).run()
     return out
+
+
+# ------------------------------------------------------------------ pages, beams, sparse attention
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class _BoundCall:
+    """A library call with its arguments checked and marshalled once; run() enqueues it
+    on the bound stream.  The tensors' contents are read then, so a loop that rewrites
+    them in place calls run() once per step.  A call that needs a workspace owns one:
+    calls that may overlap need an object each."""
+
+    def _bind(self, name, ref, stream, args, keep, dev_status=None, takes_status=True):
+        """ref: the tensor whose device (and, without `stream`, current stream) it is."""
+        for t in keep:
+            if isinstance(t, torch.Tensor) and t.device != ref.device:
+                raise ValueError("every tensor must be on the same device")
+        if takes_status:
+            if dev_status is not None:
+                _check_cuda("dev_status", dev_status, torch.int32)
+                if dev_status.device != ref.device:
+                    raise ValueError("every tensor must be on the same device")
+            args = (*args, _vp(_ptr(dev_status)))
+        self._keep = (keep, dev_status)
+        self._args = (*args, _vp(_stream(stream, ref)))
+        self._name = name
+        self._f = _bound_fn(name)
+        self._device = ref.device.index
+
+    def run(self) -> None:
+        st = _call_on(self._device, self._f, self._args)
+        if st:
+            raise PkvError(st, self._name)
+
+
+def _new(stream, ref, shape, dtype):
+    """A tensor on ref's device, allocated on `stream` (the current one by default)."""
+    with torch.cuda.stream(stream) if stream is not None else _nullcontext():
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+
+
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return (a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size() and
+            a.numel() > 0 and b.numel() > 0)
+
+
+def _check_tables(block_tables, context_lens, ref_counts):
+    _check_cuda("block_tables", block_tables, torch.int32, 2)
+    _check_cuda("context_lens", context_lens, torch.int32, 1)
+    _check_cuda("ref_counts", ref_counts, torch.int32, 1)
+    if context_lens.shape[0] != block_tables.shape[0]:
+        raise ValueError("context_lens needs one entry per row of block_tables")
+
+
+class BoundCopyBlocks(_BoundCall):
+    """copy_blocks with its arguments checked and marshalled once."""
+
+    def __init__(self, pools, src_blocks, dst_blocks, *, num_pairs=None, dev_status=None,
+                 stream=None):
+        pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+        _check_cuda("src_blocks", src_blocks, torch.int32, 1)
+        _check_cuda("dst_blocks", dst_blocks, torch.int32, 1)
+        if src_blocks.shape != dst_blocks.shape:
+            raise ValueError("src_blocks and dst_blocks must have the same length")
+        if num_pairs is not None:
+            _check_cuda("num_pairs", num_pairs, torch.int32)
+            if num_pairs.numel() != 1:
+                raise ValueError("num_pairs must hold one count")
+        arrays = (BlockArray * max(len(pools), 1))()
+        n, blocks = 0, pools[0].shape[0] if pools and pools[0].dim() else 0
+        for t in pools:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+                raise TypeError("every pool must be a contiguous CUDA tensor")
+            if t.dim() < 1 or t.shape[0] != blocks:
+                raise ValueError("every pool must have the same number of blocks")
+            row = t.numel() // blocks * t.element_size() if blocks else 0
+            if row % 4 != 0:
+                raise ValueError(f"a block's row must be a multiple of 4 bytes, got {row}")
+            if row:
+                arrays[n] = BlockArray(t.data_ptr(), row)
+                n += 1
+        self._bind("pkv_copy_blocks", src_blocks, stream,
+                   (arrays, _i32(n), _i32(blocks), _vp(src_blocks.data_ptr()),
+                    _vp(dst_blocks.data_ptr()), _i32(src_blocks.shape[0]), _vp(_ptr(num_pairs))),
+                   (src_blocks, dst_blocks, num_pairs, *pools), dev_status)
+
+
+def copy_blocks(pools, src_blocks, dst_blocks, *, num_pairs=None, dev_status=None, stream=None):
+    """Copy block src_blocks[i] to block dst_blocks[i] inside every array of `pools`
+    (pkv_copy_blocks): a tensor or a list of contiguous CUDA tensors of any type whose
+    first axis is the block (each layer's pool, 8-bit scales, block indexes).
+    src_blocks, dst_blocks: int32 [n], pairs with a negative entry are skipped;
+    num_pairs: int32 device tensor, the number of pairs that count (all by default)."""
+    BoundCopyBlocks(pools, src_blocks, dst_blocks, num_pairs=num_pairs, dev_status=dev_status,
+                    stream=stream).run()
+
+
+class BoundForkSequences(_BoundCall):
+    """fork_sequences with its arguments checked and marshalled once."""
+
+    def __init__(self, parents, block_tables, context_lens, ref_counts, new_tables,
+                 new_context_lens, *, keep_parents=False, dev_status=None, stream=None):
+        _check_tables(block_tables, context_lens, ref_counts)
+        _check_cuda("parents", parents, torch.int32, 1)
+        _check_cuda("new_tables", new_tables, torch.int32, 2)
+        _check_cuda("new_context_lens", new_context_lens, torch.int32, 1)
+        n, (rows, width) = parents.shape[0], block_tables.shape
+        if new_tables.shape != (n, width) or new_context_lens.shape[0] != n:
+            raise ValueError(f"new_tables must be [{n}, {width}] and new_context_lens [{n}]")
+        for new in (new_tables, new_context_lens):
+            for old in (block_tables, context_lens, parents, ref_counts):
+                if _overlap(new, old):
+                    raise ValueError("the new tables and lengths must not overlap the inputs")
+        self._bind("pkv_fork_sequences", block_tables, stream,
+                   (_vp(parents.data_ptr()), _i32(n), _vp(block_tables.data_ptr()),
+                    _vp(context_lens.data_ptr()), _i32(rows), _i32(width),
+                    _vp(ref_counts.data_ptr()), _i32(ref_counts.shape[0]),
+                    _i32(int(bool(keep_parents))), _vp(new_tables.data_ptr()),
+                    _vp(new_context_lens.data_ptr())),
+                   (parents, block_tables, context_lens, ref_counts, new_tables, new_context_lens),
+                   dev_status)
+
+
+def fork_sequences(parents, block_tables, context_lens, ref_counts, new_tables, new_context_lens, *,
+                   keep_parents=False, dev_status=None, stream=None):
+    """Row i of new_tables takes the blocks and the length of row parents[i] of block_tables
+    (pkv_fork_sequences; negative: an empty row).  Blocks are shared and ref_counts
+    updated in place; the old rows end unless keep_parents.  parents: int32 [n], as
+    beam_select returns them; new_tables: int32 [n, max_blocks], new_context_lens: int32 [n],
+    apart from the old ones."""
+    BoundForkSequences(parents, block_tables, context_lens, ref_counts, new_tables,
+                       new_context_lens, keep_parents=keep_parents, dev_status=dev_status,
+                       stream=stream).run()
+
+
+class BoundFreeSequences(_BoundCall):
+    """free_sequences with its arguments checked and marshalled once."""
+
+    def __init__(self, rows, block_tables, context_lens, ref_counts, *, dev_status=None,
+                 stream=None):
+        _check_tables(block_tables, context_lens, ref_counts)
+        _check_cuda("rows", rows, torch.int32, 1)
+        self._bind("pkv_free_sequences", block_tables, stream,
+                   (_vp(rows.data_ptr()), _i32(rows.shape[0]), _vp(block_tables.data_ptr()),
+                    _vp(context_lens.data_ptr()), _i32(block_tables.shape[0]),
+                    _i32(block_tables.shape[1]), _vp(ref_counts.data_ptr()),
+                    _i32(ref_counts.shape[0])),
+                   (rows, block_tables, context_lens, ref_counts), dev_status)
+
+
+def free_sequences(rows, block_tables, context_lens, ref_counts, *, dev_status=None, stream=None):
+    """End the sequences in `rows` (int32 [n], negative entries skipped): their blocks' counts
+    drop by one and their lengths become 0 (pkv_free_sequences).  A row listed twice is
+    freed once."""
+    BoundFreeSequences(rows, block_tables, context_lens, ref_counts, dev_status=dev_status,
+                       stream=stream).run()
+
+
+def _pages_workspace(stream, ref, rows, blocks):
+    return _new(stream, ref, int(_load().pkv_pages_workspace_size(rows, blocks)), torch.uint8)
+
+
+class BoundReserveBlocks(_BoundCall):
+    """reserve_blocks with its arguments checked and marshalled once."""
+
+    def __init__(self, cu_new, block_tables, context_lens, ref_counts, *, num_tokens=None,
+                 slot_mapping=None, copy_src=None, copy_dst=None, dev_status=None, stream=None):
+        _check_tables(block_tables, context_lens, ref_counts)
+        _check_cuda("cu_new", cu_new, torch.int32, 1)
+        rows, width = block_tables.shape
+        if cu_new.shape[0] != rows + 1:
+            raise ValueError("cu_new needs one entry more than block_tables has rows")
+        if slot_mapping is None:
+            if num_tokens is None:
+                raise ValueError("give num_tokens or slot_mapping")
+            slot_mapping = _new(stream, block_tables, int(num_tokens), torch.int32)
+        copy_src = _new(stream, block_tables, rows, torch.int32) if copy_src is None else copy_src
+        copy_dst = _new(stream, block_tables, rows, torch.int32) if copy_dst is None else copy_dst
+        for name, t in (("slot_mapping", slot_mapping), ("copy_src", copy_src),
+                        ("copy_dst", copy_dst)):
+            _check_cuda(name, t, torch.int32, 1)
+        if num_tokens is not None and slot_mapping.shape[0] != num_tokens:
+            raise ValueError("slot_mapping needs one entry per new token")
+        if copy_src.shape[0] != rows or copy_dst.shape[0] != rows:
+            raise ValueError("copy_src and copy_dst need one entry per row")
+        ws = _pages_workspace(stream, block_tables, rows, ref_counts.shape[0])
+        self.slot_mapping, self.copy_src, self.copy_dst = slot_mapping, copy_src, copy_dst
+        self._bind("pkv_reserve_blocks", block_tables, stream,
+                   (_vp(cu_new.data_ptr()), _vp(block_tables.data_ptr()),
+                    _vp(context_lens.data_ptr()), _i32(rows), _i32(width),
+                    _vp(ref_counts.data_ptr()), _i32(ref_counts.shape[0]),
+                    _vp(slot_mapping.data_ptr()), _i32(slot_mapping.shape[0]),
+                    _vp(copy_src.data_ptr()), _vp(copy_dst.data_ptr()), _vp(ws.data_ptr()),
+                    _i64(ws.numel())),
+                   (cu_new, block_tables, context_lens, ref_counts, slot_mapping, copy_src,
+                    copy_dst, ws), dev_status)
+
+
+def reserve_blocks(cu_new, block_tables, context_lens, ref_counts, *, num_tokens=None,
+                   slot_mapping=None, copy_src=None, copy_dst=None, dev_status=None, stream=None):
+    """Room for cu_new[r + 1] - cu_new[r] new tokens of each row r (pkv_reserve_blocks):
+    block_tables, context_lens and ref_counts are updated in place.  Returns (slot_mapping,
+    copy_src, copy_dst): the new tokens' slots for the append, and for each row the block to
+    copy before it (copy_blocks) where a partly filled one was shared, else -1.  When the
+    free blocks do not suffice nothing changes, every slot is -1 and dev_status says so."""
+    b = BoundReserveBlocks(cu_new, block_tables, context_lens, ref_counts, num_tokens=num_tokens,
+                           slot_mapping=slot_mapping, copy_src=copy_src, copy_dst=copy_dst,
+                           dev_status=dev_status, stream=stream)
+    b.run()
+    return b.slot_mapping, b.copy_src, b.copy_dst
+
+
+class BoundCompactBlocks(_BoundCall):
+    """compact_blocks with its arguments checked and marshalled once."""
+
+    def __init__(self, block_tables, context_lens, ref_counts, *, new_tables=None,
+                 new_ref_counts=None, copy_src=None, copy_dst=None, num_pairs=None, dev_status=None,
+                 stream=None):
+        _check_tables(block_tables, context_lens, ref_counts)
+        rows, width = block_tables.shape
+        blocks = ref_counts.shape[0]
+        new_tables = block_tables if new_tables is None else new_tables
+        new_ref_counts = ref_counts if new_ref_counts is None else new_ref_counts
+        if copy_src is None:
+            copy_src = _new(stream, block_tables, blocks // 2, torch.int32)
+        if copy_dst is None:
+            copy_dst = _new(stream, block_tables, copy_src.shape[0], torch.int32)
+        num_pairs = _new(stream, block_tables, 1, torch.int32) if num_pairs is None else num_pairs
+        _check_cuda("new_tables", new_tables, torch.int32, 2)
+        for name, t in (("new_ref_counts", new_ref_counts), ("copy_src", copy_src),
+                        ("copy_dst", copy_dst), ("num_pairs", num_pairs)):
+            _check_cuda(name, t, torch.int32, 1)
+        if new_tables.shape != block_tables.shape or new_ref_counts.shape != ref_counts.shape:
+            raise ValueError("the new tables and counts must have the old ones' shapes")
+        if copy_src.shape[0] < blocks // 2 or copy_dst.shape != copy_src.shape or \
+                num_pairs.shape[0] != 1:
+            raise ValueError("copy_src and copy_dst need num_blocks // 2 entries, num_pairs one")
+        for new, old in ((new_tables, block_tables), (new_ref_counts, ref_counts)):
+            if new.data_ptr() != old.data_ptr() and _overlap(new, old):
+                raise ValueError("the new tables and counts must be the old ones or apart")
+        ws = _pages_workspace(stream, block_tables, rows, blocks)
+        self.copy_src, self.copy_dst, self.num_pairs = copy_src, copy_dst, num_pairs
+        self._bind("pkv_compact_blocks", block_tables, stream,
+                   (_vp(block_tables.data_ptr()), _vp(context_lens.data_ptr()), _i32(rows),
+                    _i32(width), _vp(ref_counts.data_ptr()), _i32(blocks),
+                    _vp(new_tables.data_ptr()), _vp(new_ref_counts.data_ptr()),
+                    _vp(copy_src.data_ptr()), _vp(copy_dst.data_ptr()), _i32(copy_src.shape[0]),
+                    _vp(num_pairs.data_ptr()), _vp(ws.data_ptr()), _i64(ws.numel())),
+                   (block_tables, context_lens, ref_counts, new_tables, new_ref_counts, copy_src,
+                    copy_dst, num_pairs, ws), dev_status)
+
+
+def compact_blocks(block_tables, context_lens, ref_counts, *, new_tables=None, new_ref_counts=None,
+                   copy_src=None, copy_dst=None, num_pairs=None, dev_status=None, stream=None):
+    """Rename the blocks in use to the ids 0 .. L - 1 (pkv_compact_blocks), in place unless
+    new_tables / new_ref_counts are given.  Returns (copy_src, copy_dst, num_pairs) for the
+    copy_blocks that moves them: int32 [num_blocks // 2], -1 past the last pair, and their
+    number, int32 [1] on the device."""
+    b = BoundCompactBlocks(block_tables, context_lens, ref_counts, new_tables=new_tables,
+                           new_ref_counts=new_ref_counts, copy_src=copy_src, copy_dst=copy_dst,
+                           num_pairs=num_pairs, dev_status=dev_status, stream=stream)
+    b.run()
+    return b.copy_src, b.copy_dst, b.num_pairs
+
+
+_LOGIT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class BoundBeamSelect(_BoundCall):
+    """beam_select with its arguments checked and marshalled once."""
+
+    def __init__(self, logits, cum_scores, num_select: int, *, finished=None, pad_token=0,
+                 scores=None, tokens=None, parents=None, stream=None):
+        if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
+            raise TypeError("logits must be a CUDA tensor [requests, beams, vocab]")
+        if logits.dtype not in _LOGIT_TYPES:
+            raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+        b, k, v = logits.shape
+        row = logits.stride(1) if k > 1 else logits.stride(0) if b > 1 else v
+        if (v > 1 and logits.stride(2) != 1) or row < v or \
+                (b > 1 and k > 1 and logits.stride(0) != k * row):
+            raise ValueError("the rows of logits must be contiguous and equally far apart")
+        _check_cuda("cum_scores", cum_scores, torch.float32, 2)
+        if cum_scores.shape != (b, k):
+            raise ValueError(f"cum_scores must be [{b}, {k}]")
+        if finished is not None:
+            _check_cuda("finished", finished,
+                        torch.uint8 if finished.dtype == torch.uint8 else torch.bool, 2)
+            if finished.shape != (b, k):
+                raise ValueError(f"finished must be [{b}, {k}]")
+        m = int(num_select)
+        scores = _new(stream, logits, (b, m), torch.float32) if scores is None else scores
+        tokens = _new(stream, logits, (b, m), torch.int32) if tokens is None else tokens
+        parents = _new(stream, logits, (b, m), torch.int32) if parents is None else parents
+        for name, t, dtype in (("scores", scores, torch.float32), ("tokens", tokens, torch.int32),
+                               ("parents", parents, torch.int32)):
+            _check_cuda(name, t, dtype, 2)
+            if t.shape != (b, m):
+                raise ValueError(f"{name} must be [{b}, {m}]")
+            if _overlap(t, cum_scores):
+                raise ValueError(f"{name} must not overlap cum_scores")
+        ws = _new(stream, logits, max(int(_load().pkv_beam_workspace_size(b, k, v, m)), 16),
+                  torch.uint8)
+        self.scores, self.tokens, self.parents = scores, tokens, parents
+        self._bind("pkv_beam_select", logits, stream,
+                   (_vp(logits.data_ptr()), _i32(_LOGIT_TYPES[logits.dtype]), _i64(row),
+                    _vp(cum_scores.data_ptr()), _vp(_ptr(finished)), _i32(b), _i32(k), _i32(v),
+                    _i32(m), _i32(int(pad_token)), _vp(scores.data_ptr()), _vp(tokens.data_ptr()),
+                    _vp(parents.data_ptr()), _vp(ws.data_ptr()), _i64(ws.numel())),
+                   (logits, cum_scores, finished, scores, tokens, parents, ws), takes_status=False)
+
+
+def beam_select(logits, cum_scores, num_select: int, *, finished=None, pad_token=0, scores=None,
+                tokens=None, parents=None, stream=None):
+    """Beam search's selection (pkv_beam_select): of each request's candidates cum_scores[b, k]
+    + log_softmax(logits[b, k])[t] the num_select best, ties to the lower beam, then the lower
+    token.  Returns (scores fp32, tokens int32, parents int32), each [requests, num_select];
+    parents are row indices b * beams + k, as fork_sequences takes them.
+
+    logits: bf16, fp16 or fp32 [requests, beams, vocab], rows contiguous (they may be part of
+    a padded projection); cum_scores: fp32 [requests, beams] (-inf: a beam that is not there);
+    finished: bool [requests, beams], beams that go on as themselves with pad_token."""
+    b = BoundBeamSelect(logits, cum_scores, num_select, finished=finished, pad_token=pad_token,
+                        scores=scores, tokens=tokens, parents=parents, stream=stream)
+    b.run()
+    return b.scores, b.tokens, b.parents
+
+
+def block_index(num_blocks: int, num_kv_heads: int, head_dim: int, *, device="cuda"):
+    """An empty block index and its scales: (int8 [num_blocks, Hkv, 2, D], fp32
+    [num_blocks, Hkv])."""
+    return (torch.zeros((num_blocks, num_kv_heads, 2, head_dim), dtype=torch.int8, device=device),
+            torch.ones((num_blocks, num_kv_heads), dtype=torch.float32, device=device))
+
+
+def _check_index(index, index_scales):
+    _check_cuda("index", index, torch.int8, 4)
+    _check_cuda("index_scales", index_scales, torch.float32, 2)
+    nb, hkv, two, d = index.shape
+    if two != 2 or index_scales.shape != (nb, hkv):
+        raise ValueError("index must be [num_blocks, Hkv, 2, D] and index_scales [num_blocks, Hkv]")
+    return PoolDesc(nb, 16, hkv, d)
+
+
+class BoundIndexUpdate(_BoundCall):
+    """update_block_index with its arguments checked and marshalled once."""
+
+    def __init__(self, kv_pool, slot_mapping, index, index_scales, *, dev_status=None, stream=None):
+        _check_cuda("kv_pool", kv_pool, torch.bfloat16, 5)
+        _check_cuda("slot_mapping", slot_mapping, torch.int32, 1)
+        desc, of = pool_desc(kv_pool), _check_index(index, index_scales)
+        if (of.num_blocks, of.num_kv_heads, of.head_dim) != \
+                (desc.num_blocks, desc.num_kv_heads, desc.head_dim):
+            raise ValueError("index must have the pool's blocks, KV heads and head size")
+        self._bind("pkv_update_block_index", kv_pool, stream,
+                   (_vp(kv_pool.data_ptr()), ctypes.byref(desc), _vp(slot_mapping.data_ptr()),
+                    _i32(slot_mapping.shape[0]), _vp(index.data_ptr()),
+                    _vp(index_scales.data_ptr())),
+                   (kv_pool, slot_mapping, index, index_scales, desc), dev_status)
+
+
+def update_block_index(kv_pool, slot_mapping, index, index_scales, *, dev_status=None, stream=None):
+    """Make the bounds of the blocks that slot_mapping writes to anew from the pool, after the
+    append (pkv_update_block_index).  kv_pool: bf16; index, index_scales: block_index's."""
+    BoundIndexUpdate(kv_pool, slot_mapping, index, index_scales, dev_status=dev_status,
+                     stream=stream).run()
+
+
+def _check_step(q, cu_q_lens, context_lens, block_tables, hkv, d):
+    _check_cuda("q", q, torch.bfloat16, 3)
+    for name, t, ndim in (("cu_q_lens", cu_q_lens, 1), ("context_lens", context_lens, 1),
+                          ("block_tables", block_tables, 2)):
+        _check_cuda(name, t, torch.int32, ndim)
+    n = context_lens.shape[0]
+    if cu_q_lens.shape[0] != n + 1 or block_tables.shape[0] != n:
+        raise ValueError("cu_q_lens needs num_seqs + 1 entries and block_tables num_seqs rows")
+    if q.shape[2] != d or q.shape[1] % hkv != 0:
+        raise ValueError(f"q must be [total_q, a multiple of {hkv}, {d}]")
+
+
+class BoundSelectBlocks(_BoundCall):
+    """select_blocks with its arguments checked and marshalled once."""
+
+    def __init__(self, q, cu_q_lens, context_lens, block_tables, index, index_scales,
+                 num_select: int, *, sink_blocks=1, recent_blocks=2, selected=None, dev_status=None,
+                 stream=None):
+        desc = _check_index(index, index_scales)
+        hkv = desc.num_kv_heads
+        _check_step(q, cu_q_lens, context_lens, block_tables, hkv, desc.head_dim)
+        shape = (q.shape[0], hkv, int(num_select))
+        selected = _new(stream, q, shape, torch.int32) if selected is None else selected
+        _check_cuda("selected", selected, torch.int32, 3)
+        if selected.shape != shape:
+            raise ValueError(f"selected must be {list(shape)}")
+        width = block_tables.shape[1]
+        ws = _new(stream, q, max(int(_load().pkv_select_workspace_size(q.shape[0], hkv, width)), 16),
+                  torch.uint8)
+        self.selected = selected
+        self._bind("pkv_select_blocks", q, stream,
+                   (_vp(q.data_ptr()), _vp(cu_q_lens.data_ptr()), _vp(context_lens.data_ptr()),
+                    _vp(block_tables.data_ptr()), _i32(width), _i32(context_lens.shape[0]),
+                    _i64(q.shape[0]), _i32(q.shape[1]), _vp(index.data_ptr()),
+                    _vp(index_scales.data_ptr()), ctypes.byref(desc), _i32(int(num_select)),
+                    _i32(int(sink_blocks)), _i32(int(recent_blocks)), _vp(selected.data_ptr()),
+                    _vp(ws.data_ptr()), _i64(ws.numel())),
+                   (q, cu_q_lens, context_lens, block_tables, index, index_scales, selected, ws,
+                    desc), dev_status)
+
+
+def select_blocks(q, cu_q_lens, context_lens, block_tables, index, index_scales, num_select: int, *,
+                  sink_blocks=1, recent_blocks=2, selected=None, dev_status=None, stream=None):
+    """For each query token and KV head the num_select blocks to attend to (pkv_select_blocks):
+    the first sink_blocks, the last recent_blocks, and those with the largest bound of q . k.
+    Returns selected, int32 [total_q, Hkv, num_select]: logical blocks, ascending, then -1.
+
+    q: bf16 [total_q, Hq, D]; cu_q_lens, context_lens, block_tables: int32 CUDA tensors;
+    index, index_scales: kept by update_block_index."""
+    b = BoundSelectBlocks(q, cu_q_lens, context_lens, block_tables, index, index_scales, num_select,
+                          sink_blocks=sink_blocks, recent_blocks=recent_blocks, selected=selected,
+                          dev_status=dev_status, stream=stream)
+    b.run()
+    return b.selected
+
+
+class BoundSparseAttention(_BoundCall):
+    """paged_sparse_attention with its arguments checked and marshalled once."""
+
+    def __init__(self, q, cu_q_lens, context_lens, block_tables, selected, kv_pool, scale: float,
+                 out, *, dev_status=None, stream=None):
+        _check_cuda("kv_pool", kv_pool, torch.bfloat16, 5)
+        desc = pool_desc(kv_pool)
+        _check_step(q, cu_q_lens, context_lens, block_tables, desc.num_kv_heads, desc.head_dim)
+        _check_cuda("selected", selected, torch.int32, 3)
+        if selected.shape[:2] != (q.shape[0], desc.num_kv_heads):
+            raise ValueError(f"selected must be [{q.shape[0]}, {desc.num_kv_heads}, num_select]")
+        _check_cuda("out", out, torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if out.data_ptr() != q.data_ptr() and _overlap(out, q):
+            raise ValueError("out must be q or apart from it")
+        self.out = out
+        self._bind("pkv_paged_sparse_attention", q, stream,
+                   (_vp(q.data_ptr()), _vp(cu_q_lens.data_ptr()), _vp(context_lens.data_ptr()),
+                    _vp(block_tables.data_ptr()), _i32(block_tables.shape[1]),
+                    _i32(context_lens.shape[0]), _i64(q.shape[0]), _i32(q.shape[1]),
+                    _vp(selected.data_ptr()), _i32(selected.shape[2]), _vp(kv_pool.data_ptr()),
+                    ctypes.byref(desc), ctypes.c_float(scale), _vp(out.data_ptr())),
+                   (q, cu_q_lens, context_lens, block_tables, selected, kv_pool, out, desc),
+                   dev_status)
+
+
+def paged_sparse_attention(q, cu_q_lens, context_lens, block_tables, selected, kv_pool,
+                           scale: float, *, out=None, dev_status=None, stream=None):
+    """Attention of each query token over the keys it sees in the blocks selected for it
+    (pkv_paged_sparse_attention); returns out [total_q, Hq, D] bf16.
+
+    selected: int32 [total_q, Hkv, num_select] logical blocks (select_blocks' or a choice of
+    one's own; negative entries are skipped).  The lengths and tables are int32 CUDA tensors."""
+    out = _new(stream, q, q.shape, q.dtype) if out is None else out
+    b = BoundSparseAttention(q, cu_q_lens, context_lens, block_tables, selected, kv_pool, scale, out,
+                             dev_status=dev_status, stream=stream)
+    b.run()
+    return b.out

@@ -29,7 +29,7 @@ int device_sm_count() {
   return n;
 }
 
-constexpr int kNumKernelIds = 7;  // PKV_KERNEL_APPEND .. PKV_KERNEL_STAGE
+constexpr int kNumKernelIds = 13;  // PKV_KERNEL_APPEND .. PKV_KERNEL_SPARSE
 
 struct ProfileEvents {
   void *start[kNumKernelIds] = {};
@@ -57,9 +57,7 @@ bool profiling_active() {
   return false;
 }
 
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static pkv_status check_pool(const pkv_pool_desc *desc) {
+pkv_status check_pool(const pkv_pool_desc *desc) {
   if (!desc) return PKV_ERR_NULL;
   if (desc->block_size != kBlockSize) return PKV_ERR_UNSUPPORTED;
   if (desc->head_dim != 64 && desc->head_dim != 128) return PKV_ERR_UNSUPPORTED;
@@ -74,7 +72,7 @@ static pkv_status check_pool(const pkv_pool_desc *desc) {
 
 using namespace pkv;
 
-extern "C" int32_t pkv_version(void) { return 300; }
+extern "C" int32_t pkv_version(void) { return 400; }
 
 extern "C" int64_t pkv_kernel_launch_count(void) { return g_launches.load(); }
 

@@ -1,0 +1,548 @@
+// The block index of a bf16 pool and the selection of blocks by it.
+//
+// Index.  For each block and KV head, bounds of the keys in 8 bits: with s the smallest
+// power of two >= 2^-64 with |K| <= 127 s, lo = floor(min K / s), hi = ceil(max K / s).
+// For any q, sum_d max(q_d lo_d, q_d hi_d) s >= q . k for every key of the block.
+//
+// Score of a block for a query token and KV head: that bound summed over the G query
+// heads of the group, with q in 11 bits and a sign.  max(q lo, q hi) is q hi for q > 0 and
+// q lo for q < 0, so the sum over the heads needs two vectors only, P and N (the positive
+// and the negative parts, summed): 2 D products a block, whatever G.  All of it is
+// integer arithmetic (P, N in 16 bits, lo, hi in 8, the sum below 2^30), rounded once
+// to fp32 and scaled by a power of two: every order of summation gives the same score,
+// so the selection is reproducible to the last tie.
+//
+// Bound: the index bytes, 2 D + 4 a block and KV head, 1/32 of the block's K and V.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_sparse.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarpsCta = kThreads / 32;
+
+// Two bf16 of a word as floats; infinities and NaN as 0.
+__device__ __forceinline__ void finite_bf16x2(uint32_t w, float &a, float &b) {
+  a = __uint_as_float((w & 0x7f80u) == 0x7f80u ? 0u : w << 16);
+  b = __uint_as_float((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+__device__ __forceinline__ void finite_bf16x8(const uint4 &v, float *x) {
+  finite_bf16x2(v.x, x[0], x[1]);
+  finite_bf16x2(v.y, x[2], x[3]);
+  finite_bf16x2(v.z, x[4], x[5]);
+  finite_bf16x2(v.w, x[6], x[7]);
+}
+__device__ __forceinline__ float pow2f(int e) {  // 2^e, -126 <= e <= 127
+  return __int_as_float((e + 127) << 23);
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---------------------------------------------------------------- index update
+//
+// One warp a (token, KV head).  Of a block's tokens in the step the one with the largest
+// offset makes the bounds, from the block's rows up to it (read back from the pool: a
+// slot written again after rejected tokens gives the bounds of what is there now).
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    index_update_kernel(const uint4 *__restrict__ pool, const int32_t *__restrict__ slots,
+                        int32_t num_tokens, int32_t num_blocks, int32_t hkv,
+                        int8_t *__restrict__ index, float *__restrict__ scales,
+                        int32_t *dev_status) {
+  constexpr int kLanes = D / 8;          // lanes of a key row, 8 elements each
+  constexpr int kRows = 32 / kLanes;     // rows of one warp load
+  constexpr int kLoads = kBlockSize / kRows;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kWarpsCta + (threadIdx.x >> 5);
+  if (unit >= (int64_t)num_tokens * hkv) return;
+  const int32_t t = (int32_t)(unit / hkv), h = (int32_t)(unit % hkv);
+  const int32_t slot = __ldg(slots + t);
+  if (slot < 0) return;
+  const int32_t block = slot / kBlockSize, off = slot % kBlockSize;
+  if (block >= num_blocks) {
+    if (h == 0 && lane == 0) report(dev_status, PKV_DEV_BAD_SLOT);
+    return;
+  }
+  // another token within 15 that writes further into the block (or the same slot, later)
+  const int64_t o = (int64_t)t - 15 + lane;
+  bool other = false;
+  if (lane < 31 && o != t && o >= 0 && o < num_tokens) {
+    const int32_t s = __ldg(slots + o);
+    other = s >= 0 && s / kBlockSize == block && (s > slot || (s == slot && o > t));
+  }
+  if (__any_sync(0xffffffffu, other)) return;
+  const uint4 *rows = pool + ((int64_t)block * 2 * hkv + h) * kBlockSize * kLanes;
+  uint4 v[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u)
+    if (u * kRows + lane / kLanes <= off) v[u] = ldg128(rows + u * 32 + lane);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = INFINITY;
+    hi[i] = -INFINITY;
+  }
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u)
+    if (u * kRows + lane / kLanes <= off) {
+      float x[8];
+      finite_bf16x8(v[u], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = fminf(lo[i], x[i]);
+        hi[i] = fmaxf(hi[i], x[i]);
+      }
+    }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int w = kLanes; w < 32; w <<= 1) {
+      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], w));
+      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], w));
+    }
+    top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+  }
+  top = warp_max(top);
+  // top is 1.f 2^E with 7 bits of f; 127 = 1.984375 2^6 has f = 126
+  const uint32_t bits = __float_as_uint(top);
+  const int e = max((int)(bits >> 23) - 127 - 6 + ((bits >> 16 & 127u) == 127u), -64);
+  const float inv = pow2f(-e);
+  uint32_t w[2][2] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // a product that underflows to 0 is still below (above) 0
+    const float a = lo[i] * inv, b = hi[i] * inv;
+    const int f = a == 0.f && lo[i] < 0.f ? -1 : __float2int_rd(a);
+    const int c = b == 0.f && hi[i] > 0.f ? 1 : __float2int_ru(b);
+    w[0][i >> 2] |= (uint32_t)(f & 255) << (8 * (i & 3));
+    w[1][i >> 2] |= (uint32_t)(c & 255) << (8 * (i & 3));
+  }
+  const int64_t row = (int64_t)block * hkv + h;
+  if (lane < 2 * kLanes) {  // the second set of lanes (the same values) writes hi
+    const bool up = lane >= kLanes;
+    *reinterpret_cast<uint2 *>(index + row * 2 * D + (up ? D : 0) + (lane % kLanes) * 8) =
+        make_uint2(up ? w[1][0] : w[0][0], up ? w[1][1] : w[0][1]);
+  }
+  if (lane == 0) scales[row] = pow2f(e);
+}
+
+// ---------------------------------------------------------------- scores
+
+struct SelectParams {
+  const __nv_bfloat16 *q;
+  const int32_t *cu_q_lens, *context_lens, *block_tables;
+  const int8_t *index;
+  const float *scales;
+  float *scores;          // [tokens of the pass][Hkv][stride]
+  int32_t *selected;
+  int64_t token0;         // first token of the pass
+  int64_t stride;
+  int32_t max_blocks, num_seqs, num_blocks, num_q_heads, hkv, group;
+  int32_t num_select, sink, recent;
+  int32_t chunk, chunks;  // blocks of a CTA's range, ranges of a token
+  int32_t *dev_status;
+};
+
+// CTAs (token, range of blocks); a warp takes one KV head (or a part of the range where
+// there are fewer heads than warps), so the CTA reads the heads of a block together.
+// LPR lanes hold a block's 2 D bytes, 16 each, against weights that stay in registers;
+// eight loads are in flight a lane, and their sums over the lanes are transposed on the
+// way (8 shuffles for 16 or 32 blocks).
+template <int D>
+__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
+  constexpr int kLpr = 2 * D / 16;     // lanes of an index row
+  constexpr int kRpi = 32 / kLpr;      // blocks of one warp load
+  constexpr int kUnroll = 8;
+  constexpr int kBatch = kRpi * kUnroll;
+  __shared__ int32_t s_sum[kWarpsCta];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t local = blockIdx.x / p.chunks;
+  const TokenPlace at = find_token(p.cu_q_lens, p.context_lens, p.num_seqs, p.token0 + local, s_sum);
+  const int32_t nb = at.pos / kBlockSize + 1;  // 0 when the token has no place
+  const int32_t b_lo = max((int32_t)(blockIdx.x % p.chunks) * p.chunk, p.sink);
+  const int32_t b_hi = min((int32_t)(blockIdx.x % p.chunks) * p.chunk + p.chunk, nb - p.recent);
+  // (a token without a place, or whose blocks are all selected: nothing to score)
+  if (at.pos < 0 || nb > p.max_blocks || nb <= p.num_select || b_lo >= b_hi) {
+    pdl_wait();
+    return;
+  }
+  const int32_t *table = p.block_tables + (int64_t)at.seq * p.max_blocks;
+  const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
+  const int32_t sub_len = (p.chunk / subs + kBatch - 1) / kBatch * kBatch;
+  bool waited = false;
+  for (int item = warp; item < p.hkv * subs; item += kWarpsCta) {
+    const int h = item % p.hkv;
+    const int32_t c0 = (int32_t)(blockIdx.x % p.chunks) * p.chunk + item / p.hkv * sub_len;
+    const int32_t lo = max(c0, b_lo), hi = min(c0 + sub_len, b_hi);
+    // this lane's weights: of 16 elements from d0, N against lo or P against hi
+    const int d0 = lane % (D / 16) * 16;
+    const bool up = lane % kLpr >= D / 16;
+    const __nv_bfloat16 *q =
+        p.q + ((p.token0 + local) * p.num_q_heads + (int64_t)h * p.group) * D + d0;
+    float top = 0.f;
+    for (int g = 0; g < p.group; ++g) {
+      float x[16];
+      finite_bf16x8(ldg128_nc(q + g * D), x);
+      finite_bf16x8(ldg128_nc(q + g * D + 8), x + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+    }
+    top = warp_max(top);
+    // u = 2^(E - 10) for top = 1.f 2^E (7 bits of f: below 2047 / 1024); q / u in two
+    // exact steps
+    int e = 0;
+    if (top > 0.f) e = 10 - ((int)(__float_as_uint(top * 16777216.f) >> 23) - 127 - 24);
+    if (top >= 16777216.f) e = 10 - ((int)(__float_as_uint(top) >> 23) - 127);
+    const float f1 = pow2f(e >> 1), f2 = pow2f(e - (e >> 1));
+    int32_t sum[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = 0;
+    for (int g = 0; g < p.group; ++g) {
+      float x[16];
+      finite_bf16x8(ldg128_nc(q + g * D), x);
+      finite_bf16x8(ldg128_nc(q + g * D + 8), x + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        sum[i] += __float2int_rn((up ? fmaxf(x[i], 0.f) : fminf(x[i], 0.f)) * f1 * f2);
+    }
+    int32_t wt[8];  // 16-bit pairs
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wt[i] = (sum[2 * i] & 0xffff) | sum[2 * i + 1] << 16;
+    if (!waited) {
+      pdl_wait();  // the index and the scores' space
+      waited = true;
+    }
+    float *out = p.scores + (local * p.hkv + h) * p.stride;
+    for (int32_t b0 = lo; b0 < hi; b0 += kBatch) {
+      // lane i: block b0 + i of the batch, its id and scale
+      int32_t phys = -1;
+      if (lane < kBatch && b0 + lane < hi) {
+        phys = __ldg(table + b0 + lane);
+        if (phys < 0 || phys >= p.num_blocks) {
+          phys = -1;
+          report(p.dev_status, PKV_DEV_BAD_BLOCK);
+        }
+      }
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int32_t ph = __shfl_sync(0xffffffffu, phys, u * kRpi + lane / kLpr);
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (ph >= 0)
+          v[u] = ldg128_nc(p.index + ((int64_t)ph * p.hkv + h) * 2 * D + lane % kLpr * 16);
+      }
+      // the block whose score this lane ends up with
+      const int mine = kLpr == 16 ? (lane >> 1 & 7) * 2 + (lane >> 4) : (lane & 7) * 4 + (lane >> 3);
+      const int32_t ph = __shfl_sync(0xffffffffu, phys, mine);
+      const float scale = ph >= 0 ? __ldg(p.scales + (int64_t)ph * p.hkv + h) : 0.f;
+      int32_t a[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        int32_t s = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s = __dp2a_lo(wt[2 * i], (int32_t)w[i], s);
+          s = __dp2a_hi(wt[2 * i + 1], (int32_t)w[i], s);
+        }
+        a[u] = s;
+      }
+      // sums over the kLpr lanes of a row: halve the values and the lanes together
+      int width = kLpr / 2;
+#pragma unroll
+      for (int n = kUnroll / 2; n >= 1; n >>= 1) {
+        const bool upper = (lane & width) != 0;
+#pragma unroll
+        for (int u = 0; u < n; ++u) {
+          const int32_t keep = upper ? a[u + n] : a[u], send = upper ? a[u] : a[u + n];
+          a[u] = keep + __shfl_xor_sync(0xffffffffu, send, width);
+        }
+        width >>= 1;
+      }
+      if (kLpr == 16) a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
+      if (b0 + mine < hi && (kLpr == 8 || (lane & 1) == 0))
+        out[b0 + mine] = ph >= 0 ? __int2float_rn(a[0]) * scale : -INFINITY;
+    }
+  }
+  if (!waited) pdl_wait();
+}
+
+// ---------------------------------------------------------------- selection
+//
+// One CTA a (token, KV head): the threshold, the score of the last block taken, by
+// histograms of 2048 bins over the scores' range (at most three, each over the bin
+// before), then one ordered pass that writes the blocks above it and the first of those
+// equal to it.
+constexpr int kBins = 2048;
+constexpr int kCached = 8192;  // scores kept in shared memory; longer rows are read again
+
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
+  __shared__ uint32_t s_key[kCached];
+  __shared__ int32_t s_bin[kBins];
+  __shared__ int32_t s_sum[kWarpsCta];
+  __shared__ uint32_t s_min[kWarpsCta], s_max[kWarpsCta];
+  __shared__ int32_t s_found, s_above;
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t local = blockIdx.x / p.hkv;
+  const int h = (int)(blockIdx.x % p.hkv);
+  const int64_t token = p.token0 + local;
+  const TokenPlace at = find_token(p.cu_q_lens, p.context_lens, p.num_seqs, token, s_sum);
+  int32_t *out = p.selected + (token * p.hkv + h) * p.num_select;
+  const int32_t K = p.num_select;
+  int32_t nb = at.pos / kBlockSize + 1;
+  pdl_wait();
+  if (at.pos < 0 || nb > p.max_blocks) {
+    if (h == 0 && tid == 0 && at.seq < p.num_seqs) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
+    nb = 0;
+  }
+  if (nb <= K) {
+    for (int i = tid; i < K; i += kThreads) out[i] = i < nb ? i : -1;
+    return;
+  }
+  for (int i = tid; i < p.sink; i += kThreads) out[i] = i;
+  for (int i = tid; i < p.recent; i += kThreads) out[K - p.recent + i] = nb - p.recent + i;
+  const int32_t need = K - p.sink - p.recent, n = nb - p.sink - p.recent;  // n > need
+  if (need == 0) return;
+  const float *scores = p.scores + (local * p.hkv + h) * p.stride + p.sink;
+  auto key_of = [](float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+  };
+  uint32_t lo = ~0u, hi = 0;
+  for (int32_t i = tid; i < n; i += kThreads) {
+    const uint32_t k = key_of(scores[i]);
+    if (i < kCached) s_key[i] = k;
+    lo = min(lo, k);
+    hi = max(hi, k);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    s_min[warp] = lo;
+    s_max[warp] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarpsCta; ++w) {
+    lo = min(lo, s_min[w]);
+    hi = max(hi, s_max[w]);
+  }
+  auto key_at = [&](int32_t i) { return i < kCached ? s_key[i] : key_of(scores[i]); };
+  // keys of [lo, lo + 2^bits): the need-th largest lies there, `above` keys beyond it
+  int bits = 32 - __clz(hi - lo);
+  int32_t above = 0;
+  while (bits > 0) {
+    const int shift = max(bits - 11, 0);
+    for (int i = tid; i < kBins; i += kThreads) s_bin[i] = 0;
+    __syncthreads();
+    for (int32_t i = tid; i < n; i += kThreads) {
+      const uint32_t k = key_at(i) - lo;
+      if (bits == 32 || (k >> bits) == 0) atomicAdd(s_bin + (k >> shift), 1);
+    }
+    __syncthreads();
+    // thread t: bins [8 (255 - t), +8), from the top down
+    constexpr int kPer = kBins / kThreads;
+    const int base = kPer * (kThreads - 1 - tid);
+    int32_t own = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) own += s_bin[base + u];
+    int32_t x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int32_t before = above + x - own;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    if (before < need && before + own >= need) {  // one thread
+      int32_t c = before;
+      for (int u = kPer - 1; u >= 0; --u) {
+        if (c + s_bin[base + u] >= need) {
+          s_found = base + u;
+          s_above = c;
+          break;
+        }
+        c += s_bin[base + u];
+      }
+    }
+    __syncthreads();
+    lo += (uint32_t)s_found << shift;
+    above = s_above;
+    bits = shift;
+    __syncthreads();
+  }
+  // lo is the threshold; `above` keys are larger, the first need - above equal ones go along
+  const int32_t ties = need - above;
+  const int32_t per = ((n + kThreads - 1) / kThreads) | 1;  // odd: no bank conflicts
+  const int32_t i0 = (int32_t)min((int64_t)tid * per, (int64_t)n), i1 = min(i0 + per, n);
+  int32_t gt = 0, eq = 0;
+  for (int32_t i = i0; i < i1; ++i) {
+    const uint32_t k = key_at(i);
+    gt += k > lo;
+    eq += k == lo;
+  }
+  int32_t x = gt, y = eq;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
+  }
+  if (lane == 31) {
+    s_min[warp] = (uint32_t)x;
+    s_max[warp] = (uint32_t)y;
+  }
+  __syncthreads();
+  int32_t gt0 = x - gt, eq0 = y - eq;
+  for (int w = 0; w < warp; ++w) {
+    gt0 += (int32_t)s_min[w];
+    eq0 += (int32_t)s_max[w];
+  }
+  for (int32_t i = i0; i < i1; ++i) {
+    const uint32_t k = key_at(i);
+    const bool tie = k == lo;
+    if (k > lo || (tie && eq0 < ties)) out[p.sink + gt0 + min(eq0, ties)] = p.sink + i;
+    gt0 += k > lo;
+    eq0 += tie;
+  }
+}
+
+template <int D>
+int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_stream stream) {
+  if (prepare_kernel<score_kernel<D>>(0) != cudaSuccess ||
+      prepare_kernel<select_kernel>(0) != cudaSuccess)
+    return (int)cudaErrorUnknown;
+  const bool pdl = !profiling_active();
+  for (int64_t t0 = 0; t0 < total_q; t0 += pass_tokens) {
+    const int64_t n = std::min(pass_tokens, total_q - t0);
+    p.token0 = t0;
+    // ranges of a token: enough for four CTAs an SM, of 16 to 256 blocks
+    const int64_t want = (n * p.max_blocks) / (4ll * std::max(device_sm_count(), 1));
+    p.chunk = (int32_t)std::min<int64_t>(std::max<int64_t>((want + 15) / 16 * 16, 16), 256);
+    const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
+    p.chunk *= subs;
+    p.chunks = (p.max_blocks + p.chunk - 1) / p.chunk;
+    cudaError_t e = launch_kernel(score_kernel<D>, dim3((unsigned)(n * p.chunks)), dim3(kThreads), 0,
+                                  stream, pdl, p);
+    if (e == cudaSuccess)
+      e = launch_kernel(select_kernel, dim3((unsigned)(n * p.hkv)), dim3(kThreads), 0, stream, pdl, p);
+    if (e != cudaSuccess) return (int)e;
+    count_launches(2);
+  }
+  return (int)cudaGetLastError();
+}
+
+// fp32 scores of a token: [Hkv][max_blocks, padded to 16 bytes]
+int64_t score_bytes(int64_t hkv, int64_t max_blocks) { return hkv * align_up(max_blocks * 4, 16); }
+constexpr int64_t kMaxWorkspace = 512ll << 20;
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_desc *desc,
+                                             const int32_t *slot_mapping, int32_t num_tokens,
+                                             int8_t *index, float *index_scales,
+                                             int32_t *dev_status, pkv_stream stream) {
+  const pkv_status st = check_pool(desc);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0) return PKV_ERR_SHAPE;
+  if (num_tokens == 0) return PKV_OK;
+  if (!kv_pool || !slot_mapping || !index || !index_scales) return PKV_ERR_NULL;
+  if (!aligned16(kv_pool) || !aligned16(index) || !aligned16(index_scales) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 3u))
+    return PKV_ERR_ALIGN;
+  const int64_t units = (int64_t)num_tokens * desc->num_kv_heads;
+  const int64_t ctas = (units + kWarpsCta - 1) / kWarpsCta;
+  if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  const bool wide = desc->head_dim == 128;
+  profile_begin(PKV_KERNEL_INDEX, stream);
+  cudaError_t e = launch_kernel(wide ? index_update_kernel<128> : index_update_kernel<64>,
+                                dim3((unsigned)ctas), dim3(kThreads), 0, stream, false,
+                                static_cast<const uint4 *>(kv_pool), slot_mapping, num_tokens,
+                                desc->num_blocks, desc->num_kv_heads, index, index_scales,
+                                dev_status);
+  profile_end(PKV_KERNEL_INDEX, stream);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return PKV_ERR_CUDA;
+  count_launches(1);
+  return PKV_OK;
+}
+
+extern "C" size_t pkv_select_workspace_size(int64_t total_q, int32_t num_kv_heads,
+                                            int32_t max_blocks_per_seq) {
+  if (total_q <= 0 || num_kv_heads < 1 || max_blocks_per_seq < 1) return 0;
+  const int64_t token = score_bytes(num_kv_heads, max_blocks_per_seq);
+  return (size_t)(std::min(total_q, std::max<int64_t>(kMaxWorkspace / token, 1)) * token);
+}
+
+extern "C" pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
+                                        const int32_t *context_lens, const int32_t *block_tables,
+                                        int32_t max_blocks_per_seq, int32_t num_seqs,
+                                        int64_t total_q, int32_t num_q_heads, const int8_t *index,
+                                        const float *index_scales, const pkv_pool_desc *desc,
+                                        int32_t num_select, int32_t sink_blocks,
+                                        int32_t recent_blocks, int32_t *selected, void *workspace,
+                                        int64_t workspace_bytes, int32_t *dev_status,
+                                        pkv_stream stream) {
+  pkv_status st = check_pool(desc);
+  if (st != PKV_OK) return st;
+  st = check_sparse(desc, max_blocks_per_seq, num_seqs, total_q, num_q_heads, num_select);
+  if (st != PKV_OK) return st;
+  if (sink_blocks < 0 || recent_blocks < 1 || (int64_t)sink_blocks + recent_blocks > num_select)
+    return PKV_ERR_RANGE;
+  if (total_q == 0) return PKV_OK;
+  if (!q || !cu_q_lens || !context_lens || !block_tables || !index || !index_scales || !selected ||
+      !workspace)
+    return PKV_ERR_NULL;
+  if (!aligned16(q) || !aligned16(index) || (reinterpret_cast<uintptr_t>(index_scales) & 3u) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(selected) & 3u))
+    return PKV_ERR_ALIGN;
+  const int64_t token = score_bytes(desc->num_kv_heads, max_blocks_per_seq);
+  if (workspace_bytes < token) return PKV_ERR_WORKSPACE;
+  SelectParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.cu_q_lens = cu_q_lens;
+  p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.index = index;
+  p.scales = index_scales;
+  p.scores = static_cast<float *>(workspace);
+  p.selected = selected;
+  p.stride = align_up((int64_t)max_blocks_per_seq * 4, 16) / 4;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_blocks = desc->num_blocks;
+  p.num_q_heads = num_q_heads;
+  p.hkv = desc->num_kv_heads;
+  p.group = num_q_heads / desc->num_kv_heads;
+  p.num_select = num_select;
+  p.sink = sink_blocks;
+  p.recent = recent_blocks;
+  p.dev_status = dev_status;
+  // a pass: what the workspace holds, within the grid's size
+  int64_t pass = std::min(workspace_bytes / token, total_q);
+  pass = std::min(pass, (int64_t)INT32_MAX / std::max((max_blocks_per_seq + 15) / 16, p.hkv));
+  profile_begin(PKV_KERNEL_SELECT, stream);
+  const int e = desc->head_dim == 128 ? launch_select_t<128>(p, total_q, pass, stream)
+                                      : launch_select_t<64>(p, total_q, pass, stream);
+  profile_end(PKV_KERNEL_SELECT, stream);
+  return e ? PKV_ERR_CUDA : PKV_OK;
+}

@@ -307,6 +307,10 @@ int launch_prefill(const AttnArgs &a, int *launches);
 // head's blocks together (the copies of an 8-bit pool's blocks).
 int make_pool_map(void *map, const void *pool, const pkv_pool_desc &desc, int blocks = 1);
 
+// Checks the entry points share (pkv_api.cu).
+pkv_status check_pool(const pkv_pool_desc *desc);
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 void count_launches(int n);
 
 // Streaming multiprocessors of the calling thread's current device (cached per
