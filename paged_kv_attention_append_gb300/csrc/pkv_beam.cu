@@ -6,15 +6,17 @@
 //
 // Within a beam the score grows with the logit, so the best of a beam are its largest
 // logits and need no logarithm.  The logits are read once: a CTA goes over a range of
-// one row in tiles that stay in registers and takes from them, at the same time,
-//  - the running maximum and sum of exponentials (per thread, rescaled when its maximum
-//    moves; joined over the CTA at the end);
+// one row in tiles and takes from them, at the same time,
+//  - the running sum of exponentials: a thread keeps s = sum 2^(x L - r), with L fp32's
+//    log2 e and r its maximum of x L so far (one fma and one ex2 an element; s is rescaled
+//    when r moves).  The row's lse is (r + log2 s) / L: as the same L divides it, its
+//    rounding (2^-26 of L) moves the lse by 2^-26 times the softmax's entropy only;
 //  - the candidates: 64-bit keys (logit, lowest token first), so that no two are equal.
 //    A threshold T below the num_select-th largest key comes from the threads' maxima of
 //    the first tile; keys above T go to a buffer in shared memory, which is cut to its
-//    num_select largest (and T raised) when it fills.  After the first tile hardly any
-//    key passes: the expected number is num_select ln(tiles).
-// A second kernel, one warp a request, joins the rows' sums and merges the sorted lists
+//    num_select largest (and T raised) when it fills.  After the first tile few keys pass:
+//    num_select / i of the i-th tile are expected.
+// A second kernel, one CTA a request, joins the rows' sums and merges the sorted lists
 // by score in 64 bits.
 //
 // Which elements a thread sums depends on their place in the row alone, not on the row's
@@ -36,8 +38,8 @@ constexpr int kBeamWarps = kThreads / 32;
 constexpr int kMaxSelect = 128;
 constexpr int kBuffer = 512;        // candidate keys a CTA keeps (>= 2 kMaxSelect)
 constexpr int kMaxLists = 1024;     // sorted lists (beam, split) of a request
-constexpr int kVec = 8;             // consecutive elements a thread loads together
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMergeScores = 2048;  // scores a merge keeps in shared memory (>= kMaxLists)
+constexpr float kLog2e = 1.4426950408889634f;  // L above
 
 struct BeamParams {
   const void *logits;
@@ -45,7 +47,7 @@ struct BeamParams {
   const uint8_t *finished;
   float *scores;
   int32_t *tokens, *parents;
-  float2 *part;          // [rows][splits]: maximum, sum of exp(x - maximum)
+  float2 *part;          // [rows][splits]: r, sum of 2^(x L - r)
   uint64_t *keys;        // [rows][splits][num_select], descending, 0: none
   int64_t row_stride;
   int32_t num_beams, vocab, num_select, pad_token, splits, tiles;
@@ -62,27 +64,68 @@ __device__ __forceinline__ float key_value(uint64_t k) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Elements [at, at + 8) of a row; those past its end as -inf.
+// How a type's elements lie in 32-bit words, and its -inf.
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int32_t at, int32_t vocab, bool aligned,
-                                      float *x) {
+struct Words;
+template <>
+struct Words<float> {
+  static constexpr int kPer = 1;
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  static __device__ __forceinline__ float get(uint32_t w, int) { return __uint_as_float(w); }
+};
+template <>
+struct Words<__nv_bfloat16> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kNegInf = 0xff80u;
+  static __device__ __forceinline__ float get(uint32_t w, int i) {
+    return __uint_as_float(i ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct Words<__half> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kNegInf = 0xfc00u;
+  static __device__ __forceinline__ float get(uint32_t w, int i) {
+    return __half2float(__ushort_as_half((uint16_t)(i ? w >> 16 : w)));
+  }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t raw_bits(const T *p) {
+  if (sizeof(T) == 4) return __ldg(reinterpret_cast<const uint32_t *>(p));
+  return __ldg(reinterpret_cast<const uint16_t *>(p));
+}
+
+// Elements [at, at + kVec) of a row, as they lie in memory; those past its end as -inf.
+template <typename T, int kVec>
+__device__ __forceinline__ void load_vec(const T *row, int32_t at, int32_t vocab, bool aligned,
+                                         uint32_t *w) {
+  using W = Words<T>;
+  constexpr int kWords = kVec / W::kPer;
   if (aligned && at + kVec <= vocab) {
-    union {
-      uint4 v[sizeof(T) * kVec / 16];
-      T e[kVec];
-    } u;
+    if (kWords == 2) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row + at));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) * kVec / 16); ++i)
-      u.v[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at) + i);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = to_float(u.e[i]);
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + at) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = at + i < vocab ? to_float(row[at + i]) : -INFINITY;
+    for (int i = 0; i < kWords; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < W::kPer; ++j) {
+        const int e = at + i * W::kPer + j;
+        w[i] |= (e < vocab ? raw_bits(row + e) : W::kNegInf) << (16 * j);
+      }
+    }
   }
 }
 
@@ -122,14 +165,19 @@ __device__ __forceinline__ void sort_buffer(uint64_t *s_buf, int cnt, int keep) 
     k[u] = i < cnt ? s_buf[i] : 0;
     rank[u] = 0;
   }
-  if (cnt <= kThreads) {
-    for (int j = 0; j < cnt; ++j) rank[0] += s_buf[j] > k[0];
-  } else {
+  if (cnt > kThreads) {
     for (int j = 0; j < cnt; ++j) {
       const uint64_t o = s_buf[j];
 #pragma unroll
       for (int u = 0; u < kBuffer / kThreads; ++u) rank[u] += o > k[u];
     }
+  } else if ((int)(threadIdx.x & ~31) < cnt) {  // (a warp without a key has no ranks to find)
+    int j = 0;
+    for (; j + 1 < cnt; j += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(s_buf + j);
+      rank[0] += (o.x > k[0]) + (o.y > k[0]);
+    }
+    if (j < cnt) rank[0] += s_buf[j] > k[0];
   }
   __syncthreads();
 #pragma unroll
@@ -138,14 +186,41 @@ __device__ __forceinline__ void sort_buffer(uint64_t *s_buf, int cnt, int keep) 
   __syncthreads();
 }
 
-template <typename T, int kElems>
-__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
-  __shared__ uint64_t s_buf[kBuffer];
+// A key that at least M of the threads' keys `k` reach (0: fewer have one): every warp's
+// M-th largest is one, and so is the smallest over the warps of their ceil(M / 8)-th.
+__device__ __forceinline__ uint64_t threads_threshold(uint64_t k, int M, uint64_t *s_warp) {
+  const int warp = threadIdx.x >> 5;
+  k = warp_sort(k);
+  const uint64_t k1 = M <= 32 ? __shfl_sync(0xffffffffu, k, (M - 1) & 31) : 0;
+  const uint64_t k2 = __shfl_sync(0xffffffffu, k, (M + kBeamWarps - 1) / kBeamWarps - 1);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    s_warp[warp] = k1;
+    s_warp[kBeamWarps + warp] = k2;
+  }
+  __syncthreads();
+  uint64_t t1 = 0, t2 = ~0ull;
+#pragma unroll
+  for (int w = 0; w < kBeamWarps; ++w) {
+    t1 = max(t1, s_warp[w]);
+    t2 = min(t2, s_warp[kBeamWarps + w]);
+  }
+  return max(t1, t2);
+}
+
+// A tile is 2 kHalf elements a thread, in two sets of registers: each is filled again as
+// soon as it has been used, so loads are always in flight.
+template <typename T, int kHalf>
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams p) {
+  using W = Words<T>;
+  constexpr int kVec = kHalf < 8 ? kHalf : 8;  // consecutive elements a thread loads together
+  constexpr int kWords = kHalf / W::kPer;
+  constexpr int kHalfTile = kThreads * kHalf, kTile = 2 * kHalfTile;
+  __shared__ alignas(16) uint64_t s_buf[kBuffer];
   __shared__ uint64_t s_warp[2 * kBeamWarps];
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
   __shared__ int32_t s_sum[kBeamWarps];
   __shared__ int32_t s_cnt;
-  constexpr int kTile = kThreads * kElems;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row_id = blockIdx.x / p.splits;
@@ -156,140 +231,169 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   const int tile0 = (int)((int64_t)p.tiles * split / p.splits);
   const int tile1 = (int)((int64_t)p.tiles * (split + 1) / p.splits);
   const int M = p.num_select;
-  float m = -INFINITY, s = 0.f;
+  float r = -INFINITY, s = 0.f;
   uint64_t T_key = 0;       // candidates are the keys above this
   float T_val = -INFINITY;  // its logit: a cheaper test that lets through no fewer
+  int cnt = 0;              // keys in the buffer
   if (tid == 0) s_cnt = 0;
-  for (int tile = tile0; tile < tile1; ++tile) {
-    const int32_t at0 = tile * kTile + tid * kVec;
-    float x[kElems];
+  // element i < 2 kHalf of this thread's in a tile
+  auto token = [&](int tile, int i) {
+    return tile * kTile + i / kVec * kThreads * kVec + tid * kVec + i % kVec;
+  };
+  auto key_at = [&](int at) {
+    return at < p.vocab ? make_key(W::get(raw_bits(row + at), 0), at) : (uint64_t)0;
+  };
+  uint32_t w[2][kWords];
+  auto load = [&](int tile, int half) {
 #pragma unroll
-    for (int j = 0; j < kElems / kVec; ++j)
-      load8(row, at0 + j * kThreads * kVec, p.vocab, aligned, x + j * kVec);
+    for (int j = 0; j < kHalf / kVec; ++j)
+      load_vec<T, kVec>(row, token(tile, half * kHalf + j * kVec), p.vocab, aligned,
+                        w[half] + j * (kVec / W::kPer));
+  };
+  auto elements = [&](int half, float (&x)[kHalf]) {  // returns the largest
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) x[i] = W::get(w[half][i / W::kPer], i % W::kPer);
     float top = x[0];
 #pragma unroll
-    for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
-    const float m_new = fmaxf(m, top);
-    if (m_new > -INFINITY) {
-      s *= fast_exp2((m - m_new) * kLog2e);
+    for (int i = 1; i < kHalf; i += 2)
+      top = i + 1 < kHalf ? max3(top, x[i], x[i + 1]) : fmaxf(top, x[i]);
+    return top;
+  };
+  // half a tile into the sum; its elements at or above T_val as bits
+  auto use = [&](int half) {
+    float x[kHalf];
+    const float top = elements(half, x);
+    const float r_new = fmaxf(r, top * kLog2e);
+    if (r_new > -INFINITY) {
+      s *= fast_exp2(r - r_new);
       float a = 0.f, b = 0.f;
 #pragma unroll
-      for (int i = 0; i < kElems; i += 2) {
-        a += fast_exp2((x[i] - m_new) * kLog2e);
-        b += fast_exp2((x[i + 1] - m_new) * kLog2e);
+      for (int i = 0; i < kHalf; i += 2) {
+        a += fast_exp2(fmaf(x[i], kLog2e, -r_new));
+        b += fast_exp2(fmaf(x[i + 1], kLog2e, -r_new));
       }
       s += a + b;
-      m = m_new;
+      r = r_new;
     } else {
 #pragma unroll
-      for (int i = 0; i < kElems; ++i)  // all masked; a NaN makes the row's sum NaN
+      for (int i = 0; i < kHalf; ++i)  // all masked; a NaN makes the row's sum NaN
         if (x[i] != x[i]) s = x[i];
     }
-    auto token = [&](int i) { return at0 + (i / kVec) * kThreads * kVec + i % kVec; };
-    auto count_above = [&](uint64_t t) {
-      int32_t n = 0;
+    uint32_t some = 0;
+    if (!(top < T_val)) {
 #pragma unroll
-      for (int i = 0; i < kElems; ++i) n += token(i) < p.vocab && make_key(x[i], token(i)) > t;
-      return n;
-    };
-    if (tile == tile0) {
-      // every warp's M-th largest thread maximum is a lower bound of the M-th largest
-      // key, and so is the smallest over the warps of their ceil(M / 8)-th
-      int32_t at = at0;
-      float best = x[0];
+      for (int i = 0; i < kHalf; ++i) some |= (uint32_t)!(x[i] < T_val) << i;
+    }
+    return some << (half * kHalf);
+  };
+  load(tile0, 0);
+  load(tile0, 1);
+  {
+    uint64_t k = 0;  // this thread's largest key of the first tile
 #pragma unroll
-      for (int i = 1; i < kElems; ++i)
-        if (x[i] > best) {
-          best = x[i];
-          at = token(i);
+    for (int half = 0; half < 2; ++half) {
+      float x[kHalf];
+      const float top = elements(half, x);
+      int at = 0;
+#pragma unroll
+      for (int i = kHalf - 1; i >= 0; --i)
+        if (x[i] == top) at = i;
+      at = token(tile0, half * kHalf + at);
+      if (at < p.vocab) k = max(k, make_key(top, at));
+    }
+    T_key = threads_threshold(k, M, s_warp);
+    if (T_key) --T_key;  // that key itself is a candidate
+    T_val = T_key ? key_value(T_key + 1) : -INFINITY;
+  }
+  for (int tile = tile0; tile < tile1; ++tile) {
+    uint32_t some = use(0);
+    if (tile + 1 < tile1) load(tile + 1, 0);
+    some |= use(1);
+    if (tile + 1 < tile1) load(tile + 1, 1);
+    // (a tile without a candidate: one barrier)
+    if (!__syncthreads_or(some != 0)) continue;
+    while (true) {
+      while (some) {  // few: read again
+        const int at = token(tile, __ffs(some) - 1);
+        some &= some - 1;
+        const uint64_t k = key_at(at);
+        if (k > T_key) {
+          const int place = atomicAdd(&s_cnt, 1);
+          if (place < kBuffer) s_buf[place] = k;
         }
-      const uint64_t k = warp_sort(at < p.vocab ? make_key(best, at) : 0);
-      const uint64_t k1 = M <= 32 ? __shfl_sync(0xffffffffu, k, (M - 1) & 31) : 0;
-      const uint64_t k2 = __shfl_sync(0xffffffffu, k, (M + kBeamWarps - 1) / kBeamWarps - 1);
-      if (lane == 0) {
-        s_warp[warp] = k1;
-        s_warp[kBeamWarps + warp] = k2;
       }
       __syncthreads();
-      uint64_t t1 = 0, t2 = ~0ull;
-#pragma unroll
-      for (int w = 0; w < kBeamWarps; ++w) {
-        t1 = max(t1, s_warp[w]);
-        t2 = min(t2, s_warp[kBeamWarps + w]);
-      }
-      T_key = max(t1, t2);
-      if (T_key) --T_key;  // that key itself is a candidate
-      T_val = T_key ? key_value(T_key + 1) : -INFINITY;
-    }
-    // (a tile without a candidate: one barrier)
-    if (!__syncthreads_or(!(top < T_val))) continue;
-    while (true) {
-      const int32_t n = top < T_val ? 0 : count_above(T_key);
-      const int32_t total = block_sum(n, s_sum);
-      const int32_t cnt = s_cnt;
-      if (total == 0) break;
-      if (cnt + total <= kBuffer) {
-        __syncthreads();  // every thread has read s_cnt
-        if (n) {
-          int32_t at = atomicAdd(&s_cnt, n);
-#pragma unroll
-          for (int i = 0; i < kElems; ++i) {
-            const uint64_t k = make_key(x[i], token(i));
-            if (token(i) < p.vocab && k > T_key) s_buf[at++] = k;
-          }
-        }
-        __syncthreads();
-        if (tile == tile0 && tile + 1 < tile1 && s_cnt > M) {
-          sort_buffer(s_buf, s_cnt, M);
-          if (tid == 0) s_cnt = M;
+      const int now = s_cnt;
+      if (now <= kBuffer) {
+        cnt = now;
+        if (tile == tile0 && tile + 1 < tile1 && cnt > M) {  // a tight T for the tiles to come
+          sort_buffer(s_buf, cnt, M);
+          cnt = M;
           T_key = s_buf[M - 1];
           T_val = key_value(T_key);
-          __syncthreads();
+          if (tid == 0) s_cnt = M;
         }
+        __syncthreads();
         break;
       }
+      // too many: what this tile pushed is dropped, T raised, and the tile tried again
+      __syncthreads();
       if (cnt > M) {  // the buffer's M largest stay, and T is the last of them
         sort_buffer(s_buf, cnt, M);
-        if (tid == 0) s_cnt = M;
-        T_key = s_buf[M - 1];
+        cnt = M;
+        T_key = max(T_key, s_buf[M - 1]);
       } else {
-        // rows that rise from tile to tile: the T that leaves M keys of this tile
-        // above it, bit by bit (keys are unique, so there is one)
-        uint64_t t = 0;
-        for (int bit = 63; bit >= 0; --bit) {
-          const uint64_t c = t | 1ull << bit;
-          if (block_sum(count_above(c), s_sum) >= M) t = c;
+        // (rows that rise from tile to tile) M of this tile's keys are as large as the
+        // threshold of the threads' maxima
+        uint64_t k = 0;
+#pragma unroll 1
+        for (int i = 0; i < 2 * kHalf; ++i) k = max(k, key_at(token(tile, i)));
+        uint64_t t = threads_threshold(k, M, s_warp);
+        if (t) --t;
+        if (t <= T_key) {
+          // which does not help where ties crowd: the T that leaves M keys above it, bit
+          // by bit (keys are unique, so there is one)
+          t = 0;
+#pragma unroll 1
+          for (int bit = 63; bit >= 0; --bit) {
+            const uint64_t c = t | 1ull << bit;
+            int32_t n = 0;
+#pragma unroll 1
+            for (int i = 0; i < 2 * kHalf; ++i) n += key_at(token(tile, i)) > c;
+            if (block_sum(n, s_sum) >= M) t = c;
+          }
         }
         T_key = max(T_key, t);
       }
       T_val = key_value(T_key);
+      some = 0xffffffffu >> (32 - 2 * kHalf);
+      if (tid == 0) s_cnt = cnt;
       __syncthreads();
     }
   }
   __syncthreads();
-  const int cnt = s_cnt;
   sort_buffer(s_buf, cnt, M);
   uint64_t *out = p.keys + ((int64_t)row_id * p.splits + split) * M;
   for (int i = tid; i < M; i += kThreads) out[i] = i < cnt ? s_buf[i] : 0;
-  // the threads' sums, at the CTA's maximum
-  float wm = m;
+  // the threads' sums, at the CTA's r
+  float top = r;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  if (lane == 0) s_m[warp] = wm;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_m[warp] = top;
   __syncthreads();
-  float bm = s_m[0];
+  top = s_m[0];
 #pragma unroll
-  for (int w = 1; w < kBeamWarps; ++w) bm = fmaxf(bm, s_m[w]);
-  s *= m == bm ? 1.f : fast_exp2((m - bm) * kLog2e);
+  for (int i = 1; i < kBeamWarps; ++i) top = fmaxf(top, s_m[i]);
+  s *= r == top ? 1.f : fast_exp2(r - top);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) s_s[warp] = s;
   __syncthreads();
   if (tid == 0) {
-    float t = s_s[0];
+    float sum = s_s[0];
 #pragma unroll
-    for (int w = 1; w < kBeamWarps; ++w) t += s_s[w];
-    p.part[(int64_t)row_id * p.splits + split] = make_float2(bm, t);
+    for (int i = 1; i < kBeamWarps; ++i) sum += s_s[i];
+    p.part[(int64_t)row_id * p.splits + split] = make_float2(top, sum);
   }
 }
 
@@ -303,53 +407,72 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o ^ 1ull << 63 : ~o));
 }
 
-// One warp a request: M rounds over the heads of its sorted lists.  List k splits + j
-// holds beam k's best of its j-th range: equal scores go to the lower list.
-__global__ void __launch_bounds__(32) beam_merge_kernel(const BeamParams p) {
-  __shared__ double s_base[kMaxLists];      // cum - lse of the request's beams
-  __shared__ uint64_t s_head[kMaxLists];    // ordered score of each list's first key left
+// One CTA a request.  All threads turn the lists' keys into ordered scores in shared
+// memory (as many as fit; a list's further ones are read when it gets there); then one
+// warp goes M rounds over the heads of the lists.  List k splits + j holds beam k's best of
+// its j-th range: equal scores go to the lower list.
+__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+  __shared__ double s_base[kMaxLists];       // cum - lse of the request's beams
+  __shared__ uint64_t s_score[kMergeScores];  // [list][depth], ordered
+  __shared__ uint64_t s_head[kMaxLists];     // of each list the first score left
   __shared__ int32_t s_next[kMaxLists];
-  const int lane = threadIdx.x;
+  __shared__ uint64_t s_won[kMaxSelect];     // of each round the score (0: none left),
+  __shared__ int32_t s_list[kMaxSelect], s_at[kMaxSelect];  // its list and place in it
+  const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * p.num_beams;
   const int lists = p.num_beams * p.splits, M = p.num_select;
+  const int depth = min(M, kMergeScores / lists);
+  const uint64_t *keys = p.keys + row0 * p.splits * M;
   pdl_wait();
-  for (int k = lane; k < p.num_beams; k += 32) {
+  // the first keys on their way beside the sums
+  uint64_t first = 0;
+  if (tid < lists * depth) first = keys[(int64_t)(tid / depth) * M + tid % depth];
+  for (int k = tid; k < p.num_beams; k += kThreads) {
     double base = __ldg(p.cum + row0 + k);
     if (!(p.finished && __ldg(p.finished + row0 + k))) {
       const float2 *part = p.part + (row0 + k) * p.splits;
-      float m = part[0].x;
-      for (int j = 1; j < p.splits; ++j) m = fmaxf(m, part[j].x);
-      float s = 0.f;
+      float m = -INFINITY, s = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < p.splits; ++j) m = fmaxf(m, part[j].x);
+#pragma unroll 8
       for (int j = 0; j < p.splits; ++j)
-        s += part[j].y * (part[j].x == m ? 1.f : exp2f((part[j].x - m) * kLog2e));
-      base -= (double)m + log((double)s);
+        s += part[j].y * (part[j].x == m ? 1.f : exp2f(part[j].x - m));
+      // log2 s by its exponent and mantissa: off by half a step of a number below 1
+      int e;
+      const float f = frexpf(s, &e);
+      base -= ((double)m + (e - 1) + (double)log2f(2.f * f)) * (1.0 / (double)kLog2e);
     }
     s_base[k] = base;
   }
-  __syncwarp();
-  // the ordered score of list l's key n (0: none left)
-  auto score_of = [&](int l, int n) -> uint64_t {
+  __syncthreads();
+  // the ordered score of list l's n-th key (0: there is none)
+  auto score_of = [&](int l, int n, uint64_t key) -> uint64_t {
     const int k = l / p.splits;
     if (p.finished && __ldg(p.finished + row0 + k))
       return n == 0 && l == k * p.splits ? order_double(s_base[k]) : 0;
-    if (n >= M) return 0;
-    const uint64_t key = p.keys[(row0 * p.splits + l) * M + n];
     return key ? order_double(s_base[k] + (double)key_value(key)) : 0;
   };
-  uint64_t best = 0;
-  int best_list = lane;
+  for (int i = tid; i < lists * depth; i += kThreads) {
+    const int l = i / depth, n = i % depth;
+    const uint64_t o = score_of(l, n, i == tid ? first : keys[(int64_t)l * M + n]);
+    s_score[i] = o;
+    if (n == 0) {
+      s_head[l] = o;
+      s_next[l] = 0;
+    }
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  uint64_t best = 0;  // the best head of this lane's lists
+  int best_list = tid;
   auto look = [&] {
     best = 0;
-    for (int l = lane; l < lists; l += 32)
+    for (int l = tid; l < lists; l += 32)
       if (s_head[l] > best) {
         best = s_head[l];
         best_list = l;
       }
   };
-  for (int l = lane; l < lists; l += 32) {
-    s_head[l] = score_of(l, 0);
-    s_next[l] = 0;
-  }
   look();
   for (int i = 0; i < M; ++i) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
@@ -358,37 +481,46 @@ __global__ void __launch_bounds__(32) beam_merge_kernel(const BeamParams p) {
     const uint64_t top = (uint64_t)hi << 32 | lo;
     const uint32_t l = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)best_list : ~0u);
     if (best == top && (uint32_t)best_list == l) {  // one lane: lists are dealt out by lane
-      const int64_t o = (int64_t)blockIdx.x * M + i;
-      const int k = (int)l / p.splits;
-      if (top == 0) {
-        p.scores[o] = -INFINITY;
-        p.tokens[o] = p.parents[o] = -1;
-      } else {
-        p.scores[o] = (float)unorder_double(top);
-        p.parents[o] = (int32_t)(row0 + k);
-        p.tokens[o] = p.finished && __ldg(p.finished + row0 + k)
-                          ? p.pad_token
-                          : (int32_t)~(uint32_t)p.keys[(row0 * p.splits + l) * M + s_next[l]];
-        s_head[l] = score_of((int)l, ++s_next[l]);
+      s_won[i] = top;
+      if (top != 0) {
+        const int n = s_next[l];
+        s_list[i] = (int)l;
+        s_at[i] = n;
+        s_next[l] = n + 1;
+        s_head[l] = n + 1 >= M       ? 0
+                    : n + 1 < depth ? s_score[(int)l * depth + n + 1]
+                                    : score_of((int)l, n + 1, keys[(int64_t)l * M + n + 1]);
         look();
       }
     }
     __syncwarp();
   }
+  for (int i = tid; i < M; i += 32) {
+    const int64_t o = (int64_t)blockIdx.x * M + i;
+    const uint64_t won = s_won[i];
+    const int l = won ? s_list[i] : 0, k = l / p.splits;
+    p.scores[o] = won ? (float)unorder_double(won) : -INFINITY;
+    p.parents[o] = won ? (int32_t)(row0 + k) : -1;
+    p.tokens[o] = won == 0 ? -1
+                  : p.finished && __ldg(p.finished + row0 + k)
+                      ? p.pad_token
+                      : (int32_t)~(uint32_t)keys[(int64_t)l * M + s_at[i]];
+  }
 }
 
-// How a call's rows are cut.  Tiles of 8192 elements (32 a thread) where they give every
-// SM a few CTAs, else of 2048; splits of a row so that about 16 CTAs an SM share the
-// work (of 152 SMs: the cut must not depend on the device, the workspace goes by it).
+// How a call's rows are cut.  Tiles of 32 elements a thread where they give every SM a few
+// CTAs, else of 8; splits of a row so that about kCtasPerSm CTAs an SM
+// share the work (of 152 SMs: the cut must not depend on the device, the workspace goes
+// by it).
 struct BeamCut {
   int elems, tiles, splits;
 };
 BeamCut beam_cut(int64_t rows, int32_t num_beams, int32_t vocab) {
-  constexpr int64_t kSms = 152;
+  constexpr int64_t kSms = 152, kCtasPerSm = 4;
   BeamCut c;
-  c.elems = rows * ((vocab + 8191) / 8192) >= 2 * kSms ? 32 : 8;
+  c.elems = rows * (vocab / (kThreads * 32) + 1) >= 2 * kSms ? 32 : 8;
   c.tiles = (vocab + kThreads * c.elems - 1) / (kThreads * c.elems);
-  int64_t s = (16 * kSms + rows - 1) / std::max<int64_t>(rows, 1);
+  int64_t s = kCtasPerSm * kSms / std::max<int64_t>(rows, 1);
   s = std::min<int64_t>(s, std::min(c.tiles, std::max(kMaxLists / num_beams, 1)));
   c.splits = (int)std::max<int64_t>(s, 1);
   return c;
@@ -397,9 +529,9 @@ int64_t part_bytes(int64_t rows, int splits) { return align_up(rows * splits * 8
 
 template <typename T>
 cudaError_t launch_rows(const BeamParams &p, int elems, int64_t ctas, pkv_stream stream) {
-  auto kern = elems == 32 ? beam_rows_kernel<T, 32> : beam_rows_kernel<T, 8>;
-  const cudaError_t pe = elems == 32 ? prepare_kernel<beam_rows_kernel<T, 32>>(0)
-                                     : prepare_kernel<beam_rows_kernel<T, 8>>(0);
+  auto kern = elems == 32 ? beam_rows_kernel<T, 16> : beam_rows_kernel<T, 4>;
+  const cudaError_t pe = elems == 32 ? prepare_kernel<beam_rows_kernel<T, 16>>(0)
+                                     : prepare_kernel<beam_rows_kernel<T, 4>>(0);
   if (pe != cudaSuccess) return pe;
   return launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream, false, p);
 }
@@ -462,12 +594,12 @@ extern "C" pkv_status pkv_beam_select(const void *logits, int32_t logit_type, in
   p.tiles = c.tiles;
   if (prepare_kernel<beam_merge_kernel>(0) != cudaSuccess) return PKV_ERR_CUDA;
   profile_begin(PKV_KERNEL_BEAM, stream);
-  cudaError_t e = logit_type == PKV_BF16
-                      ? launch_rows<__nv_bfloat16>(p, c.elems, rows * c.splits, stream)
-                  : logit_type == PKV_FP16 ? launch_rows<__half>(p, c.elems, rows * c.splits, stream)
-                                           : launch_rows<float>(p, c.elems, rows * c.splits, stream);
+  const int64_t ctas = rows * c.splits;
+  cudaError_t e = logit_type == PKV_BF16   ? launch_rows<__nv_bfloat16>(p, c.elems, ctas, stream)
+                  : logit_type == PKV_FP16 ? launch_rows<__half>(p, c.elems, ctas, stream)
+                                           : launch_rows<float>(p, c.elems, ctas, stream);
   if (e == cudaSuccess)
-    e = launch_kernel(beam_merge_kernel, dim3((unsigned)num_requests), dim3(32), 0, stream,
+    e = launch_kernel(beam_merge_kernel, dim3((unsigned)num_requests), dim3(kThreads), 0, stream,
                       !profiling_active(), p);
   profile_end(PKV_KERNEL_BEAM, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
