@@ -14,8 +14,9 @@
 //  - the candidates: 64-bit keys (logit, lowest token first), so that no two are equal.
 //    A threshold T below the num_select-th largest key comes from the threads' maxima of
 //    the first tile; keys above T go to a buffer in shared memory, which is cut to its
-//    num_select largest (and T raised) when it fills.  After the first tile few keys pass:
-//    num_select / i of the i-th tile are expected.
+//    num_select largest, and T raised, whenever it has doubled.  After the first tile few
+//    keys pass: num_select / i of the i-th tile are expected.  (With the first tile's T
+//    kept, 16 passed in every tile: 512 rows of 128000 fp32 took 60 us in place of 46.)
 // A second kernel, one CTA a request, joins the rows' sums and merges the sorted lists
 // by score in 64 bits.
 //
@@ -49,7 +50,7 @@ struct BeamParams {
   int32_t *tokens, *parents;
   float2 *part;          // [rows][splits]: r, sum of 2^(x L - r)
   uint64_t *keys;        // [rows][splits][num_select], descending, 0: none
-  int64_t row_stride;
+  int64_t row_stride, num_rows;
   int32_t num_beams, vocab, num_select, pad_token, splits, tiles;
 };
 
@@ -95,36 +96,71 @@ __device__ __forceinline__ uint32_t raw_bits(const T *p) {
   return __ldg(reinterpret_cast<const uint16_t *>(p));
 }
 
+// A row of logits, and the part of the tensor's memory that 16-byte loads may touch.
+template <typename T>
+struct Row {
+  const T *data;
+  const char *lo, *hi;  // the tensor's first byte and the one past its last
+  int32_t vocab;
+  uint32_t shift;       // data's offset from 16-byte alignment, in bytes
+};
+
 // Elements [at, at + kVec) of a row, as they lie in memory; those past its end as -inf.
+// Rows that start off alignment (an odd vocabulary) are put together from the aligned
+// 16-byte pieces around them; an element at a time only at the tensor's ends.
 template <typename T, int kVec>
-__device__ __forceinline__ void load_vec(const T *row, int32_t at, int32_t vocab, bool aligned,
-                                         uint32_t *w) {
+__device__ __forceinline__ void load_vec(const Row<T> &row, int32_t at, uint32_t *w) {
   using W = Words<T>;
   constexpr int kWords = kVec / W::kPer;
-  if (aligned && at + kVec <= vocab) {
+  const T *src = row.data + at;
+  const bool whole = at + kVec <= row.vocab;
+  if (row.shift == 0 && whole) {
     if (kWords == 2) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row + at));
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src));
       w[0] = v.x;
       w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + at) + i);
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
         w[4 * i + 3] = v.w;
       }
     }
-  } else {
+    return;
+  }
+  if (kWords >= 4) {
+    const char *first = reinterpret_cast<const char *>(src) - row.shift;
+    if (whole && first >= row.lo && first + kWords * 4 + 16 <= row.hi) {
+      uint32_t v[kWords + 4];
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int j = 0; j < W::kPer; ++j) {
-        const int e = at + i * W::kPer + j;
-        w[i] |= (e < vocab ? raw_bits(row + e) : W::kNegInf) << (16 * j);
+      for (int i = 0; i < kWords / 4 + 1; ++i) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(first) + i);
+        v[4 * i] = x.x;
+        v[4 * i + 1] = x.y;
+        v[4 * i + 2] = x.z;
+        v[4 * i + 3] = x.w;
       }
+      // by 8, by 4, then by 2 bytes
+#pragma unroll
+      for (int i = 0; i < kWords + 2; ++i) v[i] = row.shift & 8 ? v[i + 2] : v[i];
+#pragma unroll
+      for (int i = 0; i < kWords + 1; ++i) v[i] = row.shift & 4 ? v[i + 1] : v[i];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = sizeof(T) == 4 ? v[i] : __funnelshift_r(v[i], v[i + 1], (row.shift & 2) * 8);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < W::kPer; ++j) {
+      const int e = i * W::kPer + j;
+      w[i] |= (at + e < row.vocab ? raw_bits(src + e) : W::kNegInf) << (16 * j);
     }
   }
 }
@@ -155,34 +191,48 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t k) {
 }
 
 // The `cnt` keys of s_buf in descending order, its first min(cnt, keep) of them: each
-// key's place is the number of larger ones.
-__device__ __forceinline__ void sort_buffer(uint64_t *s_buf, int cnt, int keep) {
-  uint64_t k[kBuffer / kThreads];
-  int rank[kBuffer / kThreads];
+// key's place is the number of larger ones.  Up to kThreads keys, the threads that are
+// left over share the counting (s_rank: kThreads ints).
+__device__ __forceinline__ void sort_buffer(uint64_t *s_buf, int32_t *s_rank, int cnt, int keep) {
+  const int tid = threadIdx.x;
+  if (cnt <= kThreads) {
+    const int lanes = cnt <= 32 ? 32 : cnt <= 64 ? 64 : cnt <= 128 ? 128 : 256;
+    const int i = tid & (lanes - 1), part = tid / lanes;
+    const int len = (cnt + kThreads / lanes - 1) / (kThreads / lanes);
+    const uint64_t k = i < cnt ? s_buf[i] : 0;
+    s_rank[tid] = 0;
+    __syncthreads();
+    if ((i & ~31) < cnt) {
+      int rank = 0;
+      const int end = min(part * len + len, cnt);
+#pragma unroll 4
+      for (int j = part * len; j < end; ++j) rank += s_buf[j] > k;
+      if (rank) atomicAdd(s_rank + i, rank);
+    }
+    __syncthreads();
+    if (tid < cnt) {
+      const int rank = s_rank[tid];
+      if (rank < keep) s_buf[rank] = k;
+    }
+  } else {
+    uint64_t k[kBuffer / kThreads];
+    int rank[kBuffer / kThreads];
 #pragma unroll
-  for (int u = 0; u < kBuffer / kThreads; ++u) {
-    const int i = threadIdx.x + u * kThreads;
-    k[u] = i < cnt ? s_buf[i] : 0;
-    rank[u] = 0;
-  }
-  if (cnt > kThreads) {
+    for (int u = 0; u < kBuffer / kThreads; ++u) {
+      const int i = tid + u * kThreads;
+      k[u] = i < cnt ? s_buf[i] : 0;
+      rank[u] = 0;
+    }
     for (int j = 0; j < cnt; ++j) {
       const uint64_t o = s_buf[j];
 #pragma unroll
       for (int u = 0; u < kBuffer / kThreads; ++u) rank[u] += o > k[u];
     }
-  } else if ((int)(threadIdx.x & ~31) < cnt) {  // (a warp without a key has no ranks to find)
-    int j = 0;
-    for (; j + 1 < cnt; j += 2) {
-      const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(s_buf + j);
-      rank[0] += (o.x > k[0]) + (o.y > k[0]);
-    }
-    if (j < cnt) rank[0] += s_buf[j] > k[0];
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int u = 0; u < kBuffer / kThreads; ++u)
-    if (threadIdx.x + u * kThreads < cnt && rank[u] < keep) s_buf[rank[u]] = k[u];
+    for (int u = 0; u < kBuffer / kThreads; ++u)
+      if (tid + u * kThreads < cnt && rank[u] < keep) s_buf[rank[u]] = k[u];
+  }
   __syncthreads();
 }
 
@@ -219,15 +269,19 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   __shared__ alignas(16) uint64_t s_buf[kBuffer];
   __shared__ uint64_t s_warp[2 * kBeamWarps];
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
-  __shared__ int32_t s_sum[kBeamWarps];
+  __shared__ int32_t s_rank[kThreads], s_sum[kBeamWarps];
   __shared__ int32_t s_cnt;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row_id = blockIdx.x / p.splits;
   const int split = blockIdx.x % p.splits;
   if (p.finished && __ldg(p.finished + row_id)) return;  // the merge does not look at its parts
-  const T *row = static_cast<const T *>(p.logits) + row_id * p.row_stride;
-  const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+  Row<T> row;
+  row.data = static_cast<const T *>(p.logits) + row_id * p.row_stride;
+  row.lo = static_cast<const char *>(p.logits);
+  row.hi = row.lo + ((p.num_rows - 1) * p.row_stride + p.vocab) * (int64_t)sizeof(T);
+  row.vocab = p.vocab;
+  row.shift = (uint32_t)(reinterpret_cast<uintptr_t>(row.data) & 15u);
   const int tile0 = (int)((int64_t)p.tiles * split / p.splits);
   const int tile1 = (int)((int64_t)p.tiles * (split + 1) / p.splits);
   const int M = p.num_select;
@@ -241,14 +295,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     return tile * kTile + i / kVec * kThreads * kVec + tid * kVec + i % kVec;
   };
   auto key_at = [&](int at) {
-    return at < p.vocab ? make_key(W::get(raw_bits(row + at), 0), at) : (uint64_t)0;
+    return at < p.vocab ? make_key(W::get(raw_bits(row.data + at), 0), at) : (uint64_t)0;
   };
   uint32_t w[2][kWords];
   auto load = [&](int tile, int half) {
 #pragma unroll
     for (int j = 0; j < kHalf / kVec; ++j)
-      load_vec<T, kVec>(row, token(tile, half * kHalf + j * kVec), p.vocab, aligned,
-                        w[half] + j * (kVec / W::kPer));
+      load_vec<T, kVec>(row, token(tile, half * kHalf + j * kVec), w[half] + j * (kVec / W::kPer));
   };
   auto elements = [&](int half, float (&x)[kHalf]) {  // returns the largest
 #pragma unroll
@@ -280,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
         if (x[i] != x[i]) s = x[i];
     }
     uint32_t some = 0;
-    if (!(top < T_val)) {
+    if (__any_sync(0xffffffffu, !(top < T_val))) {  // a branch of the whole warp
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) some |= (uint32_t)!(x[i] < T_val) << i;
     }
@@ -326,8 +379,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
       const int now = s_cnt;
       if (now <= kBuffer) {
         cnt = now;
-        if (tile == tile0 && tile + 1 < tile1 && cnt > M) {  // a tight T for the tiles to come
-          sort_buffer(s_buf, cnt, M);
+        // a tight T for the tiles to come: after the first one, then as the buffer doubles
+        // (not for the last few: they bring fewer keys than the sorting costs)
+        if (tile + 3 < tile1 && cnt > (tile == tile0 ? M : max(2 * M, 32))) {
+          sort_buffer(s_buf, s_rank, cnt, M);
           cnt = M;
           T_key = s_buf[M - 1];
           T_val = key_value(T_key);
@@ -339,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
       // too many: what this tile pushed is dropped, T raised, and the tile tried again
       __syncthreads();
       if (cnt > M) {  // the buffer's M largest stay, and T is the last of them
-        sort_buffer(s_buf, cnt, M);
+        sort_buffer(s_buf, s_rank, cnt, M);
         cnt = M;
         T_key = max(T_key, s_buf[M - 1]);
       } else {
@@ -372,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     }
   }
   __syncthreads();
-  sort_buffer(s_buf, cnt, M);
+  sort_buffer(s_buf, s_rank, cnt, M);
   uint64_t *out = p.keys + ((int64_t)row_id * p.splits + split) * M;
   for (int i = tid; i < M; i += kThreads) out[i] = i < cnt ? s_buf[i] : 0;
   // the threads' sums, at the CTA's r
@@ -408,9 +463,11 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
 }
 
 // One CTA a request.  All threads turn the lists' keys into ordered scores in shared
-// memory (as many as fit; a list's further ones are read when it gets there); then one
-// warp goes M rounds over the heads of the lists.  List k splits + j holds beam k's best of
-// its j-th range: equal scores go to the lower list.
+// memory (as many as fit; a list's further ones are read when it gets there).  Few
+// lists and up to a thread each, a candidate finds its place by counting the better ones
+// (8 lists of 16: 6.6 us, by rounds 9.4); others are merged by one warp in M rounds over
+// the heads of the lists (64 lists of 4: 7 us, by counting 8.5).  List k splits + j holds
+// beam k's best of its j-th range: equal scores go to the lower list.
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ double s_base[kMaxLists];       // cum - lse of the request's beams
   __shared__ uint64_t s_score[kMergeScores];  // [list][depth], ordered
@@ -423,13 +480,18 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   const int lists = p.num_beams * p.splits, M = p.num_select;
   const int depth = min(M, kMergeScores / lists);
   const uint64_t *keys = p.keys + row0 * p.splits * M;
+  auto done = [&](int k) { return p.finished && __ldg(p.finished + row0 + k); };
+  // (inputs of the call: the kernel before this one does not write them)
+  const bool mine = tid < p.num_beams;
+  double base = mine ? (double)__ldg(p.cum + row0 + tid) : 0.0;
+  const bool ended = mine && done(tid);
   pdl_wait();
   // the first keys on their way beside the sums
   uint64_t first = 0;
   if (tid < lists * depth) first = keys[(int64_t)(tid / depth) * M + tid % depth];
   for (int k = tid; k < p.num_beams; k += kThreads) {
-    double base = __ldg(p.cum + row0 + k);
-    if (!(p.finished && __ldg(p.finished + row0 + k))) {
+    if (k != tid) base = __ldg(p.cum + row0 + k);
+    if (!(k == tid ? ended : done(k))) {
       const float2 *part = p.part + (row0 + k) * p.splits;
       float m = -INFINITY, s = 0.f;
 #pragma unroll 8
@@ -448,10 +510,33 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   // the ordered score of list l's n-th key (0: there is none)
   auto score_of = [&](int l, int n, uint64_t key) -> uint64_t {
     const int k = l / p.splits;
-    if (p.finished && __ldg(p.finished + row0 + k))
-      return n == 0 && l == k * p.splits ? order_double(s_base[k]) : 0;
+    if (done(k)) return n == 0 && l == k * p.splits ? order_double(s_base[k]) : 0;
     return key ? order_double(s_base[k] + (double)key_value(key)) : 0;
   };
+  auto put = [&](int i, uint64_t score, int l, uint64_t key) {
+    const int64_t o = (int64_t)blockIdx.x * M + i;
+    const int k = l / p.splits;
+    p.scores[o] = score ? (float)unorder_double(score) : -INFINITY;
+    p.parents[o] = score ? (int32_t)(row0 + k) : -1;
+    p.tokens[o] = score == 0 ? -1 : done(k) ? p.pad_token : (int32_t)~(uint32_t)key;
+  };
+  if (lists * M <= kThreads && lists <= 16) {  // depth = M
+    const int n = lists * M;
+    const uint64_t own = tid < n ? score_of(tid / M, tid % M, first) : 0;
+    s_score[tid] = own;
+    const int have = __syncthreads_count(own != 0);
+    if (own) {
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const uint64_t o = s_score[j];
+        rank += o > own || (o == own && j < tid);
+      }
+      if (rank < M) put(rank, own, tid / M, first);
+    }
+    for (int i = have + tid; i < M; i += kThreads) put(i, 0, 0, 0);
+    return;
+  }
   for (int i = tid; i < lists * depth; i += kThreads) {
     const int l = i / depth, n = i % depth;
     const uint64_t o = score_of(l, n, i == tid ? first : keys[(int64_t)l * M + n]);
@@ -476,8 +561,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   look();
   for (int i = 0; i < M; ++i) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-    const bool mine = (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, mine ? (uint32_t)best : 0u);
+    const bool high = (uint32_t)(best >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, high ? (uint32_t)best : 0u);
     const uint64_t top = (uint64_t)hi << 32 | lo;
     const uint32_t l = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)best_list : ~0u);
     if (best == top && (uint32_t)best_list == l) {  // one lane: lists are dealt out by lane
@@ -496,15 +581,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     __syncwarp();
   }
   for (int i = tid; i < M; i += 32) {
-    const int64_t o = (int64_t)blockIdx.x * M + i;
     const uint64_t won = s_won[i];
-    const int l = won ? s_list[i] : 0, k = l / p.splits;
-    p.scores[o] = won ? (float)unorder_double(won) : -INFINITY;
-    p.parents[o] = won ? (int32_t)(row0 + k) : -1;
-    p.tokens[o] = won == 0 ? -1
-                  : p.finished && __ldg(p.finished + row0 + k)
-                      ? p.pad_token
-                      : (int32_t)~(uint32_t)keys[(int64_t)l * M + s_at[i]];
+    const int l = won ? s_list[i] : 0;
+    put(i, won, l, won ? keys[(int64_t)l * M + s_at[i]] : 0);
   }
 }
 
@@ -586,6 +665,7 @@ extern "C" pkv_status pkv_beam_select(const void *logits, int32_t logit_type, in
   p.part = static_cast<float2 *>(workspace);
   p.keys = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + part_bytes(rows, c.splits));
   p.row_stride = row_stride;
+  p.num_rows = rows;
   p.num_beams = num_beams;
   p.vocab = vocab;
   p.num_select = num_select;
