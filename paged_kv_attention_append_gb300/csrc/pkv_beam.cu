@@ -13,10 +13,12 @@
 //    rounding (2^-26 of L) moves the lse by 2^-26 times the softmax's entropy only;
 //  - the candidates: 64-bit keys (logit, lowest token first), so that no two are equal.
 //    A threshold T below the num_select-th largest key comes from the threads' maxima of
-//    the first tile; keys above T go to a buffer in shared memory, which is cut to its
-//    num_select largest, and T raised, whenever it has doubled.  After the first tile few
-//    keys pass: num_select / i of the i-th tile are expected.  (With the first tile's T
-//    kept, 16 passed in every tile: 512 rows of 128000 fp32 took 60 us in place of 46.)
+//    the first tile; keys above T go to their warp's buffer in shared memory, straight
+//    from the registers and without atomics or barriers.  After the tiles 0, 1, 3, 7, ..
+//    the CTA keeps its num_select largest keys and raises T to the last of them, so
+//    about num_select keys pass between two such cuts.  (With the first tile's T kept,
+//    that many passed in every tile: 512 rows of 128000 fp32 took 60 us; with keys put into
+//    one buffer by atomics after each tile, 46.)
 // A second kernel, one CTA a request, joins the rows' sums and merges the sorted lists
 // by score in 64 bits.
 //
@@ -27,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "pkv_device.cuh"
 
@@ -37,7 +40,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBeamWarps = kThreads / 32;
 constexpr int kMaxSelect = 128;
-constexpr int kBuffer = 512;        // candidate keys a CTA keeps (>= 2 kMaxSelect)
+constexpr int kWarpKeys = 128;      // new candidate keys a warp keeps (>= kMaxSelect)
+constexpr int kAllKeys = kBeamWarps * kWarpKeys + kMaxSelect + 64;
 constexpr int kMaxLists = 1024;     // sorted lists (beam, split) of a request
 constexpr int kMergeScores = 2048;  // scores a merge keeps in shared memory (>= kMaxLists)
 constexpr float kLog2e = 1.4426950408889634f;  // L above
@@ -176,86 +180,63 @@ __device__ __forceinline__ int32_t block_sum(int32_t v, int32_t *s) {
   return t;
 }
 
-// The lane keys of a warp in descending order (bitonic).
-__device__ __forceinline__ uint64_t warp_sort(uint64_t k) {
-  const int lane = threadIdx.x & 31;
+// How many of s[begin, end) are above k.  Eight at a time, all loads ahead of the compares
+// (one by one, 150 keys took 7 us); begin and end multiples of 8, s 16-byte aligned.
+__device__ __forceinline__ int count_above(const uint64_t *s, int begin, int end, uint64_t k) {
+  int n = 0;
+  for (int j = begin; j < end; j += 8) {
+    ulonglong2 v[4];
 #pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
+    for (int u = 0; u < 4; ++u) v[u] = reinterpret_cast<const ulonglong2 *>(s + j)[u];
 #pragma unroll
-    for (int o = size >> 1; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
-      const bool up = ((lane & size) == 0) == ((lane & o) == 0);  // keeps the larger
-      k = up ? (k > other ? k : other) : (k < other ? k : other);
-    }
-  return k;
+    for (int u = 0; u < 4; ++u) n += (v[u].x > k) + (v[u].y > k);
+  }
+  return n;
 }
 
-// The `cnt` keys of s_buf in descending order, its first min(cnt, keep) of them: each
+// The `cnt` keys of s_all in descending order, the first `keep` of them to s_top: each
 // key's place is the number of larger ones.  Up to kThreads keys, the threads that are
-// left over share the counting (s_rank: kThreads ints).
-__device__ __forceinline__ void sort_buffer(uint64_t *s_buf, int32_t *s_rank, int cnt, int keep) {
+// left over share the counting (s_rank: kThreads ints).  The 64 keys from cnt on are 0.
+__device__ __forceinline__ void sort_keys(const uint64_t *s_all, int cnt, uint64_t *s_top, int keep,
+                                          int32_t *s_rank) {
   const int tid = threadIdx.x;
   if (cnt <= kThreads) {
     const int lanes = cnt <= 32 ? 32 : cnt <= 64 ? 64 : cnt <= 128 ? 128 : 256;
-    const int i = tid & (lanes - 1), part = tid / lanes;
-    const int len = (cnt + kThreads / lanes - 1) / (kThreads / lanes);
-    const uint64_t k = i < cnt ? s_buf[i] : 0;
+    const int parts = kThreads / lanes, i = tid & (lanes - 1), part = tid / lanes;
+    const int len = ((cnt + parts - 1) / parts + 7) & ~7;
+    const uint64_t k = i < cnt ? s_all[i] : 0;
     s_rank[tid] = 0;
     __syncthreads();
     if ((i & ~31) < cnt) {
-      int rank = 0;
-      const int end = min(part * len + len, cnt);
-#pragma unroll 4
-      for (int j = part * len; j < end; ++j) rank += s_buf[j] > k;
+      const int rank = count_above(s_all, part * len, part * len + len, k);
       if (rank) atomicAdd(s_rank + i, rank);
     }
     __syncthreads();
-    if (tid < cnt) {
-      const int rank = s_rank[tid];
-      if (rank < keep) s_buf[rank] = k;
-    }
+    if (tid < cnt && s_rank[tid] < keep) s_top[s_rank[tid]] = k;
   } else {
-    uint64_t k[kBuffer / kThreads];
-    int rank[kBuffer / kThreads];
-#pragma unroll
-    for (int u = 0; u < kBuffer / kThreads; ++u) {
-      const int i = tid + u * kThreads;
-      k[u] = i < cnt ? s_buf[i] : 0;
-      rank[u] = 0;
+    for (int i = tid; i < cnt; i += kThreads) {
+      const uint64_t k = s_all[i];
+      const int rank = count_above(s_all, 0, (cnt + 7) & ~7, k);
+      if (rank < keep) s_top[rank] = k;
     }
-    for (int j = 0; j < cnt; ++j) {
-      const uint64_t o = s_buf[j];
-#pragma unroll
-      for (int u = 0; u < kBuffer / kThreads; ++u) rank[u] += o > k[u];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kBuffer / kThreads; ++u)
-      if (tid + u * kThreads < cnt && rank[u] < keep) s_buf[rank[u]] = k[u];
   }
   __syncthreads();
 }
 
-// A key that at least M of the threads' keys `k` reach (0: fewer have one): every warp's
-// M-th largest is one, and so is the smallest over the warps of their ceil(M / 8)-th.
-__device__ __forceinline__ uint64_t threads_threshold(uint64_t k, int M, uint64_t *s_warp) {
-  const int warp = threadIdx.x >> 5;
-  k = warp_sort(k);
-  const uint64_t k1 = M <= 32 ? __shfl_sync(0xffffffffu, k, (M - 1) & 31) : 0;
-  const uint64_t k2 = __shfl_sync(0xffffffffu, k, (M + kBeamWarps - 1) / kBeamWarps - 1);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    s_warp[warp] = k1;
-    s_warp[kBeamWarps + warp] = k2;
+// A logit that at least M elements of the CTA reach: the smallest over the warps of their
+// ceil(M / 8)-th largest thread maximum.  s: an int a warp.
+__device__ __forceinline__ float threads_threshold(float top, int M, uint32_t *s) {
+  uint32_t o = (uint32_t)(make_key(top, 0) >> 32), kth = 0;
+  for (int i = 0; i < (M + kBeamWarps - 1) / kBeamWarps; ++i) {
+    kth = __reduce_max_sync(0xffffffffu, o);
+    const uint32_t who = __ballot_sync(0xffffffffu, o == kth);
+    if ((threadIdx.x & 31) == __ffs(who) - 1) o = 0;
   }
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = kth;
   __syncthreads();
-  uint64_t t1 = 0, t2 = ~0ull;
 #pragma unroll
-  for (int w = 0; w < kBeamWarps; ++w) {
-    t1 = max(t1, s_warp[w]);
-    t2 = min(t2, s_warp[kBeamWarps + w]);
-  }
-  return max(t1, t2);
+  for (int w = 0; w < kBeamWarps; ++w) kth = min(kth, s[w]);
+  return key_value((uint64_t)kth << 32);
 }
 
 // A tile is 2 kHalf elements a thread, in two sets of registers: each is filled again as
@@ -266,11 +247,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   constexpr int kVec = kHalf < 8 ? kHalf : 8;  // consecutive elements a thread loads together
   constexpr int kWords = kHalf / W::kPer;
   constexpr int kHalfTile = kThreads * kHalf, kTile = 2 * kHalfTile;
-  __shared__ alignas(16) uint64_t s_buf[kBuffer];
-  __shared__ uint64_t s_warp[2 * kBeamWarps];
+  __shared__ uint64_t s_new[kBeamWarps][kWarpKeys];
+  __shared__ alignas(16) uint64_t s_all[kAllKeys];
+  __shared__ uint64_t s_top[kMaxSelect];
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
-  __shared__ int32_t s_rank[kThreads], s_sum[kBeamWarps];
-  __shared__ int32_t s_cnt;
+  __shared__ uint32_t s_kth[kBeamWarps];
+  __shared__ int32_t s_rank[kThreads], s_cnt[kBeamWarps], s_sum[kBeamWarps];
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row_id = blockIdx.x / p.splits;
@@ -286,16 +268,20 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   const int tile1 = (int)((int64_t)p.tiles * (split + 1) / p.splits);
   const int M = p.num_select;
   float r = -INFINITY, s = 0.f;
-  uint64_t T_key = 0;       // candidates are the keys above this
-  float T_val = -INFINITY;  // its logit: a cheaper test that lets through no fewer
-  int cnt = 0;              // keys in the buffer
-  if (tid == 0) s_cnt = 0;
+  // candidates are the keys above T_key, their logits at least T_val (a cheaper test, false
+  // for NaN too); logits of -inf never are
+  uint64_t T_key = make_key(-INFINITY, 0);
+  float T_val = -FLT_MAX;
+  int num_top = 0;          // keys in s_top, the CTA's largest so far, sorted
+  int cnt = 0;              // keys this warp found since
   // element i < 2 kHalf of this thread's in a tile
   auto token = [&](int tile, int i) {
     return tile * kTile + i / kVec * kThreads * kVec + tid * kVec + i % kVec;
   };
-  auto key_at = [&](int at) {
-    return at < p.vocab ? make_key(W::get(raw_bits(row.data + at), 0), at) : (uint64_t)0;
+  auto key_at = [&](int at) -> uint64_t {
+    if (at >= p.vocab) return 0;
+    const float x = W::get(raw_bits(row.data + at), 0);
+    return x >= -FLT_MAX ? make_key(x, at) : 0;
   };
   uint32_t w[2][kWords];
   auto load = [&](int tile, int half) {
@@ -312,8 +298,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
       top = i + 1 < kHalf ? max3(top, x[i], x[i + 1]) : fmaxf(top, x[i]);
     return top;
   };
-  // half a tile into the sum; its elements at or above T_val as bits
-  auto use = [&](int half) {
+  auto push = [&](uint64_t k) {  // by the whole warp
+    const bool pass = k > T_key;
+    const uint32_t b = __ballot_sync(0xffffffffu, pass);
+    const int place = cnt + __popc(b & ((1u << lane) - 1));
+    if (pass && place < kWarpKeys) s_new[warp][place] = k;
+    cnt += __popc(b);
+  };
+  // half a tile into the sum and the candidates
+  auto use = [&](int tile, int half) {
     float x[kHalf];
     const float top = elements(half, x);
     const float r_new = fmaxf(r, top * kLog2e);
@@ -332,104 +325,89 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
       for (int i = 0; i < kHalf; ++i)  // all masked; a NaN makes the row's sum NaN
         if (x[i] != x[i]) s = x[i];
     }
-    uint32_t some = 0;
-    if (__any_sync(0xffffffffu, !(top < T_val))) {  // a branch of the whole warp
+    if (__any_sync(0xffffffffu, top >= T_val)) {
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) some |= (uint32_t)!(x[i] < T_val) << i;
+      for (int i = 0; i < kHalf; ++i)
+        if (__any_sync(0xffffffffu, x[i] >= T_val))
+          push(x[i] >= T_val ? make_key(x[i], token(tile, half * kHalf + i)) : 0);
     }
-    return some << (half * kHalf);
+  };
+  // the CTA's largest keys of all found so far to s_top; by all threads
+  auto cut = [&] {
+    if (lane == 0) s_cnt[warp] = min(cnt, kWarpKeys);
+    for (int i = tid; i < num_top; i += kThreads) s_all[i] = s_top[i];
+    __syncthreads();
+    int before = num_top, all = num_top;
+#pragma unroll
+    for (int v = 0; v < kBeamWarps; ++v) {
+      if (v < warp) before += s_cnt[v];
+      all += s_cnt[v];
+    }
+    for (int i = lane; i < s_cnt[warp]; i += 32) s_all[before + i] = s_new[warp][i];
+    if (tid < 64) s_all[all + tid] = 0;
+    __syncthreads();
+    sort_keys(s_all, all, s_top, M, s_rank);
+    num_top = min(all, M);
+    cnt = 0;
+    if (num_top == M && s_top[M - 1] > T_key) {
+      T_key = s_top[M - 1];
+      T_val = key_value(T_key);
+    }
   };
   load(tile0, 0);
   load(tile0, 1);
   {
-    uint64_t k = 0;  // this thread's largest key of the first tile
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float x[kHalf];
-      const float top = elements(half, x);
-      int at = 0;
-#pragma unroll
-      for (int i = kHalf - 1; i >= 0; --i)
-        if (x[i] == top) at = i;
-      at = token(tile0, half * kHalf + at);
-      if (at < p.vocab) k = max(k, make_key(top, at));
+    float x[kHalf];
+    float top = elements(0, x);
+    top = fmaxf(top, elements(1, x));
+    top = threads_threshold(top, M, s_kth);
+    if (top >= T_val) {
+      T_val = top;
+      T_key = make_key(top, 0x7fffffff) - 1;  // below every key of that logit
     }
-    T_key = threads_threshold(k, M, s_warp);
-    if (T_key) --T_key;  // that key itself is a candidate
-    T_val = T_key ? key_value(T_key + 1) : -INFINITY;
   }
   for (int tile = tile0; tile < tile1; ++tile) {
-    uint32_t some = use(0);
+    int had = cnt;
+    use(tile, 0);
     if (tile + 1 < tile1) load(tile + 1, 0);
-    some |= use(1);
+    use(tile, 1);
     if (tile + 1 < tile1) load(tile + 1, 1);
-    // (a tile without a candidate: one barrier)
-    if (!__syncthreads_or(some != 0)) continue;
-    while (true) {
-      while (some) {  // few: read again
-        const int at = token(tile, __ffs(some) - 1);
-        some &= some - 1;
-        const uint64_t k = key_at(at);
-        if (k > T_key) {
-          const int place = atomicAdd(&s_cnt, 1);
-          if (place < kBuffer) s_buf[place] = k;
-        }
-      }
-      __syncthreads();
-      const int now = s_cnt;
-      if (now <= kBuffer) {
-        cnt = now;
-        // a tight T for the tiles to come: after the first one, then as the buffer doubles
-        // (not for the last few: they bring fewer keys than the sorting costs)
-        if (tile + 3 < tile1 && cnt > (tile == tile0 ? M : max(2 * M, 32))) {
-          sort_buffer(s_buf, s_rank, cnt, M);
-          cnt = M;
-          T_key = s_buf[M - 1];
-          T_val = key_value(T_key);
-          if (tid == 0) s_cnt = M;
-        }
-        __syncthreads();
-        break;
-      }
-      // too many: what this tile pushed is dropped, T raised, and the tile tried again
-      __syncthreads();
-      if (cnt > M) {  // the buffer's M largest stay, and T is the last of them
-        sort_buffer(s_buf, s_rank, cnt, M);
-        cnt = M;
-        T_key = max(T_key, s_buf[M - 1]);
+    const int n = tile - tile0 + 1;
+    // (the last few tiles bring fewer keys than a cut costs)
+    const bool due = (n & (n - 1)) == 0 && tile + 3 < tile1;
+    bool full = __syncthreads_or(cnt > kWarpKeys);
+    if (!due && !full) continue;
+    // Too many for a warp's buffer (ties, rows that rise from tile to tile): without what
+    // the tile brought, cut; then T raised by the tile itself until its keys fit.
+    while (full) {
+      cnt = had;
+      if (__syncthreads_or(had > 0)) {
+        cut();
+        had = 0;
       } else {
-        // (rows that rise from tile to tile) M of this tile's keys are as large as the
-        // threshold of the threads' maxima
-        uint64_t k = 0;
+        // the T that leaves M of the tile's keys above it (which fit), bit by bit: keys are
+        // unique, so there is one
+        uint64_t t = 0;
 #pragma unroll 1
-        for (int i = 0; i < 2 * kHalf; ++i) k = max(k, key_at(token(tile, i)));
-        uint64_t t = threads_threshold(k, M, s_warp);
-        if (t) --t;
-        if (t <= T_key) {
-          // which does not help where ties crowd: the T that leaves M keys above it, bit
-          // by bit (keys are unique, so there is one)
-          t = 0;
-#pragma unroll 1
-          for (int bit = 63; bit >= 0; --bit) {
-            const uint64_t c = t | 1ull << bit;
-            int32_t n = 0;
-#pragma unroll 1
-            for (int i = 0; i < 2 * kHalf; ++i) n += key_at(token(tile, i)) > c;
-            if (block_sum(n, s_sum) >= M) t = c;
-          }
+        for (int bit = 63; bit >= 0; --bit) {
+          const uint64_t c = t | 1ull << bit;
+          int32_t above = 0;
+#pragma unroll 4
+          for (int i = 0; i < 2 * kHalf; ++i) above += key_at(token(tile, i)) > c;
+          if (block_sum(above, s_sum) >= M) t = c;
         }
         T_key = max(T_key, t);
+        T_val = key_value(T_key);
       }
-      T_val = key_value(T_key);
-      some = 0xffffffffu >> (32 - 2 * kHalf);
-      if (tid == 0) s_cnt = cnt;
-      __syncthreads();
+#pragma unroll 1
+      for (int i = 0; i < 2 * kHalf; ++i) push(key_at(token(tile, i)));
+      full = __syncthreads_or(cnt > kWarpKeys);
     }
+    if (due) cut();
   }
-  __syncthreads();
-  sort_buffer(s_buf, s_rank, cnt, M);
+  cut();
   uint64_t *out = p.keys + ((int64_t)row_id * p.splits + split) * M;
-  for (int i = tid; i < M; i += kThreads) out[i] = i < cnt ? s_buf[i] : 0;
+  for (int i = tid; i < M; i += kThreads) out[i] = i < num_top ? s_top[i] : 0;
   // the threads' sums, at the CTA's r
   float top = r;
 #pragma unroll
@@ -465,12 +443,12 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
 // One CTA a request.  All threads turn the lists' keys into ordered scores in shared
 // memory (as many as fit; a list's further ones are read when it gets there).  Few
 // lists and up to a thread each, a candidate finds its place by counting the better ones
-// (8 lists of 16: 6.6 us, by rounds 9.4); others are merged by one warp in M rounds over
-// the heads of the lists (64 lists of 4: 7 us, by counting 8.5).  List k splits + j holds
+// (8 lists of 16: 6.5 us, by rounds 9.4); others are merged by one warp in M rounds over
+// the heads of the lists (64 lists of 4: 6.6 us, by counting 8.5).  List k splits + j holds
 // beam k's best of its j-th range: equal scores go to the lower list.
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ double s_base[kMaxLists];       // cum - lse of the request's beams
-  __shared__ uint64_t s_score[kMergeScores];  // [list][depth], ordered
+  __shared__ alignas(16) uint64_t s_score[kMergeScores];  // [list][depth], ordered
   __shared__ uint64_t s_head[kMaxLists];     // of each list the first score left
   __shared__ int32_t s_next[kMaxLists];
   __shared__ uint64_t s_won[kMaxSelect];     // of each round the score (0: none left),
@@ -526,12 +504,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     s_score[tid] = own;
     const int have = __syncthreads_count(own != 0);
     if (own) {
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const uint64_t o = s_score[j];
-        rank += o > own || (o == own && j < tid);
-      }
+      // larger ones, and equal ones before it
+      const int here = tid & ~7, end = (n + 7) & ~7;
+      int rank = count_above(s_score, 0, here, own - 1) + count_above(s_score, here, end, own);
+      for (int j = here; j < tid; ++j) rank += s_score[j] == own;
       if (rank < M) put(rank, own, tid / M, first);
     }
     for (int i = have + tid; i < M; i += kThreads) put(i, 0, 0, 0);
