@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarpsCta = kThreads / 32;
+constexpr int kMaxTok = 64;  // tokens of an index update's CTA at most
 
 // Two bf16 of a word as floats; infinities and NaN as 0.
 __device__ __forceinline__ void finite_bf16x2(uint32_t w, float &a, float &b) {
@@ -38,6 +39,20 @@ __device__ __forceinline__ void finite_bf16x8(const uint4 &v, float *x) {
   finite_bf16x2(v.z, x[4], x[5]);
   finite_bf16x2(v.w, x[6], x[7]);
 }
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
+         ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ float pow2f(int e) {  // 2^e, -126 <= e <= 127
   return __int_as_float((e + 127) << 23);
 }
@@ -49,91 +64,124 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // ---------------------------------------------------------------- index update
 //
-// One warp a (token, KV head).  Of a block's tokens in the step the one with the largest
-// offset makes the bounds, from the block's rows up to it (read back from the pool: a
-// slot written again after rejected tokens gives the bounds of what is there now).
+// A CTA takes kTok consecutive tokens.  Of a block's tokens in the step the one with the
+// largest offset makes the bounds, from the block's rows up to it (read back from the pool:
+// a slot written again after rejected tokens gives the bounds of what is there now); the
+// CTA lists its tokens that do and its warps take them, a KV head at a time.  Few tokens:
+// one a CTA, a warp a head; a prefill: 64, of which 4 do (35000 tokens of 8 heads of 128:
+// 18.5 us, 4.1 TB/s; with 16 a CTA 22.6, with a warp for
+// every (token, head) 74).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     index_update_kernel(const uint4 *__restrict__ pool, const int32_t *__restrict__ slots,
-                        int32_t num_tokens, int32_t num_blocks, int32_t hkv,
+                        int32_t num_tokens, int32_t num_blocks, int32_t hkv, int32_t tok,
                         int8_t *__restrict__ index, float *__restrict__ scales,
                         int32_t *dev_status) {
   constexpr int kLanes = D / 8;          // lanes of a key row, 8 elements each
   constexpr int kRows = 32 / kLanes;     // rows of one warp load
   constexpr int kLoads = kBlockSize / kRows;
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarpsCta + (threadIdx.x >> 5);
-  if (unit >= (int64_t)num_tokens * hkv) return;
-  const int32_t t = (int32_t)(unit / hkv), h = (int32_t)(unit % hkv);
-  const int32_t slot = __ldg(slots + t);
-  if (slot < 0) return;
-  const int32_t block = slot / kBlockSize, off = slot % kBlockSize;
-  if (block >= num_blocks) {
-    if (h == 0 && lane == 0) report(dev_status, PKV_DEV_BAD_SLOT);
-    return;
+  constexpr int kReach = kBlockSize - 1;  // how far apart a block's tokens lie at most
+  __shared__ int32_t s_slot[kMaxTok + 2 * kReach];
+  __shared__ int32_t s_list[kMaxTok], s_num;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * tok;
+  for (int i = threadIdx.x; i < tok + 2 * kReach; i += kThreads) {
+    const int64_t t = t0 - kReach + i;
+    s_slot[i] = t >= 0 && t < num_tokens ? __ldg(slots + t) : -1;
   }
-  // another token within 15 that writes further into the block (or the same slot, later)
-  const int64_t o = (int64_t)t - 15 + lane;
-  bool other = false;
-  if (lane < 31 && o != t && o >= 0 && o < num_tokens) {
-    const int32_t s = __ldg(slots + o);
-    other = s >= 0 && s / kBlockSize == block && (s > slot || (s == slot && o > t));
+  if (threadIdx.x == 0) s_num = 0;
+  __syncthreads();
+  if ((int)threadIdx.x < tok) {
+    const int at = threadIdx.x + kReach;
+    const int32_t slot = s_slot[at], block = slot / kBlockSize;
+    if (slot >= 0 && block >= num_blocks) {
+      report(dev_status, PKV_DEV_BAD_SLOT);
+    } else if (slot >= 0) {
+      // another token that writes further into the block (or the same slot, later)
+      bool other = false;
+#pragma unroll
+      for (int o = -kReach; o <= kReach; ++o) {
+        const int32_t s = s_slot[at + o];
+        other |= s >= 0 && s / kBlockSize == block && (s > slot || (s == slot && o > 0));
+      }
+      if (!other) s_list[atomicAdd(&s_num, 1)] = slot;
+    }
   }
-  if (__any_sync(0xffffffffu, other)) return;
-  const uint4 *rows = pool + ((int64_t)block * 2 * hkv + h) * kBlockSize * kLanes;
-  uint4 v[kLoads];
+  __syncthreads();
+  const int units = s_num * hkv;
+  for (int unit = warp; unit < units; unit += kWarpsCta) {
+    const int32_t slot = s_list[unit / hkv], h = unit % hkv;
+    const int32_t block = slot / kBlockSize, off = slot % kBlockSize;
+    const uint4 *rows = pool + ((int64_t)block * 2 * hkv + h) * kBlockSize * kLanes;
+    uint4 v[kLoads];
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u)
-    if (u * kRows + lane / kLanes <= off) v[u] = ldg128(rows + u * 32 + lane);
-  float lo[8], hi[8];
+    for (int u = 0; u < kLoads; ++u)
+      if (u * kRows + lane / kLanes <= off) v[u] = ldg128(rows + u * 32 + lane);
+    // bounds of pairs of elements; values that are not finite (found by their exponent, a
+    // carry into the sign's place) count as 0
+    uint32_t odd = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
+    for (int u = 0; u < kLoads; ++u)
+      if (u * kRows + lane / kLanes <= off)
+        odd |= (((v[u].x & 0x7f807f80u) + 0x00800080u) | ((v[u].y & 0x7f807f80u) + 0x00800080u) |
+                ((v[u].z & 0x7f807f80u) + 0x00800080u) | ((v[u].w & 0x7f807f80u) + 0x00800080u)) &
+               0x80008000u;
+    if (__any_sync(0xffffffffu, odd != 0)) {
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u)
-    if (u * kRows + lane / kLanes <= off) {
-      float x[8];
-      finite_bf16x8(v[u], x);
+      for (int u = 0; u < kLoads; ++u)
+        v[u] = make_uint4(finite_only(v[u].x), finite_only(v[u].y), finite_only(v[u].z),
+                          finite_only(v[u].w));
+    }
+    uint32_t l2[4] = {0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u};  // inf
+    uint32_t h2[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo[i] = fminf(lo[i], x[i]);
-        hi[i] = fmaxf(hi[i], x[i]);
+    for (int u = 0; u < kLoads; ++u)
+      if (u * kRows + lane / kLanes <= off) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          l2[i] = min_bf16x2(l2[i], w[i]);
+          h2[i] = max_bf16x2(h2[i], w[i]);
+        }
+      }
+    float lo[8], hi[8], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int w = kLanes; w < 32; w <<= 1) {
+        l2[i] = min_bf16x2(l2[i], __shfl_xor_sync(0xffffffffu, l2[i], w));
+        h2[i] = max_bf16x2(h2[i], __shfl_xor_sync(0xffffffffu, h2[i], w));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        lo[2 * i + j] = __uint_as_float(j ? l2[i] & 0xffff0000u : l2[i] << 16);
+        hi[2 * i + j] = __uint_as_float(j ? h2[i] & 0xffff0000u : h2[i] << 16);
+        top = fmaxf(top, fmaxf(fabsf(lo[2 * i + j]), fabsf(hi[2 * i + j])));
       }
     }
-  float top = 0.f;
+    top = warp_max(top);
+    // top is 1.f 2^E with 7 bits of f; 127 = 1.984375 2^6 has f = 126
+    const uint32_t bits = __float_as_uint(top);
+    const int e = max((int)(bits >> 23) - 127 - 6 + ((bits >> 16 & 127u) == 127u), -64);
+    const float inv = pow2f(-e);
+    uint32_t w[2][2] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int w = kLanes; w < 32; w <<= 1) {
-      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], w));
-      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], w));
+    for (int i = 0; i < 8; ++i) {
+      // a product that underflows to 0 is still below (above) 0
+      const float a = lo[i] * inv, b = hi[i] * inv;
+      const int f = a == 0.f && lo[i] < 0.f ? -1 : __float2int_rd(a);
+      const int c = b == 0.f && hi[i] > 0.f ? 1 : __float2int_ru(b);
+      w[0][i >> 2] |= (uint32_t)(f & 255) << (8 * (i & 3));
+      w[1][i >> 2] |= (uint32_t)(c & 255) << (8 * (i & 3));
     }
-    top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    const int64_t row = (int64_t)block * hkv + h;
+    if (lane < 2 * kLanes) {  // the second set of lanes (the same values) writes hi
+      const bool up = lane >= kLanes;
+      *reinterpret_cast<uint2 *>(index + row * 2 * D + (up ? D : 0) + (lane % kLanes) * 8) =
+          make_uint2(up ? w[1][0] : w[0][0], up ? w[1][1] : w[0][1]);
+    }
+    if (lane == 0) scales[row] = pow2f(e);
   }
-  top = warp_max(top);
-  // top is 1.f 2^E with 7 bits of f; 127 = 1.984375 2^6 has f = 126
-  const uint32_t bits = __float_as_uint(top);
-  const int e = max((int)(bits >> 23) - 127 - 6 + ((bits >> 16 & 127u) == 127u), -64);
-  const float inv = pow2f(-e);
-  uint32_t w[2][2] = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // a product that underflows to 0 is still below (above) 0
-    const float a = lo[i] * inv, b = hi[i] * inv;
-    const int f = a == 0.f && lo[i] < 0.f ? -1 : __float2int_rd(a);
-    const int c = b == 0.f && hi[i] > 0.f ? 1 : __float2int_ru(b);
-    w[0][i >> 2] |= (uint32_t)(f & 255) << (8 * (i & 3));
-    w[1][i >> 2] |= (uint32_t)(c & 255) << (8 * (i & 3));
-  }
-  const int64_t row = (int64_t)block * hkv + h;
-  if (lane < 2 * kLanes) {  // the second set of lanes (the same values) writes hi
-    const bool up = lane >= kLanes;
-    *reinterpret_cast<uint2 *>(index + row * 2 * D + (up ? D : 0) + (lane % kLanes) * 8) =
-        make_uint2(up ? w[1][0] : w[0][0], up ? w[1][1] : w[0][1]);
-  }
-  if (lane == 0) scales[row] = pow2f(e);
 }
 
 // ---------------------------------------------------------------- scores
@@ -469,15 +517,17 @@ extern "C" pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool
   if (!aligned16(kv_pool) || !aligned16(index) || !aligned16(index_scales) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 3u))
     return PKV_ERR_ALIGN;
-  const int64_t units = (int64_t)num_tokens * desc->num_kv_heads;
-  const int64_t ctas = (units + kWarpsCta - 1) / kWarpsCta;
-  if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  // tokens a CTA: about two CTAs an SM
+  const int64_t share = num_tokens / (2 * std::max(device_sm_count(), 1));
+  int tok = 1;
+  while (tok < kMaxTok && tok * 2 <= share) tok *= 2;
+  const int64_t ctas = ((int64_t)num_tokens + tok - 1) / tok;
   const bool wide = desc->head_dim == 128;
   profile_begin(PKV_KERNEL_INDEX, stream);
   cudaError_t e = launch_kernel(wide ? index_update_kernel<128> : index_update_kernel<64>,
                                 dim3((unsigned)ctas), dim3(kThreads), 0, stream, false,
                                 static_cast<const uint4 *>(kv_pool), slot_mapping, num_tokens,
-                                desc->num_blocks, desc->num_kv_heads, index, index_scales,
+                                desc->num_blocks, desc->num_kv_heads, tok, index, index_scales,
                                 dev_status);
   profile_end(PKV_KERNEL_INDEX, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
