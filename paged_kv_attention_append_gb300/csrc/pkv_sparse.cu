@@ -27,7 +27,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kCtasPerSm = 3;
+
 
 struct SparseParams {
   const __nv_bfloat16 *q;
@@ -40,6 +41,10 @@ struct SparseParams {
 
 template <int D>
 struct SparseCfg {
+  // 8 KB a warp and stage at D = 128: with two stages three CTAs share an SM, so that the
+  // (token, head) pairs of a call spread more evenly (192 pairs of 128 blocks: 38 us; three
+  // stages and two CTAs 46)
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kSlabBytes = D / 64 * kBoxBytes;
   static constexpr int kStageBytes = 2 * kSlabBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
@@ -85,10 +90,10 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     sparse_kernel(const __grid_constant__ CUtensorMap pool_map, const SparseParams p) {
   using C = SparseCfg<D>;
-  constexpr int kL = D / 32, kNt = D / 8;
+  constexpr int kL = D / 32, kNt = D / 8, kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int32_t s_sum[kWarps];
   // (the same offset in every CTA of a cluster, which map_rank relies on)
@@ -269,8 +274,8 @@ cudaError_t launch_sparse_t(const CUtensorMap &map, const SparseParams &p, int64
   using C = SparseCfg<D>;
   const cudaError_t pe = prepare_kernel<sparse_kernel<D>>(C::kSmemBytes);
   if (pe != cudaSuccess) return pe;
-  // CTAs of a (token, KV head): more while there are fewer CTAs than the SMs hold at once
-  // (two each) and every warp would still have a block
+  // CTAs of a (token, KV head): more while there are fewer than two CTAs an SM and every
+  // warp would still have a block (192 pairs of 128 blocks: two each 38 us, four 45)
   int ranks = 1;
   while (ranks < 8 && total_q * p.hkv * ranks < 2ll * std::max(device_sm_count(), 1) &&
          2 * ranks * kWarps <= p.num_select)
