@@ -530,7 +530,8 @@ int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_st
     p.chunks = (p.max_blocks + p.chunk - 1) / p.chunk;
     cudaError_t e = launch_kernel(score_kernel<D>, dim3((unsigned)(n * p.chunks)), dim3(kThreads), 0,
                                   stream, pdl, p);
-    // (rows of more than 1024 scores by four times the threads: 192 rows of 5000, 22 us ->)
+    // (rows of more than 1024 scores by four times the threads: 192 rows of 1900 to 8200 in 16
+    // us, with 256 threads 22)
     const bool wide = p.max_blocks > 1024;
     if (e == cudaSuccess)
       e = launch_kernel(wide ? select_kernel<1024> : select_kernel<256>, dim3((unsigned)(n * p.hkv)),

