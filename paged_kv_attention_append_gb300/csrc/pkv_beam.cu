@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
   __shared__ uint32_t s_kth[kBeamWarps];
   __shared__ int32_t s_rank[kThreads], s_cnt[kBeamWarps], s_sum[kBeamWarps];
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();  // only now: the merge reads the call's inputs before its own wait
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row_id = blockIdx.x / p.splits;
   const int split = blockIdx.x % p.splits;
@@ -588,7 +589,8 @@ cudaError_t launch_rows(const BeamParams &p, int elems, int64_t ctas, pkv_stream
   const cudaError_t pe = elems == 32 ? prepare_kernel<beam_rows_kernel<T, 16>>(0)
                                      : prepare_kernel<beam_rows_kernel<T, 4>>(0);
   if (pe != cudaSuccess) return pe;
-  return launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream, false, p);
+  return launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream,
+                       !profiling_active(), p);
 }
 
 }  // namespace

@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kReach = kBlockSize - 1;  // how far apart a block's tokens lie at most
   __shared__ int32_t s_slot[kMaxTok + 2 * kReach];
   __shared__ int32_t s_list[kMaxTok], s_num;
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * tok;
   for (int i = threadIdx.x; i < tok + 2 * kReach; i += kThreads) {
@@ -571,7 +572,7 @@ extern "C" pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool
   const bool wide = desc->head_dim == 128;
   profile_begin(PKV_KERNEL_INDEX, stream);
   cudaError_t e = launch_kernel(wide ? index_update_kernel<128> : index_update_kernel<64>,
-                                dim3((unsigned)ctas), dim3(kThreads), 0, stream, false,
+                                dim3((unsigned)ctas), dim3(kThreads), 0, stream, !profiling_active(),
                                 static_cast<const uint4 *>(kv_pool), slot_mapping, num_tokens,
                                 desc->num_blocks, desc->num_kv_heads, tok, index, index_scales,
                                 dev_status);

@@ -10,6 +10,9 @@
 // counts meet in distributed shared memory, and each ranks its range, with a cluster
 // barrier where a second kernel would be launched.  A pool of a million blocks takes 32
 // rounds of that (4096 ids a CTA each).  Copies are bound by HBM.
+//
+// Every kernel here may be launched while the one before it ends, and waits for it before
+// it touches anything; none but compact's first lets its own dependents launch early.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -90,6 +93,7 @@ __device__ __forceinline__ void copy_unit(char *data, int64_t row_bytes, int32_t
 }
 
 __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const __grid_constant__ CopyParams p) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t per_pair = p.unit_end[p.num_arrays - 1];
   const int32_t pairs =
@@ -141,6 +145,7 @@ __global__ void __launch_bounds__(kThreads)
                 int32_t num_blocks, int32_t keep_parents, int32_t *__restrict__ new_tables,
                 int32_t *__restrict__ new_ctx, int32_t *dev_status) {
   __shared__ int32_t s_sum[kThreads / 32];
+  pdl_wait();
   const int64_t row = blockIdx.x / col_ctas;
   const int32_t col0 = (int32_t)(blockIdx.x % col_ctas) * kForkCols;
   if (row < num_new) {
@@ -182,6 +187,7 @@ __global__ void __launch_bounds__(kFreeThreads)
                 int32_t *__restrict__ ctx_lens, int32_t num_rows, int32_t width,
                 int32_t *__restrict__ refs, int32_t num_blocks, int32_t *dev_status) {
   __shared__ int32_t s_ctx;
+  pdl_wait();
   const int64_t row = __ldg(rows + blockIdx.x);
   if (row < 0) return;
   if (row >= num_rows) {
@@ -657,7 +663,7 @@ extern "C" pkv_status pkv_copy_blocks(const pkv_block_array *arrays, int32_t num
     const int64_t cap = 4ll * std::max(device_sm_count(), 1);  // one resident wave
     const int e = profiled(PKV_KERNEL_COPY, stream, [&] {
       return launch_kernel(copy_blocks_kernel, dim3((unsigned)std::min(ctas, cap)), dim3(kThreads), 0,
-                           stream, false, p);
+                           stream, !profiling_active(), p);
     });
     if (e) return PKV_ERR_CUDA;
     count_launches(1);
@@ -688,7 +694,7 @@ extern "C" pkv_status pkv_fork_sequences(const int32_t *parents, int32_t num_new
   const int64_t ctas = ((int64_t)num_new + num_rows) * cols;
   if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
-    return launch_kernel(fork_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, false, parents,
+    return launch_kernel(fork_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, !profiling_active(), parents,
                          num_new, block_tables, context_lens, num_rows, max_blocks_per_seq,
                          (int32_t)cols, ref_counts, num_blocks, keep_parents, new_tables,
                          new_context_lens, dev_status);
@@ -711,7 +717,7 @@ extern "C" pkv_status pkv_free_sequences(const int32_t *rows, int32_t num_listed
       misaligned4(ref_counts))
     return PKV_ERR_ALIGN;
   const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
-    return launch_kernel(free_kernel, dim3((unsigned)num_listed), dim3(kFreeThreads), 0, stream, false,
+    return launch_kernel(free_kernel, dim3((unsigned)num_listed), dim3(kFreeThreads), 0, stream, !profiling_active(),
                          rows, block_tables, context_lens, num_rows, max_blocks_per_seq, ref_counts,
                          num_blocks, dev_status);
   });
@@ -785,7 +791,7 @@ extern "C" pkv_status pkv_reserve_blocks(const int32_t *cu_new, int32_t *block_t
   const int smem = std::max(12 * p.hash_size, 4 * (kSegIds + num_rows));  // 16 to 192 KB
   if (prepare_kernel<reserve_kernel>(12 * 16384) != cudaSuccess) return PKV_ERR_CUDA;
   const int e = profiled(PKV_KERNEL_PAGES, stream,
-                         [&] { return launch_cluster<reserve_kernel>(smem, stream, false, p); });
+                         [&] { return launch_cluster<reserve_kernel>(smem, stream, !profiling_active(), p); });
   if (e) return PKV_ERR_CUDA;
   count_launches(1);
   return PKV_OK;
@@ -839,7 +845,7 @@ extern "C" pkv_status pkv_compact_blocks(const int32_t *block_tables, const int3
   if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const bool pdl = !profiling_active();
   const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
-    const cudaError_t le = launch_cluster<compact_pairs_kernel>(0, stream, false, p);
+    const cudaError_t le = launch_cluster<compact_pairs_kernel>(0, stream, pdl, p);
     if (le != cudaSuccess) return le;
     return launch_kernel(compact_rename_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, pdl,
                          p, ref_ctas, (int32_t)cols);
