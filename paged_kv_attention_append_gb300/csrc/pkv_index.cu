@@ -198,7 +198,7 @@ struct SelectParams {
 // eight loads are in flight a lane, and their sums over the lanes are transposed on the
 // way (8 shuffles for 16 or 32 blocks).
 template <int D>
-__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 4) score_kernel(const SelectParams p) {
   constexpr int kLpr = 2 * D / 16;     // lanes of an index row
   constexpr int kRpi = 32 / kLpr;      // blocks of one warp load
   constexpr int kUnroll = 8;
@@ -292,29 +292,33 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
       waited = true;
     }
     float *out = p.scores + (local * p.hkv + h) * p.stride;
+    // (index vectors and scales are numbered below 2^31)
+    const uint4 *rows = reinterpret_cast<const uint4 *>(p.index + (int64_t)h * 2 * D) + lane % kLpr;
+    const uint32_t block_vecs = (uint32_t)(p.hkv * 2 * D / 16);
+    const float *scales = p.scales + h;
     auto entry = [&](int32_t b0) {  // lane i: the id of block b0 + i
       return lane < kBatch && b0 + lane < hi ? __ldg(table + b0 + lane) : -1;
     };
+    bool bad = false;  // a block outside the pool: reported behind the loop
     int32_t next = entry(lo);  // a batch's ids are read while the one before is scored
     for (int32_t b0 = lo; b0 < hi; b0 += kBatch) {
       int32_t phys = next;
       next = entry(b0 + kBatch);
-      if (lane < kBatch && b0 + lane < hi && (phys < 0 || phys >= p.num_blocks)) {
+      if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
         phys = -1;
-        report(p.dev_status, PKV_DEV_BAD_BLOCK);
+        bad |= lane < kBatch && b0 + lane < hi;
       }
       uint4 v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int32_t ph = __shfl_sync(0xffffffffu, phys, u * kRpi + lane / kLpr);
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (ph >= 0)
-          v[u] = ldg128_nc(p.index + ((int64_t)ph * p.hkv + h) * 2 * D + lane % kLpr * 16);
+        // (block 0 in the place of none: a load without a branch)
+        const uint32_t ph = (uint32_t)max(__shfl_sync(0xffffffffu, phys, u * kRpi + lane / kLpr), 0);
+        v[u] = __ldg(rows + ph * block_vecs);
       }
       // the block whose score this lane ends up with
       const int mine = kLpr == 16 ? (lane >> 1 & 7) * 2 + (lane >> 4) : (lane & 7) * 4 + (lane >> 3);
       const int32_t ph = __shfl_sync(0xffffffffu, phys, mine);
-      const float scale = ph >= 0 ? __ldg(p.scales + (int64_t)ph * p.hkv + h) : 0.f;
+      const float scale = __ldg(scales + (uint32_t)max(ph, 0) * (uint32_t)p.hkv);
       int32_t a[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -343,6 +347,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
       if (b0 + mine < hi && (kLpr == 8 || (lane & 1) == 0))
         out[b0 + mine] = ph >= 0 ? __int2float_rn(a[0]) * scale : -INFINITY;
     }
+    if (bad) report(p.dev_status, PKV_DEV_BAD_BLOCK);
   }
   if (!waited) pdl_wait();
 }
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
   }
 }
 
-constexpr int64_t kScoreCtas = 8, kScoreBlocks = 128;
+constexpr int64_t kScoreCtas = 6, kScoreBlocks = 256;
 
 template <int D>
 int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_stream stream) {
@@ -606,6 +611,7 @@ extern "C" pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
   if (sink_blocks < 0 || recent_blocks < 1 || (int64_t)sink_blocks + recent_blocks > num_select)
     return PKV_ERR_RANGE;
   if (total_q == 0) return PKV_OK;
+  if (desc->num_blocks == 0) return PKV_ERR_SHAPE;
   if (!q || !cu_q_lens || !context_lens || !block_tables || !index || !index_scales || !selected ||
       !workspace)
     return PKV_ERR_NULL;
