@@ -6,10 +6,10 @@
 // over the counts, and the only atomics are sums, whose order does not matter.
 //
 // The bookkeeping is bound by latency: a few hundred KB of counts and tables.  Reserve and
-// the pairing of compact run as one cluster of eight CTAs: each counts a range of ids, the
-// counts meet in distributed shared memory, and each ranks its range, with a cluster
-// barrier where a second kernel would be launched.  A pool of a million blocks takes 32
-// rounds of that (4096 ids a CTA each).  Copies are bound by HBM.
+// the pairing of compact run as one cluster of up to eight CTAs (one for 4096 ids): each
+// counts a range of ids, the counts meet in distributed shared memory, and each ranks its
+// range, with a cluster barrier where a second kernel would be launched.  A pool of a
+// million blocks takes 32 rounds of that.  Copies are bound by HBM.
 //
 // Every kernel here may be launched while the one before it ends, and waits for it before
 // it touches anything; none but compact's first lets its own dependents launch early.
@@ -212,16 +212,17 @@ __global__ void __launch_bounds__(kFreeThreads)
 
 // ---------------------------------------------------------------- ranges of ids
 //
-// CTA `rank` of the cluster of kRanks looks after the ids [rank, rank + 1) range_ids(..), a
-// multiple of kSegIds, kSegIds of them at a time: kSegPer consecutive ids a thread.
+// CTA `rank` of the cluster (the whole grid) looks after the ids [rank, rank + 1)
+// range_ids(..), a multiple of kSegIds, kSegIds of them at a time: kSegPer consecutive ids
+// a thread.
 
-constexpr int kRanks = 8;
+constexpr int kMaxRanks = 8;
 constexpr int kRankThreads = 1024;
 constexpr int kSegPer = 4;
 constexpr int kSegIds = kRankThreads * kSegPer;
 
-__host__ __device__ __forceinline__ int64_t range_ids(int32_t num_blocks) {
-  const int64_t per = ((int64_t)num_blocks + kRanks - 1) / kRanks;
+__device__ __forceinline__ int64_t range_ids(int32_t num_blocks, int32_t ranks) {
+  const int64_t per = ((int64_t)num_blocks + ranks - 1) / ranks;
   return (per + kSegIds - 1) / kSegIds * kSegIds;
 }
 
@@ -262,14 +263,16 @@ __device__ __forceinline__ int32_t peer_int(const int32_t *p, uint32_t rank) {
 
 template <auto Kern, typename P>
 cudaError_t launch_cluster(int smem, pkv_stream stream, bool pdl, const P &p) {
+  const int64_t segs = ((int64_t)p.num_blocks + kSegIds - 1) / kSegIds;
+  const unsigned ranks = (unsigned)std::min<int64_t>(std::max<int64_t>(segs, 1), kMaxRanks);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kRanks);
+  cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kRankThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kRanks;
+  attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -400,9 +403,9 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
   int32_t *s_base = s_mem + kSegIds;  // [num_rows] row_base
   __shared__ int32_t s_sum[32], s_fail, s_free, s_demand;
   const int tid = threadIdx.x;
-  const int32_t rank = (int32_t)blockIdx.x;
+  const int32_t rank = (int32_t)blockIdx.x, ranks = (int32_t)gridDim.x;
   pdl_wait();
-  const int64_t range = range_ids(p.num_blocks), id_lo = rank * range;
+  const int64_t range = range_ids(p.num_blocks, ranks), id_lo = rank * range;
   const int64_t id_hi = min(id_lo + range, (int64_t)p.num_blocks);
   int32_t n = 0;
   for (int64_t i = id_lo; i < id_hi; i += kSegIds)
@@ -417,14 +420,13 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
   cluster_sync();
   demand = peer_int(&s_demand, 0);
   int32_t before = 0, total = 0;
-#pragma unroll
-  for (int k = 0; k < kRanks; ++k) {
+  for (int k = 0; k < ranks; ++k) {
     const int32_t f = peer_int(&s_free, k);
     if (k < rank) before += f;
     total += f;
   }
   cluster_arrive();  // what the others keep for this CTA is read; they wait for it at their end
-  const int32_t gtid = rank * kRankThreads + tid, threads = kRanks * kRankThreads;
+  const int32_t gtid = rank * kRankThreads + tid, threads = ranks * kRankThreads;
   if (demand < 0 || demand > total) {
     for (int32_t i = gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
     for (int32_t r = gtid; r < p.num_rows; r += threads) p.copy_src[r] = p.copy_dst[r] = -1;
@@ -508,10 +510,10 @@ struct CompactParams {
 __global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const CompactParams p) {
   __shared__ int32_t s_sum[32], s_live, s_stay;
   const int tid = threadIdx.x;
-  const int32_t rank = (int32_t)blockIdx.x;
+  const int32_t rank = (int32_t)blockIdx.x, ranks = (int32_t)gridDim.x;
   pdl_wait();
   pdl_trigger();  // the renaming waits for all of this
-  const int64_t range = range_ids(p.num_blocks), id_lo = rank * range;
+  const int64_t range = range_ids(p.num_blocks, ranks), id_lo = rank * range;
   const int64_t id_hi = min(id_lo + range, (int64_t)p.num_blocks);
   int32_t n = 0;
   for (int64_t i = id_lo; i < id_hi; i += kSegIds)
@@ -520,8 +522,7 @@ __global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const Compa
   if (tid == 0) s_live = n;
   cluster_sync();
   int32_t before = 0, L = 0;
-#pragma unroll
-  for (int k = 0; k < kRanks; ++k) {
+  for (int k = 0; k < ranks; ++k) {
     const int32_t f = peer_int(&s_live, k);
     if (k < rank) before += f;
     L += f;
@@ -537,8 +538,7 @@ __global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const Compa
   if (tid == 0) s_stay = n;
   cluster_sync();
   int32_t stay = 0;
-#pragma unroll
-  for (int k = 0; k < kRanks; ++k) stay += peer_int(&s_stay, k);
+  for (int k = 0; k < ranks; ++k) stay += peer_int(&s_stay, k);
   cluster_arrive();  // (waited for at the end: no CTA ends while others read its counts)
   const int32_t pairs = L - stay;
   int32_t live = before;  // live ids before the segment
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const Compa
     *p.num_pairs = pairs;
     *p.live = L;
   }
-  for (int32_t i = pairs + gtid; i < p.num_pairs_max; i += kRanks * kRankThreads)
+  for (int32_t i = pairs + gtid; i < p.num_pairs_max; i += ranks * kRankThreads)
     p.copy_src[i] = p.copy_dst[i] = -1;
   cluster_wait();
 }
