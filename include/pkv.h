@@ -598,8 +598,9 @@ PKV_API pkv_status pkv_state_checkpoint(const void *src, const int32_t *dst_slot
  *  - A used entry outside [0, num_blocks) is left out of the counts (copied as it is)
  *    and reported, PKV_DEV_BAD_BLOCK.  Counts that do not match the tables are
  *    reported where a call sees it, PKV_DEV_BAD_COUNT.
- *  - None of these kernels lets its dependents launch before it has finished, so the
- *    appends and the attention may follow directly.
+ *  - The kernels are launched with programmatic stream serialisation and wait for the
+ *    preceding kernel before they touch anything; a call does not let its dependents
+ *    launch before it has finished, so the appends and the attention may follow directly.
  *
  * pkv_copy_blocks: whole blocks copied inside every array of `arrays` (each layer's
  * pool, the scales of 8-bit pools, block indexes: whatever is stored by block):
@@ -715,7 +716,9 @@ PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t
  *   token -1 and parent -1 fill the rest.  parents is what pkv_fork_sequences takes.
  *   logit_type: PKV_BF16, PKV_FP16 or PKV_FP32; logits aligned to their type.
  *   num_select <= 128, num_beams <= 1024, vocab >= 1.  workspace: device, 16-byte
- *   aligned, pkv_beam_workspace_size(...) bytes; one call at a time.
+ *   aligned, pkv_beam_workspace_size(...) bytes, contents do not matter; one call at a
+ *   time.  scores, tokens and parents must not overlap the inputs.  The first kernel waits
+ *   for the preceding one before it reads anything.
  */
 #define PKV_BF16 0
 #define PKV_FP16 1
@@ -772,7 +775,10 @@ PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_de
  *   (PKV_DEV_PLAN_MISMATCH for the latter).
  *   workspace: device, 16-byte aligned; any size from pkv_select_workspace_size(1, ...)
  *   on serves (fewer bytes than pkv_select_workspace_size(total_q, ...): the tokens in
- *   several passes); one call at a time.
+ *   several passes); contents do not matter, one call at a time.
+ *   As in pkv_paged_varlen_attention, q, the lengths and the tables may be read before the
+ *   preceding kernel of the stream has completed (a kernel that lets its dependents launch
+ *   early must not write them); index, index_scales and the workspace are touched after it.
  */
 PKV_API size_t pkv_select_workspace_size(int64_t total_q, int32_t num_kv_heads,
                                          int32_t max_blocks_per_seq);
@@ -799,7 +805,9 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   entry is left as it was; one whose context is shorter than its window too,
  *   PKV_DEV_PLAN_MISMATCH.  num_q_heads / Hkv <= 16.  Weights are rounded to bf16 for
  *   the product with V, sums are fp32, out is rounded once to bf16.  Bytes of a
- *   visible block past the token's position do not reach its row.
+ *   visible block past the token's position do not reach its row.  out may be q itself, and
+ *   must not overlap the inputs otherwise.  q and the lengths may be read before the preceding
+ *   kernel has completed, selected, the tables and the pool are read after it.
  */
 PKV_API pkv_status pkv_paged_sparse_attention(const void *q, const int32_t *cu_q_lens,
                                               const int32_t *context_lens,

@@ -88,7 +88,8 @@ REFUSED = [
         (dict(cu=None), NULL), (dict(index=None), NULL), (dict(scales=None), NULL),
         (dict(selected=None), NULL), (dict(ws=None), NULL), (dict(q=A + 8), ALIGN),
         (dict(index=A + 8), ALIGN), (dict(ws=A + 8), ALIGN), (dict(wsb=95), WORKSPACE),
-        (dict(desc=dict(DESC, d=32)), UNSUPPORTED), (dict(total=0), OK),
+        (dict(desc=dict(DESC, d=32)), UNSUPPORTED), (dict(desc=dict(DESC, nb=0)), SHAPE),
+        (dict(total=0), OK),
         (dict(total=0, seqs=0, width=0), OK)]),
     ("paged_sparse_attention", SPARSE, [
         (dict(width=-1), SHAPE), (dict(num=0), SHAPE), (dict(hq=7), SHAPE), (dict(hq=34), UNSUPPORTED),
