@@ -58,9 +58,9 @@ __device__ __forceinline__ float warp_max(float v) {
 // largest offset makes the bounds, from the block's rows up to it (read back from the pool:
 // a slot written again after rejected tokens gives the bounds of what is there now); the
 // CTA lists its tokens that do and its warps take them, a KV head at a time.  Few tokens:
-// one a CTA, a warp a head; a prefill: 64, of which 4 do (35000 tokens of 8 heads of 128:
-// 18.5 us, 4.1 TB/s; with 16 a CTA 22.6, with a warp for
-// every (token, head) 74).
+// one a CTA, a warp a head (256 tokens 3.4 us); a prefill: 64, of which 4 do (35000 tokens
+// of 8 heads of 128, 76 MB: 16.4 us, 4.6 TB/s; with 16 a CTA 4 us more, with a warp for
+// every (token, head) 74; unpacking every value to fp32 took 7 us more).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     index_update_kernel(const uint4 *__restrict__ pool, const int32_t *__restrict__ slots,
@@ -194,9 +194,12 @@ struct SelectParams {
 
 // CTAs (token, range of blocks); a warp takes one KV head (or a part of the range where
 // there are fewer heads than warps), so the CTA reads the heads of a block together.
-// LPR lanes hold a block's 2 D bytes, 16 each, against weights that stay in registers;
+// kLpr lanes hold a block's 2 D bytes, 16 each, against weights that stay in registers;
 // eight loads are in flight a lane, and their sums over the lanes are transposed on the
-// way (8 shuffles for 16 or 32 blocks).
+// way (8 shuffles for 16 or 32 blocks).  The loads are not predicated (a block that is not
+// there reads block 0's row): with a branch each, 24 tokens of 1900 to 8200 blocks (254 MB)
+// took 62 us, now 48.  Ranges of 128 blocks instead of 208: 55; of 512: 57 (few, uneven
+// CTAs).  Loads alone, in one even wave, take 40.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) score_kernel(const SelectParams p) {
   constexpr int kLpr = 2 * D / 16;     // lanes of an index row
@@ -529,7 +532,8 @@ int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_st
   for (int64_t t0 = 0; t0 < total_q; t0 += pass_tokens) {
     const int64_t n = std::min(pass_tokens, total_q - t0);
     p.token0 = t0;
-    // a warp's blocks: enough CTAs for kScoreCtas an SM, 16 to kScoreBlocks
+    // a warp's blocks: enough CTAs for kScoreCtas an SM, 16 to kScoreBlocks (the lengths are
+    // not known here: the table's width stands for every token's)
     const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
     const int64_t want = n * p.max_blocks / (kScoreCtas * std::max(device_sm_count(), 1) * subs);
     p.chunk = subs * (int32_t)std::min<int64_t>(std::max<int64_t>(want / 16 * 16, 16), kScoreBlocks);
