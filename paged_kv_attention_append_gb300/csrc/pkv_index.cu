@@ -358,15 +358,15 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const SelectParams p
 // ---------------------------------------------------------------- selection
 //
 // One CTA a (token, KV head): the threshold, the score of the last block taken, by
-// histograms of 2048 bins over the scores' range (each over the bin before, at most three;
-// mostly the second bin holds one score and ends it), then one ordered pass that writes
-// the blocks above it and the first of those equal to it.
-constexpr int kBins = 2048;
-constexpr int kCached = 8192;  // scores kept in shared memory; longer rows are read again
-
+// histograms over the scores' range (each over the bin before, at most four; mostly the
+// second bin holds one score and ends it), then one ordered pass that writes the blocks
+// above it and the first of those equal to it.  Two bins a thread, and eight scores a
+// thread kept in shared memory (longer rows are read again).
 template <int kT>
 __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
-  constexpr int kW = kT / 32;
+  constexpr int kW = kT / 32, kPer = 2, kBins = kPer * kT, kCached = 8 * kT;
+  constexpr int kBinBits = kT == 256 ? 9 : 11;
+  static_assert(kBins == 1 << kBinBits, "a bin for every value of the digit");
   __shared__ uint32_t s_key[kCached];
   __shared__ int32_t s_bin[kBins];
   __shared__ int32_t s_sum[kW], s_gt[kW], s_eq[kW];
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
   int bits = 32 - __clz(hi - lo);
   int32_t above = 0;
   while (bits > 0) {
-    const int shift = max(bits - 11, 0);
+    const int shift = max(bits - kBinBits, 0);
 #pragma unroll 4
     for (int32_t i = tid; i < n; i += kT) {
       const uint32_t k = key_at(i) - lo;
@@ -439,7 +439,6 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
     }
     __syncthreads();
     // thread t: bins [kPer (kT - 1 - t), + kPer), from the top down
-    constexpr int kPer = kBins / kT;
     const int base = kPer * (kT - 1 - tid);
     int32_t own = 0, bin[kPer];
 #pragma unroll
@@ -456,8 +455,7 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
     }
     if (lane == 31) s_sum[warp] = x;
     __syncthreads();
-    int32_t before = above + x - own;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    const int32_t before = above + x - own + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
     if (before < need && before + own >= need) {  // one thread
       int32_t c = before;
 #pragma unroll
@@ -505,11 +503,8 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
     s_eq[warp] = y;
   }
   __syncthreads();
-  int32_t gt0 = x - gt, eq0 = y - eq;
-  for (int w = 0; w < warp; ++w) {
-    gt0 += s_gt[w];
-    eq0 += s_eq[w];
-  }
+  int32_t gt0 = x - gt + __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+  int32_t eq0 = y - eq + __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
   if (gt == 0 && (eq == 0 || eq0 >= ties)) return;
   for (int32_t i = i0; i < i1; ++i) {
     const uint32_t k = key_at(i);
