@@ -275,10 +275,12 @@ cudaError_t launch_sparse_t(const CUtensorMap &map, const SparseParams &p, int64
   const cudaError_t pe = prepare_kernel<sparse_kernel<D>>(C::kSmemBytes);
   if (pe != cudaSuccess) return pe;
   // CTAs of a (token, KV head): more while there are fewer than two CTAs an SM and every
-  // warp would still have a block (192 pairs of 128 blocks: two each 38 us, four 45)
+  // warp would still have two blocks (192 pairs of 128 blocks: two each 38 us, four 45; the
+  // 8 pairs of one token, 32 blocks: the three calls 10.8 us with four each, 11.5 with
+  // eight, 11.7 with two)
   int ranks = 1;
   while (ranks < 8 && total_q * p.hkv * ranks < 2ll * std::max(device_sm_count(), 1) &&
-         2 * ranks * kWarps <= p.num_select)
+         4 * ranks * kWarps <= p.num_select)
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total_q * p.hkv * ranks));

@@ -513,6 +513,71 @@ def test_page_calls_captured_and_on_another_stream(pkv, cuda_device):
         check(room)
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_the_life_of_a_pool(pkv, cuda_device, seed):
+    """Random forks (all rows reordered, or some added), reservations with their copies and
+    writes, ends of sequences and compactions over one small pool: after each, tables, lengths and
+    counts are those of the plain forms, and every row's blocks hold what the row has written."""
+    dev, rng = cuda_device, np.random.default_rng(4000 + seed)
+    rows, width, blocks = 12, 7, 70
+    tables, ctx, refs = (np.full((rows, width), -1), np.zeros(rows, dtype=np.int64),
+                         np.zeros(blocks, dtype=np.int64))
+    pool = torch.zeros((blocks, 16), dtype=torch.int32, device=dev)   # a number a slot
+    rowed = [[] for _ in range(rows)]
+    d_tables, d_ctx, d_refs = (dev_i32(x, dev) for x in (tables, ctx, refs))
+    st, stamp = status_of(dev), 0
+    for step in range(80):
+        kind = rng.choice(["fork", "reserve", "reserve", "free", "compact"])
+        if kind == "fork":
+            parents = np.where(rng.random(rows) < 0.6, np.arange(rows), rng.integers(-1, rows, rows))
+            new, new_ctx = np.full((rows, width), -1), np.zeros(rows, dtype=np.int64)
+            ref.fork(parents, tables, ctx, refs, new, new_ctx, False)
+            d_new, d_new_ctx = dev_i32(np.full((rows, width), -1), dev), dev_i32(np.zeros(rows), dev)
+            pkv.fork_sequences(dev_i32(parents, dev), d_tables, d_ctx, d_refs, d_new, d_new_ctx,
+                               dev_status=st)
+            tables, ctx, d_tables, d_ctx = new, new_ctx, d_new, d_new_ctx
+            rowed = [list(rowed[p]) if p >= 0 else [] for p in parents]
+        elif kind == "reserve":
+            n = np.where(rng.random(rows) < 0.5, 0, rng.integers(0, 20, rows))
+            cu = np.concatenate([[0], np.cumsum(n)])
+            want = [tables.copy(), ctx.copy(), refs.copy()]
+            got = ref.reserve(cu, *want)
+            slots, src, dst = pkv.reserve_blocks(dev_i32(cu, dev), d_tables, d_ctx, d_refs,
+                                                 num_tokens=int(cu[-1]), dev_status=st)
+            if got is None:
+                assert int(st.item()) == 7 and (slots.numel() == 0 or int(slots.max()) == -1)
+                st.zero_()
+            else:
+                tables, ctx, refs = want
+                for a, b in zip((slots, src, dst), got):
+                    same(a, b)
+                pkv.copy_blocks(pool, src, dst, dev_status=st)
+                stamps = np.arange(stamp, stamp + int(cu[-1]))
+                stamp += int(cu[-1])
+                pool.view(-1)[slots.long()] = dev_i32(stamps, dev)
+                for r in range(rows):
+                    rowed[r] += stamps[cu[r]:cu[r + 1]].tolist()
+        elif kind == "free":
+            listed = rng.integers(-1, rows, 3)
+            ref.free(listed, tables, ctx, refs)
+            pkv.free_sequences(dev_i32(listed, dev), d_tables, d_ctx, d_refs, dev_status=st)
+            for r in listed[listed >= 0]:
+                rowed[r] = []
+        else:
+            tables, refs, src, dst = ref.compact(tables, ctx, refs)
+            a, b, n = pkv.compact_blocks(d_tables, d_ctx, d_refs, dev_status=st)
+            assert int(n.item()) == len(src) and a.tolist()[:len(src)] == src and b.tolist()[:len(src)] == dst
+            pkv.copy_blocks([pool], a, b, num_pairs=n, dev_status=st)
+        assert int(st.item()) == 0
+        same(d_ctx, ctx)
+        same(d_refs, refs)
+        table, held = d_tables.cpu().numpy(), pool.cpu().numpy()
+        for r in range(rows):
+            n = ref.used(ctx[r])
+            assert table[r, :n].tolist() == tables[r, :n].tolist()
+            assert held[table[r, :n]].reshape(-1)[:ctx[r]].tolist() == rowed[r], (step, kind, r)
+
+
 def test_python_refusals_on_device_tensors(pkv, cuda_device):
     dev = cuda_device
     t, c, r = dev_i32(np.zeros((4, 5)), dev), dev_i32(np.zeros(4), dev), dev_i32(np.zeros(9), dev)
