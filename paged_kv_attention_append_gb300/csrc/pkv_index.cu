@@ -177,6 +177,8 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------- scores
 
+constexpr int kScoreCtas = 4;  // an SM, by their registers
+
 struct SelectParams {
   const __nv_bfloat16 *q;
   const int32_t *cu_q_lens, *context_lens, *block_tables;
@@ -184,49 +186,114 @@ struct SelectParams {
   const float *scales;
   float *scores;          // [tokens of the pass][Hkv][stride]
   int32_t *selected;
-  int64_t token0;         // first token of the pass
+  int64_t token0, tokens;  // tokens of the pass
   int64_t stride;
   int32_t max_blocks, num_seqs, num_blocks, num_q_heads, hkv, group;
   int32_t num_select, sink, recent;
-  int32_t chunk, chunks;  // blocks of a CTA's range, ranges of a token
+  int32_t shares;         // into how many the blocks to score are cut
   int32_t *dev_status;
 };
 
-// CTAs (token, range of blocks); a warp takes one KV head (or a part of the range where
-// there are fewer heads than warps), so the CTA reads the heads of a block together.
+// A token's blocks to score are cut into equal ranges, one a CTA, of about a kScoreCtas * SMs'th
+// of all that the pass has to score: every CTA finds that share, and which range is its
+// own, from the lengths (a sequence's tokens count with the last one's blocks), so wide
+// tables and ragged contexts cost nothing.  A warp takes one KV head (or a part of the range
+// where there are fewer heads than warps), so the CTA reads the heads of a block together.
 // kLpr lanes hold a block's 2 D bytes, 16 each, against weights that stay in registers;
 // eight loads are in flight a lane, and their sums over the lanes are transposed on the
 // way (8 shuffles for 16 or 32 blocks).  The loads are not predicated (a block that is not
 // there reads block 0's row): with a branch each, 24 tokens of 1900 to 8200 blocks (254 MB)
-// took 62 us, now 48.  Ranges of 128 blocks instead of 208: 55; of 512: 57 (few, uneven
-// CTAs).  Loads alone, in one even wave, take 40.
+// took 62 us, now 48.  Loads alone, in one even wave, take 40.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kScoreCtas) score_kernel(const SelectParams p) {
   constexpr int kLpr = 2 * D / 16;     // lanes of an index row
   constexpr int kRpi = 32 / kLpr;      // blocks of one warp load
   constexpr int kUnroll = 8;
   constexpr int kBatch = kRpi * kUnroll;
-  __shared__ int32_t s_sum[kWarpsCta];
+  __shared__ int32_t s_sum[kWarpsCta], s_seq, s_range;
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t local = blockIdx.x / p.chunks;
-  const TokenPlace at = find_token(p.cu_q_lens, p.context_lens, p.num_seqs, p.token0 + local, s_sum);
-  const int32_t nb = at.pos / kBlockSize + 1;  // 0 when the token has no place
-  const int32_t b_lo = max((int32_t)(blockIdx.x % p.chunks) * p.chunk, p.sink);
-  const int32_t b_hi = min((int32_t)(blockIdx.x % p.chunks) * p.chunk + p.chunk, nb - p.recent);
-  // (a token without a place, or whose blocks are all selected: nothing to score)
-  if (at.pos < 0 || nb > p.max_blocks || nb <= p.num_select || b_lo >= b_hi) {
+  const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
+  // a sequence's tokens in this pass, and the blocks to score of the last of them
+  struct Span {
+    int32_t first, tokens, blocks, pos;  // first: counted from token0; pos: of the first
+  };
+  auto span = [&](int32_t s) {
+    const int32_t c0 = __ldg(p.cu_q_lens + s), c1 = __ldg(p.cu_q_lens + s + 1);
+    const int32_t ctx = __ldg(p.context_lens + s);
+    const int64_t a = max((int64_t)c0, p.token0), e = min((int64_t)c1, p.token0 + p.tokens);
+    Span x;
+    x.first = (int32_t)(a - p.token0);
+    x.tokens = e > a ? (int32_t)(e - a) : 0;
+    x.pos = ctx - (int32_t)(c1 - a);
+    const int32_t nb = (x.pos + x.tokens - 1) / kBlockSize + 1;
+    x.blocks = x.tokens > 0 && c1 - c0 <= ctx && (ctx - 1) / kBlockSize < p.max_blocks &&
+                       nb > p.num_select
+                   ? nb - p.sink - p.recent
+                   : 0;
+    return x;
+  };
+  // sum over the CTA (one barrier round), or over the threads before this one
+  auto cta_sum = [&](int32_t v, int32_t &before) {
+    int32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    const int32_t w = lane < kWarpsCta ? s_sum[lane] : 0;
+    before = x - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    return __reduce_add_sync(0xffffffffu, w);
+  };
+  int32_t work = 0, before;
+  for (int32_t s = threadIdx.x; s < p.num_seqs; s += kThreads) {
+    const Span x = span(s);
+    work += x.tokens * x.blocks;
+  }
+  const int32_t total = cta_sum(work, before), grain = kBatch * subs;
+  const int32_t share = max((total + p.shares - 1) / p.shares + grain - 1, grain) / grain * grain;
+  if (threadIdx.x == 0) s_seq = -1;
+  int32_t base = 0;
+  for (int32_t s0 = 0; s0 < p.num_seqs && base <= (int32_t)blockIdx.x; s0 += kThreads) {
+    const int32_t s = s0 + threadIdx.x;
+    int32_t own = 0;
+    if (s < p.num_seqs) {
+      const Span x = span(s);
+      own = x.tokens * ((x.blocks + share - 1) / share);
+    }
+    const int32_t sum = cta_sum(own, before), at = (int32_t)blockIdx.x - base - before;
+    if (at >= 0 && at < own) {  // one thread, in one of the rounds
+      s_seq = s;
+      s_range = at;
+    }
+    base += sum;
+  }
+  __syncthreads();
+  const int32_t seq = s_seq;
+  if (seq < 0) {
     pdl_wait();
     return;
   }
-  const int32_t *table = p.block_tables + (int64_t)at.seq * p.max_blocks;
-  const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
-  const int32_t sub_len = (p.chunk / subs + kBatch - 1) / kBatch * kBatch;
+  const Span sp = span(seq);
+  const int32_t ranges = (sp.blocks + share - 1) / share;
+  const int32_t range = ((sp.blocks + ranges - 1) / ranges + grain - 1) / grain * grain;
+  const int64_t local = sp.first + s_range / ranges;
+  const int32_t c0 = p.sink + s_range % ranges * range;
+  const int32_t nb = (sp.pos + s_range / ranges) / kBlockSize + 1;
+  const int32_t b_lo = c0, b_hi = min(c0 + range, nb - p.recent);
+  if (nb <= p.num_select || b_lo >= b_hi) {  // (an earlier token of a window: fewer blocks)
+    pdl_wait();
+    return;
+  }
+  const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks;
+  const int32_t sub_len = range / subs;  // a multiple of kBatch
   bool waited = false;
   for (int item = warp; item < p.hkv * subs; item += kWarpsCta) {
     const int h = item % p.hkv;
-    const int32_t c0 = (int32_t)(blockIdx.x % p.chunks) * p.chunk + item / p.hkv * sub_len;
-    const int32_t lo = max(c0, b_lo), hi = min(c0 + sub_len, b_hi);
+    const int32_t lo = c0 + item / p.hkv * sub_len, hi = min(lo + sub_len, b_hi);
     // this lane's weights: of 16 elements from d0, N against lo or P against hi.  The
     // kRpi sets of lanes that hold the same ones take every kRpi-th head each.
     const int d0 = lane % (D / 16) * 16, part = lane / kLpr;
@@ -515,8 +582,6 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
   }
 }
 
-constexpr int64_t kScoreCtas = 6, kScoreBlocks = 256;
-
 template <int D>
 int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_stream stream) {
   if (prepare_kernel<score_kernel<D>>(0) != cudaSuccess ||
@@ -527,17 +592,14 @@ int launch_select_t(SelectParams p, int64_t total_q, int64_t pass_tokens, pkv_st
   for (int64_t t0 = 0; t0 < total_q; t0 += pass_tokens) {
     const int64_t n = std::min(pass_tokens, total_q - t0);
     p.token0 = t0;
-    // a warp's blocks: enough CTAs for kScoreCtas an SM, 16 to kScoreBlocks (the lengths are
-    // not known here: the table's width stands for every token's)
-    const int subs = p.hkv >= kWarpsCta ? 1 : kWarpsCta / p.hkv;
-    const int64_t want = n * p.max_blocks / (kScoreCtas * std::max(device_sm_count(), 1) * subs);
-    p.chunk = subs * (int32_t)std::min<int64_t>(std::max<int64_t>(want / 16 * 16, 16), kScoreBlocks);
-    p.chunks = (p.max_blocks + p.chunk - 1) / p.chunk;
-    cudaError_t e = launch_kernel(score_kernel<D>, dim3((unsigned)(n * p.chunks)), dim3(kThreads), 0,
+    p.tokens = n;
+    // one resident wave of shares, and a remainder for every token
+    p.shares = kScoreCtas * std::max(device_sm_count(), 1);
+    cudaError_t e = launch_kernel(score_kernel<D>, dim3((unsigned)(p.shares + n)), dim3(kThreads), 0,
                                   stream, pdl, p);
-    // (rows of more than 1024 scores by four times the threads: 192 rows of 1900 to 8200 in 16
-    // us, with 256 threads 22)
-    const bool wide = p.max_blocks > 1024;
+    // (few rows of more than 1024 scores by four times the threads: 192 of 1900 to 8200 in 14
+    // us, with 256 threads 22; 2048 rows of 60 under a table of 8192 take 24 us more with them)
+    const bool wide = p.max_blocks > 1024 && n * p.hkv <= 2 * std::max(device_sm_count(), 1);
     if (e == cudaSuccess)
       e = launch_kernel(wide ? select_kernel<1024> : select_kernel<256>, dim3((unsigned)(n * p.hkv)),
                         dim3(wide ? 1024 : 256), 0, stream, pdl, p);
@@ -639,9 +701,9 @@ extern "C" pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
   p.sink = sink_blocks;
   p.recent = recent_blocks;
   p.dev_status = dev_status;
-  // a pass: what the workspace holds, within the grid's size
+  // a pass: what the workspace holds, its blocks and the grids counted in 32 bits
   int64_t pass = std::min(workspace_bytes / token, total_q);
-  pass = std::min(pass, (int64_t)INT32_MAX / std::max((max_blocks_per_seq + 15) / 16, p.hkv));
+  pass = std::min(pass, (int64_t)(1 << 30) / std::max(max_blocks_per_seq, p.hkv));
   profile_begin(PKV_KERNEL_SELECT, stream);
   const int e = desc->head_dim == 128 ? launch_select_t<128>(p, total_q, pass, stream)
                                       : launch_select_t<64>(p, total_q, pass, stream);
