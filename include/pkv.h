@@ -658,8 +658,9 @@ PKV_API pkv_status pkv_free_sequences(const int32_t *rows, int32_t num_listed,
  * Reserve: room for the new tokens of a step.  Row r gets n = cu_new[r + 1] -
  * cu_new[r] of them (0 where negative; device int32 [num_rows + 1]): its table the
  * blocks they need, context_lens[r] += n, and slot_mapping[cu_new[r] + i] the slot of
- * position context_lens[r] + i (old length), for the append; entries of slot_mapping
- * past num_tokens are not written.
+ * position context_lens[r] + i (old length), for the append.  Entries of slot_mapping
+ * before cu_new[0] or from cu_new[num_rows] on (a step padded to num_tokens) get -1,
+ * which the append skips; entries past num_tokens are not written.
  *   A partly filled last block that other rows hold too is not written to: the row
  *   takes a new block in its place, copy_src[r] and copy_dst[r] say which (-1 where
  *   there is none), for a pkv_copy_blocks before the append.  When every holder of such

@@ -1300,7 +1300,8 @@ def reserve_blocks(cu_new, block_tables, context_lens, ref_counts, *, num_tokens
     """Room for cu_new[r + 1] - cu_new[r] new tokens of each row r (pkv_reserve_blocks):
     block_tables, context_lens and ref_counts are updated in place.  Returns (slot_mapping,
     copy_src, copy_dst): the new tokens' slots for the append, and for each row the block to
-    copy before it (copy_blocks) where a partly filled one was shared, else -1.  When the
+    copy before it (copy_blocks) where a partly filled one was shared, else -1.  Slots behind
+    the last row's tokens (a padded step) are -1, which the append skips.  When the
     free blocks do not suffice nothing changes, every slot is -1 and dev_status says so."""
     b = BoundReserveBlocks(cu_new, block_tables, context_lens, ref_counts, num_tokens=num_tokens,
                            slot_mapping=slot_mapping, copy_src=copy_src, copy_dst=copy_dst,

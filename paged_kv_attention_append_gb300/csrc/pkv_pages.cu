@@ -411,6 +411,12 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
   for (int64_t i = id_lo; i < id_hi; i += kSegIds)
     n += kSegPer - __popc(load_used(p.refs, i + tid * kSegPer, p.num_blocks, true));
   n = cta_sum(n, s_sum);
+  const int32_t gtid = rank * kRankThreads + tid, threads = ranks * kRankThreads;
+  // slots that are no row's (the padding of a step behind its last row); before the barrier,
+  // the rows' own come after it
+  const int32_t cu_lo = __ldg(p.cu_new), cu_hi = __ldg(p.cu_new + p.num_rows);
+  for (int64_t i = gtid; i < min(cu_lo, p.num_tokens); i += threads) p.slots[i] = -1;
+  for (int64_t i = (int64_t)max(cu_hi, 0) + gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
   int32_t demand = 0;
   if (rank == 0) demand = plan_rows(p, s_mem, s_sum, &s_fail);
   if (tid == 0) {
@@ -426,9 +432,8 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
     total += f;
   }
   cluster_arrive();  // what the others keep for this CTA is read; they wait for it at their end
-  const int32_t gtid = rank * kRankThreads + tid, threads = ranks * kRankThreads;
   if (demand < 0 || demand > total) {
-    for (int32_t i = gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
+    for (int64_t i = gtid; i < p.num_tokens; i += threads) p.slots[i] = -1;
     for (int32_t r = gtid; r < p.num_rows; r += threads) p.copy_src[r] = p.copy_dst[r] = -1;
     if (gtid == 0)
       report(p.dev_status, demand == -2   ? PKV_DEV_BAD_BLOCK
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kRankThreads) compact_pairs_kernel(const Compa
     *p.num_pairs = pairs;
     *p.live = L;
   }
-  for (int32_t i = pairs + gtid; i < p.num_pairs_max; i += ranks * kRankThreads)
+  for (int64_t i = pairs + gtid; i < p.num_pairs_max; i += ranks * kRankThreads)
     p.copy_src[i] = p.copy_dst[i] = -1;
   cluster_wait();
 }
@@ -603,6 +608,11 @@ __global__ void __launch_bounds__(kThreads)
     }
     p.new_tables[row * p.width + j] = b;
   }
+}
+
+// CTAs of a row of a table.
+int64_t fork_ctas(int32_t width) {
+  return std::max<int64_t>(((int64_t)width + kForkCols - 1) / kForkCols, 1);
 }
 
 bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
@@ -690,7 +700,7 @@ extern "C" pkv_status pkv_fork_sequences(const int32_t *parents, int32_t num_new
   if ((num_new > 0 && num_rows > 0) &&
       (new_tables == block_tables || new_context_lens == context_lens))
     return PKV_ERR_SHAPE;
-  const int64_t cols = std::max((max_blocks_per_seq + kForkCols - 1) / kForkCols, 1);
+  const int64_t cols = fork_ctas(max_blocks_per_seq);
   const int64_t ctas = ((int64_t)num_new + num_rows) * cols;
   if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const int e = profiled(PKV_KERNEL_PAGES, stream, [&] {
@@ -840,7 +850,7 @@ extern "C" pkv_status pkv_compact_blocks(const int32_t *block_tables, const int3
   p.dev_status = dev_status;
   const int32_t ref_ctas = std::max(std::min((num_blocks + kThreads - 1) / kThreads,
                                              2 * std::max(device_sm_count(), 1)), 1);
-  const int64_t cols = std::max((max_blocks_per_seq + kForkCols - 1) / kForkCols, 1);
+  const int64_t cols = fork_ctas(max_blocks_per_seq);
   const int64_t ctas = ref_ctas + num_rows * cols;
   if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const bool pdl = !profiling_active();

@@ -241,6 +241,25 @@ def test_reserve_leaves_everything_when_it_cannot(pkv, cuda_device):
             assert set(x.cpu().tolist()) == {-1}
 
 
+@pytest.mark.parametrize("rows", [1, 5, 1300])
+@pytest.mark.parametrize("before,behind", [(0, 3), (4, 0), (2, 20000)])
+def test_reserve_gives_padding_no_slot(pkv, cuda_device, rows, before, behind):
+    """Slots before the first row's tokens and behind the last one's are -1, whatever they were;
+    those past num_tokens are left."""
+    rng = np.random.default_rng(rows)
+    tables, ctx, refs = ref.random_tables(rng, rows, 4, 4 * rows + 20000, 0.5, 30)
+    n = rng.integers(0, 20, rows)
+    cu = before + np.concatenate([[0], np.cumsum(n)])
+    want = [tables.copy(), ctx.copy(), refs.copy()]
+    slots, _, _ = ref.reserve(cu, *want)
+    d = [dev_i32(x, cuda_device) for x in (cu, tables, ctx, refs)]
+    whole = dev_i32(np.full(len(slots) + behind + 5, 77), cuda_device)
+    pkv.reserve_blocks(*d, slot_mapping=whole[:-5])
+    same(whole, np.concatenate([slots, np.full(behind, -1), np.full(5, 77)]))
+    for got, w in zip(d[1:], want):
+        same(got, w)
+
+
 def test_reserve_just_enough_and_unaligned_counts(pkv, cuda_device):
     """Every free block is taken, from counts that do not start on 16 bytes."""
     rng = np.random.default_rng(5)
