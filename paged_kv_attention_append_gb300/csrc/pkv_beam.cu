@@ -43,6 +43,7 @@ constexpr int kMaxSelect = 128;
 constexpr int kWarpKeys = 128;      // new candidate keys a warp keeps (>= kMaxSelect)
 constexpr int kAllKeys = kBeamWarps * kWarpKeys + kMaxSelect + 64;
 constexpr int kMaxLists = 1024;     // sorted lists (beam, split) of a request
+constexpr int32_t kMaxVocab = INT32_MAX - 65536;  // tiles count past its end in 32 bits
 constexpr int kMergeScores = 2048;  // scores a merge keeps in shared memory (>= kMaxLists)
 constexpr float kLog2e = 1.4426950408889634f;  // L above
 
@@ -419,6 +420,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
 #pragma unroll
   for (int i = 1; i < kBeamWarps; ++i) top = fmaxf(top, s_m[i]);
   s *= r == top ? 1.f : fast_exp2(r - top);
+  if (top == -INFINITY && num_top > 0) {
+    // all of the range masked by a lowest value, which times L is -inf: how often its largest
+    // logit is there (fp32's step in this place is 2^104, so no other one counts)
+    const float x0 = key_value(s_top[0]);
+    const int end = min(tile1 * kTile, p.vocab);
+    for (int at = tile0 * kTile + tid; at < end; at += kThreads)
+      s += W::get(raw_bits(row.data + at), 0) == x0 ? 1.f : 0.f;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) s_s[warp] = s;
@@ -448,7 +457,8 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
 // the heads of the lists (64 lists of 4: 6.6 us, by counting 8.5).  List k splits + j holds
 // beam k's best of its j-th range: equal scores go to the lower list.
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
-  __shared__ double s_base[kMaxLists];       // cum - lse of the request's beams
+  __shared__ double s_base[kMaxLists];       // cum - (lse - shift) of the request's beams,
+  __shared__ float s_shift[kMaxLists];       // shift 0 unless all of a row is as low as it gets
   __shared__ alignas(16) uint64_t s_score[kMergeScores];  // [list][depth], ordered
   __shared__ uint64_t s_head[kMaxLists];     // of each list the first score left
   __shared__ int32_t s_next[kMaxLists];
@@ -470,6 +480,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   if (tid < lists * depth) first = keys[(int64_t)(tid / depth) * M + tid % depth];
   for (int k = tid; k < p.num_beams; k += kThreads) {
     if (k != tid) base = __ldg(p.cum + row0 + k);
+    float shift = 0.f;
     if (!(k == tid ? ended : done(k))) {
       const float2 *part = p.part + (row0 + k) * p.splits;
       float m = -INFINITY, s = 0.f;
@@ -478,19 +489,31 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 #pragma unroll 8
       for (int j = 0; j < p.splits; ++j)
         s += part[j].y * (part[j].x == m ? 1.f : exp2f(part[j].x - m));
+      if (m == -INFINITY && s > 0.f) {
+        // the parts are counts of their largest logits: those of the row's largest
+        uint32_t best = 0;
+        for (int j = 0; j < p.splits; ++j)
+          best = max(best, (uint32_t)(keys[((int64_t)k * p.splits + j) * M] >> 32));
+        s = 0.f;
+        for (int j = 0; j < p.splits; ++j)
+          if ((uint32_t)(keys[((int64_t)k * p.splits + j) * M] >> 32) == best) s += part[j].y;
+        shift = key_value((uint64_t)best << 32);
+        m = 0.f;
+      }
       // log2 s by its exponent and mantissa: off by half a step of a number below 1
       int e;
       const float f = frexpf(s, &e);
       base -= ((double)m + (e - 1) + (double)log2f(2.f * f)) * (1.0 / (double)kLog2e);
     }
     s_base[k] = base;
+    s_shift[k] = shift;
   }
   __syncthreads();
   // the ordered score of list l's n-th key (0: there is none)
   auto score_of = [&](int l, int n, uint64_t key) -> uint64_t {
     const int k = l / p.splits;
     if (done(k)) return n == 0 && l == k * p.splits ? order_double(s_base[k]) : 0;
-    return key ? order_double(s_base[k] + (double)key_value(key)) : 0;
+    return key ? order_double(s_base[k] + ((double)key_value(key) - (double)s_shift[k])) : 0;
   };
   auto put = [&](int i, uint64_t score, int l, uint64_t key) {
     const int64_t o = (int64_t)blockIdx.x * M + i;
@@ -600,7 +623,8 @@ using namespace pkv;
 
 extern "C" size_t pkv_beam_workspace_size(int32_t num_requests, int32_t num_beams, int32_t vocab,
                                           int32_t num_select) {
-  if (num_requests <= 0 || num_beams < 1 || num_beams > kMaxLists || vocab < 1 || num_select < 1)
+  if (num_requests <= 0 || num_beams < 1 || num_beams > kMaxLists || vocab < 1 ||
+      vocab > kMaxVocab || num_select < 1)
     return 0;
   const int64_t rows = (int64_t)num_requests * num_beams;
   const BeamCut c = beam_cut(rows, num_beams, vocab);
@@ -619,8 +643,7 @@ extern "C" pkv_status pkv_beam_select(const void *logits, int32_t logit_type, in
     return PKV_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)num_requests * num_beams;
   if (rows > 1 && row_stride < vocab) return PKV_ERR_SHAPE;
-  // tokens of a tile are numbered in 32 bits past the vocabulary's end
-  if (vocab > INT32_MAX - 65536) return PKV_ERR_UNSUPPORTED;
+  if (vocab > kMaxVocab) return PKV_ERR_UNSUPPORTED;
   if (num_requests == 0) return PKV_OK;
   if (!logits || !cum_scores || !scores || !tokens || !parents || !workspace) return PKV_ERR_NULL;
   const uintptr_t size = logit_type == PKV_FP32 ? 4 : 2;

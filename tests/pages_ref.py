@@ -108,8 +108,8 @@ def beam(logits, cum, num, finished=None, pad=0):
     b, k, v = logits.shape
     with np.errstate(all="ignore"):
         top = logits.max(axis=2, keepdims=True)
-        lse = top[..., 0] + np.log(np.exp(logits - top).sum(axis=2))
-        score = np.asarray(cum, dtype=np.float64)[..., None] + (logits - lse[..., None])
+        lse = np.log(np.exp(logits - top).sum(axis=2, keepdims=True))  # above top
+        score = np.asarray(cum, dtype=np.float64)[..., None] + (logits - top - lse)
     if finished is not None:
         score[finished] = -np.inf
         score[finished, pad] = np.asarray(cum, dtype=np.float64)[finished]

@@ -378,6 +378,7 @@ def test_beam_select(pkv, cuda_device, case, dtype, pad, offset):
     check_beams(got, want[:3], want[3], f64, finished)
 
 
+LOWEST = float(torch.finfo(torch.float32).min)
 SHAPES = {  # rows that find the buffer's limits
     "equal": lambda rng, v: np.zeros(v),
     "rising": lambda rng, v: np.arange(v) / 64,
@@ -388,6 +389,10 @@ SHAPES = {  # rows that find the buffer's limits
     "one": lambda rng, v: np.where(np.arange(v) == v - 1, 50.0, -50.0),
     "masked": lambda rng, v: np.where(rng.random(v) < 0.999, -np.inf, rng.standard_normal(v)),
     "large": lambda rng, v: rng.standard_normal(v) * 60000,
+    "lowest": lambda rng, v: np.full(v, LOWEST),
+    "lows": lambda rng, v: rng.choice([LOWEST, -3e38, -2.4e38, -np.inf], v, p=[.9, .05, .04, .01]),
+    "lows apart": lambda rng, v: np.where(np.arange(v) < v // 2, LOWEST, -3e38),
+    "few not lowest": lambda rng, v: np.where(rng.random(v) < 0.999, LOWEST, rng.standard_normal(v)),
 }
 
 
@@ -430,6 +435,23 @@ def test_equal_beams_tie_to_the_lower_beam(pkv, cuda_device, dtype, v, pad):
     value = np.tile(row.double().numpy(), k)       # by logit, then beam, then token
     want = np.lexsort((np.arange(k * v), -value))[:num]
     assert p[0].tolist() == (want // v).tolist() and t[0].tolist() == (want % v).tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("v", [7, 3001, 200000])
+def test_rows_masked_by_the_lowest_value(pkv, cuda_device, dtype, v):
+    """All of a beam masked: every token alike, log v below the beam's score.  A NaN among them
+    still takes the beam out, and a beam with one token left goes on with that."""
+    low = torch.finfo(dtype).min
+    x = torch.full((1, 4, v), low, dtype=dtype)
+    x[0, 1, v // 2] = float("nan")
+    x[0, 2, v - 1] = 1.0
+    cum = np.array([[-1.0, 0.0, -20.0, -2.0]], dtype=np.float32)
+    f64 = x.double().numpy()
+    want = ref.beam(f64, cum, 9)
+    got = pkv.beam_select(x.to(cuda_device), torch.from_numpy(cum).to(cuda_device), 9)
+    check_beams(got, want[:3], want[3], f64, None)
+    assert got[2][0, 0].item() == 0 and abs(got[0][0, 0].item() + 1 + np.log(v)) < 1e-4
 
 
 def test_beams_that_are_not_there(pkv, cuda_device):
