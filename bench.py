@@ -78,7 +78,7 @@ PREFILL_MIN_Q = 64   # sequences with at least this many query tokens run on the
 # Sources that decide what a kernel does for a given workload: its own file,
 # the planner (its work lists), the entry points and the shared headers.
 KERNEL_SOURCES = {
-    "decode_kernel": ["pkv_decode.cu", "pkv_decode.cuh", "pkv_plan.cpp"],
+    "decode_kernel": ["pkv_decode.cu", "pkv_decode.cuh", "pkv_block.cuh", "pkv_plan.cpp"],
     "prefill_kernel": ["pkv_prefill.cu", "pkv_plan.cpp"],
     "state_checkpoint_kernel": ["pkv_state.cu"],
 }
