@@ -170,17 +170,6 @@ __device__ __forceinline__ void load_vec(const Row<T> &row, int32_t at, uint32_t
   }
 }
 
-__device__ __forceinline__ int32_t block_sum(int32_t v, int32_t *s) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int32_t t = 0;
-#pragma unroll
-  for (int w = 0; w < kBeamWarps; ++w) t += s[w];
-  return t;
-}
-
 // How many of s[begin, end) are above k.  Eight at a time, all loads ahead of the compares
 // (one by one, 150 keys took 7 us); begin and end multiples of 8, s 16-byte aligned.
 __device__ __forceinline__ int count_above(const uint64_t *s, int begin, int end, uint64_t k) {
@@ -224,16 +213,16 @@ __device__ __forceinline__ void sort_keys(const uint64_t *s_all, int cnt, uint64
   __syncthreads();
 }
 
-// A logit that at least M elements of the CTA reach: the smallest over the warps of their
-// ceil(M / 8)-th largest thread maximum.  s: an int a warp.
-__device__ __forceinline__ float threads_threshold(float top, int M, uint32_t *s) {
+// A logit that at least M elements of the CTA reach: the smallest over the first `warps` warps
+// of their ceil(M / warps)-th largest thread maximum (NaN: too few threads).  s: an int a warp.
+__device__ __forceinline__ float threads_threshold(float top, int M, int warps, uint32_t *s) {
   uint32_t o = (uint32_t)(make_key(top, 0) >> 32), kth = 0;
-  for (int i = 0; i < (M + kBeamWarps - 1) / kBeamWarps; ++i) {
+  for (int i = 0; i < M; i += warps) {
     kth = __reduce_max_sync(0xffffffffu, o);
     const uint32_t who = __ballot_sync(0xffffffffu, o == kth);
     if ((threadIdx.x & 31) == __ffs(who) - 1) o = 0;
   }
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = kth;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = (int)threadIdx.x >> 5 < warps ? kth : ~0u;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kBeamWarps; ++w) kth = min(kth, s[w]);
@@ -253,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   __shared__ uint64_t s_top[kMaxSelect];
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
   __shared__ uint32_t s_kth[kBeamWarps];
-  __shared__ int32_t s_rank[kThreads], s_cnt[kBeamWarps], s_sum[kBeamWarps];
+  __shared__ int32_t s_rank[kThreads], s_cnt[kBeamWarps];
   pdl_wait();
   pdl_trigger();  // only now: the merge reads the call's inputs before its own wait
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -352,8 +341,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     num_top = min(all, M);
     cnt = 0;
     if (num_top == M && s_top[M - 1] > T_key) {
+      // (the elements still to come are of higher tokens: equal logits do not pass any more)
       T_key = s_top[M - 1];
-      T_val = key_value(T_key);
+      T_val = key_value(T_key + (1ull << 32));
     }
   };
   load(tile0, 0);
@@ -362,7 +352,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     float x[kHalf];
     float top = elements(0, x);
     top = fmaxf(top, elements(1, x));
-    top = threads_threshold(top, M, s_kth);
+    // (warps whose threads all have elements: rows of 300 to 600, or as short a last range, took
+    // 15 to 160 us with the others counted in, as then every element was a candidate)
+    const int left = p.vocab - tile0 * kTile;
+    top = threads_threshold(top, M, max(min(left / (32 * kVec), kBeamWarps), 1), s_kth);
     if (top >= T_val) {
       T_val = top;
       T_key = make_key(top, 0x7fffffff) - 1;  // below every key of that logit
@@ -377,33 +370,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     const int n = tile - tile0 + 1;
     // (the last few tiles bring fewer keys than a cut costs)
     const bool due = (n & (n - 1)) == 0 && tile + 3 < tile1;
-    bool full = __syncthreads_or(cnt > kWarpKeys);
-    if (!due && !full) continue;
-    // Too many for a warp's buffer (ties, rows that rise from tile to tile): without what
-    // the tile brought, cut; then T raised by the tile itself until its keys fit.
-    while (full) {
+    const bool full = __syncthreads_or(cnt > kWarpKeys);
+    // Too many for a warp's buffer (ties, rows that rise from tile to tile): the tile once more,
+    // an element a thread at a time, with a cut as soon as a warp has a few
+    if (full) {
       cnt = had;
-      if (__syncthreads_or(had > 0)) {
-        cut();
-        had = 0;
-      } else {
-        // the T that leaves M of the tile's keys above it (which fit), bit by bit: keys are
-        // unique, so there is one
-        uint64_t t = 0;
 #pragma unroll 1
-        for (int bit = 63; bit >= 0; --bit) {
-          const uint64_t c = t | 1ull << bit;
-          int32_t above = 0;
-#pragma unroll 4
-          for (int i = 0; i < 2 * kHalf; ++i) above += key_at(token(tile, i)) > c;
-          if (block_sum(above, s_sum) >= M) t = c;
-        }
-        T_key = max(T_key, t);
-        T_val = key_value(T_key);
+      for (int i = -1; i < 2 * kHalf; ++i) {
+        if (i >= 0) push(key_at(token(tile, i)));
+        if (__syncthreads_or(cnt > kWarpKeys / 8)) cut();
       }
-#pragma unroll 1
-      for (int i = 0; i < 2 * kHalf; ++i) push(key_at(token(tile, i)));
-      full = __syncthreads_or(cnt > kWarpKeys);
     }
     if (due) cut();
   }
@@ -588,16 +564,16 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 }
 
 // How a call's rows are cut.  Tiles of 32 elements a thread where they give every SM a few
-// CTAs, else of 8; splits of a row so that about kCtasPerSm CTAs an SM
-// share the work (of 152 SMs: the cut must not depend on the device, the workspace goes
-// by it).
+// CTAs and a row fills half of one, else of 8 (836 rows of 8009 fp16 19 us, by 8 23; 516 of 586
+// bf16 14 us, by 32 16); splits of a row so that about kCtasPerSm CTAs an SM share the work (of
+// 152 SMs: the cut must not depend on the device, the workspace goes by it).
 struct BeamCut {
   int elems, tiles, splits;
 };
 BeamCut beam_cut(int64_t rows, int32_t num_beams, int32_t vocab) {
-  constexpr int64_t kSms = 152, kCtasPerSm = 4;
+  constexpr int64_t kSms = 152, kCtasPerSm = 4, kLargeTiles = 4096;
   BeamCut c;
-  c.elems = rows * (vocab / (kThreads * 32) + 1) >= 2 * kSms ? 32 : 8;
+  c.elems = rows * (vocab / (kThreads * 32) + 1) >= 2 * kSms && vocab >= kLargeTiles ? 32 : 8;
   c.tiles = (vocab + kThreads * c.elems - 1) / (kThreads * c.elems);
   int64_t s = kCtasPerSm * kSms / std::max<int64_t>(rows, 1);
   s = std::min<int64_t>(s, std::min(c.tiles, std::max(kMaxLists / num_beams, 1)));

@@ -354,7 +354,8 @@ def beam_case(rng, b, k, v, dtype, spread=3.0, pad=0, offset=0):
 
 BEAMS = [(1, 1, 1, 1), (1, 4, 5, 9), (2, 3, 7, 4), (1, 4, 32000, 4), (3, 5, 50257, 10), (2, 8, 8193, 16),
          (5, 1, 2048, 33), (1, 64, 1000, 128), (7, 12, 333, 36), (40, 8, 20000, 8), (1, 1024, 40, 5),
-         (2, 2, 128000, 128)]
+         (2, 2, 128000, 128), (15, 2, 9047, 5), (41, 8, 295, 5), (43, 12, 586, 13), (1, 3, 200, 40),
+         (80, 8, 4100, 9)]
 
 
 @pytest.mark.parametrize("case", range(len(BEAMS)))
@@ -389,6 +390,7 @@ SHAPES = {  # rows that find the buffer's limits
     "one": lambda rng, v: np.where(np.arange(v) == v - 1, 50.0, -50.0),
     "masked": lambda rng, v: np.where(rng.random(v) < 0.999, -np.inf, rng.standard_normal(v)),
     "large": lambda rng, v: rng.standard_normal(v) * 60000,
+    "filled": lambda rng, v: np.where(rng.random(v) < 0.99, -1e4, rng.standard_normal(v)),
     "lowest": lambda rng, v: np.full(v, LOWEST),
     "lows": lambda rng, v: rng.choice([LOWEST, -3e38, -2.4e38, -np.inf], v, p=[.9, .05, .04, .01]),
     "lows apart": lambda rng, v: np.where(np.arange(v) < v // 2, LOWEST, -3e38),
