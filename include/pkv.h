@@ -710,8 +710,8 @@ PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t
  * pad_token with score cum_scores[r], and its logits are not read.  The num_select
  * best candidates of each request, by score, then beam, then token, go to scores
  * (fp32), tokens and parents (int32; r, the row index), [num_requests][num_select].
- *   Within a beam candidates are ranked by their logits, between beams by the score in
- *   64 bits (of a log-sum accumulated in 32).  Candidates whose score is not finite
+ *   Within a beam candidates are ranked by their logits, between beams by the score to
+ *   39 bits or more (of a log-sum accumulated in 32).  Candidates whose score is not finite
  *   (masked logits of -inf; every one of a beam whose logits hold NaN or more than 2^127, or with a
  *   cum_scores that is not finite) are never selected; where too few remain, score -inf,
  *   token -1 and parent -1 fill the rest.  parents is what pkv_fork_sequences takes.

@@ -185,26 +185,27 @@ __device__ __forceinline__ int count_above(const uint64_t *s, int begin, int end
 }
 
 // The `cnt` keys of s_all in descending order, the first `keep` of them to s_top: each
-// key's place is the number of larger ones.  Up to kThreads keys, the threads that are
-// left over share the counting (s_rank: kThreads ints).  The 64 keys from cnt on are 0.
+// key's place is the number of larger ones.  Up to kT keys, the threads that are left over
+// share the counting (s_rank: kT ints).  The 64 keys from cnt on are 0.  By all kT threads.
+template <int kT>
 __device__ __forceinline__ void sort_keys(const uint64_t *s_all, int cnt, uint64_t *s_top, int keep,
                                           int32_t *s_rank) {
   const int tid = threadIdx.x;
-  if (cnt <= kThreads) {
-    const int lanes = cnt <= 32 ? 32 : cnt <= 64 ? 64 : cnt <= 128 ? 128 : 256;
-    const int parts = kThreads / lanes, i = tid & (lanes - 1), part = tid / lanes;
-    const int len = ((cnt + parts - 1) / parts + 7) & ~7;
+  if (cnt <= kT) {
+    const int lanes = cnt <= 32 ? 32 : 1 << (32 - __clz(cnt - 1));
+    const int parts = kT / lanes, i = tid & (lanes - 1), part = tid / lanes;
+    const int len = ((cnt + parts - 1) / parts + 7) & ~7, all = (cnt + 7) & ~7;
     const uint64_t k = i < cnt ? s_all[i] : 0;
     s_rank[tid] = 0;
     __syncthreads();
     if ((i & ~31) < cnt) {
-      const int rank = count_above(s_all, part * len, part * len + len, k);
+      const int rank = count_above(s_all, part * len, min(part * len + len, all), k);
       if (rank) atomicAdd(s_rank + i, rank);
     }
     __syncthreads();
     if (tid < cnt && s_rank[tid] < keep) s_top[s_rank[tid]] = k;
   } else {
-    for (int i = tid; i < cnt; i += kThreads) {
+    for (int i = tid; i < cnt; i += kT) {
       const uint64_t k = s_all[i];
       const int rank = count_above(s_all, 0, (cnt + 7) & ~7, k);
       if (rank < keep) s_top[rank] = k;
@@ -213,10 +214,11 @@ __device__ __forceinline__ void sort_keys(const uint64_t *s_all, int cnt, uint64
   __syncthreads();
 }
 
-// A logit that at least M elements of the CTA reach: the smallest over the first `warps` warps
-// of their ceil(M / warps)-th largest thread maximum (NaN: too few threads).  s: an int a warp.
-__device__ __forceinline__ float threads_threshold(float top, int M, int warps, uint32_t *s) {
-  uint32_t o = (uint32_t)(make_key(top, 0) >> 32), kth = 0;
+// A value that at least M of the CTA's threads reach: the smallest over the first `warps` of its
+// kWarps warps of their ceil(M / warps)-th largest (0: there are too few).  s: an int a warp.
+template <int kWarps>
+__device__ __forceinline__ uint32_t threads_threshold(uint32_t o, int M, int warps, uint32_t *s) {
+  uint32_t kth = 0;
   for (int i = 0; i < M; i += warps) {
     kth = __reduce_max_sync(0xffffffffu, o);
     const uint32_t who = __ballot_sync(0xffffffffu, o == kth);
@@ -225,8 +227,8 @@ __device__ __forceinline__ float threads_threshold(float top, int M, int warps, 
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = (int)threadIdx.x >> 5 < warps ? kth : ~0u;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kBeamWarps; ++w) kth = min(kth, s[w]);
-  return key_value((uint64_t)kth << 32);
+  for (int w = 0; w < kWarps; ++w) kth = min(kth, s[w]);
+  return kth;
 }
 
 // A tile is 2 kHalf elements a thread, in two sets of registers: each is filled again as
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     for (int i = lane; i < s_cnt[warp]; i += 32) s_all[before + i] = s_new[warp][i];
     if (tid < 64) s_all[all + tid] = 0;
     __syncthreads();
-    sort_keys(s_all, all, s_top, M, s_rank);
+    sort_keys<kThreads>(s_all, all, s_top, M, s_rank);
     num_top = min(all, M);
     cnt = 0;
     if (num_top == M && s_top[M - 1] > T_key) {
@@ -355,7 +357,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     // (warps whose threads all have elements: rows of 300 to 600, or as short a last range, took
     // 15 to 160 us with the others counted in, as then every element was a candidate)
     const int left = p.vocab - tile0 * kTile;
-    top = threads_threshold(top, M, max(min(left / (32 * kVec), kBeamWarps), 1), s_kth);
+    const int full = max(min(left / (32 * kVec), kBeamWarps), 1);
+    const uint32_t o = threads_threshold<kBeamWarps>((uint32_t)(make_key(top, 0) >> 32), M, full, s_kth);
+    top = key_value((uint64_t)o << 32);  // (0 is a NaN)
     if (top >= T_val) {
       T_val = top;
       T_key = make_key(top, 0x7fffffff) - 1;  // below every key of that logit
@@ -426,56 +430,87 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o ^ 1ull << 63 : ~o));
 }
 
-// One CTA a request.  All threads turn the lists' keys into ordered scores in shared
-// memory (as many as fit; a list's further ones are read when it gets there).  Few
-// lists and up to a thread each, a candidate finds its place by counting the better ones
-// (8 lists of 16: 6.5 us, by rounds 9.4); others are merged by one warp in M rounds over
-// the heads of the lists (64 lists of 4: 6.6 us, by counting 8.5).  List k splits + j holds
-// beam k's best of its j-th range: equal scores go to the lower list.
-__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+// One CTA a request.  List k splits + j holds beam k's best of its j-th range: equal scores go
+// to the lower list.  Where they are few (by_counting below) two sorts by counting do: of the
+// lists' heads, so that the num_select best lists stay, and of the one of rank r num_select - r
+// keys only; then of those (15 lists by 10: the call 19.7 us, merged by rounds or one sort of
+// all 22.5; 11 lists by 31: this kernel 8.8, by rounds 14.7).  Of more than kFewLists heads a
+// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  Otherwise one warp merges them in num_select rounds over the heads, with as many scores as fit
+// in shared memory (a list's further ones are read when it gets there).
+//
+// Scores are fp64, which keeps the order of a beam's logits.  To be sorted they take their
+// key's place in the lists into their last 13 bits: equal to 2^-39 they count as equal.
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
+constexpr int kFewLists = 64, kPlaces = 8192, kMostKeys = 512;
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ double s_base[kMaxLists];       // cum - (lse - shift) of the request's beams,
   __shared__ float s_shift[kMaxLists];       // shift 0 unless all of a row is as low as it gets
-  __shared__ alignas(16) uint64_t s_score[kMergeScores];  // [list][depth], ordered
-  __shared__ uint64_t s_head[kMaxLists];     // of each list the first score left
+  __shared__ bool s_done[kMaxLists];
+  // keys as they are (counting, if they fit), or [list][depth] ordered scores (rounds)
+  __shared__ uint64_t s_score[kMergeScores];
+  __shared__ alignas(16) uint64_t s_head[kMaxLists + 64];  // of each list the first score left
   __shared__ int32_t s_next[kMaxLists];
   __shared__ uint64_t s_won[kMaxSelect];     // of each round the score (0: none left),
   __shared__ int32_t s_list[kMaxSelect], s_at[kMaxSelect];  // its list and place in it
+  __shared__ uint32_t s_kth[kMergeWarps];
+  __shared__ int32_t s_count;
   const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * p.num_beams;
   const int lists = p.num_beams * p.splits, M = p.num_select;
-  const int depth = min(M, kMergeScores / lists);
   const uint64_t *keys = p.keys + row0 * p.splits * M;
-  auto done = [&](int k) { return p.finished && __ldg(p.finished + row0 + k); };
+  // a beam's parts are joined by a group of up to 32 lanes (50 parts by one thread: 8 us)
+  int group = 32;
+  while (group > 1 && group / 2 >= p.splits) group /= 2;
+  const int lead = tid / group, lane = tid % group;
   // (inputs of the call: the kernel before this one does not write them)
-  const bool mine = tid < p.num_beams;
-  double base = mine ? (double)__ldg(p.cum + row0 + tid) : 0.0;
-  const bool ended = mine && done(tid);
+  float cum = 0.f;
+  bool ended = false;
+  auto inputs = [&](int k) {
+    cum = __ldg(p.cum + row0 + k);
+    ended = p.finished && __ldg(p.finished + row0 + k);
+  };
+  if (lead < p.num_beams) inputs(lead);
+  // lists that can have keys among the best, and how many those can be together
+  const int R = min(lists, M), most = R * M - R * (R - 1) / 2;
+  const bool by_counting = most <= kMostKeys && lists * M <= kPlaces;
+  const bool copied = by_counting && lists * M <= kMergeScores;
+  if (tid == 0) s_count = 0;
   pdl_wait();
   // the first keys on their way beside the sums
-  uint64_t first = 0;
-  if (tid < lists * depth) first = keys[(int64_t)(tid / depth) * M + tid % depth];
-  for (int k = tid; k < p.num_beams; k += kThreads) {
-    if (k != tid) base = __ldg(p.cum + row0 + k);
-    float shift = 0.f;
-    if (!(k == tid ? ended : done(k))) {
-      const float2 *part = p.part + (row0 + k) * p.splits;
-      float m = -INFINITY, s = 0.f;
-#pragma unroll 8
-      for (int j = 0; j < p.splits; ++j) m = fmaxf(m, part[j].x);
-#pragma unroll 8
-      for (int j = 0; j < p.splits; ++j)
-        s += part[j].y * (part[j].x == m ? 1.f : exp2f(part[j].x - m));
-      if (m == -INFINITY && s > 0.f) {
-        // the parts are counts of their largest logits: those of the row's largest
-        uint32_t best = 0;
-        for (int j = 0; j < p.splits; ++j)
-          best = max(best, (uint32_t)(keys[((int64_t)k * p.splits + j) * M] >> 32));
-        s = 0.f;
-        for (int j = 0; j < p.splits; ++j)
-          if ((uint32_t)(keys[((int64_t)k * p.splits + j) * M] >> 32) == best) s += part[j].y;
+  const uint64_t first = copied && tid < lists * M ? keys[tid] : 0;
+  for (int k0 = 0; k0 < p.num_beams; k0 += kMergeThreads / group) {
+    const int k = k0 + lead;
+    if (k0 > 0 && k < p.num_beams) inputs(k);
+    const int parts = k < p.num_beams && !ended ? p.splits : 0;
+    const float2 *part = p.part + (row0 + k) * p.splits;
+    const uint64_t *heads = keys + (int64_t)k * p.splits * M;  // every M-th
+    float m = -INFINITY, s = 0.f, shift = 0.f;
+#pragma unroll 4
+    for (int j = lane; j < parts; j += group) m = fmaxf(m, part[j].x);
+    for (int o = group / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+    for (int j = lane; j < parts; j += group)
+      s += part[j].y * (part[j].x == m ? 1.f : exp2f(part[j].x - m));
+    for (int o = group / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const bool low = m == -INFINITY && s > 0.f;
+    if (__any_sync(0xffffffffu, low)) {
+      // the parts are counts of their largest logits: those of the row's largest
+      uint32_t best = 0;
+      for (int j = lane; j < parts; j += group) best = max(best, (uint32_t)(heads[(int64_t)j * M] >> 32));
+      for (int o = group / 2; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+      float n = 0.f;
+      for (int j = lane; j < parts; j += group)
+        if ((uint32_t)(heads[(int64_t)j * M] >> 32) == best) n += part[j].y;
+      for (int o = group / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (low) {
+        s = n;
         shift = key_value((uint64_t)best << 32);
         m = 0.f;
       }
+    }
+    if (lane != 0 || k >= p.num_beams) continue;
+    double base = cum;
+    if (!ended) {
       // log2 s by its exponent and mantissa: off by half a step of a number below 1
       int e;
       const float f = frexpf(s, &e);
@@ -483,39 +518,80 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
     s_base[k] = base;
     s_shift[k] = shift;
+    s_done[k] = ended;
+  }
+  if (copied) {
+    s_score[tid] = first;
+#pragma unroll 4
+    for (int i = tid + kMergeThreads; i < lists * M; i += kMergeThreads) s_score[i] = keys[i];
   }
   __syncthreads();
-  // the ordered score of list l's n-th key (0: there is none)
-  auto score_of = [&](int l, int n, uint64_t key) -> uint64_t {
+  // the ordered score of a key of list l, its first or not (0: there is none); the difference
+  // of two logits as low as a shift is exact
+  auto score_of = [&](int l, bool lead, uint64_t key) -> uint64_t {
     const int k = l / p.splits;
-    if (done(k)) return n == 0 && l == k * p.splits ? order_double(s_base[k]) : 0;
-    return key ? order_double(s_base[k] + ((double)key_value(key) - (double)s_shift[k])) : 0;
+    if (s_done[k]) return lead && l == k * p.splits ? order_double(s_base[k]) : 0;
+    return key ? order_double(s_base[k] + (double)(key_value(key) - s_shift[k])) : 0;
   };
   auto put = [&](int i, uint64_t score, int l, uint64_t key) {
     const int64_t o = (int64_t)blockIdx.x * M + i;
     const int k = l / p.splits;
     p.scores[o] = score ? (float)unorder_double(score) : -INFINITY;
     p.parents[o] = score ? (int32_t)(row0 + k) : -1;
-    p.tokens[o] = score == 0 ? -1 : done(k) ? p.pad_token : (int32_t)~(uint32_t)key;
+    p.tokens[o] = score == 0 ? -1 : s_done[k] ? p.pad_token : (int32_t)~(uint32_t)key;
   };
-  if (lists * M <= kThreads && lists <= 16) {  // depth = M
-    const int n = lists * M;
-    const uint64_t own = tid < n ? score_of(tid / M, tid % M, first) : 0;
-    s_score[tid] = own;
-    const int have = __syncthreads_count(own != 0);
-    if (own) {
-      // larger ones, and equal ones before it
-      const int here = tid & ~7, end = (n + 7) & ~7;
-      int rank = count_above(s_score, 0, here, own - 1) + count_above(s_score, here, end, own);
-      for (int j = here; j < tid; ++j) rank += s_score[j] == own;
-      if (rank < M) put(rank, own, tid / M, first);
+  if (by_counting) {
+    constexpr uint64_t kPlace = kPlaces - 1;
+    auto place_of = [](uint64_t o) { return (int)(~o & kPlace); };
+    auto key_at = [&](int at) { return copied ? s_score[at] : keys[at]; };
+    // key `at` of all, the d-th of list l: lower lists, and earlier keys, go first
+    auto sort_score = [&](int at, int l, int d) -> uint64_t {
+      const uint64_t o = score_of(l, d == 0, key_at(at));
+      return o ? (o & ~kPlace) | (kPlace - at) : 0;
+    };
+    uint64_t *s_some = s_head, *s_best = s_won;  // to be sorted, and the best of them
+    if (tid < M) s_best[tid] = 0;
+    int some = lists;
+    if (lists <= kFewLists) {
+      if (tid < lists) s_some[tid] = sort_score(tid * M, tid, 0);
+    } else {
+      static_assert(kMaxLists <= 2 * kMergeThreads, "two heads a thread");
+      // every 16th list a warp's, so that each has some of every beam
+      const int one = tid % 32 * kMergeWarps + tid / 32, other = one + kMergeThreads;
+      const uint64_t a = one < lists ? sort_score(one * M, one, 0) : 0;
+      const uint64_t b = other < lists ? sort_score(other * M, other, 0) : 0;
+      const uint32_t T =
+          threads_threshold<kMergeWarps>((uint32_t)(max(a, b) >> 32), M, kMergeWarps, s_kth);
+      if (a && (uint32_t)(a >> 32) >= T) s_some[atomicAdd(&s_count, 1)] = a;
+      if (b && (uint32_t)(b >> 32) >= T) s_some[atomicAdd(&s_count, 1)] = b;
+      __syncthreads();
+      some = s_count;
     }
-    for (int i = have + tid; i < M; i += kThreads) put(i, 0, 0, 0);
+    if (tid < 64) s_some[some + tid] = 0;
+    __syncthreads();
+    sort_keys<kMergeThreads>(s_some, some, s_best, M, s_next);
+    // key d of the list of rank r, to place r M - r (r - 1) / 2 + d
+    for (int i = tid; i < R * M; i += kMergeThreads) {
+      const int r = i / M, d = i % M, at = place_of(s_best[r]) + d;
+      if (r + d >= M) continue;
+      s_some[i - r * (r - 1) / 2] = s_best[r] ? sort_score(at, at / M, d) : 0;
+    }
+    if (tid < 64) s_some[most + tid] = 0;
+    __syncthreads();
+    if (tid < M) s_best[tid] = 0;
+    __syncthreads();
+    sort_keys<kMergeThreads>(s_some, most, s_best, M, s_next);
+    if (tid < M) {
+      const uint64_t best = s_best[tid];
+      const int at = best ? place_of(best) : 0;
+      put(tid, best & ~kPlace, at / M, key_at(at));
+    }
     return;
   }
-  for (int i = tid; i < lists * depth; i += kThreads) {
+  const int depth = min(M, kMergeScores / lists);
+  for (int i = tid; i < lists * depth; i += kMergeThreads) {
     const int l = i / depth, n = i % depth;
-    const uint64_t o = score_of(l, n, i == tid ? first : keys[(int64_t)l * M + n]);
+    const uint64_t o = score_of(l, n == 0, keys[(int64_t)l * M + n]);
     s_score[i] = o;
     if (n == 0) {
       s_head[l] = o;
@@ -550,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         s_next[l] = n + 1;
         s_head[l] = n + 1 >= M       ? 0
                     : n + 1 < depth ? s_score[(int)l * depth + n + 1]
-                                    : score_of((int)l, n + 1, keys[(int64_t)l * M + n + 1]);
+                                    : score_of((int)l, false, keys[(int64_t)l * M + n + 1]);
         look();
       }
     }
@@ -656,8 +732,8 @@ extern "C" pkv_status pkv_beam_select(const void *logits, int32_t logit_type, in
                   : logit_type == PKV_FP16 ? launch_rows<__half>(p, c.elems, ctas, stream)
                                            : launch_rows<float>(p, c.elems, ctas, stream);
   if (e == cudaSuccess)
-    e = launch_kernel(beam_merge_kernel, dim3((unsigned)num_requests), dim3(kThreads), 0, stream,
-                      !profiling_active(), p);
+    e = launch_kernel(beam_merge_kernel, dim3((unsigned)num_requests), dim3(kMergeThreads), 0,
+                      stream, !profiling_active(), p);
   profile_end(PKV_KERNEL_BEAM, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return PKV_ERR_CUDA;
