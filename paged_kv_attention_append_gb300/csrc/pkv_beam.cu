@@ -111,14 +111,18 @@ struct Row {
 };
 
 // Elements [at, at + kVec) of a row, as they lie in memory; those past its end as -inf.
-// Rows that start off alignment (an odd vocabulary) are put together from the aligned
-// 16-byte pieces around them; an element at a time only at the tensor's ends.
+// Rows of 16 bits that start off alignment (an odd vocabulary) are put together from the
+// aligned 16-byte pieces around them; an element at a time only at the tensor's ends.
 template <typename T, int kVec>
 __device__ __forceinline__ void load_vec(const Row<T> &row, int32_t at, uint32_t *w) {
   using W = Words<T>;
   constexpr int kWords = kVec / W::kPer;
   const T *src = row.data + at;
   const bool whole = at + kVec <= row.vocab;
+  if (kVec == 1) {  // (4-byte types)
+    w[0] = whole ? raw_bits(src) : W::kNegInf;
+    return;
+  }
   if (row.shift == 0 && whole) {
     if (kWords == 2) {
       const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src));
@@ -136,7 +140,7 @@ __device__ __forceinline__ void load_vec(const Row<T> &row, int32_t at, uint32_t
     }
     return;
   }
-  if (kWords >= 4) {
+  if (kWords >= 4 && sizeof(T) == 2) {
     const char *first = reinterpret_cast<const char *>(src) - row.shift;
     if (whole && first >= row.lo && first + kWords * 4 + 16 <= row.hi) {
       uint32_t v[kWords + 4];
@@ -155,7 +159,7 @@ __device__ __forceinline__ void load_vec(const Row<T> &row, int32_t at, uint32_t
       for (int i = 0; i < kWords + 1; ++i) v[i] = row.shift & 4 ? v[i + 1] : v[i];
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
-        w[i] = sizeof(T) == 4 ? v[i] : __funnelshift_r(v[i], v[i + 1], (row.shift & 2) * 8);
+        w[i] = __funnelshift_r(v[i], v[i + 1], (row.shift & 2) * 8);
       return;
     }
   }
@@ -233,10 +237,10 @@ __device__ __forceinline__ uint32_t threads_threshold(uint32_t o, int M, int war
 
 // A tile is 2 kHalf elements a thread, in two sets of registers: each is filled again as
 // soon as it has been used, so loads are always in flight.
-template <typename T, int kHalf>
+// kVec: consecutive elements a thread loads together.
+template <typename T, int kHalf, int kVec>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams p) {
   using W = Words<T>;
-  constexpr int kVec = kHalf < 8 ? kHalf : 8;  // consecutive elements a thread loads together
   constexpr int kWords = kHalf / W::kPer;
   constexpr int kHalfTile = kThreads * kHalf, kTile = 2 * kHalfTile;
   __shared__ uint64_t s_new[kBeamWarps][kWarpKeys];
@@ -435,8 +439,9 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
 // lists' heads, so that the num_select best lists stay, and of the one of rank r num_select - r
 // keys only; then of those (15 lists by 10: the call 19.7 us, merged by rounds or one sort of
 // all 22.5; 11 lists by 31: this kernel 8.8, by rounds 14.7).  Of more than kFewLists heads a
-// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  Otherwise one warp merges them in num_select rounds over the heads, with as many scores as fit
-// in shared memory (a list's further ones are read when it gets there).
+// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  Otherwise
+// one warp merges them in num_select rounds over the heads, with as many scores as fit in
+// shared memory (a list's further ones are read when it gets there).
 //
 // Scores are fp64, which keeps the order of a beam's logits.  To be sorted they take their
 // key's place in the lists into their last 13 bits: equal to 2^-39 they count as equal.
@@ -658,14 +663,26 @@ BeamCut beam_cut(int64_t rows, int32_t num_beams, int32_t vocab) {
 }
 int64_t part_bytes(int64_t rows, int splits) { return align_up(rows * splits * 8, 16); }
 
+template <typename T, int kHalf, int kVec>
+cudaError_t launch_rows_t(const BeamParams &p, int64_t ctas, pkv_stream stream) {
+  constexpr auto kern = beam_rows_kernel<T, kHalf, kVec>;
+  const cudaError_t pe = prepare_kernel<kern>(0);
+  if (pe != cudaSuccess) return pe;
+  return launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream, !profiling_active(), p);
+}
+
+// fp32 rows of which some start off 16-byte alignment: an element a load, a warp's next to each
+// other (512 rows of 128000 in 58 us; put together from 16-byte pieces 78, aligned ones 51).  It
+// is the same for all rows of a call, so that equal rows get equal sums.
 template <typename T>
 cudaError_t launch_rows(const BeamParams &p, int elems, int64_t ctas, pkv_stream stream) {
-  auto kern = elems == 32 ? beam_rows_kernel<T, 16> : beam_rows_kernel<T, 4>;
-  const cudaError_t pe = elems == 32 ? prepare_kernel<beam_rows_kernel<T, 16>>(0)
-                                     : prepare_kernel<beam_rows_kernel<T, 4>>(0);
-  if (pe != cudaSuccess) return pe;
-  return launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream,
-                       !profiling_active(), p);
+  if constexpr (sizeof(T) == 4) {
+    if ((reinterpret_cast<uintptr_t>(p.logits) & 15u) || (p.num_rows > 1 && p.row_stride % 4 != 0))
+      return elems == 32 ? launch_rows_t<T, 16, 1>(p, ctas, stream)
+                         : launch_rows_t<T, 4, 1>(p, ctas, stream);
+  }
+  return elems == 32 ? launch_rows_t<T, 16, 8>(p, ctas, stream)
+                     : launch_rows_t<T, 4, 4>(p, ctas, stream);
 }
 
 }  // namespace
