@@ -3,7 +3,7 @@
 //   out[t][hq] = sum_p softmax_p(scale q . K[p]) V[p],  p over the visible keys of the
 //   selected blocks.
 //
-// A CTA of four warps, or a cluster of up to eight such CTAs, takes one (token, KV head):
+// A CTA of four warps (or two), or a cluster of up to eight such CTAs, takes one (token, KV head):
 // the G query heads are the rows of the m16 tiles, so a block is read once for all of
 // them.  The selected blocks are dealt out over the warps; each streams its share through
 // a ring of its own (TMA boxes of a block's K and V, as the split-KV kernel reads them)
@@ -25,11 +25,6 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 3;
-
-
 struct SparseParams {
   const __nv_bfloat16 *q;
   __nv_bfloat16 *out;
@@ -39,8 +34,9 @@ struct SparseParams {
   int32_t *dev_status;
 };
 
-template <int D>
+template <int D, int kWarps>
 struct SparseCfg {
+  static constexpr int kCtasPerSm = 12 / kWarps;
   // 8 KB a warp and stage at D = 128: with two stages three CTAs share an SM, so that the
   // (token, head) pairs of a call spread more evenly (192 pairs of 128 blocks: 38 us; three
   // stages and two CTAs 46)
@@ -89,10 +85,11 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int D, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
     sparse_kernel(const __grid_constant__ CUtensorMap pool_map, const SparseParams p) {
-  using C = SparseCfg<D>;
+  using C = SparseCfg<D, kWarps>;
+  constexpr int kThreads = 32 * kWarps;
   constexpr int kL = D / 32, kNt = D / 8, kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int32_t s_sum[kWarps];
@@ -268,23 +265,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   cluster_sync();  // no CTA ends while another reads its shared memory
 }
 
-template <int D>
+template <int D, int kWarps>
 cudaError_t launch_sparse_t(const CUtensorMap &map, const SparseParams &p, int64_t total_q,
-                            pkv_stream stream) {
-  using C = SparseCfg<D>;
-  const cudaError_t pe = prepare_kernel<sparse_kernel<D>>(C::kSmemBytes);
+                            int ranks, pkv_stream stream) {
+  using C = SparseCfg<D, kWarps>;
+  const cudaError_t pe = prepare_kernel<sparse_kernel<D, kWarps>>(C::kSmemBytes);
   if (pe != cudaSuccess) return pe;
-  // CTAs of a (token, KV head): more while there are fewer than two CTAs an SM and every
-  // warp would still have two blocks (192 pairs of 128 blocks: two each 38 us, four 45; the
-  // 8 pairs of one token, 32 blocks: the three calls 10.8 us with four each, 11.5 with
-  // eight, 11.7 with two)
-  int ranks = 1;
-  while (ranks < 8 && total_q * p.hkv * ranks < 2ll * std::max(device_sm_count(), 1) &&
-         4 * ranks * kWarps <= p.num_select)
-    ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total_q * p.hkv * ranks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -295,7 +284,28 @@ cudaError_t launch_sparse_t(const CUtensorMap &map, const SparseParams &p, int64
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = profiling_active() ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, sparse_kernel<D>, map, p);
+  return cudaLaunchKernelEx(&cfg, sparse_kernel<D, kWarps>, map, p);
+}
+
+template <int D>
+cudaError_t launch_sparse(const CUtensorMap &map, const SparseParams &p, int64_t total_q,
+                          pkv_stream stream) {
+  // CTAs of a (token, KV head): more while there are fewer than two CTAs an SM and every
+  // warp would still have two blocks (192 pairs of 128 blocks: two each 38 us, four 45; the
+  // 8 pairs of one token, 32 blocks: the three calls 10.8 us with four each, 11.5 with
+  // eight, 11.7 with two)
+  int ranks = 1;
+  while (ranks < 8 && total_q * p.hkv * ranks < 2ll * std::max(device_sm_count(), 1) &&
+         16 * ranks <= p.num_select)
+    ranks *= 2;
+  // CTAs of two warps, twice as many of them an SM, where there are more (token, KV head)s than
+  // CTAs of four fit at a time and few blocks each, so that their start and end overlap more
+  // (the three calls: 2400 pairs of up to 5 blocks 35 -> 24 us, 2500 of 32 60 -> 53, 2048 of
+  // 16 59 -> 57; of 64 85 -> 90; one warp for up to 8 blocks 3 % less again)
+  constexpr int32_t kFewBlocks = 32;
+  if (total_q * p.hkv > 3ll * std::max(device_sm_count(), 1) && p.num_select <= kFewBlocks)
+    return launch_sparse_t<D, 2>(map, p, total_q, ranks, stream);
+  return launch_sparse_t<D, 4>(map, p, total_q, ranks, stream);
 }
 
 }  // namespace
@@ -338,8 +348,8 @@ extern "C" pkv_status pkv_paged_sparse_attention(
   p.scale_log2 = scale * 1.4426950408889634f;
   p.dev_status = dev_status;
   profile_begin(PKV_KERNEL_SPARSE, stream);
-  cudaError_t e = desc->head_dim == 128 ? launch_sparse_t<128>(map, p, total_q, stream)
-                                        : launch_sparse_t<64>(map, p, total_q, stream);
+  cudaError_t e = desc->head_dim == 128 ? launch_sparse<128>(map, p, total_q, stream)
+                                        : launch_sparse<64>(map, p, total_q, stream);
   profile_end(PKV_KERNEL_SPARSE, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return PKV_ERR_CUDA;

@@ -151,6 +151,8 @@ SELECTS = [  # (hq, hkv, d, q_lens, contexts, num, sink, recent)
     (6, 3, 128, [30], [1000], 7, 0, 1),
     (64, 16, 64, [1, 1, 1], [777, 20000, 40], 50, 3, 3),
     (2, 2, 64, [1], [170000], 300, 1, 1),
+    (24, 12, 128, [9, 9, 1, 9, 9, 9, 0, 2], [9, 10, 400, 67, 150, 33, 5, 900], 6, 1, 2),  # many pairs
+    (32, 16, 64, [4] * 8, [900, 4, 600, 513, 15, 1000, 530, 700], 32, 2, 3),
 ]
 
 
