@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
         }
     if (c == 0) ml[row] = half ? make_float2(m_hi, l_hi) : make_float2(m_lo, l_lo);
   }
-  cluster_sync();
+  if (ranks == 1) __syncthreads();
+  else cluster_sync();
   // (row, 4 columns) by thread, over the warps of every CTA of the cluster
   constexpr int kChunks = D / 4;
   for (int x = (int)rank * kThreads + threadIdx.x; x < p.group * kChunks; x += (int)ranks * kThreads) {
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
     *reinterpret_cast<uint2 *>(p.out + (token * p.num_q_heads + (int64_t)h * p.group + row) * D +
                                4 * ch) = pk;
   }
-  cluster_sync();  // no CTA ends while another reads its shared memory
+  if (ranks > 1) cluster_sync();  // no CTA ends while another reads its shared memory
 }
 
 template <int D, int kWarps>
@@ -277,13 +278,18 @@ cudaError_t launch_sparse_t(const CUtensorMap &map, const SparseParams &p, int64
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = profiling_active() ? 1 : 2;
+  if (ranks > 1) {  // (without: a cluster of one)
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)ranks;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (!profiling_active()) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, sparse_kernel<D, kWarps>, map, p);
 }
 
