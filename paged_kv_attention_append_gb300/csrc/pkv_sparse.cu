@@ -9,7 +9,8 @@
 // a ring of its own (TMA boxes of a block's K and V, as the split-KV kernel reads them)
 // with an online softmax in registers.  The warps' (m, l, O) meet in shared memory, over
 // the cluster through distributed shared memory, each CTA joining a part of the columns:
-// one launch, no workspace, and a fixed order of every sum.
+// one launch, no workspace, and a fixed order of every sum.  (A pair of one CTA is launched
+// without clusters: 256 decodes of 64 blocks 81 us for the three calls, with them 85.)
 //
 // Bound: the selected blocks' K and V, 64 D bytes a block and KV head.
 #include <cuda_runtime.h>
@@ -306,8 +307,8 @@ cudaError_t launch_sparse(const CUtensorMap &map, const SparseParams &p, int64_t
     ranks *= 2;
   // CTAs of two warps, twice as many of them an SM, where there are more (token, KV head)s than
   // CTAs of four fit at a time and few blocks each, so that their start and end overlap more
-  // (the three calls: 2400 pairs of up to 5 blocks 35 -> 24 us, 2500 of 32 60 -> 53, 2048 of
-  // 16 59 -> 57; of 64 85 -> 90; one warp for up to 8 blocks 3 % less again)
+  // (the three calls: 2300 pairs of up to 5 blocks 28 -> 20 us, 2400 of 32 53 -> 48.5, 2048 of
+  // 16 52.6 -> 51, 1200 of 28 20.5 -> 21.3; of 64 81 -> 87)
   constexpr int32_t kFewBlocks = 32;
   if (total_q * p.hkv > 3ll * std::max(device_sm_count(), 1) && p.num_select <= kFewBlocks)
     return launch_sparse_t<D, 2>(map, p, total_q, ranks, stream);
