@@ -804,9 +804,9 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   is there twice counts twice).  A block id outside the pool is skipped,
  *   PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past cu_q_lens' last
  *   entry is left as it was; one whose context is shorter than its window too,
- *   PKV_DEV_PLAN_MISMATCH.  num_q_heads / Hkv <= 16.  Weights are rounded to bf16 for
- *   the product with V, sums are fp32, out is rounded once to bf16.  Bytes of a
- *   visible block past the token's position do not reach its row.  out may be q itself, and
+ *   PKV_DEV_PLAN_MISMATCH.  num_q_heads / Hkv <= 16.  Weights go into the
+ *   product with V as two bf16 parts (2^-14 of a weight at most is lost), sums are fp32, out is
+ *   rounded once to bf16.  Bytes of a visible block past the token's position do not reach its row.  out may be q itself, and
  *   must not overlap the inputs otherwise.  q and the lengths may be read before the preceding
  *   kernel has completed, selected, the tables and the pool are read after it.
  */

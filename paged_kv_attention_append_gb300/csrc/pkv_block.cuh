@@ -23,7 +23,10 @@ __device__ __forceinline__ uint32_t blk_off(int row, int chunk) {
 // One paged block (16 keys at positions p0 ..) of a row group: S = Q K^T, causal
 // mask, online softmax in log2 units, O += P V.  sK / sV: the block's K and V in
 // shared memory (blk_off layout).  The warp's running (m, l, O) are updated.
-template <int D>
+// P goes into the product as one bf16 (2^-8 of a weight at most is lost), or with kTwoParts as
+// the sum of two, 2^-14: the first is the leading bits of P (1 - 2^-8), so that the second is
+// never 0 (nor negative) beside a weight, and an infinite V keeps its sign.
+template <int D, bool kTwoParts = false>
 __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uint32_t (&qa)[D / 16][4],
                                              int p0, int q_pos0, int lim_lo, int lim_hi, float sl2,
                                              int r, int c, float &m_lo, float &m_hi, float &l_lo,
@@ -91,6 +94,22 @@ __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uin
     }
   }
   // P (bf16) as the A operand: keys are the k dimension
+  uint32_t pb[2][2];  // the first parts, if there are two
+  if constexpr (kTwoParts) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t b[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float &x = s[nt][2 * u + j];
+          b[j] = __float_as_uint(x * 0.99609375f) & 0xffff0000u;
+          x -= __uint_as_float(b[j]);  // exact
+        }
+        pb[nt][u] = __byte_perm(b[0], b[1], 0x7632);
+      }
+  }
   const uint32_t pa0 = pack_bf16x2(s[0][0], s[0][1]);
   const uint32_t pa1 = pack_bf16x2(s[0][2], s[0][3]);
   const uint32_t pa2 = pack_bf16x2(s[1][0], s[1][1]);
@@ -109,10 +128,16 @@ __device__ __forceinline__ void block_update(uint32_t sK, uint32_t sV, const uin
     const uint32_t w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      mma_16816(o[8 * hh + 2 * k], pa0, pa1, pa2, pa3, __byte_perm(w0[k], w1[k], 0x5410),
-                __byte_perm(w2[k], w3[k], 0x5410));
-      mma_16816(o[8 * hh + 2 * k + 1], pa0, pa1, pa2, pa3,
-                __byte_perm(w0[k], w1[k], 0x7632), __byte_perm(w2[k], w3[k], 0x7632));
+      const uint32_t even0 = __byte_perm(w0[k], w1[k], 0x5410);
+      const uint32_t even1 = __byte_perm(w2[k], w3[k], 0x5410);
+      const uint32_t odd0 = __byte_perm(w0[k], w1[k], 0x7632);
+      const uint32_t odd1 = __byte_perm(w2[k], w3[k], 0x7632);
+      mma_16816(o[8 * hh + 2 * k], pa0, pa1, pa2, pa3, even0, even1);
+      mma_16816(o[8 * hh + 2 * k + 1], pa0, pa1, pa2, pa3, odd0, odd1);
+      if constexpr (kTwoParts) {
+        mma_16816(o[8 * hh + 2 * k], pb[0][0], pb[0][1], pb[1][0], pb[1][1], even0, even1);
+        mma_16816(o[8 * hh + 2 * k + 1], pb[0][0], pb[0][1], pb[1][0], pb[1][1], odd0, odd1);
+      }
     }
   }
 }

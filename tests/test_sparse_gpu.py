@@ -594,3 +594,47 @@ def test_python_refusals_on_device_tensors(pkv, cuda_device):
         pkv.paged_sparse_attention(both[:4], cu, ctx, table, sel, pool, 0.1, out=both[1:])
     with pytest.raises(pkv.PkvError):
         pkv.paged_sparse_attention(q, cu, ctx, table, sel, pool, float("nan"))
+
+
+# ------------------------------------------------------------------------- weights
+
+@pytest.mark.parametrize("case", range(len(SELECTS)))
+@pytest.mark.parametrize("keys", [2, 5, 300])
+def test_weights_keep_sixteen_bits(pkv, cuda_device, case, keys):
+    """A weight goes into the product with V as two bf16 parts: the first is its leading bits, at
+    least (1 - 2^-8) (1 - 2^-7) of it, so the second is below 2^-6 of it and rounded by 2^-8 of
+    itself.  That leaves 2^-14 of A where one bf16 part would leave 2^-8; the rest as above."""
+    hq, hkv, d = SELECTS[case][:3]
+    rng = np.random.default_rng(900 + case)
+    n, ctx = [1] * 40, rng.integers(1, keys + 1, 40).tolist()
+    meta = workloads.build_step("weights", 1, n, ctx, hq, hkv, d, rng=rng)
+    pool = make_pool(rng, meta.num_blocks, hkv, d)
+    q = bf16(rng.standard_normal((meta.total_q, hq, d)))
+    sel = np.tile(np.arange(-(-keys // 16)), (meta.total_q, hkv, 1))
+    out, st = attend(pkv, cuda_device, meta, q, pool, sel)
+    assert st == 0
+    held, x = pool.double().numpy(), q.double().numpy()
+    rows = [ref.sparse_attention(x[t], c - 1, meta.block_tables[t], sel[t], held, meta.scale)
+            for t, c in enumerate(ctx)]
+    want, mag, dots = (np.stack(r) for r in zip(*rows))
+    e = (d + 4) * 2.0 ** -24 * dots[..., None] + 2.0 ** -22 + 2.0 ** -14
+    tol = 2.0 ** -8 * np.abs(want) + mag * (2.0 ** -14 + 2 * e)
+    over = np.abs(out.double().cpu().numpy() - want) - tol
+    assert (over <= 0).all(), f"worst {over.max():.3e}, {int((over > 0).sum())} of {over.size}"
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_an_infinite_value_stays_infinite(pkv, cuda_device, value):
+    """V of infinity at a visible key with a weight: the output is that infinity, not NaN, also
+    where the weight is a power of two (one key, or keys alike)."""
+    dev = cuda_device
+    meta = workloads.build_step("inf", 1, [1, 1, 1], [1, 16, 40], 8, 2, 64, rng=np.random.default_rng(2))
+    pool = make_pool(np.random.default_rng(3), meta.num_blocks, 2, 64)
+    pool[:, 0] = 0.5
+    for s in range(3):
+        pool[meta.block_tables[s, 0], 1, :, 0, 5] = value
+    q = bf16(np.random.default_rng(4).standard_normal((3, 8, 64)))
+    sel = np.tile(np.arange(3), (3, 2, 1))
+    out, _ = attend(pkv, dev, meta, q, pool, sel)
+    assert bool((out[:, :, 5] == value).all())
+    assert bool(torch.isfinite(torch.cat([out[:, :, :5], out[:, :, 6:]], dim=2)).all())
