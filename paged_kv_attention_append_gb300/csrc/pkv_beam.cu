@@ -20,7 +20,7 @@
 //    that many passed in every tile: 512 rows of 128000 fp32 took 60 us; with keys put into
 //    one buffer by atomics after each tile, 46.)
 // A second kernel, one CTA a request, joins the rows' sums and merges the sorted lists
-// by score in 64 bits.
+// by score in 64 bits, within a beam by key.
 //
 // Which elements a thread sums depends on their place in the row alone, not on the row's
 // address: equal rows get equal sums, and their ties go by the beam.
@@ -434,6 +434,76 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o ^ 1ull << 63 : ~o));
 }
 
+// A merge that compares candidates by score (all 64 bits), then beam, then key: by one warp, in
+// num_select rounds over the lists' heads, with their keys beside their scores.
+struct ByKey {
+  const uint64_t *keys;     // [lists][num_select]
+  const double *base;       // of each beam, as is what follows
+  const float *shift;
+  const bool *done;
+  uint64_t *head, *low;     // [lists]: score and key of each list's first one left
+  int32_t *next;            // [lists]: its place in the list
+  uint64_t *won;            // [num_select]: of each round the score (0: none left),
+  int32_t *list, *at;       // its list and place in it
+  int lists, splits, num_select;
+};
+__device__ __forceinline__ uint64_t candidate_score(double base, float shift, uint64_t key) {
+  return key ? order_double(base + (double)(key_value(key) - shift)) : 0;
+}
+__device__ __noinline__ void merge_by_key(const ByKey &m) {
+  const int lane = threadIdx.x & 31;
+  auto enter = [&](int l, int n) {  // the n-th of list l as its head
+    const int k = l / m.splits;
+    const uint64_t key = n < m.num_select ? m.keys[(int64_t)l * m.num_select + n] : 0;
+    m.next[l] = n;
+    m.low[l] = key;
+    if (!m.done[k]) m.head[l] = candidate_score(m.base[k], m.shift[k], key);
+    else m.head[l] = n == 0 && l == k * m.splits ? order_double(m.base[k]) : 0;
+  };
+  for (int l = lane; l < m.lists; l += 32) enter(l, 0);
+  uint64_t best, best_key;  // of this lane's lists
+  int best_list, best_beam;
+  auto look = [&] {
+    best = best_key = 0;
+    best_list = best_beam = 0;
+    for (int l = lane; l < m.lists; l += 32) {
+      const uint64_t o = m.head[l];
+      if (o == 0 || o < best) continue;
+      const int k = l / m.splits;
+      if (o > best || (k == best_beam && m.low[l] > best_key)) {
+        best = o;
+        best_key = m.low[l];
+        best_list = l;
+        best_beam = k;
+      }
+    }
+  };
+  look();
+  for (int i = 0; i < m.num_select; ++i) {
+    bool mine = best != 0;  // of the lanes' best, by what is compared first
+    auto keep_max = [&](uint32_t x) {  // (by all lanes)
+      const uint32_t top = __reduce_max_sync(0xffffffffu, mine ? x : 0u);
+      mine = mine && x == top;
+    };
+    keep_max((uint32_t)(best >> 32));
+    keep_max((uint32_t)best);
+    keep_max(~(uint32_t)best_beam);
+    keep_max((uint32_t)(best_key >> 32));
+    keep_max((uint32_t)best_key);
+    if (!__any_sync(0xffffffffu, mine)) {
+      if (lane == 0) m.won[i] = 0;
+    } else if (mine) {  // one lane: a beam's keys are all different
+      const int l = best_list, n = m.next[l];
+      m.won[i] = best;
+      m.list[i] = l;
+      m.at[i] = n;
+      enter(l, n + 1);
+      look();
+    }
+    __syncwarp();
+  }
+}
+
 // One CTA a request.  List k splits + j holds beam k's best of its j-th range: equal scores go
 // to the lower list.  Where they are few (by_counting below) two sorts by counting do: of the
 // lists' heads, so that the num_select best lists stay, and of the one of rank r num_select - r
@@ -443,11 +513,19 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
 // one warp merges them in num_select rounds over the heads, with as many scores as fit in
 // shared memory (a list's further ones are read when it gets there).
 //
-// Scores are fp64, which keeps the order of a beam's logits.  To be sorted they take their
-// key's place in the lists into their last 13 bits: equal to 2^-39 they count as equal.
+// Scores are fp64; to be sorted they take their key's place in the lists into their last 13 bits:
+// equal to 2^-39 they count as equal.  Within a beam that is the order of the keys as long as
+// different logits have different scores: those of exponent e are 2^(e - 24) apart at least, scores
+// of exponent E are told apart by 2^(E - 39), by 2^(E - 52) in the rounds.  Where a candidate
+// fails that test (a beam at -1e9, a logit of 1e-5) and a beam has several lists, all is done
+// again by merge_by_key (4 beams of 32000 of which three are at -1e9: the call 12.6 us, else 7.5; 8 of
+// 128000, 16 kept: 46, else 12.4.  Keys compared everywhere instead: 8.8 us for any 4 beams, 79
+// instead of 50 for 128 kept of 63 lists).
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
 constexpr int kFewLists = 64, kPlaces = 8192, kMostKeys = 512;
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
+constexpr int kSortReach = 39 - 24 - 2, kRoundReach = 52 - 24 - 2;  // (E is the base's here)
+// (two CTAs an SM, so 64 registers: left to itself the compiler takes 40 and spills about the call)
+__global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const BeamParams p) {
   __shared__ double s_base[kMaxLists];       // cum - (lse - shift) of the request's beams,
   __shared__ float s_shift[kMaxLists];       // shift 0 unless all of a row is as low as it gets
   __shared__ bool s_done[kMaxLists];
@@ -533,10 +611,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   __syncthreads();
   // the ordered score of a key of list l, its first or not (0: there is none); the difference
   // of two logits as low as a shift is exact
-  auto score_of = [&](int l, bool lead, uint64_t key) -> uint64_t {
+  bool close = false;  // whether one of this thread's scores may be another logit's, too
+  auto score_of = [&](int l, bool lead, uint64_t key, int reach) -> uint64_t {
     const int k = l / p.splits;
-    if (s_done[k]) return lead && l == k * p.splits ? order_double(s_base[k]) : 0;
-    return key ? order_double(s_base[k] + (double)(key_value(key) - s_shift[k])) : 0;
+    const double base = s_base[k];
+    if (s_done[k]) return lead && l == k * p.splits ? order_double(base) : 0;
+    const float shift = s_shift[k];
+    const uint64_t o = candidate_score(base, shift, key);
+    const int e_base = (__double2hiint(base) >> 20 & 0x7ff) - 1023;
+    const int e = (int)(__float_as_uint(key_value(key)) >> 23 & 0xff) - 127;
+    if (o != 0 && (e_base - e > reach || shift != 0.f)) close = true;
+    return o;
   };
   auto put = [&](int i, uint64_t score, int l, uint64_t key) {
     const int64_t o = (int64_t)blockIdx.x * M + i;
@@ -545,13 +630,25 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     p.parents[o] = score ? (int32_t)(row0 + k) : -1;
     p.tokens[o] = score == 0 ? -1 : s_done[k] ? p.pad_token : (int32_t)~(uint32_t)key;
   };
+  auto put_won = [&] {  // by one warp
+    for (int i = tid; i < M; i += 32) {
+      const uint64_t won = s_won[i];
+      const int l = won ? s_list[i] : 0;
+      put(i, won, l, won ? keys[(int64_t)l * M + s_at[i]] : 0);
+    }
+  };
+  auto put_by_key = [&] {
+    merge_by_key({keys, s_base, s_shift, s_done, s_head, s_score, s_next, s_won, s_list, s_at, lists,
+                  p.splits, M});
+    put_won();
+  };
   if (by_counting) {
     constexpr uint64_t kPlace = kPlaces - 1;
     auto place_of = [](uint64_t o) { return (int)(~o & kPlace); };
     auto key_at = [&](int at) { return copied ? s_score[at] : keys[at]; };
     // key `at` of all, the d-th of list l: lower lists, and earlier keys, go first
     auto sort_score = [&](int at, int l, int d) -> uint64_t {
-      const uint64_t o = score_of(l, d == 0, key_at(at));
+      const uint64_t o = score_of(l, d == 0, key_at(at), kSortReach);
       return o ? (o & ~kPlace) | (kPlace - at) : 0;
     };
     uint64_t *s_some = s_head, *s_best = s_won;  // to be sorted, and the best of them
@@ -586,22 +683,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     if (tid < M) s_best[tid] = 0;
     __syncthreads();
     sort_keys<kMergeThreads>(s_some, most, s_best, M, s_next);
-    if (tid < M) {
-      const uint64_t best = s_best[tid];
-      const int at = best ? place_of(best) : 0;
-      put(tid, best & ~kPlace, at / M, key_at(at));
+    if (p.splits == 1 || !__syncthreads_or(close)) {
+      if (tid < M) {
+        const uint64_t best = s_best[tid];
+        const int at = best ? place_of(best) : 0;
+        put(tid, best & ~kPlace, at / M, key_at(at));
+      }
+      return;
     }
+    if (tid >= 32) return;
+    put_by_key();
     return;
   }
   const int depth = min(M, kMergeScores / lists);
   for (int i = tid; i < lists * depth; i += kMergeThreads) {
     const int l = i / depth, n = i % depth;
-    const uint64_t o = score_of(l, n == 0, keys[(int64_t)l * M + n]);
+    const uint64_t o = score_of(l, n == 0, keys[(int64_t)l * M + n], kRoundReach);
     s_score[i] = o;
     if (n == 0) {
       s_head[l] = o;
       s_next[l] = 0;
     }
+  }
+  if (p.splits > 1 && __syncthreads_or(close)) {
+    if (tid < 32) put_by_key();
+    return;
   }
   __syncthreads();
   if (tid >= 32) return;
@@ -631,17 +737,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
         s_next[l] = n + 1;
         s_head[l] = n + 1 >= M       ? 0
                     : n + 1 < depth ? s_score[(int)l * depth + n + 1]
-                                    : score_of((int)l, false, keys[(int64_t)l * M + n + 1]);
+                                    : score_of((int)l, false, keys[(int64_t)l * M + n + 1],
+                                               kRoundReach);
         look();
       }
     }
     __syncwarp();
   }
-  for (int i = tid; i < M; i += 32) {
-    const uint64_t won = s_won[i];
-    const int l = won ? s_list[i] : 0;
-    put(i, won, l, won ? keys[(int64_t)l * M + s_at[i]] : 0);
-  }
+  if (p.splits > 1 && __any_sync(0xffffffffu, close)) put_by_key();
+  else put_won();
 }
 
 // How a call's rows are cut.  Tiles of 32 elements a thread where they give every SM a few

@@ -656,3 +656,46 @@ def test_python_refusals_on_device_tensors(pkv, cuda_device):
         pkv.beam_select(x, cum, 3, scores=cum)
     with pytest.raises(pkv.PkvError):
         pkv.beam_select(x, cum, 129)
+
+
+# ------------------------------------------------------------------------- beams: far scores, far logits
+
+def live_rows(rng, x, live, mask):
+    """All but `live` random tokens of each row masked by `mask`."""
+    for row in x.view(-1, x.shape[-1]):
+        row[torch.from_numpy(rng.permutation(len(row))[live:])] = mask
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("b,k,v,num", [(1, 1, 128000, 16), (1, 4, 32000, 16), (2, 2, 128000, 128),
+                                       (1, 1, 50257, 128), (3, 40, 9001, 33)])
+@pytest.mark.parametrize("far", [-1e6, -1e9, -1e12, -1e25, LOWEST])
+def test_beams_far_below_are_ranked_by_their_logits(pkv, cuda_device, dtype, b, k, v, num, far):
+    """Scores so low that the logits' differences vanish in them: the first beam has three tokens
+    left, the others' candidates follow by their logits, over all ranges a row is cut into."""
+    rng = np.random.default_rng(v + num)
+    x = beam_case(rng, b, k, v, dtype)
+    if k > 1:
+        live_rows(rng, x[:, 0], 3, -np.inf)
+    cum = np.full((b, k), far, dtype=np.float32)
+    cum[:, 0] = -1.0 if k > 1 else far
+    f64 = x.double().numpy()
+    want = ref.beam(f64, cum, num)
+    got = pkv.beam_select(x.to(cuda_device), torch.from_numpy(cum).to(cuda_device), num)
+    check_beams(got, want[:3], want[3], f64, None)
+
+
+@pytest.mark.parametrize("b,k,v,num", [(1, 1, 128000, 16), (1, 3, 32000, 128), (90, 4, 9001, 5)])
+def test_logits_closer_than_a_score_can_tell(pkv, cuda_device, b, k, v, num):
+    """Logits of 1e-30: every score of a beam is the same number, the order is the logits'."""
+    rng = np.random.default_rng(v)
+    x = (beam_case(rng, b, k, v, torch.float32) * 1e-30).float()
+    cum = np.tile(-5.0 - np.arange(k, dtype=np.float32), (b, 1))
+    f64 = x.double().numpy()
+    s, t, p = (g.cpu().numpy() for g in
+               pkv.beam_select(x.to(cuda_device), torch.from_numpy(cum).to(cuda_device), num))
+    for i in range(b):
+        best = np.lexsort((np.arange(v), -f64[i, 0]))[:num]
+        assert t[i].tolist() == best.tolist() and (p[i] == i * k).all()
+    assert (np.abs(s - (-5.0 - np.log(v))) <= LSE_TOL + 2.0 ** -24 * 20).all()
