@@ -712,8 +712,8 @@ PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t
  * (fp32), tokens and parents (int32; r, the row index), [num_requests][num_select].
  *   Within a beam candidates are ranked by their logits, between beams by the score to
  *   39 bits or more (of a log-sum accumulated in 32).  Candidates whose score is not finite
- *   (masked logits of -inf; every one of a beam whose logits hold NaN or more than 2^127, or with a
- *   cum_scores that is not finite) are never selected; where too few remain, score -inf,
+ *   in fp32 (masked logits of -inf; every one of a beam whose logits hold NaN or +inf, or with a
+ *   cum_scores that is not finite) are never selected; finite logits may have any size; where too few remain, score -inf,
  *   token -1 and parent -1 fill the rest.  parents is what pkv_fork_sequences takes.
  *   logit_type: PKV_BF16, PKV_FP16 or PKV_FP32; logits aligned to their type.
  *   num_select <= 128, num_beams <= 1024, vocab >= 1.  workspace: device, 16-byte

@@ -10,7 +10,10 @@
 //  - the running sum of exponentials: a thread keeps s = sum 2^(x L - r), with L fp32's
 //    log2 e and r its maximum of x L so far (one fma and one ex2 an element; s is rescaled
 //    when r moves).  The row's lse is (r + log2 s) / L: as the same L divides it, its
-//    rounding (2^-26 of L) moves the lse by 2^-26 times the softmax's entropy only;
+//    rounding (2^-26 of L) moves the lse by 2^-26 times the softmax's entropy only.  r starts at
+//    -kFar: far masked values (-1e30, whatever r would be rounded to there) weigh 0 from the first
+//    on.  Where a range's largest x L is not within kFar, fp32's step is 64 or more, so that only
+//    the logits equal to the largest one count, and they are counted;
 //  - the candidates: 64-bit keys (logit, lowest token first), so that no two are equal.
 //    A threshold T below the num_select-th largest key comes from the threads' maxima of
 //    the first tile; keys above T go to their warp's buffer in shared memory, straight
@@ -46,6 +49,7 @@ constexpr int kMaxLists = 1024;     // sorted lists (beam, split) of a request
 constexpr int32_t kMaxVocab = INT32_MAX - 65536;  // tiles count past its end in 32 bits
 constexpr int kMergeScores = 2048;  // scores a merge keeps in shared memory (>= kMaxLists)
 constexpr float kLog2e = 1.4426950408889634f;  // L above
+constexpr float kFar = 1073741824.f;  // 2^30: r is off by 32 below it, so s by 2^32
 
 struct BeamParams {
   const void *logits;
@@ -53,7 +57,7 @@ struct BeamParams {
   const uint8_t *finished;
   float *scores;
   int32_t *tokens, *parents;
-  float2 *part;          // [rows][splits]: r, sum of 2^(x L - r)
+  float2 *part;          // [rows][splits]: r, sum of 2^(x L - r); beyond kFar +-inf, a count
   uint64_t *keys;        // [rows][splits][num_select], descending, 0: none
   int64_t row_stride, num_rows;
   int32_t num_beams, vocab, num_select, pad_token, splits, tiles;
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   const int tile0 = (int)((int64_t)p.tiles * split / p.splits);
   const int tile1 = (int)((int64_t)p.tiles * (split + 1) / p.splits);
   const int M = p.num_select;
-  float r = -INFINITY, s = 0.f;
+  float r = -kFar, s = 0.f;
   // candidates are the keys above T_key, their logits at least T_val (a cheaper test, false
   // for NaN too); logits of -inf never are
   uint64_t T_key = make_key(-INFINITY, 0);
@@ -307,21 +311,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     float x[kHalf];
     const float top = elements(half, x);
     const float r_new = fmaxf(r, top * kLog2e);
-    if (r_new > -INFINITY) {
-      s *= fast_exp2(r - r_new);
-      float a = 0.f, b = 0.f;
+    s *= fast_exp2(r - r_new);
+    float a = 0.f, b = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHalf; i += 2) {
-        a += fast_exp2(fmaf(x[i], kLog2e, -r_new));
-        b += fast_exp2(fmaf(x[i + 1], kLog2e, -r_new));
-      }
-      s += a + b;
-      r = r_new;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i)  // all masked; a NaN makes the row's sum NaN
-        if (x[i] != x[i]) s = x[i];
+    for (int i = 0; i < kHalf; i += 2) {
+      a += fast_exp2(fmaf(x[i], kLog2e, -r_new));  // (a NaN makes the row's sum NaN)
+      b += fast_exp2(fmaf(x[i + 1], kLog2e, -r_new));
     }
+    s += a + b;
+    r = r_new;
     if (__any_sync(0xffffffffu, top >= T_val)) {
 #pragma unroll
       for (int i = 0; i < kHalf; ++i)
@@ -404,13 +402,17 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
 #pragma unroll
   for (int i = 1; i < kBeamWarps; ++i) top = fmaxf(top, s_m[i]);
   s *= r == top ? 1.f : fast_exp2(r - top);
-  if (top == -INFINITY && num_top > 0) {
-    // all of the range masked by a lowest value, which times L is -inf: how often its largest
-    // logit is there (fp32's step in this place is 2^104, so no other one counts)
-    const float x0 = key_value(s_top[0]);
-    const int end = min(tile1 * kTile, p.vocab);
-    for (int at = tile0 * kTile + tid; at < end; at += kThreads)
-      s += W::get(raw_bits(row.data + at), 0) == x0 ? 1.f : 0.f;
+  if (fabsf(top) >= kFar) {
+    if (num_top > 0) {  // how often its largest logit is there; NaN and +inf are still no numbers
+      const float x0 = key_value(s_top[0]);
+      const int end = min(tile1 * kTile, p.vocab);
+      s = 0.f;
+      for (int at = tile0 * kTile + tid; at < end; at += kThreads) {
+        const float x = W::get(raw_bits(row.data + at), 0);
+        s += !(x <= FLT_MAX) ? NAN : x == x0 ? 1.f : 0.f;
+      }
+    }  // (else all of it is -inf, or NaN: s is 0 or NaN)
+    top = copysignf(INFINITY, top);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -424,10 +426,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   }
 }
 
-// A double as an integer of the same order, 0 for what is not finite.
+// A double as an integer of the same order, 0 for what is not finite in fp32.
 __device__ __forceinline__ uint64_t order_double(double x) {
-  if (!isfinite(x)) return 0;
   const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+  if ((b & ~(1ull << 63)) >= 0x47effffff0000000ull) return 0;  // 2^128 - 2^103 on, inf, NaN
   return b >> 63 ? ~b : b | 1ull << 63;
 }
 __device__ __forceinline__ double unorder_double(uint64_t o) {
@@ -527,7 +529,7 @@ constexpr int kSortReach = 39 - 24 - 2, kRoundReach = 52 - 24 - 2;  // (E is the
 // (two CTAs an SM, so 64 registers: left to itself the compiler takes 40 and spills about the call)
 __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const BeamParams p) {
   __shared__ double s_base[kMaxLists];       // cum - (lse - shift) of the request's beams,
-  __shared__ float s_shift[kMaxLists];       // shift 0 unless all of a row is as low as it gets
+  __shared__ float s_shift[kMaxLists];       // shift 0 unless a row's largest logit is beyond kFar
   __shared__ bool s_done[kMaxLists];
   // keys as they are (counting, if they fit), or [list][depth] ordered scores (rounds)
   __shared__ uint64_t s_score[kMergeScores];
@@ -575,8 +577,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
     for (int j = lane; j < parts; j += group)
       s += part[j].y * (part[j].x == m ? 1.f : exp2f(part[j].x - m));
     for (int o = group / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const bool low = m == -INFINITY && s > 0.f;
-    if (__any_sync(0xffffffffu, low)) {
+    const bool far = fabsf(m) == INFINITY && s > 0.f;
+    if (__any_sync(0xffffffffu, far)) {
       // the parts are counts of their largest logits: those of the row's largest
       uint32_t best = 0;
       for (int j = lane; j < parts; j += group) best = max(best, (uint32_t)(heads[(int64_t)j * M] >> 32));
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       for (int j = lane; j < parts; j += group)
         if ((uint32_t)(heads[(int64_t)j * M] >> 32) == best) n += part[j].y;
       for (int o = group / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (low) {
+      if (far) {
         s = n;
         shift = key_value((uint64_t)best << 32);
         m = 0.f;
@@ -609,8 +611,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
     for (int i = tid + kMergeThreads; i < lists * M; i += kMergeThreads) s_score[i] = keys[i];
   }
   __syncthreads();
-  // the ordered score of a key of list l, its first or not (0: there is none); the difference
-  // of two logits as low as a shift is exact
+  // the ordered score of a key of list l, its first or not (0: there is none)
   bool close = false;  // whether one of this thread's scores may be another logit's, too
   auto score_of = [&](int l, bool lead, uint64_t key, int reach) -> uint64_t {
     const int k = l / p.splits;

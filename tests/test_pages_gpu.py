@@ -699,3 +699,59 @@ def test_logits_closer_than_a_score_can_tell(pkv, cuda_device, b, k, v, num):
         best = np.lexsort((np.arange(v), -f64[i, 0]))[:num]
         assert t[i].tolist() == best.tolist() and (p[i] == i * k).all()
     assert (np.abs(s - (-5.0 - np.log(v))) <= LSE_TOL + 2.0 ** -24 * 20).all()
+
+
+FAR = [-1e8, -7.4e8, -7.5e8, -1e9, -1e10, -1e12, -1e20, -1e30, -1e38, -2.3e38, -2.4e38, LOWEST]
+
+
+@pytest.mark.parametrize("mask", FAR)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v,many", [(7, False), (300, False), (3001, False), (70001, False), (9001, True)])
+def test_rows_masked_by_any_low_value(pkv, cuda_device, mask, dtype, v, many):
+    """Most of a row, all of it, all but its last token, one end of it, or all but a second low
+    value masked by a finite number: the live tokens' scores are those of the live tokens alone."""
+    rng = np.random.default_rng(v)
+    b, k = (60, 5) if many else (1, 5)
+    x = beam_case(rng, 1, k, v, dtype)
+    live_rows(rng, x[:, 0], max(v // 100, 1), mask)
+    x[0, 1] = mask
+    x[0, 2, :-1] = mask
+    x[0, 3, v // 3:] = mask
+    x[0, 4] = mask
+    x[0, 4, [1, v // 2]] = max(2 * mask, LOWEST)
+    cum = np.array([[-0.5, 0.0, -20.0, -2.0, -1.5]], dtype=np.float32)
+    f64 = x.double().numpy()
+    for num in (3, 40):
+        want = ref.beam(f64, cum, num)
+        got = pkv.beam_select(x.to(cuda_device).expand(b, k, v).contiguous(),
+                              torch.from_numpy(cum).to(cuda_device).expand(b, k).contiguous(), num)
+        check_beams([g[:1] for g in got], want[:3], want[3], f64, None)
+        assert torch.equal(got[1], got[1][:1].expand_as(got[1]))
+
+
+@pytest.mark.parametrize("top", [1e8, 7.4e8, 7.5e8, 1e10, 1e20, 2e38, 2.5e38, -LOWEST])
+@pytest.mark.parametrize("v,many", [(7, False), (3001, False), (70001, False), (9001, True)])
+def test_logits_of_any_finite_size(pkv, cuda_device, top, v, many):
+    """Huge logits are numbers like others: one, several alike, beside ordinary and low ones."""
+    rng = np.random.default_rng(v)
+    b, k = (60, 4) if many else (1, 4)
+    x = beam_case(rng, 1, k, v, torch.float32)
+    x[0, 0, v // 2] = top
+    x[0, 1, [0, v // 3, v - 1]] = top
+    x[0, 2, v - 2], x[0, 2, v - 1] = top, top / 2
+    x[0, 3] = torch.from_numpy(np.where(rng.random(v) < 0.5, top, -1e5)).float()
+    cum = np.array([[-1.0, -2.0, -0.5, 0.0]], dtype=np.float32)
+    f64 = x.double().numpy()
+    for num in (4, 33):
+        want = ref.beam(f64, cum, num)
+        got = pkv.beam_select(x.to(cuda_device).expand(b, k, v).contiguous(),
+                              torch.from_numpy(cum).to(cuda_device).expand(b, k).contiguous(), num)
+        check_beams([g[:1] for g in got], want[:3], want[3], f64, None)
+        assert torch.equal(got[1], got[1][:1].expand_as(got[1]))
+
+
+def test_scores_past_fp32_are_not_candidates(pkv, cuda_device):
+    x = torch.tensor([[[-LOWEST, LOWEST, -LOWEST], [LOWEST, LOWEST, LOWEST]]], device=cuda_device)
+    s, t, p = pkv.beam_select(x, torch.tensor([[0.0, LOWEST]], device=cuda_device), 6)
+    assert t[0].tolist() == [0, 2, 0, 1, 2, -1] and p[0].tolist() == [0, 0, 1, 1, 1, -1]
+    assert s[0, 2:5].tolist() == [LOWEST] * 3 and bool(torch.isneginf(s[0, 5]))
