@@ -771,9 +771,9 @@ PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_de
  *   cu_q_lens, context_lens, block_tables: DEVICE arrays as pkv_paged_varlen_attention
  *   takes them.  selected: device int32 [total_q][Hkv][num_select]: logical blocks,
  *   ascending, then -1.  1 <= recent_blocks, 0 <= sink_blocks, their sum <= num_select.
- *   A block id outside the pool has score -inf, PKV_DEV_BAD_BLOCK; a token past cu_q_lens'
- *   last entry, or one whose context is shorter than its window, gets -1 throughout
- *   (PKV_DEV_PLAN_MISMATCH for the latter).
+ *   A block id outside the pool has score -inf, PKV_DEV_BAD_BLOCK.  A token past cu_q_lens'
+ *   last entry gets -1 throughout; so does every token of a sequence whose context is shorter
+ *   than its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.
  *   workspace: device, 16-byte aligned; any size from pkv_select_workspace_size(1, ...)
  *   on serves (fewer bytes than pkv_select_workspace_size(total_q, ...): the tokens in
  *   several passes); contents do not matter, one call at a time.
@@ -803,8 +803,9 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   own choice in any order (entries outside the token's blocks are skipped; one that
  *   is there twice counts twice).  A block id outside the pool is skipped,
  *   PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past cu_q_lens' last
- *   entry is left as it was; one whose context is shorter than its window too,
- *   PKV_DEV_PLAN_MISMATCH.  num_q_heads / Hkv <= 16.  Weights go into the
+ *   entry is left as it was; so is every token of a sequence whose context is shorter than
+ *   its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.
+ *   num_q_heads / Hkv <= 16.  Weights go into the
  *   product with V as two bf16 parts (2^-14 of a weight at most is lost), sums are fp32, out is
  *   rounded once to bf16.  Bytes of a visible block past the token's position do not reach its row.  out may be q itself, and
  *   must not overlap the inputs otherwise.  q and the lengths may be read before the preceding

@@ -444,12 +444,13 @@ __global__ void __launch_bounds__(kT) select_kernel(const SelectParams p) {
   const int64_t local = blockIdx.x / p.hkv;
   const int h = (int)(blockIdx.x % p.hkv);
   const int64_t token = p.token0 + local;
-  const TokenPlace at = find_token(p.cu_q_lens, p.context_lens, p.num_seqs, token, s_sum);
+  const TokenPlace at =
+      find_token(p.cu_q_lens, p.context_lens, p.num_seqs, p.max_blocks, token, s_sum);
   int32_t *out = p.selected + (token * p.hkv + h) * p.num_select;
   const int32_t K = p.num_select;
   int32_t nb = at.pos / kBlockSize + 1;
   pdl_wait();
-  if (at.pos < 0 || nb > p.max_blocks) {
+  if (at.pos < 0) {
     if (h == 0 && tid == 0 && at.seq < p.num_seqs) report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
     nb = 0;
   }

@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
     fence_mbar_init();
   }
   // q, the lengths and the tables are not written by the kernels this one follows
-  const TokenPlace at = find_token(p.cu_q_lens, p.context_lens, p.num_seqs, token, s_sum);
+  const TokenPlace at =
+      find_token(p.cu_q_lens, p.context_lens, p.num_seqs, p.max_blocks, token, s_sum);
   uint32_t qa[2 * kL][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
   pdl_wait();
   // (the same for the whole cluster)
   const int32_t own = at.pos / kBlockSize;
-  if (at.pos < 0 || own >= p.max_blocks) {
+  if (at.pos < 0) {
     if (at.seq < p.num_seqs && h == 0 && rank == 0 && threadIdx.x == 0)
       report(p.dev_status, PKV_DEV_PLAN_MISMATCH);
     return;

@@ -9,7 +9,7 @@ namespace pkv {
 namespace {
 
 // A query token's sequence and position; pos < 0: none (seq = num_seqs: past the last
-// sequence, else a context shorter than its window).
+// sequence, else a context shorter than its window or longer than the table's row).
 struct TokenPlace {
   int32_t seq, pos;
 };
@@ -18,7 +18,7 @@ struct TokenPlace {
 // one round of loads for as many sequences as threads.  s: one int per warp.
 __device__ __forceinline__ TokenPlace find_token(const int32_t *cu_q_lens,
                                                  const int32_t *context_lens, int32_t num_seqs,
-                                                 int64_t token, int32_t *s) {
+                                                 int32_t max_blocks, int64_t token, int32_t *s) {
   int32_t n = 0;
   for (int32_t i = threadIdx.x; i < num_seqs; i += blockDim.x) n += __ldg(cu_q_lens + i + 1) <= token;
   n = __reduce_add_sync(0xffffffffu, n);
@@ -31,7 +31,8 @@ __device__ __forceinline__ TokenPlace find_token(const int32_t *cu_q_lens,
   if (at.seq < num_seqs) {
     const int32_t end = __ldg(cu_q_lens + at.seq + 1), first = __ldg(cu_q_lens + at.seq);
     const int32_t ctx = __ldg(context_lens + at.seq);
-    if (end - first <= ctx && token >= first) at.pos = ctx - (int32_t)(end - token);
+    if (end - first <= ctx && (ctx - 1) / kBlockSize < max_blocks && token >= first)
+      at.pos = ctx - (int32_t)(end - token);
   }
   return at;
 }

@@ -638,3 +638,46 @@ def test_an_infinite_value_stays_infinite(pkv, cuda_device, value):
     out, _ = attend(pkv, dev, meta, q, pool, sel)
     assert bool((out[:, :, 5] == value).all())
     assert bool(torch.isfinite(torch.cat([out[:, :, :5], out[:, :, 6:]], dim=2)).all())
+
+
+# ------------------------------------------------------------------------- contexts past the table
+
+@pytest.mark.parametrize("over", [1, 2, 3, 17])
+@pytest.mark.parametrize("passes", [False, True])
+def test_windows_that_cross_the_tables_last_column(pkv, cuda_device, over, passes):
+    """A sequence whose context its table cannot hold has no token that is served, the first
+    ones of its window neither, whatever the workspace held; the others are as ever."""
+    dev = cuda_device
+    hq, hkv, d, num = 8, 2, 64, 4
+    n, ctx = [2, 3, 1], [300, 16 * 20 + over, 17]
+    rng = np.random.default_rng(over)
+    pool = make_pool(rng, 64, hkv, d)
+    index, unit = whole_index(pool)
+    table = rng.permutation(60).reshape(3, 20)
+    q = bf16(rng.standard_normal((6, hq, d)))
+    cu = np.concatenate([[0], np.cumsum(n)])
+    on = [q.to(dev), *(dev_i32(x, dev) for x in (cu, ctx, table))]
+    lib = pkv._load()
+    one = lib.pkv_select_workspace_size(1, hkv, 20)
+    import ctypes
+    want = np.full((6, hkv, num), -1)
+    x = q.double().numpy()
+    for t, (s, pos) in {0: (0, 298), 1: (0, 299), 5: (2, 16)}.items():
+        want[t] = ref.select(x[t], pos, table[s], index, unit, num, 1, 1)
+    di, du = torch.as_tensor(index).to(dev), torch.as_tensor(unit).to(dev)
+    for fill in (255, 0, 63):
+        ws = torch.full((one if passes else 6 * one,), fill, dtype=torch.uint8, device=dev)
+        sel, st = torch.full((6, hkv, num), -7, dtype=torch.int32, device=dev), status_of(dev)
+        code = lib.pkv_select_blocks(
+            on[0].data_ptr(), on[1].data_ptr(), on[2].data_ptr(), on[3].data_ptr(), 20, 3, 6, hq,
+            di.data_ptr(), du.data_ptr(), ctypes.byref(pkv.PoolDesc(64, 16, hkv, d)), num, 1, 1,
+            sel.data_ptr(), ws.data_ptr(), ws.numel(), st.data_ptr(),
+            torch.cuda.current_stream(dev).cuda_stream)
+        assert code == 0 and int(st.item()) == 4
+        np.testing.assert_array_equal(sel.cpu().numpy(), want)
+    st.zero_()
+    out = torch.full_like(on[0], 7.0)
+    pkv.paged_sparse_attention(*on, dev_i32(np.where(want < 0, 0, want), dev), pool.to(dev), 0.1, out=out,
+                               dev_status=st)
+    assert int(st.item()) == 4 and bool((out[2:5] == 7.0).all())
+    assert not bool((out[[0, 1, 5]] == 7.0).any())
