@@ -660,7 +660,9 @@ PKV_API pkv_status pkv_free_sequences(const int32_t *rows, int32_t num_listed,
  * blocks they need, context_lens[r] += n, and slot_mapping[cu_new[r] + i] the slot of
  * position context_lens[r] + i (old length), for the append.  Entries of slot_mapping
  * before cu_new[0] or from cu_new[num_rows] on (a step padded to num_tokens) get -1,
- * which the append skips; entries past num_tokens are not written.
+ * which the append skips; entries past num_tokens are not written.  num_rows == 0 enqueues
+ * nothing: slot_mapping stays as it is, and a caller that appends all the same fills it with -1
+ * (the Python call does).
  *   A partly filled last block that other rows hold too is not written to: the row
  *   takes a new block in its place, copy_src[r] and copy_dst[r] say which (-1 where
  *   there is none), for a pkv_copy_blocks before the append.  When every holder of such

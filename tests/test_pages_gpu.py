@@ -755,3 +755,23 @@ def test_scores_past_fp32_are_not_candidates(pkv, cuda_device):
     s, t, p = pkv.beam_select(x, torch.tensor([[0.0, LOWEST]], device=cuda_device), 6)
     assert t[0].tolist() == [0, 2, 0, 1, 2, -1] and p[0].tolist() == [0, 0, 1, 1, 1, -1]
     assert s[0, 2:5].tolist() == [LOWEST] * 3 and bool(torch.isneginf(s[0, 5]))
+
+
+# ------------------------------------------------------------------------- reserve without rows
+
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_reserve_of_no_rows_gives_no_slot(pkv, cuda_device, on_stream):
+    """A padded step none of whose rows is there: every slot is -1, whatever it was."""
+    dev = cuda_device
+    t, c, r = (torch.zeros(s, dtype=torch.int32, device=dev) for s in ((0, 4), (0,), (9,)))
+    cu, whole = dev_i32([0], dev), dev_i32(np.full(12, 77), dev)
+    stream = torch.cuda.Stream(dev) if on_stream else None
+    torch.cuda.synchronize(dev)
+    bound = pkv.BoundReserveBlocks(cu, t, c, r, slot_mapping=whole[:7], stream=stream)
+    bound.run()
+    torch.cuda.synchronize(dev)
+    assert whole.cpu().tolist() == [-1] * 7 + [77] * 5
+    slots, src, dst = pkv.reserve_blocks(cu, t, c, r, num_tokens=5)
+    assert slots.cpu().tolist() == [-1] * 5 and src.numel() == 0 and dst.numel() == 0
+    assert r.cpu().tolist() == [0] * 9
+    pkv.reserve_blocks(cu, t, c, r, num_tokens=0)
