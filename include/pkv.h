@@ -600,7 +600,9 @@ PKV_API pkv_status pkv_state_checkpoint(const void *src, const int32_t *dst_slot
  *    reported where a call sees it, PKV_DEV_BAD_COUNT.
  *  - The kernels are launched with programmatic stream serialisation and wait for the
  *    preceding kernel before they touch anything; a call does not let its dependents
- *    launch before it has finished, so the appends and the attention may follow directly.
+ *    launch before it has finished, and the lengths it wrote are visible to the whole GPU by
+ *    then, so the appends, the selection and the sparse attention may follow directly.
+ *    pkv_paged_varlen_attention, which reads the tables ahead of its wait too, follows an append.
  *
  * pkv_copy_blocks: whole blocks copied inside every array of `arrays` (each layer's
  * pool, the scales of 8-bit pools, block indexes: whatever is stored by block):
@@ -779,9 +781,9 @@ PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_de
  *   workspace: device, 16-byte aligned; any size from pkv_select_workspace_size(1, ...)
  *   on serves (fewer bytes than pkv_select_workspace_size(total_q, ...): the tokens in
  *   several passes); contents do not matter, one call at a time.
- *   As in pkv_paged_varlen_attention, q, the lengths and the tables may be read before the
- *   preceding kernel of the stream has completed (a kernel that lets its dependents launch
- *   early must not write them); index, index_scales and the workspace are touched after it.
+ *   cu_q_lens and context_lens may be read before the preceding kernel of the stream has
+ *   completed (one that lets its dependents launch early must not write them; none of this
+ *   library does); everything else is touched after it.
  */
 PKV_API size_t pkv_select_workspace_size(int64_t total_q, int32_t num_kv_heads,
                                          int32_t max_blocks_per_seq);
@@ -801,7 +803,7 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   out[t][hq][:] = sum_p softmax_p(scale * q[t][hq] . K[p][h]) V[p][h],  h = hq / G,
  *   over the positions p <= the token's, p / 16 in selected[t][h].
  *   With every block of its context selected a token's result is that of
- *   pkv_paged_varlen_attention.  selected: as pkv_select_blocks writes it, or a caller's
+ *   pkv_paged_varlen_attention, but for the rounding of its weights.  selected: as pkv_select_blocks writes it, or a caller's
  *   own choice in any order (entries outside the token's blocks are skipped; one that
  *   is there twice counts twice).  A block id outside the pool is skipped,
  *   PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past cu_q_lens' last
@@ -809,9 +811,11 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.
  *   num_q_heads / Hkv <= 16.  Weights go into the
  *   product with V as two bf16 parts (2^-14 of a weight at most is lost), sums are fp32, out is
- *   rounded once to bf16.  Bytes of a visible block past the token's position do not reach its row.  out may be q itself, and
- *   must not overlap the inputs otherwise.  q and the lengths may be read before the preceding
- *   kernel has completed, selected, the tables and the pool are read after it.
+ *   rounded once to bf16.  Bytes of a visible block past the token's position do not
+ *   reach its row.  out may be q itself, and must not overlap the inputs otherwise.  The lengths
+ *   may be read before the preceding kernel has completed, everything else is touched after it.
+ *   The next kernel may be launched while this one runs: out must not be the q of a
+ *   pkv_paged_varlen_attention directly behind it (this call and the selection wait).
  */
 PKV_API pkv_status pkv_paged_sparse_attention(const void *q, const int32_t *cu_q_lens,
                                               const int32_t *context_lens,

@@ -12,7 +12,9 @@
 // million blocks takes 32 rounds of that.  Copies are bound by HBM.
 //
 // Every kernel here may be launched while the one before it ends, and waits for it before
-// it touches anything; none but compact's first lets its own dependents launch early.
+// it touches anything; none but compact's first lets its own dependents launch early.  The
+// selection and the attention read lengths ahead of their wait, so a thread that writes some
+// makes them visible to the whole GPU (a fence) before its CTA ends.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -156,7 +158,10 @@ __global__ void __launch_bounds__(kThreads)
     } else if (p >= 0) {
       ctx = max(__ldg(ctx_lens + p), 0);
     }
-    if (col0 == 0 && threadIdx.x == 0) new_ctx[row] = ctx;
+    if (col0 == 0 && threadIdx.x == kThreads - 1) {  // (beside the others' copies)
+      new_ctx[row] = ctx;
+      __threadfence();
+    }
     const int32_t used = used_blocks(ctx, width);
     const int32_t end = min(used, col0 + kForkCols);
     for (int32_t j = col0 + threadIdx.x; j < end; j += kThreads)
@@ -196,6 +201,7 @@ __global__ void __launch_bounds__(kFreeThreads)
   }
   if (threadIdx.x == 0) s_ctx = atomicExch(ctx_lens + row, 0);
   __syncthreads();
+  if (threadIdx.x == kFreeThreads - 1) __threadfence();  // (what came before the barrier, too)
   const int32_t used = used_blocks(s_ctx, width);
   const int32_t *entries = tables + row * width;
 #pragma unroll 4
@@ -442,6 +448,14 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
     cluster_wait();
     return;
   }
+  // the lengths, by the threads that have least to do with the ids (the fence takes 0.5 us)
+  if (threads - 1 - gtid < p.num_rows) {
+    for (int32_t r = threads - 1 - gtid; r < p.num_rows; r += threads) {
+      const RowPlan pl = p.row_plan[r];
+      if (pl.n > 0) p.ctx_lens[r] = pl.ctx + pl.n;
+    }
+    __threadfence();
+  }
   if (id_lo < id_hi && before < demand)
     for (int32_t r = tid; r < p.num_rows; r += kRankThreads) s_base[r] = p.row_base[r];
   for (int64_t i = id_lo; i < id_hi && before < demand; i += kSegIds) {
@@ -484,7 +498,6 @@ __global__ void __launch_bounds__(kRankThreads) reserve_kernel(const ReservePara
     if (pl.old_block < 0) p.copy_dst[r] = -1;
     else atomicSub(p.refs + pl.old_block, 1);
     if (pl.n <= 0) continue;
-    p.ctx_lens[r] = pl.ctx + pl.n;
     if (pl.old_block < 0 && pl.ctx % kBlockSize != 0) {  // slots in the block it goes on filling
       const int32_t b = p.tables[(int64_t)r * p.width + pl.ctx / kBlockSize];
       const int32_t c0 = __ldg(p.cu_new + r);

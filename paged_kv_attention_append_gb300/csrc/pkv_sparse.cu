@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
     for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[s]), 1);
     fence_mbar_init();
   }
-  // q, the lengths and the tables are not written by the kernels this one follows
+  // (the kernels that write lengths make them visible before they let this one be launched)
   const TokenPlace at =
       find_token(p.cu_q_lens, p.context_lens, p.num_seqs, p.max_blocks, token, s_sum);
+  pdl_wait();
   uint32_t qa[2 * kL][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -133,7 +134,6 @@ __global__ void __launch_bounds__(32 * kWarps, SparseCfg<D, kWarps>::kCtasPerSm)
       qa[2 * L + 1][2 + half] = v.w;
     }
   }
-  pdl_wait();
   // (the same for the whole cluster)
   const int32_t own = at.pos / kBlockSize;
   if (at.pos < 0) {

@@ -681,3 +681,65 @@ def test_windows_that_cross_the_tables_last_column(pkv, cuda_device, over, passe
                                dev_status=st)
     assert int(st.item()) == 4 and bool((out[2:5] == 7.0).all())
     assert not bool((out[[0, 1, 5]] == 7.0).any())
+
+
+# ------------------------------------------------------------------------- right behind the page calls
+
+@pytest.mark.parametrize("first", ["reserve", "fork", "free"])
+def test_selection_and_attention_right_behind_a_page_call(pkv, cuda_device, first):
+    """Nothing between the call that writes lengths and tables and those that read them; the
+    queries are written in place by the attention before, too."""
+    dev, rng = cuda_device, np.random.default_rng(31)
+    rows, width, hq, hkv, d, num, scale = 24, 40, 8, 2, 64, 5, 0.125
+    blocks = rows * width + 8
+    pool = make_pool(rng, blocks, hkv, d)
+    index, unit = whole_index(pool)
+    on_pool, di, du = pool.to(dev), torch.as_tensor(index).to(dev), torch.as_tensor(unit).to(dev)
+    table = rng.permutation(blocks)[:rows * width].reshape(rows, width)
+    ctx = rng.integers(17, width * 16 - 40, rows)
+    refs = np.zeros(blocks)
+    for r in range(rows):
+        refs[table[r, :ref.used(ctx[r])]] += 1
+    q = bf16(rng.standard_normal((rows, hq, d))).to(dev)
+    one = dev_i32(np.arange(rows + 1), dev)
+    for step in range(8):
+        tabs, lens, counts = dev_i32(table, dev), dev_i32(ctx, dev), dev_i32(refs, dev)
+        new, new_lens = dev_i32(np.zeros((rows, width)), dev), dev_i32(np.zeros(rows), dev)
+        n = rng.integers(1, 40, rows)
+        cu = dev_i32(np.concatenate([[0], np.cumsum(n)]), dev)
+        parents, ended = dev_i32(rng.integers(0, rows, rows), dev), dev_i32(rng.integers(0, rows, 9), dev)
+        x, st = q.clone(), status_of(dev)
+        if first == "reserve":
+            call = pkv.BoundReserveBlocks(cu, tabs, lens, counts, num_tokens=int(n.sum()), dev_status=st)
+            read = (tabs, lens)
+        elif first == "fork":
+            call = pkv.BoundForkSequences(parents, tabs, lens, counts, new, new_lens, dev_status=st)
+            read = (new, new_lens)
+        else:
+            call = pkv.BoundFreeSequences(ended, tabs, lens, counts, dev_status=st)
+            read = (tabs, lens)
+        stt = status_of(dev)
+        own = pkv.BoundSparseAttention(x, one, read[1], read[0],
+                                       dev_i32(np.zeros((rows, hkv, num)), dev), on_pool, scale, x)
+        sel = pkv.BoundSelectBlocks(x, one, read[1], read[0], di, du, num, dev_status=stt)
+        att = pkv.BoundSparseAttention(x, one, read[1], read[0], sel.selected, on_pool, scale,
+                                       torch.full_like(q, 7.0), dev_status=stt)
+        torch.cuda.synchronize(dev)
+        call.run()
+        own.run()
+        sel.run()
+        att.run()
+        torch.cuda.synchronize(dev)
+        assert int(st.item()) == 0 and int(stt.item()) == (4 if first == "free" else 0)
+        t, c, xs = read[0].cpu().numpy(), read[1].cpu().numpy(), x.double().cpu().numpy()
+        gone = set(ended.cpu().tolist()) if first == "free" else set()
+        assert [int(z) for z in c[sorted(gone)]] == [0] * len(gone)
+        held = pool.double().numpy()
+        for r in range(rows):
+            if r in gone:
+                assert int(sel.selected[r].max()) == -1 and bool((att.out[r] == 7.0).all())
+                continue
+            chosen = ref.select(xs[r], c[r] - 1, t[r], index, unit, num, 1, 2)
+            np.testing.assert_array_equal(sel.selected[r].cpu().numpy(), chosen)
+            want, mag, dots = ref.sparse_attention(xs[r], c[r] - 1, t[r], chosen, held, scale)
+            check_out(att.out[r], want, mag, dots, d)
