@@ -775,6 +775,7 @@ PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_de
  *   cu_q_lens, context_lens, block_tables: DEVICE arrays as pkv_paged_varlen_attention
  *   takes them.  selected: device int32 [total_q][Hkv][num_select]: logical blocks,
  *   ascending, then -1.  1 <= recent_blocks, 0 <= sink_blocks, their sum <= num_select.
+ *   max_blocks_per_seq > 2^30: PKV_ERR_UNSUPPORTED.
  *   A block id outside the pool has score -inf, PKV_DEV_BAD_BLOCK.  A token past cu_q_lens'
  *   last entry gets -1 throughout; so does every token of a sequence whose context is shorter
  *   than its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.

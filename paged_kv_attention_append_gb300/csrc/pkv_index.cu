@@ -709,6 +709,7 @@ extern "C" pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
   // a pass: what the workspace holds, its blocks and the grids counted in 32 bits
   int64_t pass = std::min(workspace_bytes / token, total_q);
   pass = std::min(pass, (int64_t)(1 << 30) / std::max(max_blocks_per_seq, p.hkv));
+  if (pass < 1) return PKV_ERR_UNSUPPORTED;  // more columns than a pass may count
   profile_begin(PKV_KERNEL_SELECT, stream);
   const int e = desc->head_dim == 128 ? launch_select_t<128>(p, total_q, pass, stream)
                                       : launch_select_t<64>(p, total_q, pass, stream);

@@ -208,3 +208,10 @@ def test_plain_bounds_and_scores_by_hand():
         top = 2.0 ** -10 * 2.0 ** np.floor(np.log2(np.abs(q[h]).max()))
         s = ref.scores(q[h], b[None, h], u[None, h])[0] * top
         assert s >= sum((k[h] @ x).max() for x in q[h]) - 1e-3
+
+
+def test_select_refuses_tables_wider_than_a_pass(lib):
+    kw = dict(SELECT, width=(1 << 30) + 1, desc=ctypes.byref(pkv.PoolDesc(*DESC.values())))
+    before = pkv.kernel_launch_count()
+    assert lib.pkv_select_blocks(*kw.values()) == UNSUPPORTED
+    assert pkv.kernel_launch_count() == before
