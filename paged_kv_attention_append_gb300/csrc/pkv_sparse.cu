@@ -311,11 +311,18 @@ cudaError_t launch_sparse(const CUtensorMap &map, const SparseParams &p, int64_t
          16 * ranks <= p.num_select)
     ranks *= 2;
   // CTAs of two warps, twice as many of them an SM, where there are more (token, KV head)s than
-  // CTAs of four fit at a time and few blocks each, so that their start and end overlap more
-  // (the three calls: 2300 pairs of up to 5 blocks 28 -> 20 us, 2400 of 32 53 -> 48.5, 2048 of
-  // 16 52.6 -> 51, 1200 of 28 20.5 -> 21.3; of 64 81 -> 87)
-  constexpr int32_t kFewBlocks = 32;
-  if (total_q * p.hkv > 3ll * std::max(device_sm_count(), 1) && p.num_select <= kFewBlocks)
+  // CTAs of four fit at a time: their start and end overlap more.  Few blocks gain most (this call
+  // alone at D = 128: 2400 pairs of 8 blocks 38.2 -> 34.6 us, 4000 of 4 48.4 -> 35.2; D = 64: 25.8
+  // -> 18.7, 32.6 -> 23.5).  More blocks each gain where the waves come out even (1600 pairs of 28
+  // 64.6 -> 61.4 us, 480 of 32 29.2 -> 24.3, 2400 of 48 143.3 -> 140.8); an odd number of waves of
+  // four-warp CTAs ends with a wave of two-warp ones that is half empty (1200 of 28 50.0 -> 52.3,
+  // 2048 of 32 88.3 -> 90.0), which nine waves no longer feel (4000 of 24: 125 either way, D = 64
+  // 78.8 -> 71.9).  2048 of 64 take 81 -> 87 us with the selection.
+  constexpr int32_t kFewBlocks = 16, kMostBlocks = 48;
+  const int64_t slots = 3ll * std::max(device_sm_count(), 1), pairs = total_q * p.hkv;
+  const int64_t waves = (pairs + slots - 1) / slots;
+  if (waves > 1 && (p.num_select <= kFewBlocks ||
+                    (p.num_select <= kMostBlocks && (waves % 2 == 0 || waves > 8))))
     return launch_sparse_t<D, 2>(map, p, total_q, ranks, stream);
   return launch_sparse_t<D, 4>(map, p, total_q, ranks, stream);
 }
