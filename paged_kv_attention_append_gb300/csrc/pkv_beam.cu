@@ -436,8 +436,7 @@ __device__ __forceinline__ double unorder_double(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o ^ 1ull << 63 : ~o));
 }
 
-// A merge that compares candidates by score (all 64 bits), then beam, then key: by one warp, in
-// num_select rounds over the lists' heads, with their keys beside their scores.
+// What the two functions below work on, which a merge needs where scores are coarse.
 struct ByKey {
   const uint64_t *keys;     // [lists][num_select]
   const double *base;       // of each beam, as is what follows
@@ -452,6 +451,54 @@ struct ByKey {
 __device__ __forceinline__ uint64_t candidate_score(double base, float shift, uint64_t key) {
   return key ? order_double(base + (double)(key_value(key) - shift)) : 0;
 }
+// Whether another logit than this key's may have the same score, told apart as `reach` says.
+__device__ __forceinline__ bool score_is_coarse(double base, float shift, uint64_t key, int reach) {
+  const int e_base = (__double2hiint(base) >> 20 & 0x7ff) - 1023;
+  const int e = (int)(__float_as_uint(key_value(key)) >> 23 & 0xff) - 127;
+  return e_base - e > reach || shift != 0.f;
+}
+
+// Whether two of the `cnt` scores are one beam's, equal and of different logits, as seen by this
+// warp; by all threads.  Bits of `low` do not count; they hold a score's ~place in the lists,
+// or (low 0) score i is that of list i / depth, place i % depth.
+__device__ __noinline__ bool equal_scores_hide_keys(const ByKey &m, const uint64_t *score,
+                                                    uint64_t low, int cnt, int depth, int reach) {
+  const int lane = threadIdx.x & 31, M = m.num_select;
+  auto place_of = [&](int i) { return low ? (int)(~score[i] & low) : i / depth * M + i % depth; };
+  bool hidden = false;
+  for (int i0 = threadIdx.x - lane; i0 < cnt; i0 += blockDim.x) {
+    const int i = i0 + lane;
+    uint64_t mine = 0;
+    uint32_t logit = 0;
+    int beam = 0;
+    bool coarse = false;
+    if (i < cnt && score[i] != 0) {
+      const int at = place_of(i);
+      const uint64_t key = m.keys[at];
+      beam = at / M / m.splits;
+      mine = score[i] | low;
+      logit = (uint32_t)(key >> 32);
+      coarse = !m.done[beam] && score_is_coarse(m.base[beam], m.shift[beam], key, reach);
+    }
+    // the warp goes over all scores for each of its coarse ones
+    for (uint32_t left = __ballot_sync(0xffffffffu, coarse); left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      const uint64_t o = __shfl_sync(0xffffffffu, mine, from);
+      const uint32_t x = __shfl_sync(0xffffffffu, logit, from);
+      const int k = __shfl_sync(0xffffffffu, beam, from);
+      for (int j = lane; j < cnt; j += 32) {
+        if (score[j] == 0 || (score[j] | low) != o) continue;
+        const int at = place_of(j);
+        if (at / M / m.splits == k && (uint32_t)(m.keys[at] >> 32) != x) hidden = true;
+      }
+      if (__any_sync(0xffffffffu, hidden)) return true;
+    }
+  }
+  return hidden;
+}
+
+// A merge that compares candidates by score (all 64 bits), then beam, then key: by one warp, in
+// num_select rounds over the lists' heads, with their keys beside their scores.
 __device__ __noinline__ void merge_by_key(const ByKey &m) {
   const int lane = threadIdx.x & 31;
   auto enter = [&](int l, int n) {  // the n-th of list l as its head
@@ -511,7 +558,9 @@ __device__ __noinline__ void merge_by_key(const ByKey &m) {
 // lists' heads, so that the num_select best lists stay, and of the one of rank r num_select - r
 // keys only; then of those (15 lists by 10: the call 19.7 us, merged by rounds or one sort of
 // all 22.5; 11 lists by 31: this kernel 8.8, by rounds 14.7).  Of more than kFewLists heads a
-// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  Otherwise
+// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  From kMostKeys
+// on (32 kept of 32 lists; the call with 63 lists, counting / rounds: 32 kept 17.8 / 19.1 us, 36
+// 20.8 / 20.3, 44 31.3 / 22.9; 64 28.5 by rounds, 128 49) and beyond kPlaces
 // one warp merges them in num_select rounds over the heads, with as many scores as fit in
 // shared memory (a list's further ones are read when it gets there).
 //
@@ -519,10 +568,11 @@ __device__ __noinline__ void merge_by_key(const ByKey &m) {
 // equal to 2^-39 they count as equal.  Within a beam that is the order of the keys as long as
 // different logits have different scores: those of exponent e are 2^(e - 24) apart at least, scores
 // of exponent E are told apart by 2^(E - 39), by 2^(E - 52) in the rounds.  Where a candidate
-// fails that test (a beam at -1e9, a logit of 1e-5) and a beam has several lists, all is done
-// again by merge_by_key (4 beams of 32000 of which three are at -1e9: the call 12.6 us, else 7.5; 8 of
-// 128000, 16 kept: 46, else 12.4.  Keys compared everywhere instead: 8.8 us for any 4 beams, 79
-// instead of 50 for 128 kept of 63 lists).
+// fails that test (a beam at -1e9, a logit of 1e-5) and a beam has several lists, equal scores are
+// looked for, and where they hide different logits all is done again by merge_by_key (4 beams of
+// 32000 of which three are at -1e9: the call 20.7 us, else 7.5; 128 kept of a row at -1e12: 119, else
+// 50; 8 beams of 128000 log-probabilities, whose best are next to 0: 17, without the look 47.
+// Keys compared everywhere instead: 8.8 us for any 4 beams, 79 for 128 kept of 63 lists).
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
 constexpr int kFewLists = 64, kPlaces = 8192, kMostKeys = 512;
 constexpr int kSortReach = 39 - 24 - 2, kRoundReach = 52 - 24 - 2;  // (E is the base's here)
@@ -612,16 +662,14 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
   }
   __syncthreads();
   // the ordered score of a key of list l, its first or not (0: there is none)
-  bool close = false;  // whether one of this thread's scores may be another logit's, too
+  bool coarse = false;  // whether one of this thread's scores may be another logit's, too
   auto score_of = [&](int l, bool lead, uint64_t key, int reach) -> uint64_t {
     const int k = l / p.splits;
     const double base = s_base[k];
     if (s_done[k]) return lead && l == k * p.splits ? order_double(base) : 0;
     const float shift = s_shift[k];
     const uint64_t o = candidate_score(base, shift, key);
-    const int e_base = (__double2hiint(base) >> 20 & 0x7ff) - 1023;
-    const int e = (int)(__float_as_uint(key_value(key)) >> 23 & 0xff) - 127;
-    if (o != 0 && (e_base - e > reach || shift != 0.f)) close = true;
+    if (o != 0 && score_is_coarse(base, shift, key, reach)) coarse = true;
     return o;
   };
   auto put = [&](int i, uint64_t score, int l, uint64_t key) {
@@ -638,9 +686,12 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       put(i, won, l, won ? keys[(int64_t)l * M + s_at[i]] : 0);
     }
   };
+  auto by_key = [&] {
+    return ByKey{keys,   s_base, s_shift, s_done, s_head, s_score,  s_next,
+                 s_won,  s_list, s_at,    lists,  p.splits, M};
+  };
   auto put_by_key = [&] {
-    merge_by_key({keys, s_base, s_shift, s_done, s_head, s_score, s_next, s_won, s_list, s_at, lists,
-                  p.splits, M});
+    merge_by_key(by_key());
     put_won();
   };
   if (by_counting) {
@@ -671,7 +722,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       some = s_count;
     }
     if (tid < 64) s_some[some + tid] = 0;
-    __syncthreads();
+    bool look_closer = __syncthreads_or(coarse) && p.splits > 1, hidden = false;
+    if (look_closer)
+      hidden = equal_scores_hide_keys(by_key(), s_some, kPlace, some, 0, kSortReach);
     sort_keys<kMergeThreads>(s_some, some, s_best, M, s_next);
     // key d of the list of rank r, to place r M - r (r - 1) / 2 + d
     for (int i = tid; i < R * M; i += kMergeThreads) {
@@ -680,11 +733,13 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       s_some[i - r * (r - 1) / 2] = s_best[r] ? sort_score(at, at / M, d) : 0;
     }
     if (tid < 64) s_some[most + tid] = 0;
-    __syncthreads();
+    look_closer = __syncthreads_or(coarse) && p.splits > 1;
+    if (look_closer)  // (by all threads, whatever they have seen)
+      hidden |= equal_scores_hide_keys(by_key(), s_some, kPlace, most, 0, kSortReach);
     if (tid < M) s_best[tid] = 0;
     __syncthreads();
     sort_keys<kMergeThreads>(s_some, most, s_best, M, s_next);
-    if (p.splits == 1 || !__syncthreads_or(close)) {
+    if (!look_closer || !__syncthreads_or(hidden)) {
       if (tid < M) {
         const uint64_t best = s_best[tid];
         const int at = best ? place_of(best) : 0;
@@ -706,11 +761,18 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       s_next[l] = 0;
     }
   }
-  if (p.splits > 1 && __syncthreads_or(close)) {
-    if (tid < 32) put_by_key();
-    return;
+  // (of many coarse ones each would be compared with up to 2048)
+  const int num_coarse = __syncthreads_count(coarse);
+  if (num_coarse > 0 && p.splits > 1) {
+    bool hidden = num_coarse > 32;
+    if (!hidden)
+      hidden = equal_scores_hide_keys(by_key(), s_score, 0, lists * depth, depth, kRoundReach);
+    coarse = false;
+    if (__syncthreads_or(hidden)) {
+      if (tid < 32) put_by_key();
+      return;
+    }
   }
-  __syncthreads();
   if (tid >= 32) return;
   uint64_t best = 0;  // the best head of this lane's lists
   int best_list = tid;
@@ -745,7 +807,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
     }
     __syncwarp();
   }
-  if (p.splits > 1 && __any_sync(0xffffffffu, close)) put_by_key();
+  if (p.splits > 1 && __any_sync(0xffffffffu, coarse)) put_by_key();
   else put_won();
 }
 

@@ -775,3 +775,21 @@ def test_reserve_of_no_rows_gives_no_slot(pkv, cuda_device, on_stream):
     assert slots.cpu().tolist() == [-1] * 5 and src.numel() == 0 and dst.numel() == 0
     assert r.cpu().tolist() == [0] * 9
     pkv.reserve_blocks(cu, t, c, r, num_tokens=0)
+
+
+@pytest.mark.parametrize("b,k,v,num", [(1, 4, 32000, 8), (1, 1, 128000, 16), (1, 2, 128000, 128), (3, 70, 9001, 20)])
+def test_log_probabilities_of_confident_beams(pkv, cuda_device, b, k, v, num):
+    """Logits that are log-probabilities: the best of a beam next to 0, or 0 itself, beside others
+    far below; and some of them closer to each other than a score can tell."""
+    rng = np.random.default_rng(num)
+    x = beam_case(rng, b, k, v, torch.float32)
+    x[:, ::2, v // 3] = 30.0
+    x = torch.log_softmax(x, dim=-1)
+    x[:, ::3, v // 2] = 0.0
+    near = [v // 5, v // 4, v - 3]
+    x[:, k - 1, near] = torch.tensor([-1e-9, -3e-9, -2e-9])
+    cum = rng.uniform(-30, 0, (b, k)).astype(np.float32)
+    f64 = x.double().numpy()
+    want = ref.beam(f64, cum, num)
+    got = pkv.beam_select(x.to(cuda_device), torch.from_numpy(cum).to(cuda_device), num)
+    check_beams(got, want[:3], want[3], f64, None)
