@@ -717,8 +717,9 @@ PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t
  *   Within a beam candidates are ranked by their logits, between beams by the score to
  *   39 bits or more (of a log-sum accumulated in 32).  Candidates whose score is not finite
  *   in fp32 (masked logits of -inf; every one of a beam whose logits hold NaN or +inf, or with a
- *   cum_scores that is not finite) are never selected; finite logits may have any size; where too few remain, score -inf,
- *   token -1 and parent -1 fill the rest.  parents is what pkv_fork_sequences takes.
+ *   cum_scores that is not finite) are never selected; finite logits may have any size.  Where
+ *   too few candidates remain, score -inf, token -1 and parent -1 fill the rest.  parents is
+ *   what pkv_fork_sequences takes.
  *   logit_type: PKV_BF16, PKV_FP16 or PKV_FP32; logits aligned to their type.
  *   num_select <= 128, num_beams <= 1024, vocab >= 1.  workspace: device, 16-byte
  *   aligned, pkv_beam_workspace_size(...) bytes, contents do not matter; one call at a
@@ -765,12 +766,15 @@ PKV_API pkv_status pkv_update_block_index(const void *kv_pool, const pkv_pool_de
  * num_select of its blocks 0 .. p / 16: all of them if there are no more; otherwise
  * the first sink_blocks, the last recent_blocks (that of p among them) and, of the
  * rest, those with the largest scores, ties to the lower block.
- *   Score: an upper bound of the sum over the group's heads of q . k over the keys of
- *   the block.  With u the smallest power of two with |q| <= 2047 u in the group
- *   (infinities and NaN count as 0), P and N the sums over the heads of the positive
- *   and the negative elements of q / u, each rounded to an integer (to even):
+ *   Score: an upper bound, but for the rounding of q below, of the sum over the group's heads
+ *   of q . k over the keys of the block.  With u the smallest power of two with |q| <= 2047 u
+ *   in the group (infinities and NaN count as 0), P and N the sums over the heads of the
+ *   positive and the negative elements of q / u, each rounded to an integer (to even):
  *     score = float(sum_d P[d] hi[d] + N[d] lo[d]) * index_scale,
  *   an integer rounded once to fp32 and scaled: the same number in any order.
+ *   Every token reads its blocks' index rows for itself, so long chunks are for
+ *   pkv_paged_varlen_attention: with 64 blocks of 32 / 8 heads, D = 128, selection and
+ *   attention are faster up to some 64 tokens at 32768 keys and 400 at 131072.
  *   q: device bf16 [total_q][num_q_heads][D]; the group (num_q_heads / Hkv) is at most 16.
  *   cu_q_lens, context_lens, block_tables: DEVICE arrays as pkv_paged_varlen_attention
  *   takes them.  selected: device int32 [total_q][Hkv][num_select]: logical blocks,
@@ -804,17 +808,17 @@ PKV_API pkv_status pkv_select_blocks(const void *q, const int32_t *cu_q_lens,
  *   out[t][hq][:] = sum_p softmax_p(scale * q[t][hq] . K[p][h]) V[p][h],  h = hq / G,
  *   over the positions p <= the token's, p / 16 in selected[t][h].
  *   With every block of its context selected a token's result is that of
- *   pkv_paged_varlen_attention, but for the rounding of its weights.  selected: as pkv_select_blocks writes it, or a caller's
- *   own choice in any order (entries outside the token's blocks are skipped; one that
- *   is there twice counts twice).  A block id outside the pool is skipped,
- *   PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past cu_q_lens' last
- *   entry is left as it was; so is every token of a sequence whose context is shorter than
- *   its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.
- *   num_q_heads / Hkv <= 16.  Weights go into the
- *   product with V as two bf16 parts (2^-14 of a weight at most is lost), sums are fp32, out is
- *   rounded once to bf16.  Bytes of a visible block past the token's position do not
- *   reach its row.  out may be q itself, and must not overlap the inputs otherwise.  The lengths
- *   may be read before the preceding kernel has completed, everything else is touched after it.
+ *   pkv_paged_varlen_attention, but for the rounding of its weights.  selected: as
+ *   pkv_select_blocks writes it, or a caller's own choice in any order (entries outside the
+ *   token's blocks are skipped; one that is there twice counts twice).  A block id outside the
+ *   pool is skipped, PKV_DEV_BAD_BLOCK.  A token that sees no key gets zeros; one past
+ *   cu_q_lens' last entry is left as it was; so is every token of a sequence whose context is
+ *   shorter than its window or has more blocks than the table columns, PKV_DEV_PLAN_MISMATCH.
+ *   num_q_heads / Hkv <= 16.  Weights go into the product with V as two bf16 parts (2^-14 of a
+ *   weight at most is lost), sums are fp32, out is rounded once to bf16.  Bytes of a visible
+ *   block past the token's position do not reach its row.  out may be q itself, and must not
+ *   overlap the inputs otherwise.  The lengths may be read before the preceding kernel has
+ *   completed, everything else is touched after it.
  *   The next kernel may be launched while this one runs: out must not be the q of a
  *   pkv_paged_varlen_attention directly behind it (this call and the selection wait).
  */

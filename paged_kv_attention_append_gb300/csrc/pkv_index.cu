@@ -2,7 +2,8 @@
 //
 // Index.  For each block and KV head, bounds of the keys in 8 bits: with s the smallest
 // power of two >= 2^-64 with |K| <= 127 s, lo = floor(min K / s), hi = ceil(max K / s).
-// For any q, sum_d max(q_d lo_d, q_d hi_d) s >= q . k for every key of the block.
+// For any q, sum_d max(q_d lo_d, q_d hi_d) s >= q . k for every key of the block (the published
+// idea of bounding a page's q . k by its keys' least and largest values).
 //
 // Score of a block for a query token and KV head: that bound summed over the G query
 // heads of the group, with q in 11 bits and a sign.  max(q lo, q hi) is q hi for q > 0 and
