@@ -1284,9 +1284,9 @@ class BoundReserveBlocks(_BoundCall):
             raise ValueError("copy_src and copy_dst need one entry per row")
         ws = _pages_workspace(stream, block_tables, rows, ref_counts.shape[0])
         self.slot_mapping, self.copy_src, self.copy_dst = slot_mapping, copy_src, copy_dst
-        # without rows the library has nothing to do, but no slot is any row's
-        self._no_rows = rows == 0
-        self._torch_stream = stream or torch.cuda.current_stream(block_tables.device)
+        if rows == 0:   # the library has nothing to do, but no slot is any row's
+            self._fill_on = stream or torch.cuda.current_stream(block_tables.device)
+            self.run = self._run_without_rows
         self._bind("pkv_reserve_blocks", block_tables, stream,
                    (_vp(cu_new.data_ptr()), _vp(block_tables.data_ptr()),
                     _vp(context_lens.data_ptr()), _i32(rows), _i32(width),
@@ -1297,11 +1297,9 @@ class BoundReserveBlocks(_BoundCall):
                    (cu_new, block_tables, context_lens, ref_counts, slot_mapping, copy_src,
                     copy_dst, ws), dev_status)
 
-    def run(self) -> None:
-        super().run()
-        if self._no_rows:
-            with torch.cuda.stream(self._torch_stream):
-                self.slot_mapping.fill_(-1)
+    def _run_without_rows(self) -> None:
+        with torch.cuda.stream(self._fill_on):
+            self.slot_mapping.fill_(-1)
 
 
 def reserve_blocks(cu_new, block_tables, context_lens, ref_counts, *, num_tokens=None,
