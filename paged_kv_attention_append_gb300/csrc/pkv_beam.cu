@@ -451,6 +451,11 @@ struct ByKey {
 __device__ __forceinline__ uint64_t candidate_score(double base, float shift, uint64_t key) {
   return key ? order_double(base + (double)(key_value(key) - shift)) : 0;
 }
+// Whether that difference is rounded (then merge_by_key takes it in 64 bits).
+__device__ __forceinline__ bool difference_is_rounded(float shift, uint64_t key) {
+  const float x = key_value(key);
+  return shift != 0.f && (x - shift) + shift != x;
+}
 // Whether another logit than this key's may have the same score, told apart as `reach` says.
 __device__ __forceinline__ bool score_is_coarse(double base, float shift, uint64_t key, int reach) {
   const int e_base = (__double2hiint(base) >> 20 & 0x7ff) - 1023;
@@ -458,10 +463,10 @@ __device__ __forceinline__ bool score_is_coarse(double base, float shift, uint64
   return e_base - e > reach || shift != 0.f;
 }
 
-// Whether two of the `cnt` scores are one beam's, equal and of different logits, as seen by this
-// warp; by all threads.  Bits of `low` do not count; they hold a score's ~place in the lists,
+// Whether two of the `cnt` scores are one beam's, equal and of different logits, or one is not
+// as exact as it could be, as seen by this warp; by all threads.  Bits of `low` do not count; they hold a score's ~place in the lists,
 // or (low 0) score i is that of list i / depth, place i % depth.
-__device__ __noinline__ bool equal_scores_hide_keys(const ByKey &m, const uint64_t *score,
+__device__ __noinline__ bool scores_hide_keys(const ByKey &m, const uint64_t *score,
                                                     uint64_t low, int cnt, int depth, int reach) {
   const int lane = threadIdx.x & 31, M = m.num_select;
   auto place_of = [&](int i) { return low ? (int)(~score[i] & low) : i / depth * M + i % depth; };
@@ -479,6 +484,7 @@ __device__ __noinline__ bool equal_scores_hide_keys(const ByKey &m, const uint64
       mine = score[i] | low;
       logit = (uint32_t)(key >> 32);
       coarse = !m.done[beam] && score_is_coarse(m.base[beam], m.shift[beam], key, reach);
+      hidden |= coarse && difference_is_rounded(m.shift[beam], key);
     }
     // the warp goes over all scores for each of its coarse ones
     for (uint32_t left = __ballot_sync(0xffffffffu, coarse); left; left &= left - 1) {
@@ -506,7 +512,9 @@ __device__ __noinline__ void merge_by_key(const ByKey &m) {
     const uint64_t key = n < m.num_select ? m.keys[(int64_t)l * m.num_select + n] : 0;
     m.next[l] = n;
     m.low[l] = key;
-    if (!m.done[k]) m.head[l] = candidate_score(m.base[k], m.shift[k], key);
+    if (!m.done[k])
+      m.head[l] =
+          key ? order_double(m.base[k] + ((double)key_value(key) - (double)m.shift[k])) : 0;
     else m.head[l] = n == 0 && l == k * m.splits ? order_double(m.base[k]) : 0;
   };
   for (int l = lane; l < m.lists; l += 32) enter(l, 0);
@@ -662,6 +670,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
   }
   __syncthreads();
   // the ordered score of a key of list l, its first or not (0: there is none)
+  // (the order within a list is the keys' anyway, so with one list a beam only shifts matter)
+  const int sort_reach = p.splits > 1 ? kSortReach : INT32_MAX;
+  const int round_reach = p.splits > 1 ? kRoundReach : INT32_MAX;
   bool coarse = false;  // whether one of this thread's scores may be another logit's, too
   auto score_of = [&](int l, bool lead, uint64_t key, int reach) -> uint64_t {
     const int k = l / p.splits;
@@ -700,7 +711,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
     auto key_at = [&](int at) { return copied ? s_score[at] : keys[at]; };
     // key `at` of all, the d-th of list l: lower lists, and earlier keys, go first
     auto sort_score = [&](int at, int l, int d) -> uint64_t {
-      const uint64_t o = score_of(l, d == 0, key_at(at), kSortReach);
+      const uint64_t o = score_of(l, d == 0, key_at(at), sort_reach);
       return o ? (o & ~kPlace) | (kPlace - at) : 0;
     };
     uint64_t *s_some = s_head, *s_best = s_won;  // to be sorted, and the best of them
@@ -722,9 +733,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       some = s_count;
     }
     if (tid < 64) s_some[some + tid] = 0;
-    bool look_closer = __syncthreads_or(coarse) && p.splits > 1, hidden = false;
-    if (look_closer)
-      hidden = equal_scores_hide_keys(by_key(), s_some, kPlace, some, 0, kSortReach);
+    bool look_closer = __syncthreads_or(coarse), hidden = false;
+    if (look_closer) hidden = scores_hide_keys(by_key(), s_some, kPlace, some, 0, sort_reach);
     sort_keys<kMergeThreads>(s_some, some, s_best, M, s_next);
     // key d of the list of rank r, to place r M - r (r - 1) / 2 + d
     for (int i = tid; i < R * M; i += kMergeThreads) {
@@ -733,9 +743,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
       s_some[i - r * (r - 1) / 2] = s_best[r] ? sort_score(at, at / M, d) : 0;
     }
     if (tid < 64) s_some[most + tid] = 0;
-    look_closer = __syncthreads_or(coarse) && p.splits > 1;
+    look_closer = __syncthreads_or(coarse);
     if (look_closer)  // (by all threads, whatever they have seen)
-      hidden |= equal_scores_hide_keys(by_key(), s_some, kPlace, most, 0, kSortReach);
+      hidden |= scores_hide_keys(by_key(), s_some, kPlace, most, 0, sort_reach);
     if (tid < M) s_best[tid] = 0;
     __syncthreads();
     sort_keys<kMergeThreads>(s_some, most, s_best, M, s_next);
@@ -754,7 +764,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
   const int depth = min(M, kMergeScores / lists);
   for (int i = tid; i < lists * depth; i += kMergeThreads) {
     const int l = i / depth, n = i % depth;
-    const uint64_t o = score_of(l, n == 0, keys[(int64_t)l * M + n], kRoundReach);
+    const uint64_t o = score_of(l, n == 0, keys[(int64_t)l * M + n], round_reach);
     s_score[i] = o;
     if (n == 0) {
       s_head[l] = o;
@@ -763,10 +773,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
   }
   // (of many coarse ones each would be compared with up to 2048)
   const int num_coarse = __syncthreads_count(coarse);
-  if (num_coarse > 0 && p.splits > 1) {
+  if (num_coarse > 0) {
     bool hidden = num_coarse > 32;
     if (!hidden)
-      hidden = equal_scores_hide_keys(by_key(), s_score, 0, lists * depth, depth, kRoundReach);
+      hidden = scores_hide_keys(by_key(), s_score, 0, lists * depth, depth, round_reach);
     coarse = false;
     if (__syncthreads_or(hidden)) {
       if (tid < 32) put_by_key();
@@ -801,13 +811,13 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
         s_head[l] = n + 1 >= M       ? 0
                     : n + 1 < depth ? s_score[(int)l * depth + n + 1]
                                     : score_of((int)l, false, keys[(int64_t)l * M + n + 1],
-                                               kRoundReach);
+                                               round_reach);
         look();
       }
     }
     __syncwarp();
   }
-  if (p.splits > 1 && __any_sync(0xffffffffu, coarse)) put_by_key();
+  if (__any_sync(0xffffffffu, coarse)) put_by_key();
   else put_won();
 }
 

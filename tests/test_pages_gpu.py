@@ -793,3 +793,10 @@ def test_log_probabilities_of_confident_beams(pkv, cuda_device, b, k, v, num):
     want = ref.beam(f64, cum, num)
     got = pkv.beam_select(x.to(cuda_device), torch.from_numpy(cum).to(cuda_device), num)
     check_beams(got, want[:3], want[3], f64, None)
+
+
+def test_scores_of_far_logits_are_rounded_once(pkv, cuda_device):
+    """-1e10 beside -1e9: the difference is a tie between two fp32 numbers, the score is not."""
+    x = torch.tensor([[[-1e9, -1e10, -1e10]]], device=cuda_device)
+    s, t, _ = pkv.beam_select(x, torch.tensor([[-28.85]], device=cuda_device), 3)
+    assert t[0].tolist() == [0, 1, 2] and s[0].tolist() == [np.float32(-28.85), -9000000512.0, -9000000512.0]
