@@ -31,7 +31,8 @@ __device__ __forceinline__ TokenPlace find_token(const int32_t *cu_q_lens,
   if (at.seq < num_seqs) {
     const int32_t end = __ldg(cu_q_lens + at.seq + 1), first = __ldg(cu_q_lens + at.seq);
     const int32_t ctx = __ldg(context_lens + at.seq);
-    if (end - first <= ctx && (ctx - 1) / kBlockSize < max_blocks && token >= first)
+    // (token < end always, unless cu_q_lens falls: then a position may be past the table)
+    if (end - first <= ctx && (ctx - 1) / kBlockSize < max_blocks && token >= first && token < end)
       at.pos = ctx - (int32_t)(end - token);
   }
   return at;

@@ -743,3 +743,23 @@ def test_selection_and_attention_right_behind_a_page_call(pkv, cuda_device, firs
             np.testing.assert_array_equal(sel.selected[r].cpu().numpy(), chosen)
             want, mag, dots = ref.sparse_attention(xs[r], c[r] - 1, t[r], chosen, held, scale)
             check_out(att.out[r], want, mag, dots, d)
+
+
+def test_lengths_that_fall_stay_in_bounds(pkv, cuda_device):
+    """cu_q_lens that is not non-decreasing: a token behind the end of the sequence it is counted
+    into has no place, so no position past the table is looked up."""
+    dev = cuda_device
+    rng = np.random.default_rng(6)
+    pool = make_pool(rng, 64, 1, 64)
+    index, unit = (torch.as_tensor(x).to(dev) for x in whole_index(pool))
+    table = rng.permutation(64)[:40].reshape(4, 10)
+    q = bf16(rng.standard_normal((400, 2, 64))).to(dev)
+    on = [q, *(dev_i32(x, dev) for x in ([0, 300, 1, 2, 400], [160, 160, 160, 160], table))]
+    st = status_of(dev)
+    sel = pkv.select_blocks(*on, index, unit, 4, dev_status=st)
+    assert int(st.item()) == 4 and int(sel[2:300].max()) == -1 and int(sel.max()) < 10
+    st.zero_()
+    out = torch.full_like(q, 7.0)
+    pkv.paged_sparse_attention(*on, dev_i32(np.zeros((400, 1, 4)), dev), pool.to(dev), 0.1, out=out,
+                               dev_status=st)
+    assert int(st.item()) == 4 and bool((out[2:300] == 7.0).all())
