@@ -695,7 +695,8 @@ PKV_API pkv_status pkv_reserve_blocks(const int32_t *cu_new, int32_t *block_tabl
  * to *num_pairs (device int32), for a pkv_copy_blocks.  new_tables gets the used entries
  * renamed, new_ref_counts the counts at the new ids.  new_tables may be block_tables and
  * new_ref_counts ref_counts (in place).  A used entry of a block whose count is 0 and whose
- * id is >= L keeps its id, PKV_DEV_BAD_COUNT.  workspace as for pkv_reserve_blocks.
+ * id is >= L keeps its id, PKV_DEV_BAD_COUNT.  A caller that holds blocks outside the tables
+ * renames them by the pairs.  workspace as for pkv_reserve_blocks.
  */
 PKV_API pkv_status pkv_compact_blocks(const int32_t *block_tables, const int32_t *context_lens,
                                       int32_t num_rows, int32_t max_blocks_per_seq,

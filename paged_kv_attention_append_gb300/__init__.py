@@ -1362,7 +1362,7 @@ def compact_blocks(block_tables, context_lens, ref_counts, *, new_tables=None, n
     """Rename the blocks in use to the ids 0 .. L - 1 (pkv_compact_blocks), in place unless
     new_tables / new_ref_counts are given.  Returns (copy_src, copy_dst, num_pairs) for the
     copy_blocks that moves them: int32 [num_blocks // 2], -1 past the last pair, and their
-    number, int32 [1] on the device."""
+    number, int32 [1] on the device.  Blocks held outside the tables are renamed by the pairs."""
     b = BoundCompactBlocks(block_tables, context_lens, ref_counts, new_tables=new_tables,
                            new_ref_counts=new_ref_counts, copy_src=copy_src, copy_dst=copy_dst,
                            num_pairs=num_pairs, dev_status=dev_status, stream=stream)

@@ -463,11 +463,11 @@ __device__ __forceinline__ bool score_is_coarse(double base, float shift, uint64
   return e_base - e > reach || shift != 0.f;
 }
 
-// Whether two of the `cnt` scores are one beam's, equal and of different logits, or one is not
-// as exact as it could be, as seen by this warp; by all threads.  Bits of `low` do not count; they hold a score's ~place in the lists,
-// or (low 0) score i is that of list i / depth, place i % depth.
-__device__ __noinline__ bool scores_hide_keys(const ByKey &m, const uint64_t *score,
-                                                    uint64_t low, int cnt, int depth, int reach) {
+// Whether two of the `cnt` scores are one beam's, equal and of different logits, or one is of a
+// rounded difference, as seen by this warp; by all threads.  Bits of `low` do not count; they
+// hold a score's ~place in the lists, or (low 0) score i is that of list i / depth, place i % depth.
+__device__ __noinline__ bool scores_hide_keys(const ByKey &m, const uint64_t *score, uint64_t low,
+                                              int cnt, int depth, int reach) {
   const int lane = threadIdx.x & 31, M = m.num_select;
   auto place_of = [&](int i) { return low ? (int)(~score[i] & low) : i / depth * M + i % depth; };
   bool hidden = false;
@@ -566,21 +566,21 @@ __device__ __noinline__ void merge_by_key(const ByKey &m) {
 // lists' heads, so that the num_select best lists stay, and of the one of rank r num_select - r
 // keys only; then of those (15 lists by 10: the call 19.7 us, merged by rounds or one sort of
 // all 22.5; 11 lists by 31: this kernel 8.8, by rounds 14.7).  Of more than kFewLists heads a
-// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  From kMostKeys
-// on (32 kept of 32 lists; the call with 63 lists, counting / rounds: 32 kept 17.8 / 19.1 us, 36
-// 20.8 / 20.3, 44 31.3 / 22.9; 64 28.5 by rounds, 128 49) and beyond kPlaces
-// one warp merges them in num_select rounds over the heads, with as many scores as fit in
-// shared memory (a list's further ones are read when it gets there).
+// threshold leaves a few to sort (600 lists by 3: the call 13.7 us, by rounds 18).  Beyond
+// kMostKeys (32 kept of 32 lists; the call with 63 lists, by counting / by rounds: 32 kept 17.8 /
+// 19.1 us, 36 20.8 / 20.3, 44 31.3 / 22.9; by rounds 64 28.5, 128 49) and beyond kPlaces one warp
+// merges them in num_select rounds over the heads, with as many scores as fit in shared memory (a
+// list's further ones are read when it gets there).
 //
 // Scores are fp64; to be sorted they take their key's place in the lists into their last 13 bits:
 // equal to 2^-39 they count as equal.  Within a beam that is the order of the keys as long as
 // different logits have different scores: those of exponent e are 2^(e - 24) apart at least, scores
 // of exponent E are told apart by 2^(E - 39), by 2^(E - 52) in the rounds.  Where a candidate
 // fails that test (a beam at -1e9, a logit of 1e-5) and a beam has several lists, equal scores are
-// looked for, and where they hide different logits all is done again by merge_by_key (4 beams of
-// 32000 of which three are at -1e9: the call 20.7 us, else 7.5; 128 kept of a row at -1e12: 119, else
-// 50; 8 beams of 128000 log-probabilities, whose best are next to 0: 17, without the look 47.
-// Keys compared everywhere instead: 8.8 us for any 4 beams, 79 for 128 kept of 63 lists).
+// looked for, and where they hide different logits all is done again by merge_by_key (4 beams
+// of 32000 of which three are at -1e9: the call 20.7 us, else 7.5; 128 kept of a row at -1e12:
+// 119, else 50; 8 beams of 128000 log-probabilities, whose best are next to 0: 17, without the
+// look 47.  Keys compared everywhere instead: 8.8 us for any 4 beams, 79 for 128 of 63 lists).
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
 constexpr int kFewLists = 64, kPlaces = 8192, kMostKeys = 512;
 constexpr int kSortReach = 39 - 24 - 2, kRoundReach = 52 - 24 - 2;  // (E is the base's here)
@@ -698,8 +698,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) beam_merge_kernel(const Beam
     }
   };
   auto by_key = [&] {
-    return ByKey{keys,   s_base, s_shift, s_done, s_head, s_score,  s_next,
-                 s_won,  s_list, s_at,    lists,  p.splits, M};
+    return ByKey{keys,  s_base, s_shift, s_done, s_head,   s_score, s_next,
+                 s_won, s_list, s_at,    lists,  p.splits, M};
   };
   auto put_by_key = [&] {
     merge_by_key(by_key());
