@@ -10,11 +10,11 @@
 // with an online softmax in registers.  The warps' (m, l, O) meet in shared memory, over
 // the cluster through distributed shared memory, each CTA joining a part of the columns:
 // one launch, no workspace, and a fixed order of every sum.  (A pair of one CTA is launched
-// without clusters: 256 decodes of 64 blocks 81 us for the three calls, with them 85.)
+// without clusters: 256 decodes of 64 blocks 84 us for the three calls, with them 89.)
 //
 // Weights go into the product with V as two bf16 parts, so that the output is as exact as with
 // weights of 32 bits (2-norm error 0.0017, all of it the last rounding; with one part 0.0021;
-// 24 decodes of 128 blocks 107.2 us for the three calls, 107.0 with one).
+// 24 decodes of 128 blocks 107.2 us for the three calls, 107.0 with one; 61 windows 20.1, 19.0).
 //
 // Bound: the selected blocks' K and V, 64 D bytes a block and KV head.
 #include <cuda_runtime.h>
@@ -44,7 +44,7 @@ struct SparseCfg {
   static constexpr int kCtasPerSm = 12 / kWarps;
   // 8 KB a warp and stage at D = 128: with two stages three CTAs share an SM, so that the
   // (token, head) pairs of a call spread more evenly (192 pairs of 128 blocks: 38 us; three
-  // stages and two CTAs 46)
+  // stages and two CTAs 45)
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kSlabBytes = D / 64 * kBoxBytes;
   static constexpr int kStageBytes = 2 * kSlabBytes;
@@ -303,9 +303,9 @@ template <int D>
 cudaError_t launch_sparse(const CUtensorMap &map, const SparseParams &p, int64_t total_q,
                           pkv_stream stream) {
   // CTAs of a (token, KV head): more while there are fewer than two CTAs an SM and every
-  // warp would still have two blocks (192 pairs of 128 blocks: two each 38 us, four 45; the
-  // 8 pairs of one token, 32 blocks: the three calls 10.8 us with four each, 11.5 with
-  // eight, 11.7 with two)
+  // warp would still have two blocks (192 pairs of 128 blocks: two each 38 us, four 42.5; the
+  // 8 pairs of one token, 32 blocks: the three calls 11.8 us with four each, 12.2 with
+  // eight, 12.8 with two)
   int ranks = 1;
   while (ranks < 8 && total_q * p.hkv * ranks < 2ll * std::max(device_sm_count(), 1) &&
          16 * ranks <= p.num_select)
